@@ -28,6 +28,7 @@ __all__ = [
     "gemm_q4_ws", "gemm_q4_workspace_size", "Q4_DEQUANT_ROWS",
     "Q4_AUTO", "Q4_FFMA", "Q4_MMA", "gemm_set_q4_kernel",
     "gemm_ex", "gemm_get_tuning", "MX_E4M3", "MX_E2M1", "gemm_mx", "gemm_mx_workspace_size",
+    "gemm_grouped", "gemm_grouped_wgrad", "gemm_i8", "gemm_i8_grouped", "gemm_i8_quantize", "MAX_GROUPS", "I8_MAX_K",
     "gemm_set_tile_policy", "gemm_query_tile", "gemm_set_schedule", "gemm_builtin_scratch", "gemm_wait_selftest",
     "gemm_device_status", "gemm_status_string", "gemm_version", "LIB_PATH", "lib",
 ]
@@ -53,6 +54,8 @@ Q4_MAX_ROWS = 8
 Q4_DEQUANT_ROWS = 384  # GEMM_Q4_DEQUANT_ROWS: from this many rows of x gemm_q4_ws expands W once
 # gemm_q4_kernel_t
 Q4_AUTO, Q4_FFMA, Q4_MMA = 0, 1, 2
+MAX_GROUPS = 1024    # GEMM_MAX_GROUPS: groups (experts) of one grouped call
+I8_MAX_K = 131071    # GEMM_I8_MAX_K: longest sum of the 8-bit integer products
 # gemm_mx_elem_t
 MX_E4M3, MX_E2M1 = 0, 1
 # gemm_status_t
@@ -148,6 +151,19 @@ lib.gemm_mx.argtypes = [_i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _i64, _vp, 
                         _int, _vp, _sz, _vp]
 lib.gemm_mx_workspace_size.restype = _sz
 lib.gemm_mx_workspace_size.argtypes = [_i64, _i64, _i64, _int]
+lib.gemm_grouped.restype = _int
+lib.gemm_grouped.argtypes = [_i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _vp, _i64, _int,
+                             _f32, _f32, _vp, _int, _vp, _vp]
+lib.gemm_grouped_wgrad.restype = _int
+lib.gemm_grouped_wgrad.argtypes = [_i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64,
+                                   _int, _f32, _f32, _vp, _vp]
+lib.gemm_i8.restype = _int
+lib.gemm_i8.argtypes = [_i64, _i64, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _int, _f32, _f32, _vp, _int, _vp]
+lib.gemm_i8_grouped.restype = _int
+lib.gemm_i8_grouped.argtypes = [_i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _int,
+                                _f32, _f32, _vp, _int, _vp]
+lib.gemm_i8_quantize.restype = _int
+lib.gemm_i8_quantize.argtypes = [_i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp]
 lib.gemm_device_status.restype = _int
 lib.gemm_device_status.argtypes = [_vp]
 lib.gemm_status_string.restype = ctypes.c_char_p
@@ -328,6 +344,50 @@ def gemm_mx(M, N, K, elem, A, lda, a_scale, B, ldb, b_scale, C, ldc, c_dtype, al
 
 def gemm_mx_workspace_size(M, N, K, elem) -> int:
     return int(lib.gemm_mx_workspace_size(M, N, K, elem))
+
+
+def gemm_grouped(G, M, N, K, ab_dtype, offsets, A, a_stride_m, a_stride_k, B, b_stride_g, b_stride_k, b_stride_n, C,
+                 ldc, c_dtype, alpha, beta, bias, epilogue, row_scale=None, stream=None) -> int:
+    """Products grouped by expert: rows offsets[g]..offsets[g+1]-1 of A (M x K) times B[g] (K x N), with the
+    epilogue and bias[g]; ``offsets`` is an int32 device array of G + 1.  Swap b_stride_k and b_stride_n for
+    the gradient of the rows.  See include/gemm_gb300.h."""
+    st = lib.gemm_grouped(G, M, N, K, ab_dtype, _ptr(offsets), _ptr(A), a_stride_m, a_stride_k, _ptr(B), b_stride_g,
+                          b_stride_k, b_stride_n, _ptr(C), ldc, c_dtype, alpha, beta, _ptr(bias), epilogue,
+                          _ptr(row_scale), _stream(stream))
+    return _check(st, "gemm_grouped")
+
+
+def gemm_grouped_wgrad(G, T, M, N, ab_dtype, offsets, A, a_stride_r, a_stride_m, D, d_stride_r, d_stride_n, C,
+                       c_stride_g, ldc, c_dtype, alpha, beta, a_sum=None, stream=None) -> int:
+    """Weight gradient of gemm_grouped: C[g] = alpha * A_g^T D_g + beta * C[g] over the rows of group g, and
+    (optional) a_sum[g] = alpha * column sums of A_g + beta * a_sum[g], the bias gradient."""
+    st = lib.gemm_grouped_wgrad(G, T, M, N, ab_dtype, _ptr(offsets), _ptr(A), a_stride_r, a_stride_m, _ptr(D),
+                                d_stride_r, d_stride_n, _ptr(C), c_stride_g, ldc, c_dtype, alpha, beta, _ptr(a_sum),
+                                _stream(stream))
+    return _check(st, "gemm_grouped_wgrad")
+
+
+def gemm_i8(M, N, K, X, ldx, x_scale, W, ldw, w_scale, C, ldc, c_dtype, alpha, beta, bias, epilogue,
+            stream=None) -> int:
+    """C = cast(epilogue(alpha * x_scale[i] * w_scale[j] * sum_k X[i][k] W[j][k] + beta*C + bias)) over 8-bit
+    integers (X: M x ldx, W: N x ldw), the integer sum exact."""
+    st = lib.gemm_i8(M, N, K, _ptr(X), ldx, _ptr(x_scale), _ptr(W), ldw, _ptr(w_scale), _ptr(C), ldc, c_dtype, alpha,
+                     beta, _ptr(bias), epilogue, _stream(stream))
+    return _check(st, "gemm_i8")
+
+
+def gemm_i8_grouped(G, M, N, K, offsets, X, ldx, x_scale, W, w_stride_g, ldw, w_scale, C, ldc, c_dtype, alpha, beta,
+                    bias, epilogue, stream=None) -> int:
+    """gemm_i8 grouped by expert (W: G x N x ldw with w_stride_g between experts, w_scale and bias G x N)."""
+    st = lib.gemm_i8_grouped(G, M, N, K, _ptr(offsets), _ptr(X), ldx, _ptr(x_scale), _ptr(W), w_stride_g, ldw,
+                             _ptr(w_scale), _ptr(C), ldc, c_dtype, alpha, beta, _ptr(bias), epilogue, _stream(stream))
+    return _check(st, "gemm_i8_grouped")
+
+
+def gemm_i8_quantize(M, K, x_dtype, X, ldx, Q, ldq, scale, stream=None) -> int:
+    """Rows of X to 8-bit codes Q = round(127 x / max|x|) and scale = max|x| / 127 (fp32, one per row)."""
+    st = lib.gemm_i8_quantize(M, K, x_dtype, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale), _stream(stream))
+    return _check(st, "gemm_i8_quantize")
 
 
 def gemm_last_launch() -> dict:

@@ -1282,6 +1282,223 @@ gemm_status_t gemm_mx(int64_t M, int64_t N, int64_t K, gemm_mx_elem_t elem, cons
     return record(launch_mx(elem, c_dtype, ta, tb, a, grid, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
 }
 
+// ------------------------------------------------- grouped and 8-bit products --
+
+// Blocks of a CUDA-core grouped kernel: at most eight per SM, never more than its tiles could be.
+static int simt_grid(const DeviceState *dev, int64_t row_tiles, int64_t col_tiles) {
+    const int64_t cap = static_cast<int64_t>(dev->num_sms) * 8;
+    if (row_tiles >= cap || col_tiles >= cap) return static_cast<int>(cap);
+    return static_cast<int>(std::min(cap, std::max<int64_t>(1, row_tiles * col_tiles)));
+}
+
+// Bytes from the first to the last element of an n0 x n1 x n2 array with element strides s0, s1, s2 (all
+// non-negative); a size no allocation has where the product leaves 62 bits.
+static size_t extent_bytes(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64_t n2, int64_t s2, int es) {
+    if (n0 <= 0 || n1 <= 0 || n2 <= 0) return 0;
+    using Wide = unsigned __int128;
+    const Wide last = Wide(n0 - 1) * Wide(s0) + Wide(n1 - 1) * Wide(s1) + Wide(n2 - 1) * Wide(s2);
+    constexpr Wide kMost = Wide(1) << 62;
+    return static_cast<size_t>(last >= kMost ? kMost : std::min(kMost, (last + 1) * Wide(es)));
+}
+
+// Argument rules that every grouped call shares.  Sets *noop where there is nothing to do.
+static gemm_status_t grouped_rules(int64_t G, int64_t M, int64_t N, int64_t K, const void *C, int64_t ldc, int cd,
+                                   const float *bias, int epi, bool *noop) {
+    *noop = false;
+    if (G < 0 || M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+    if (!valid_dtype(cd) || epi < GEMM_EPI_NONE || epi > GEMM_EPI_BIAS_RELU) return GEMM_ERR_INVALID_ARG;
+    if (cd == GEMM_E4M3) return GEMM_ERR_UNSUPPORTED;
+    if (G == 0 || M == 0 || N == 0) {
+        *noop = true;
+        return GEMM_OK;
+    }
+    if (G > GEMM_MAX_GROUPS || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (C == nullptr || ldc < N) return GEMM_ERR_INVALID_ARG;
+    if (epi != GEMM_EPI_NONE && bias == nullptr) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+// The product behind gemm_grouped, gemm_i8 and gemm_i8_grouped (ab: a gemm_dtype_t or kDtI8), arguments checked.
+static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, DeviceState *dev, cudaStream_t s) {
+    gemm_launch_info_t info = {};
+    info.path = args.K == 0 ? GEMM_PATH_EPILOGUE_ONLY : GEMM_PATH_SIMT;
+    const int grid = simt_grid(dev, (args.M + 63) / 64 + args.G, (args.N + 63) / 64);
+    return record(launch_grouped_simt(ab, cd, args, grid, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
+}
+
+gemm_status_t gemm_grouped(int64_t G, int64_t M, int64_t N, int64_t K, gemm_dtype_t ab_dtype, const int32_t *offsets,
+                           const void *A, int64_t a_stride_m, int64_t a_stride_k, const void *B, int64_t b_stride_g,
+                           int64_t b_stride_k, int64_t b_stride_n, void *C, int64_t ldc, gemm_dtype_t c_dtype,
+                           float alpha, float beta, const float *bias, gemm_epilogue_t epilogue,
+                           const float *row_scale, gemm_stream_t stream) {
+    bool noop;
+    gemm_status_t st = grouped_rules(G, M, N, K, C, ldc, c_dtype, bias, epilogue, &noop);
+    if (st != GEMM_OK) return st;
+    if (!valid_dtype(ab_dtype)) return GEMM_ERR_INVALID_ARG;
+    if (ab_dtype == GEMM_E4M3 || (ab_dtype == GEMM_F32 && c_dtype != GEMM_F32)) return GEMM_ERR_UNSUPPORTED;
+    if (noop) return record(GEMM_OK, gemm_launch_info_t{});
+    if (offsets == nullptr) return GEMM_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(offsets) & 3u) != 0) return GEMM_ERR_MISALIGNED;
+    const bool product = K > 0 && alpha != 0.0f;
+    if (product) {
+        if (A == nullptr || B == nullptr) return GEMM_ERR_INVALID_ARG;
+        if (a_stride_m < 0 || a_stride_k < 0 || b_stride_g < 0 || b_stride_k < 0 || b_stride_n < 0)
+            return GEMM_ERR_INVALID_ARG;
+    }
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    const int es = elem_bytes(ab_dtype);
+    if ((st = check_range(offsets, static_cast<size_t>(G + 1) * 4)) != GEMM_OK) return st;
+    if ((st = check_range(C, extent_bytes(1, 0, M, ldc, N, 1, elem_bytes(c_dtype)))) != GEMM_OK) return st;
+    if (epilogue != GEMM_EPI_NONE && (st = check_range(bias, static_cast<size_t>(G) * N * 4)) != GEMM_OK) return st;
+    if (product) {
+        if ((st = check_range(A, extent_bytes(1, 0, M, a_stride_m, K, a_stride_k, es))) != GEMM_OK) return st;
+        if ((st = check_range(B, extent_bytes(G, b_stride_g, K, b_stride_k, N, b_stride_n, es))) != GEMM_OK) return st;
+        if (row_scale != nullptr && (st = check_range(row_scale, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
+    }
+    GroupedArgs a = {};
+    a.G = static_cast<int>(G);
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = product ? static_cast<int>(K) : 0;
+    a.offsets = offsets;
+    a.A = A; a.sam = a_stride_m; a.sak = a_stride_k;
+    a.B = B; a.sbg = b_stride_g; a.sbk = b_stride_k; a.sbn = b_stride_n;
+    a.C = C; a.ldc = ldc;
+    a.bias = bias;
+    a.row_scale = product ? row_scale : nullptr;
+    a.alpha = alpha; a.beta = beta; a.epilogue = epilogue;
+    a.status = dev->status;
+    return grouped_launch(a, ab_dtype, c_dtype, dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gemm_dtype_t ab_dtype,
+                                 const int32_t *offsets, const void *A, int64_t a_stride_r, int64_t a_stride_m,
+                                 const void *D, int64_t d_stride_r, int64_t d_stride_n, void *C, int64_t c_stride_g,
+                                 int64_t ldc, gemm_dtype_t c_dtype, float alpha, float beta, float *a_sum,
+                                 gemm_stream_t stream) {
+    if (G < 0 || T < 0 || M < 0 || N < 0) return GEMM_ERR_INVALID_ARG;
+    if (!valid_dtype(ab_dtype) || !valid_dtype(c_dtype)) return GEMM_ERR_INVALID_ARG;
+    if (ab_dtype == GEMM_E4M3 || c_dtype == GEMM_E4M3 || (ab_dtype == GEMM_F32 && c_dtype != GEMM_F32))
+        return GEMM_ERR_UNSUPPORTED;
+    if (G == 0 || M == 0 || N == 0) return record(GEMM_OK, gemm_launch_info_t{});
+    if (G > GEMM_MAX_GROUPS || T > INT32_MAX || M > INT32_MAX || N > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (offsets == nullptr || C == nullptr || ldc < N) return GEMM_ERR_INVALID_ARG;
+    // groups of C must not overlap: they are written
+    if (G > 1 && (c_stride_g < 0 || extent_bytes(1, 0, M, ldc, N, 1, 1) > static_cast<size_t>(c_stride_g)))
+        return GEMM_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(offsets) & 3u) != 0 || (reinterpret_cast<uintptr_t>(a_sum) & 3u) != 0)
+        return GEMM_ERR_MISALIGNED;
+    const bool product = T > 0 && alpha != 0.0f;
+    if (product) {
+        if (A == nullptr || D == nullptr) return GEMM_ERR_INVALID_ARG;
+        if (a_stride_r < 0 || a_stride_m < 0 || d_stride_r < 0 || d_stride_n < 0) return GEMM_ERR_INVALID_ARG;
+    }
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    gemm_status_t st;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    const int es = elem_bytes(ab_dtype), ces = elem_bytes(c_dtype);
+    if ((st = check_range(offsets, static_cast<size_t>(G + 1) * 4)) != GEMM_OK) return st;
+    if ((st = check_range(C, extent_bytes(G, G > 1 ? c_stride_g : 0, M, ldc, N, 1, ces))) != GEMM_OK) return st;
+    if (a_sum != nullptr && (st = check_range(a_sum, static_cast<size_t>(G) * M * 4)) != GEMM_OK) return st;
+    if (product) {
+        if ((st = check_range(A, extent_bytes(1, 0, T, a_stride_r, M, a_stride_m, es))) != GEMM_OK) return st;
+        if ((st = check_range(D, extent_bytes(1, 0, T, d_stride_r, N, d_stride_n, es))) != GEMM_OK) return st;
+    }
+    WgradArgs a = {};
+    a.G = static_cast<int>(G);
+    a.T = static_cast<int>(T);
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.offsets = offsets;
+    a.A = A; a.sar = a_stride_r; a.sam = a_stride_m;
+    a.D = D; a.sdr = d_stride_r; a.sdn = d_stride_n;
+    a.C = C; a.scg = c_stride_g; a.ldc = ldc;
+    a.a_sum = a_sum;
+    a.alpha = product ? alpha : 0.0f;
+    a.beta = beta;
+    a.status = dev->status;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (a_sum != nullptr && launch_grouped_colsum(ab_dtype, a, s) != cudaSuccess) return GEMM_ERR_CUDA;
+    gemm_launch_info_t info = {};
+    info.path = product ? GEMM_PATH_SIMT : GEMM_PATH_EPILOGUE_ONLY;
+    const int grid = simt_grid(dev, G * ((M + 63) / 64), (N + 63) / 64);
+    return record(launch_wgrad_simt(ab_dtype, c_dtype, a, grid, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
+}
+
+gemm_status_t gemm_i8_grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *offsets, const int8_t *X,
+                              int64_t ldx, const float *x_scale, const int8_t *W, int64_t w_stride_g, int64_t ldw,
+                              const float *w_scale, void *C, int64_t ldc, gemm_dtype_t c_dtype, float alpha,
+                              float beta, const float *bias, gemm_epilogue_t epilogue, gemm_stream_t stream) {
+    bool noop;
+    gemm_status_t st = grouped_rules(G, M, N, K, C, ldc, c_dtype, bias, epilogue, &noop);
+    if (st != GEMM_OK) return st;
+    if (noop) return record(GEMM_OK, gemm_launch_info_t{});
+    if (K > GEMM_I8_MAX_K) return GEMM_ERR_UNSUPPORTED;
+    if (offsets == nullptr && G != 1) return GEMM_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(offsets) & 3u) != 0) return GEMM_ERR_MISALIGNED;
+    const bool product = K > 0 && alpha != 0.0f;
+    if (product && (X == nullptr || W == nullptr || ldx < K || ldw < K || w_stride_g < 0)) return GEMM_ERR_INVALID_ARG;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if (offsets != nullptr && (st = check_range(offsets, static_cast<size_t>(G + 1) * 4)) != GEMM_OK) return st;
+    if ((st = check_range(C, extent_bytes(1, 0, M, ldc, N, 1, elem_bytes(c_dtype)))) != GEMM_OK) return st;
+    if (epilogue != GEMM_EPI_NONE && (st = check_range(bias, static_cast<size_t>(G) * N * 4)) != GEMM_OK) return st;
+    if (product) {
+        if ((st = check_range(X, extent_bytes(1, 0, M, ldx, K, 1, 1))) != GEMM_OK) return st;
+        if ((st = check_range(W, extent_bytes(G, w_stride_g, N, ldw, K, 1, 1))) != GEMM_OK) return st;
+        if (x_scale != nullptr && (st = check_range(x_scale, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
+        if (w_scale != nullptr && (st = check_range(w_scale, static_cast<size_t>(G) * N * 4)) != GEMM_OK) return st;
+    }
+    GroupedArgs a = {};
+    a.G = static_cast<int>(G);
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = product ? static_cast<int>(K) : 0;
+    a.offsets = offsets;
+    a.A = X; a.sam = ldx; a.sak = 1;
+    a.B = W; a.sbg = w_stride_g; a.sbk = 1; a.sbn = ldw;
+    a.C = C; a.ldc = ldc;
+    a.bias = bias;
+    a.row_scale = product ? x_scale : nullptr;
+    a.col_scale = product ? w_scale : nullptr;
+    a.alpha = alpha; a.beta = beta; a.epilogue = epilogue;
+    a.status = dev->status;
+    return grouped_launch(a, kDtI8, c_dtype, dev, reinterpret_cast<cudaStream_t>(stream));
+}
+
+gemm_status_t gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t ldx, const float *x_scale,
+                      const int8_t *W, int64_t ldw, const float *w_scale, void *C, int64_t ldc, gemm_dtype_t c_dtype,
+                      float alpha, float beta, const float *bias, gemm_epilogue_t epilogue, gemm_stream_t stream) {
+    return gemm_i8_grouped(1, M, N, K, nullptr, X, ldx, x_scale, W, 0, ldw, w_scale, C, ldc, c_dtype, alpha, beta,
+                           bias, epilogue, stream);
+}
+
+gemm_status_t gemm_i8_quantize(int64_t M, int64_t K, gemm_dtype_t x_dtype, const void *X, int64_t ldx, int8_t *Q,
+                               int64_t ldq, float *scale, gemm_stream_t stream) {
+    if (M < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+    if (!valid_dtype(x_dtype)) return GEMM_ERR_INVALID_ARG;
+    if (x_dtype == GEMM_E4M3) return GEMM_ERR_UNSUPPORTED;
+    if (M == 0) return GEMM_OK;
+    if (M > INT32_MAX || K > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (scale == nullptr || (K > 0 && (X == nullptr || Q == nullptr))) return GEMM_ERR_INVALID_ARG;
+    if (ldx < K || ldq < K) return GEMM_ERR_INVALID_ARG;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    gemm_status_t st;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if ((st = check_range(scale, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
+    if ((st = check_range(X, extent_bytes(1, 0, M, ldx, K, 1, elem_bytes(x_dtype)))) != GEMM_OK) return st;
+    if ((st = check_range(Q, extent_bytes(1, 0, M, ldq, K, 1, 1))) != GEMM_OK) return st;
+    return launch_i8_quantize(x_dtype, M, K, X, ldx, reinterpret_cast<signed char *>(Q), ldq, scale,
+                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMM_OK
+               : GEMM_ERR_CUDA;
+}
+
 gemm_status_t gemm_wait_selftest(const unsigned int *never_set, uint64_t limit_ns, gemm_stream_t stream) {
     if (never_set == nullptr || limit_ns == 0 || limit_ns > 1000000000ull) return GEMM_ERR_INVALID_ARG;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;

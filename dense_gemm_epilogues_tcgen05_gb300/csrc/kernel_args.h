@@ -14,6 +14,8 @@ enum : int { kDtF32 = 0, kDtF16 = 1, kDtBF16 = 2, kDtE4M3 = 3 };
 // Internal operand format of the tensor-core fp32 path: each operand split into
 // a tf32 "hi" and an fp32 "lo" part, stacked in one K-major array (3xTF32).
 enum : int { kDtTF32x3 = 4 };
+// Internal operand type of the 8-bit integer products.
+enum : int { kDtI8 = 5 };
 enum : int { kEpiNone = 0, kEpiBias = 1, kEpiBiasGelu = 2, kEpiBiasGeluTanh = 3, kEpiBiasSilu = 4,
              kEpiBiasRelu = 5 };
 
@@ -115,7 +117,53 @@ struct MxArgs {
     unsigned int *status;
 };
 
+// Most groups one grouped call takes (the size of the kernels' group table).
+constexpr int kMaxGroups = 1024;
+
+// Product grouped by expert: rows offsets[g] .. offsets[g+1]-1 of A times B[g].
+// Also the integer products (A = codes of the rows, B[g] = codes of the
+// weights given N x K: sbk == 1, sbn the row pitch).
+struct GroupedArgs {
+    int G, M, N, K;
+    const int *offsets;             // device, G + 1; NULL: one group of M rows
+    const void *A;
+    long long sam, sak;
+    const void *B;
+    long long sbg, sbk, sbn;
+    void *C;                        // M x ldc row-major
+    long long ldc;
+    const float *bias;              // G x N, NULL without
+    const float *row_scale;         // M, NULL: 1
+    const float *col_scale;         // G x N, NULL: 1
+    float alpha, beta;
+    int epilogue;
+    unsigned int *status;
+};
+
+// Weight gradient of the grouped product: C[g] = alpha * A_g^T D_g + beta * C[g]
+// over the rows of group g, and a_sum[g] = alpha * column sums of A_g + beta * a_sum[g].
+struct WgradArgs {
+    int G, T, M, N;
+    const int *offsets;
+    const void *A;
+    long long sar, sam;
+    const void *D;
+    long long sdr, sdn;
+    void *C;
+    long long scg, ldc;
+    float *a_sum;                   // G x M, NULL without
+    float alpha, beta;
+    unsigned int *status;
+};
+
 // Launchers (each returns the launch's cudaError_t), defined by the kernel files.
+//   grouped products on the CUDA cores, any strides (ab: F32, F16, BF16 or kDtI8), `grid` blocks:
+cudaError_t launch_grouped_simt(int ab, int out, const GroupedArgs &args, int grid, cudaStream_t stream);
+cudaError_t launch_wgrad_simt(int ab, int out, const WgradArgs &args, int grid, cudaStream_t stream);
+cudaError_t launch_grouped_colsum(int ab, const WgradArgs &args, cudaStream_t stream);
+//   per-row 8-bit quantisation:
+cudaError_t launch_i8_quantize(int x_dtype, long long M, long long K, const void *X, long long ldx, signed char *Q,
+                               long long ldq, float *scale, cudaStream_t stream);
 //   one-SM tcgen05 kernel, `bn` = 256 or 128, `grid` CTAs:
 cudaError_t launch_tcgen05_f16(int out, int bn, const CUtensorMap &, const CUtensorMap &, const TcArgs &, int grid,
                                cudaStream_t);

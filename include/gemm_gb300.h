@@ -619,6 +619,120 @@ gemm_status_t gemm_baseline(gemm_baseline_t kind, int64_t M, int64_t N, int64_t 
 gemm_status_t gemm_device_status(gemm_stream_t stream);
 
 /*
+ * Products grouped by expert.  A mixture of experts sends each row (token) to
+ * some of G experts; with the rows sorted by expert, the rows of expert g are
+ * rows offsets[g] .. offsets[g+1]-1 of one array, and each expert multiplies
+ * its own rows.  The pages know one matrix product per call; this is G of them
+ * with ragged row counts in one launch, for the same epilogues.
+ *
+ *   offsets        int32[G + 1] on the DEVICE, non-decreasing, 0 <= offsets <=
+ *                  M.  The host never reads it: a router's counts need no copy
+ *                  back.  Groups may be empty; rows below offsets[0] or from
+ *                  offsets[G] on are not touched.  Values outside these rules
+ *                  are clamped to [0, M] (no access leaves the arrays), with
+ *                  unspecified results.  At most GEMM_MAX_GROUPS groups.
+ */
+#define GEMM_MAX_GROUPS 1024
+
+/*
+ * gemm_grouped -- for every row r of group g and every column j:
+ *
+ *     z = alpha * row_scale[r] * sum_k A[r][k] * B[g][k][j] + beta * C[r][j] + bias[g][j]
+ *     C[r][j] = cast(act(z))
+ *
+ * with fp32 accumulation and rounding to nearest even once.
+ *   A              element (r, k) at A[r*a_stride_m + k*a_stride_k], M rows.
+ *   B              element (g, k, j) at B[g*b_stride_g + k*b_stride_k + j*b_stride_n].
+ *                  Weights stored G x N x K are b_stride_k = 1, b_stride_n =
+ *                  their pitch; swapping the two strides multiplies by the
+ *                  transposed weights, which is the gradient of the rows.
+ *   C, ldc         M x ldc row-major, as in gemm().
+ *   types          ab_dtype F16 or BF16 with c_dtype F32, F16 or BF16; or all F32.
+ *   bias           fp32[G x N] (row g: expert g's), required unless GEMM_EPI_NONE.
+ *   row_scale      fp32[M] or NULL (1): e.g. the router's weight of each row.
+ *                  Not read when K == 0 or alpha == 0 (the product term is 0).
+ * F16 / BF16 inputs run on the tensor cores when A is contiguous along k, B
+ * along k or j, both bases are 16-byte aligned and the other strides multiples
+ * of 16 bytes; anything else on the CUDA cores.  The activations take the
+ * forms of fp32 outputs whatever c_dtype.  C must not overlap the inputs.
+ * Asynchronous on `stream`; errors as gemm(), GEMM_ERR_MISALIGNED for an
+ * offsets array that is not 4-byte aligned.
+ */
+gemm_status_t gemm_grouped(int64_t G, int64_t M, int64_t N, int64_t K, gemm_dtype_t ab_dtype, const int32_t *offsets,
+                           const void *A, int64_t a_stride_m, int64_t a_stride_k, const void *B, int64_t b_stride_g,
+                           int64_t b_stride_k, int64_t b_stride_n, void *C, int64_t ldc, gemm_dtype_t c_dtype,
+                           float alpha, float beta, const float *bias, gemm_epilogue_t epilogue,
+                           const float *row_scale, gemm_stream_t stream);
+
+/*
+ * gemm_grouped_wgrad -- the weight gradient of gemm_grouped: for every group g,
+ *
+ *     C[g][m][n] = cast(alpha * sum_{r in g} A[r][m] * D[r][n] + beta * C[g][m][n])
+ *     a_sum[g][m] = alpha * sum_{r in g} A[r][m] + beta * a_sum[g][m]
+ *
+ * over the T rows of A (T x M) and D (T x N), element (r, m) at
+ * A[r*a_stride_r + m*a_stride_m], D likewise.  With A = the gradient of the
+ * rows' outputs and D = the rows, C[g] is the gradient of weights stored N x K
+ * and a_sum the gradient of the bias; beta = 1 accumulates into main gradients.
+ * A group without rows gets beta * C[g] (zeros for beta == 0, C unread).
+ *   C              element (g, m, n) at C[g*c_stride_g + m*ldc + n]; the groups
+ *                  must not overlap (c_stride_g >= (M-1)*ldc + N).
+ *   a_sum          fp32[G x M] or NULL.
+ *   types          as gemm_grouped.
+ * Sums run in a fixed order: the same call gives the same bits.  F16 / BF16
+ * inputs run on the tensor cores when both are contiguous along m / n with
+ * 16-byte aligned bases and row pitches.  Errors as gemm_grouped.
+ */
+gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gemm_dtype_t ab_dtype,
+                                 const int32_t *offsets, const void *A, int64_t a_stride_r, int64_t a_stride_m,
+                                 const void *D, int64_t d_stride_r, int64_t d_stride_n, void *C, int64_t c_stride_g,
+                                 int64_t ldc, gemm_dtype_t c_dtype, float alpha, float beta, float *a_sum,
+                                 gemm_stream_t stream);
+
+/*
+ * Products of 8-bit integers with a scale for each row (token) and each output
+ * channel: "X3: Metal GEMM" section 7's quantized matmul with the rows quantised
+ * too.
+ *
+ * gemm_i8 -- C[i][j] = cast(act(alpha * x_scale[i] * w_scale[j] * sum_k
+ * X[i][k] * W[j][k] + beta * C[i][j] + bias[j])).
+ *   X, ldx         int8, M x ldx row-major, ldx >= K.
+ *   W, ldw         int8, N x ldw row-major, ldw >= K (output channels x inputs).
+ *   x_scale        fp32[M] or NULL (1); w_scale fp32[N] or NULL (1).  Not read
+ *                  when K == 0 or alpha == 0.
+ *   K              at most GEMM_I8_MAX_K: the integer sum is exact (32 bits)
+ *                  for all codes -128 .. 127, so the result does not depend on
+ *                  M or on the kernel that a call runs.  It is rounded to fp32
+ *                  once, scaled, and rounded to c_dtype (F32, F16 or BF16).
+ *   bias           fp32[N]; C, ldc, alpha, beta, epilogue as in gemm().
+ * Any alignment; 16-byte aligned bases and pitches run on the fast kernels.
+ *
+ * gemm_i8_grouped -- the same, grouped by expert: rows of group g use W[g] =
+ * W + g*w_stride_g, w_scale[g] and bias[g] (fp32[G x N] each); offsets as in
+ * gemm_grouped.
+ */
+#define GEMM_I8_MAX_K 131071
+gemm_status_t gemm_i8(int64_t M, int64_t N, int64_t K, const int8_t *X, int64_t ldx, const float *x_scale,
+                      const int8_t *W, int64_t ldw, const float *w_scale, void *C, int64_t ldc, gemm_dtype_t c_dtype,
+                      float alpha, float beta, const float *bias, gemm_epilogue_t epilogue, gemm_stream_t stream);
+gemm_status_t gemm_i8_grouped(int64_t G, int64_t M, int64_t N, int64_t K, const int32_t *offsets, const int8_t *X,
+                              int64_t ldx, const float *x_scale, const int8_t *W, int64_t w_stride_g, int64_t ldw,
+                              const float *w_scale, void *C, int64_t ldc, gemm_dtype_t c_dtype, float alpha,
+                              float beta, const float *bias, gemm_epilogue_t epilogue, gemm_stream_t stream);
+
+/*
+ * gemm_i8_quantize -- the rows that gemm_i8 takes, from F32, F16 or BF16 values:
+ *
+ *     scale[i] = max_k |X[i][k]| / 127,   Q[i][k] = round_even(127 * X[i][k] / max_k |X[i][k]|)
+ *
+ * A row of zeros (or K == 0) gets scale 0 and codes 0.  A row that holds a NaN
+ * or an infinity gets a NaN scale, so that the product's row shows it, and
+ * codes 0.  Columns K..ldq-1 of Q are not written.
+ */
+gemm_status_t gemm_i8_quantize(int64_t M, int64_t K, gemm_dtype_t x_dtype, const void *X, int64_t ldx, int8_t *Q,
+                               int64_t ldq, float *scale, gemm_stream_t stream);
+
+/*
  * gemm_wait_selftest -- exercise the bounded waits the GEMM kernels rely on
  * instead of hanging.  Enqueues on `stream` a one-warp kernel that waits on an
  * mbarrier nobody arrives at and then on *never_set (a device word the caller
