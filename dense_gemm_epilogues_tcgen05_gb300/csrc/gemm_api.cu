@@ -1318,9 +1318,78 @@ static gemm_status_t grouped_rules(int64_t G, int64_t M, int64_t N, int64_t K, c
     return GEMM_OK;
 }
 
+// 3-D map over (inner, rows, groups) of 16-bit elements, boxes of 64 x box_rows x 1, 128-byte swizzle, zero
+// fill.  Strides of extents of one are never used to address an element.
+static gemm_status_t encode_3d(CUtensorMap *map, int ab, const void *base, int64_t inner, int64_t rows,
+                               int64_t row_stride, int64_t groups, int64_t group_stride, uint32_t box_rows) {
+    const cuuint64_t pitch = rows == 1 ? 16 : static_cast<cuuint64_t>(row_stride) * 2;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(groups)};
+    cuuint64_t strides[2] = {pitch, groups == 1 ? 16 : static_cast<cuuint64_t>(group_stride) * 2};
+    cuuint32_t box[3] = {64u, box_rows, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = driver_fns().encode(map, tma_dtype(ab), 3, const_cast<void *>(base), dims, strides, box, estr,
+                                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// Whether a stride between matrices can be a tensor map's: a multiple of 16 bytes (0: one matrix for all
+// groups, which the map then has once).
+static bool group_stride_ok(int64_t G, int64_t stride, int es) {
+    return G == 1 || (stride > 0 && stride * es % 16 == 0 && stride * es < (int64_t(1) << 40));
+}
+
+// 16-bit outputs stored two columns at a time: even pitch, 4-byte aligned base.
+static int pair_stores(const void *C, int64_t ldc, int64_t group_stride) {
+    return (reinterpret_cast<uintptr_t>(C) & 3u) == 0 && ldc % 2 == 0 && group_stride % 2 == 0;
+}
+
+// Record of a pair launch over at most `tiles` tiles; returns its clusters.
+static int pair_clusters(const DeviceState *dev, int64_t tiles, gemm_launch_info_t *info) {
+    const int clusters = static_cast<int>(std::min<int64_t>(tiles, dev->num_sms / 2));
+    info->path = GEMM_PATH_TCGEN05;
+    info->kind = 2;
+    info->bn = 256;
+    info->transposed = 1;
+    info->cluster_ctas = 2;
+    info->grid_ctas = 2 * clusters;
+    info->tiles = static_cast<int>(std::min<int64_t>(tiles, INT32_MAX));
+    return clusters;
+}
+
 // The product behind gemm_grouped, gemm_i8 and gemm_i8_grouped (ab: a gemm_dtype_t or kDtI8), arguments checked.
 static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, DeviceState *dev, cudaStream_t s) {
     gemm_launch_info_t info = {};
+    if (args.K > 0 && (ab == GEMM_F16 || ab == GEMM_BF16)) {
+        const bool k_major = tma_ok(args.B, args.N, args.sbk, args.sbn, 2);
+        const bool n_major = !k_major && tma_ok(args.B, args.K, args.sbn, args.sbk, 2);
+        if (tma_ok(args.A, args.M, args.sak, args.sam, 2) && (k_major || n_major) &&
+            group_stride_ok(args.G, args.sbg, 2)) {
+            CUtensorMap ta, tb, tb16;
+            gemm_status_t st;
+            st = k_major ? encode_3d(&ta, ab, args.B, args.K, args.N, args.sbn, args.G, args.sbg, 128)
+                         : encode_3d(&ta, ab, args.B, args.N, args.K, args.sbk, args.G, args.sbg, 64);
+            if (st != GEMM_OK) return st;
+            if ((st = encode_3d(&tb, ab, args.A, args.K, args.M, args.sam, 1, 0, 64)) != GEMM_OK) return st;
+            if ((st = encode_3d(&tb16, ab, args.A, args.K, args.M, args.sam, 1, 0, 16)) != GEMM_OK) return st;
+            GtcArgs t = {};
+            t.G = args.G; t.T = args.M; t.F = args.N; t.K = args.K;
+            t.tiles_f = (args.N + 255) / 256;
+            t.offsets = args.offsets;
+            t.C = args.C; t.ldc = args.ldc;
+            t.bias = args.bias; t.row_scale = args.row_scale;
+            t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
+            t.pairs = pair_stores(args.C, args.ldc, 0);
+            t.a_mn = n_major ? 1u : 0u;
+            t.status = args.status;
+            // at most: every 256 rows a tile, and one more ragged tile per group that can have rows
+            const int64_t row_tiles = args.M / 256 + std::min(args.G, args.M);
+            const int clusters = pair_clusters(dev, row_tiles * t.tiles_f, &info);
+            return record(launch_grouped_tc(false, ab, cd, ta, tb, tb16, t, clusters, s) == cudaSuccess
+                              ? GEMM_OK : GEMM_ERR_CUDA, info);
+        }
+    }
     info.path = args.K == 0 ? GEMM_PATH_EPILOGUE_ONLY : GEMM_PATH_SIMT;
     const int grid = simt_grid(dev, (args.M + 63) / 64 + args.G, (args.N + 63) / 64);
     return record(launch_grouped_simt(ab, cd, args, grid, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
@@ -1423,6 +1492,23 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (a_sum != nullptr && launch_grouped_colsum(ab_dtype, a, s) != cudaSuccess) return GEMM_ERR_CUDA;
     gemm_launch_info_t info = {};
+    if (product && es == 2 && tma_ok(A, T, a_stride_m, a_stride_r, 2) && tma_ok(D, T, d_stride_n, d_stride_r, 2)) {
+        CUtensorMap ta, tb;
+        if ((st = encode_3d(&ta, ab_dtype, D, N, T, d_stride_r, 1, 0, 64)) != GEMM_OK) return st;
+        if ((st = encode_3d(&tb, ab_dtype, A, M, T, a_stride_r, 1, 0, 64)) != GEMM_OK) return st;
+        GtcArgs t = {};
+        t.G = a.G; t.T = a.T; t.F = a.N; t.R = a.M;
+        t.tiles_f = (a.N + 255) / 256;
+        t.tiles_r = (a.M + 255) / 256;
+        t.offsets = offsets;
+        t.C = C; t.scg = c_stride_g; t.ldc = ldc;
+        t.alpha = alpha; t.beta = beta; t.epi = kEpiNone;
+        t.pairs = pair_stores(C, ldc, G > 1 ? c_stride_g : 0);
+        t.status = dev->status;
+        const int clusters = pair_clusters(dev, G * t.tiles_f * t.tiles_r, &info);
+        return record(launch_grouped_tc(true, ab_dtype, c_dtype, ta, tb, tb, t, clusters, s) == cudaSuccess
+                          ? GEMM_OK : GEMM_ERR_CUDA, info);
+    }
     info.path = product ? GEMM_PATH_SIMT : GEMM_PATH_EPILOGUE_ONLY;
     const int grid = simt_grid(dev, G * ((M + 63) / 64), (N + 63) / 64);
     return record(launch_wgrad_simt(ab_dtype, c_dtype, a, grid, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);

@@ -1,0 +1,425 @@
+// gemm_grouped_tc.cu -- products grouped by expert on pairs of SMs (tcgen05
+// cta_group::2), forward and weight gradient.
+//
+//   forward    C[r][f] = sum_k A[r][k] B[g][k][f] over the rows r of group g
+//   gradient   C[g][m][f] = sum_r A[r][m] D[r][f] over the rows r of group g
+//
+// Both are computed transposed: the MMA's 256 rows are columns f of C (the
+// weights' output channels; the gradient's contiguous index) and its up to 256
+// columns are the rows of C (tokens; the index m).  The ragged index is then
+// the MMA's N, whose width a tile chooses at run time in steps of 32: a group
+// of m rows takes ceil(m / 256) tiles of one common width, so 300 rows cost
+// two tiles of 160 columns, and 5 rows one of 32, where 256-row tiles of
+// tokens would compute 512 and 256.  In the gradient the ragged index is the
+// summed one.
+//
+// One persistent cluster of two CTAs per SM pair walks the tiles, which it
+// finds from `offsets` itself (grouped.cuh).  Roles, per CTA:
+//
+//   warp 0       TMA producer: its own 128 rows of the MMA's first operand and
+//                its own half of the columns' operand, 64 deep, into a ring of
+//                six 32 KB stages, counted on the leader's barrier;
+//   warp 1       MMA issuer (leader CTA only), two 256-column accumulators;
+//   warp 2       gradient only: the last k-block of a group reaches into the
+//                next group's rows (or past T).  They are zeroed in shared
+//                memory before the MMA reads them -- in both operands, since
+//                zero times a neighbour's infinity or NaN would be NaN.  Such
+//                a block is loaded on a barrier of its own CTA, warp 2 clears
+//                rows valid .. 63 and arrives on the leader's `fixed` barrier;
+//   warps 3-10   epilogue: two per 32-lane quadrant of tensor memory, each
+//                half of the tile's columns (store_chunk_t).
+//
+// Bound: the weights' bytes when groups are small (each expert's weights are
+// read once per 256 of its rows, from L2 after the first), the tensor pipe when
+// they are large; the gradient's output bytes when groups are small.
+#include "gemm_tcgen05.cuh"
+#include "grouped.cuh"
+
+namespace gb300 {
+
+namespace {
+
+struct GtcConfig {
+    static constexpr int BK = 64, STAGES = 6;
+    static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int EPI_WARP0 = 3, EPI_WARPS = 8;
+    static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
+    static constexpr int TMEM_COLS = 512, ACC_STRIDE = 256;
+    static constexpr int BAR_OFF = STAGES * STAGE_BYTES, BAR_BYTES = 256;
+    static constexpr int TABLE_OFF = BAR_OFF + BAR_BYTES;
+    static_assert((4 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
+    static int smem_bytes(int G) { return 1024 + TABLE_OFF + (group_table_bytes(G) + 15) / 16 * 16; }
+};
+static_assert(1024 + GtcConfig::TABLE_OFF + group_table_bytes(kMaxGroups) <= 232448, "fits the shared memory");
+static_assert(1024 + GtcConfig::TABLE_OFF > 232448 / 2, "one CTA per SM: a pair allocates all 512 TMEM columns");
+
+// Columns of the MMA for each of the ceil(n / 256) tiles that n rows are split into.
+__device__ __forceinline__ int tile_width(int n, int tiles) {
+    const int per = (n + tiles - 1) / tiles;
+    return (per + 31) & ~31;
+}
+
+struct RowTiles256 {
+    __device__ int operator()(int rows) const { return (rows + 255) >> 8; }
+};
+
+struct GtcTile {
+    int g;          // group
+    int f0;         // first column of C (256 of them)
+    int r0, nr;     // first row of C (forward: of A; gradient: m) and how many this tile stores
+    int bn;         // MMA columns, nr rounded up to 32
+    int k0, nk;     // gradient: first row summed and how many; forward: 0 and K
+};
+
+// Walks this cluster's tiles.
+template <bool WG>
+struct GtcIter {
+    const GroupTable &t;
+    const GtcArgs &a;
+    long long tile, tiles;
+    int step;
+    __device__ __forceinline__ GtcIter(const GroupTable &t_, const GtcArgs &a_, int cluster, int nclusters)
+        : t(t_), a(a_), tile(cluster), step(nclusters) {
+        tiles = WG ? static_cast<long long>(a.G) * a.tiles_r * a.tiles_f
+                   : static_cast<long long>(t.first[a.G]) * a.tiles_f;
+    }
+    __device__ __forceinline__ bool next(GtcTile &o) {
+        if (tile >= tiles) return false;
+        const int rt = static_cast<int>(tile / a.tiles_f);
+        o.f0 = static_cast<int>(tile - static_cast<long long>(rt) * a.tiles_f) * 256;
+        if constexpr (WG) {
+            o.g = rt / a.tiles_r;
+            const int in = rt - o.g * a.tiles_r;
+            const int w = tile_width(a.R, a.tiles_r);
+            o.r0 = in * w;
+            o.nr = min(w, a.R - o.r0);
+            o.k0 = t.lo[o.g];
+            o.nk = t.hi[o.g] - o.k0;
+        } else {
+            o.g = group_of(t, rt);
+            const int lo = t.lo[o.g], n = t.hi[o.g] - lo, nt = t.first[o.g + 1] - t.first[o.g];
+            const int w = tile_width(n, nt);
+            o.r0 = lo + (rt - t.first[o.g]) * w;
+            o.nr = min(w, lo + n - o.r0);
+            o.k0 = 0;
+            o.nk = a.K;
+        }
+        o.bn = max(32, (o.nr + 31) & ~31);
+        tile += step;
+        return true;
+    }
+};
+
+template <bool WG, int AB, int OUT>
+__global__ void __launch_bounds__(GtcConfig::THREADS, 1)
+    grouped_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ GtcArgs args) {
+    using Cfg = GtcConfig;
+    constexpr int BK = Cfg::BK, STAGES = Cfg::STAGES, CL = 2;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFF);
+    uint64_t *empty = full + STAGES;
+    uint64_t *landed = empty + STAGES;   // gradient, last k-blocks: this CTA's bytes have landed
+    uint64_t *fixed = landed + STAGES;   // (leader's) both CTAs have cleared the foreign rows
+    uint64_t *tfull = fixed + STAGES;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *mma_done = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();  // 0: leader
+    const int cluster = blockIdx.x / CL, nclusters = gridDim.x / CL;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+            mbar_init(&landed[s], 1);
+            mbar_init(&fixed[s], CL);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], CL * Cfg::EPI_WARPS);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        if (!WG) tma_prefetch_desc(&tmB16);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    grid_dep_wait();
+    grid_dep_launch();
+    const GroupTable table = group_table_build(reinterpret_cast<int *>(smem + Cfg::TABLE_OFF), args.offsets, args.G,
+                                               args.T, threadIdx.x, Cfg::THREADS, RowTiles256());
+    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), 0);
+    const uint32_t fixed0_leader = mapa_shared(smem_u32(&fixed[0]), 0);
+    const uint32_t tempty0_leader = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t abort_local = smem_u32(const_cast<int *>(abort_flag));
+    GtcIter<WG> it(table, args, cluster, nclusters);
+    GtcTile t;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ------------------------------------------------ TMA producer --
+            uint32_t stage = 0, phase = 0;
+            bool ok = true, issued = false;
+            const uint64_t keep = l2_policy_evict_last();
+            while (ok && it.next(t)) {
+                const int f = t.f0 + static_cast<int>(rank) * 128;
+                const int bnh = t.bn >> 1;
+                const int c0 = t.r0 + static_cast<int>(rank) * bnh;  // first of this CTA's MMA columns
+                const int num_kb = (t.nk + BK - 1) / BK;
+                const uint32_t bytes = Cfg::A_BYTES + (WG ? ((bnh + 63) >> 6) * 64u * 128u : bnh * 128u);
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!pair_wait<CL>(&empty[stage], phase ^ 1u, abort_flag, args.status, abort_local, rank)) {
+                        ok = false;
+                        break;
+                    }
+                    issued = true;
+                    unsigned char *sA = smem + stage * Cfg::STAGE_BYTES;
+                    unsigned char *sB = sA + Cfg::A_BYTES;
+                    const int k = t.k0 + kb * BK;
+                    if (WG && (kb + 1) * BK > t.nk) {
+                        // reaches past the group: on this CTA's own barrier, for warp 2
+                        if (rank == 0) mbar_arrive(&full[stage]);
+                        mbar_arrive_expect_tx(&landed[stage], bytes);
+                        for (int j = 0; j < 2; ++j)
+                            tma_load_3d_hint(sA + j * 64 * 128, &tmA, &landed[stage], f + j * 64, k, 0, keep);
+                        for (int j = 0; j * 64 < bnh; ++j)
+                            tma_load_3d_hint(sB + j * 64 * 128, &tmB, &landed[stage], c0 + j * 64, k, 0, keep);
+                    } else {
+                        const uint32_t fbar = full0_leader + 8u * stage;
+                        if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+                        if (WG || args.a_mn) {
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_3d_pair(sA + j * 64 * 128, &tmA, fbar, f + j * 64, k, WG ? 0 : t.g, keep);
+                        } else {
+                            tma_load_3d_pair(sA, &tmA, fbar, k, f, t.g, keep);
+                        }
+                        if (WG) {
+                            for (int j = 0; j * 64 < bnh; ++j)
+                                tma_load_3d_pair(sB + j * 64 * 128, &tmB, fbar, c0 + j * 64, k, 0, keep);
+                        } else {
+                            // boxes of 64 rows, then of 16
+                            int r = 0;
+                            for (; r + 64 <= bnh; r += 64)
+                                tma_load_3d_pair(sB + r * 128, &tmB, fbar, k, c0 + r, 0, keep);
+                            for (; r < bnh; r += 16)
+                                tma_load_3d_pair(sB + r * 128, &tmB16, fbar, k, c0 + r, 0, keep);
+                        }
+                    }
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (*abort_flag && issued) {
+                // Unwinding: loads in flight complete within microseconds; give
+                // them time to land before this CTA's shared memory is released.
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) sleep_ns(10000);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            // ---------------------------------------------------- MMA issuer --
+            const uint32_t a_mn = WG ? 1u : args.a_mn, b_mn = WG ? 1u : 0u;
+            const uint32_t a_lbo = a_mn ? 128u * BK : 16u, b_lbo = b_mn ? 128u * BK : 16u;
+            const uint32_t a_kstep = a_mn ? 128u * 16 : 32u, b_kstep = b_mn ? 128u * 16 : 32u;
+            uint32_t stage = 0, phase = 0, fixed_parity = 0;
+            bool ok = true, issued = false;
+            int local = 0;
+            while (ok && it.next(t)) {
+                const int num_kb = (t.nk + BK - 1) / BK;
+                if (num_kb == 0) continue;  // a group without rows: the epilogue alone
+                const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
+                ++local;
+                if (!pair_wait<CL>(&tempty[acc], acc_phase ^ 1u, abort_flag, args.status, abort_local, rank)) break;
+                tc_fence_after();
+                const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
+                const uint32_t idesc = mma_idesc(TcTraits<AB>::kFmt, TcTraits<AB>::kFmt, 256, t.bn) | (a_mn << 15) |
+                                       (b_mn << 16);
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    ok = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
+                    if (WG && ok && (kb + 1) * BK > t.nk) {
+                        ok = pair_wait_acquire<CL>(&fixed[stage], (fixed_parity >> stage) & 1u, abort_flag,
+                                                   args.status, abort_local, rank);
+                        fixed_parity ^= 1u << stage;
+                    }
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a_addr = smem_u32(smem + stage * Cfg::STAGE_BYTES);
+                    const uint32_t b_addr = a_addr + Cfg::A_BYTES;
+#pragma unroll
+                    for (int ks = 0; ks < BK / 16; ++ks)
+                        tc_mma_pair<kKindF16>(d_tmem, sw128_desc(a_addr + ks * a_kstep, a_lbo, 1024u),
+                                              sw128_desc(b_addr + ks * b_kstep, b_lbo, 1024u), idesc,
+                                              (kb | ks) != 0 ? 1u : 0u);
+                    issued = true;
+                    tc_commit_pair(&empty[stage], 0x3);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (ok) tc_commit_pair(&tfull[acc], 0x3);
+            }
+            if (*abort_flag && issued) {
+                tc_commit_pair(mma_done, 1u);
+                mbar_drain_wait(mma_done, 0, 100000000ull);
+            }
+        }
+    } else if (warp == 2) {
+        if constexpr (WG) {
+            // ------------------------------------------------ foreign rows --
+            uint32_t stage = 0, parity = 0;
+            bool ok = true;
+            while (ok && it.next(t)) {
+                const int num_kb = (t.nk + BK - 1) / BK;
+                const int valid = t.nk - (num_kb - 1) * BK;  // rows of the last k-block
+                if (num_kb > 0 && valid < BK) {
+                    const uint32_t s = (stage + num_kb - 1) % STAGES;
+                    const bool got =
+                        pair_wait<CL>(&landed[s], (parity >> s) & 1u, abort_flag, args.status, abort_local, rank);
+                    if (!__all_sync(0xffffffffu, got)) break;
+                    parity ^= 1u << s;
+                    // every operand box is 64 rows (k) of 128 bytes; a row's swizzle stays inside it
+                    unsigned char *st = smem + s * Cfg::STAGE_BYTES;
+                    const int boxes = 2 + (((t.bn >> 1) + 63) >> 6);
+                    for (int b = 0; b < boxes; ++b) {
+                        uint4 *row = reinterpret_cast<uint4 *>(st + b * 64 * 128 + valid * 128);
+                        for (int i = lane; i < (BK - valid) * 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote_release(fixed0_leader + 8u * s);
+                }
+                stage = (stage + num_kb) % STAGES;
+            }
+        }
+    } else {
+        // ------------------------------------------------------- epilogue --
+        using OutT = typename Elem<OUT>::T;
+        const int quad = warp & 3;                      // TMEM lanes 32*quad ..
+        const int half = (warp - Cfg::EPI_WARP0) >> 2;  // which half of the tile's columns
+        const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi, args.pairs};
+        int local = 0;
+        while (it.next(t)) {
+            const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
+            const bool have = t.nk > 0;
+            const int f = t.f0 + static_cast<int>(rank) * 128 + quad * 32 + lane;
+            const float bias = (args.epi != kEpiNone && f < args.F)
+                                   ? args.bias[static_cast<long long>(t.g) * args.F + f] : 0.0f;
+            OutT *c = static_cast<OutT *>(args.C) + (WG ? t.g * args.scg : 0ll) + t.r0 * args.ldc + f;
+            const float *rs = args.row_scale != nullptr ? args.row_scale + t.r0 : nullptr;
+            if (have) {
+                ++local;
+                const bool got = pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank);
+                if (!__all_sync(0xffffffffu, got)) break;
+                tc_fence_after();
+            }
+            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::ACC_STRIDE;
+            const int chunks = t.bn >> 5;
+            const int c_begin = half ? (chunks + 1) >> 1 : 0, c_end = half ? chunks : (chunks + 1) >> 1;
+#pragma unroll 1
+            for (int ch = c_begin; ch < c_end; ++ch) {
+                float v[32];
+                if (have) {
+                    uint32_t raw[32];
+                    __syncwarp();
+                    tmem_ld_issue(t_row + ch * 32, raw);
+                    tmem_ld_wait(raw);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                }
+                if (have && ch + 1 == c_end) {
+                    // the accumulator is in registers: free it before the stores
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
+                }
+                store_chunk_t<OUT>(v, c + ch * 32 * args.ldc, args.F - f, t.nr - ch * 32,
+                                   rs != nullptr ? rs + ch * 32 : nullptr, 1.0f, bias, e);
+            }
+            if (have && c_begin == c_end) {  // a 32-column tile has no second half
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
+            }
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();  // no CTA leaves while its peer may still signal into it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+template <bool WG, int AB, int OUT>
+cudaError_t launch_gtc(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb16, const GtcArgs &args,
+                       int clusters, cudaStream_t stream) {
+    auto kern = grouped_tc_kernel<WG, AB, OUT>;
+    const int smem = GtcConfig::smem_bytes(args.G);
+    cudaError_t err =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GtcConfig::smem_bytes(kMaxGroups));
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(GtcConfig::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tb16, args);
+}
+
+template <bool WG, int AB>
+cudaError_t launch_gtc_out(int out, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb16,
+                           const GtcArgs &args, int clusters, cudaStream_t stream) {
+    if (out == kDtF32) return launch_gtc<WG, AB, kDtF32>(ta, tb, tb16, args, clusters, stream);
+    if (out == kDtF16) return launch_gtc<WG, AB, kDtF16>(ta, tb, tb16, args, clusters, stream);
+    if (out == kDtBF16) return launch_gtc<WG, AB, kDtBF16>(ta, tb, tb16, args, clusters, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const CUtensorMap &ta, const CUtensorMap &tb,
+                              const CUtensorMap &tb16, const GtcArgs &args, int clusters, cudaStream_t stream) {
+    if (ab == kDtF16)
+        return wgrad ? launch_gtc_out<true, kDtF16>(out, ta, tb, tb16, args, clusters, stream)
+                     : launch_gtc_out<false, kDtF16>(out, ta, tb, tb16, args, clusters, stream);
+    if (ab == kDtBF16)
+        return wgrad ? launch_gtc_out<true, kDtBF16>(out, ta, tb, tb16, args, clusters, stream)
+                     : launch_gtc_out<false, kDtBF16>(out, ta, tb, tb16, args, clusters, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gb300

@@ -85,6 +85,80 @@ __device__ __forceinline__ float grouped_value(float acc, float scale, float bet
     return activate_one<OUT>(z + bias, epi, true);
 }
 
+// ------------------------------------------------- transposed accumulators --
+// The tensor-core kernels compute C^T: the weights' output channels (or, for
+// the weight gradient, its contiguous index) are the MMA's rows and lie in
+// tensor-memory lanes, the tokens are its columns -- so that a ragged group
+// costs columns in steps of 32, not rows in steps of 256.  A warp then holds
+// 32 consecutive columns of C in its lanes and 32 rows of C in its registers,
+// and one store instruction writes whole 64- or 128-byte runs of C's rows:
+// no staging through shared memory, and any row pitch.
+struct StoreArgs {
+    long long ldc;
+    float alpha, beta;
+    int epi;
+    int pairs;  // 16-bit output: base and pitch allow 32-bit stores of two columns
+};
+
+// v: this lane's column at 32 consecutive rows, of which the first nrow are
+// stored (before any scale); c: element (row 0, this lane's column); the lane's
+// column is `left` columns before the end of C's rows (<= 0: outside).
+// row_scale: of row 0 on, or NULL; col_scale and bias: this lane's column's.
+// Warp-collective.
+template <int OUT>
+__device__ __forceinline__ void store_chunk_t(float (&v)[32], typename Elem<OUT>::T *c, int left, int nrow,
+                                              const float *row_scale, float col_scale, float bias,
+                                              const StoreArgs &e) {
+    const int lane = threadIdx.x & 31;
+    const bool f_ok = left > 0;
+    const float a = e.alpha * col_scale;
+    if (row_scale != nullptr) {
+        const float rs = lane < nrow ? row_scale[lane] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] *= a * __shfl_sync(0xffffffffu, rs, j);
+    } else {
+        scale_alpha(v, a);
+    }
+    if (e.beta != 0.0f) {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (f_ok && j < nrow) v[j] = fmaf(e.beta, Elem<OUT>::load(c + j * e.ldc), v[j]);
+    }
+    if (e.epi != kEpiNone) {
+        const uint64_t b2 = f2_splat(bias);
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) f2_unpack(f2_add(f2_pack(v[j], v[j + 1]), b2), v[j], v[j + 1]);
+        if (e.epi >= kEpiBiasGelu) activate_run<OUT, 32>(v, 0, e.epi, true);
+    }
+    if constexpr (OUT != kDtF32) {
+        if (e.pairs) {
+            // Lanes 2p and 2p + 1 trade values so that each stores 32-bit words
+            // (columns 2p, 2p + 1) of every other row: two rows per instruction.
+            const int odd = lane & 1;
+            const int pair_left = left + odd;  // columns from 2p on
+            typename Elem<OUT>::T *cw = c - odd + odd * e.ldc;  // column 2p, row `odd`
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+                const float lo = odd ? got : v[2 * i], hi = odd ? v[2 * i + 1] : got;
+                if (2 * i + odd < nrow) {
+                    if (pair_left > 1)
+                        *reinterpret_cast<uint32_t *>(cw) = pack2_out<OUT>(lo, hi);
+                    else if (pair_left == 1)
+                        *cw = Elem<OUT>::cvt(lo);
+                }
+                cw += 2 * e.ldc;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        if (f_ok && j < nrow) *c = Elem<OUT>::cvt(v[j]);
+        c += e.ldc;
+    }
+}
+
 // ------------------------------------------------------------ operand types --
 template <int AB> struct SimtAcc { using T = float; };
 template <> struct SimtAcc<kDtI8> { using T = int; };

@@ -156,7 +156,30 @@ struct WgradArgs {
     unsigned int *status;
 };
 
+// Grouped products on the tensor cores (gemm_grouped_tc.cu), forward or weight
+// gradient; operands come through tensor maps.  F: columns of C (the
+// contiguous index), R: rows of C per group (gradient), T: rows of the ragged
+// arrays, K: the forward product's depth.
+struct GtcArgs {
+    int G, T, F, R, K;
+    int tiles_f, tiles_r;           // ceil(F / 256); gradient: ceil(R / 256)
+    const int *offsets;
+    void *C;
+    long long scg, ldc;             // gradient: elements between groups of C
+    const float *bias, *row_scale;  // G x F, T; NULL when absent
+    float alpha, beta;
+    int epi;
+    int pairs;                      // 16-bit C: base and pitch allow 32-bit stores of two columns
+    uint32_t a_mn;                  // forward: the weights are contiguous along F
+    unsigned int *status;
+};
+
 // Launchers (each returns the launch's cudaError_t), defined by the kernel files.
+//   grouped products on the tensor cores, `clusters` SM pairs.  Forward: ta = weights (K, F, G) in boxes
+//   of 64 x 128 (a_mn: (F, K, G) in 64 x 64), tb / tb16 = rows (K, T) in boxes of 64 x 64 and 64 x 16.
+//   Gradient: ta = (F, T), tb = (R, T), boxes of 64 x 64; tb16 unused.  All 3-D, 128-byte swizzle.
+cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const CUtensorMap &ta, const CUtensorMap &tb,
+                              const CUtensorMap &tb16, const GtcArgs &args, int clusters, cudaStream_t stream);
 //   grouped products on the CUDA cores, any strides (ab: F32, F16, BF16 or kDtI8), `grid` blocks:
 cudaError_t launch_grouped_simt(int ab, int out, const GroupedArgs &args, int grid, cudaStream_t stream);
 cudaError_t launch_wgrad_simt(int ab, int out, const WgradArgs &args, int grid, cudaStream_t stream);
