@@ -1318,17 +1318,18 @@ static gemm_status_t grouped_rules(int64_t G, int64_t M, int64_t N, int64_t K, c
     return GEMM_OK;
 }
 
-// 3-D map over (inner, rows, groups) of 16-bit elements, boxes of 64 x box_rows x 1, 128-byte swizzle, zero
-// fill.  Strides of extents of one are never used to address an element.
+// 3-D map over (inner, rows, groups), boxes of 128 bytes x box_rows x 1, 128-byte swizzle, zero fill (ab: a
+// gemm_dtype_t of 16 bits or kDtI8).  Strides of extents of one are never used to address an element.
 static gemm_status_t encode_3d(CUtensorMap *map, int ab, const void *base, int64_t inner, int64_t rows,
                                int64_t row_stride, int64_t groups, int64_t group_stride, uint32_t box_rows) {
-    const cuuint64_t pitch = rows == 1 ? 16 : static_cast<cuuint64_t>(row_stride) * 2;
+    const int es = ab == kDtI8 ? 1 : 2;
+    const cuuint64_t pitch = rows == 1 ? 16 : static_cast<cuuint64_t>(row_stride) * es;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
                           static_cast<cuuint64_t>(groups)};
-    cuuint64_t strides[2] = {pitch, groups == 1 ? 16 : static_cast<cuuint64_t>(group_stride) * 2};
-    cuuint32_t box[3] = {64u, box_rows, 1u};
+    cuuint64_t strides[2] = {pitch, groups == 1 ? 16 : static_cast<cuuint64_t>(group_stride) * es};
+    cuuint32_t box[3] = {128u / es, box_rows, 1u};
     cuuint32_t estr[3] = {1, 1, 1};
-    CUresult r = driver_fns().encode(map, tma_dtype(ab), 3, const_cast<void *>(base), dims, strides, box, estr,
+    CUresult r = driver_fns().encode(map, ab == kDtI8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : tma_dtype(ab), 3, const_cast<void *>(base), dims, strides, box, estr,
                                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
@@ -1389,6 +1390,28 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
             return record(launch_grouped_tc(false, ab, cd, ta, tb, tb16, t, clusters, s) == cudaSuccess
                               ? GEMM_OK : GEMM_ERR_CUDA, info);
         }
+    }
+    if (args.K > 0 && ab == kDtI8 && tma_ok(args.A, args.M, 1, args.sam, 1) && tma_ok(args.B, args.N, 1, args.sbn, 1) &&
+        group_stride_ok(args.G, args.sbg, 1)) {
+        CUtensorMap tw, tx32, tx16;
+        gemm_status_t st;
+        if ((st = encode_3d(&tw, kDtI8, args.B, args.K, args.N, args.sbn, args.G, args.sbg, 128)) != GEMM_OK) return st;
+        if ((st = encode_3d(&tx32, kDtI8, args.A, args.K, args.M, args.sam, 1, 0, 32)) != GEMM_OK) return st;
+        if ((st = encode_3d(&tx16, kDtI8, args.A, args.K, args.M, args.sam, 1, 0, 16)) != GEMM_OK) return st;
+        GtcArgs t = {};
+        t.G = args.G; t.T = args.M; t.F = args.N; t.K = args.K;
+        t.tiles_f = (args.N + 255) / 256;
+        t.offsets = args.offsets;
+        t.C = args.C; t.ldc = args.ldc;
+        t.bias = args.bias; t.row_scale = args.row_scale; t.col_scale = args.col_scale;
+        t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
+        t.pairs = pair_stores(args.C, args.ldc, 0);
+        t.most = kI8TileRows;
+        t.status = args.status;
+        const int64_t row_tiles = args.M / t.most + std::min(args.G, args.M);
+        const int clusters = pair_clusters(dev, row_tiles * t.tiles_f, &info);
+        info.bn = t.most;
+        return record(launch_i8_tc(cd, tw, tx32, tx16, t, clusters, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
     }
     info.path = args.K == 0 ? GEMM_PATH_EPILOGUE_ONLY : GEMM_PATH_SIMT;
     const int grid = simt_grid(dev, (args.M + 63) / 64 + args.G, (args.N + 63) / 64);

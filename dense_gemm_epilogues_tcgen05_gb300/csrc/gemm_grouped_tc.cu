@@ -53,24 +53,6 @@ struct GtcConfig {
 static_assert(1024 + GtcConfig::TABLE_OFF + group_table_bytes(kMaxGroups) <= 232448, "fits the shared memory");
 static_assert(1024 + GtcConfig::TABLE_OFF > 232448 / 2, "one CTA per SM: a pair allocates all 512 TMEM columns");
 
-// Columns of the MMA for each of the ceil(n / 256) tiles that n rows are split into.
-__device__ __forceinline__ int tile_width(int n, int tiles) {
-    const int per = (n + tiles - 1) / tiles;
-    return (per + 31) & ~31;
-}
-
-struct RowTiles256 {
-    __device__ int operator()(int rows) const { return (rows + 255) >> 8; }
-};
-
-struct GtcTile {
-    int g;          // group
-    int f0;         // first column of C (256 of them)
-    int r0, nr;     // first row of C (forward: of A; gradient: m) and how many this tile stores
-    int bn;         // MMA columns, nr rounded up to 32
-    int k0, nk;     // gradient: first row summed and how many; forward: 0 and K
-};
-
 // Walks this cluster's tiles.
 template <bool WG>
 struct GtcIter {
@@ -83,28 +65,22 @@ struct GtcIter {
         tiles = WG ? static_cast<long long>(a.G) * a.tiles_r * a.tiles_f
                    : static_cast<long long>(t.first[a.G]) * a.tiles_f;
     }
-    __device__ __forceinline__ bool next(GtcTile &o) {
+    __device__ __forceinline__ bool next(GroupedTile &o) {
         if (tile >= tiles) return false;
-        const int rt = static_cast<int>(tile / a.tiles_f);
-        o.f0 = static_cast<int>(tile - static_cast<long long>(rt) * a.tiles_f) * 256;
         if constexpr (WG) {
+            const int rt = static_cast<int>(tile / a.tiles_f);
+            o.f0 = static_cast<int>(tile - static_cast<long long>(rt) * a.tiles_f) * 256;
             o.g = rt / a.tiles_r;
             const int in = rt - o.g * a.tiles_r;
             const int w = tile_width(a.R, a.tiles_r);
             o.r0 = in * w;
             o.nr = min(w, a.R - o.r0);
+            o.bn = (o.nr + 31) & ~31;
             o.k0 = t.lo[o.g];
             o.nk = t.hi[o.g] - o.k0;
         } else {
-            o.g = group_of(t, rt);
-            const int lo = t.lo[o.g], n = t.hi[o.g] - lo, nt = t.first[o.g + 1] - t.first[o.g];
-            const int w = tile_width(n, nt);
-            o.r0 = lo + (rt - t.first[o.g]) * w;
-            o.nr = min(w, lo + n - o.r0);
-            o.k0 = 0;
-            o.nk = a.K;
+            o = row_tile(t, tile, a.tiles_f, a.K);
         }
-        o.bn = max(32, (o.nr + 31) & ~31);
         tile += step;
         return true;
     }
@@ -162,14 +138,14 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
     grid_dep_wait();
     grid_dep_launch();
     const GroupTable table = group_table_build(reinterpret_cast<int *>(smem + Cfg::TABLE_OFF), args.offsets, args.G,
-                                               args.T, threadIdx.x, Cfg::THREADS, RowTiles256());
+                                               args.T, threadIdx.x, Cfg::THREADS, RowTilesOf{256});
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), 0);
     const uint32_t fixed0_leader = mapa_shared(smem_u32(&fixed[0]), 0);
     const uint32_t tempty0_leader = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t abort_local = smem_u32(const_cast<int *>(abort_flag));
     GtcIter<WG> it(table, args, cluster, nclusters);
-    GtcTile t;
+    GroupedTile t;
 
     if (warp == 0) {
         if (lane == 0) {

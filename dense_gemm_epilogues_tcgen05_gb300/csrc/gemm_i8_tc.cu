@@ -1,0 +1,395 @@
+// gemm_i8_tc.cu -- 8-bit integer products on the tensor cores, dense (one
+// group) or grouped by expert:
+//
+//     C[r][f] = act(alpha xs[r] ws[g][f] sum_k X[r][k] W[g][f][k] + beta C[r][f] + bias[g][f])
+//
+// sm_103a's tensor cores have no fast integer kind, but every 8-bit integer is
+// a binary16 number and so is every product's value in the fp32 accumulator's
+// 24 bits: 1024 products of at most 128 * 128 sum to at most 2^24.  So the
+// codes are expanded to binary16 on the way to the MMA (kind::f16, the bf16
+// rate), and every 1024 k the epilogue warps take the fp32 accumulator --
+// exact so far -- into 32-bit integers in registers, while the MMA fills the
+// other accumulator.  The integer sum is exact for any K the interface allows,
+// whatever the codes.
+//
+// The product is computed transposed on SM pairs, as in gemm_grouped_tc.cu: W's
+// 256 rows are the MMA's rows, up to 192 rows of X its columns.  Per CTA:
+//
+//   warp 0        TMA producer: 128 rows of W and half of the tile's rows of X,
+//                 128 k (bytes) deep, into a ring of five 28 KB stages of codes,
+//                 on this CTA's own barriers;
+//   warp 1        MMA issuer (leader CTA only);
+//   warps 4-11    converters, two sets of four; set h takes the 64-k half h of
+//                 every stage.  A thread expands one row of W into tensor
+//                 memory (the MMA's first operand: 32 columns of two values, so
+//                 expanded W never crosses shared memory), and a warp one
+//                 16-byte column of each row of X into a swizzled 16-bit tile;
+//                 four slots of each;
+//   warps 12-19   epilogue: two per 32-lane quadrant, half of the columns each;
+//                 96 integer sums per thread, then store_chunk_t.
+//
+// A code becomes binary16 by a byte permute into the mantissa of 1024 (the sign
+// bit flipped first: 1024 + 128 + code) and one subtraction of 1152: five
+// instructions for four codes, all exact.
+//
+// Registers: 20 warps launch with 96 each; the warpgroups then trade them (40
+// for the issuers, 64 for each converter set, 152 for each epilogue set: 472
+// of the 480 that five warps of a sub-partition launched with).
+//
+// Bound: at large sizes shared-memory bandwidth -- per 128 k a CTA moves 32 KB
+// of W (codes in, codes out) and 768 bytes per row of X (codes in and out,
+// 16-bit in and out) against the MMA's 8 clocks per row, 1.08 of the
+// 128 B/clk at 192 columns (1.25 at 128) -- and the weights' bytes at small M.
+#include "gemm_tcgen05.cuh"
+#include "grouped.cuh"
+
+namespace gb300 {
+
+namespace {
+
+struct I8Config {
+    static constexpr int BK = 128, STAGES = 5, SLOTS = 4;
+    static constexpr int X_ROWS = kI8TileRows / 2;                 // rows of X per CTA
+    static constexpr int W_BYTES = 128 * BK, X_BYTES = X_ROWS * BK, STAGE_BYTES = W_BYTES + X_BYTES;
+    static constexpr int SLOT_BYTES = X_ROWS * 128;                // X's 64 k in 16 bits
+    static constexpr int CHUNK_HALVES = 1024 / 64;                 // 64-k halves summed in fp32
+    static constexpr int ACC_STRIDE = kI8TileRows, W_SLOT = 2 * ACC_STRIDE, W_SLOT_COLS = 32, TMEM_COLS = 512;
+    static constexpr int CONV_WARP0 = 4, EPI_WARP0 = 12, THREADS = 640;
+    static constexpr int LAUNCH_REGS = 96;
+    static constexpr int SLOT_OFF = STAGES * STAGE_BYTES, BAR_OFF = SLOT_OFF + SLOTS * SLOT_BYTES, BAR_BYTES = 256;
+    static constexpr int TABLE_OFF = BAR_OFF + BAR_BYTES;
+    static_assert(STAGE_BYTES % 1024 == 0 && W_BYTES % 1024 == 0 && SLOT_BYTES % 1024 == 0, "swizzle atoms aligned");
+    static_assert(W_SLOT + SLOTS * W_SLOT_COLS <= TMEM_COLS, "W slots fit beside the accumulators");
+    static_assert((2 * STAGES + 2 * SLOTS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
+    static int smem_bytes(int G) { return 1024 + TABLE_OFF + (group_table_bytes(G) + 15) / 16 * 16; }
+};
+static_assert(1024 + I8Config::TABLE_OFF + group_table_bytes(kMaxGroups) <= 232448, "fits the shared memory");
+static_assert(1024 + I8Config::TABLE_OFF > 232448 / 2, "one CTA per SM: a pair allocates all 512 TMEM columns");
+
+// Four codes to two pairs of binary16.
+__device__ __forceinline__ void expand4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = codes ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
+template <int OUT>
+__global__ void __launch_bounds__(I8Config::THREADS, 1)
+    i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX32,
+                 const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ GtcArgs args) {
+    using Cfg = I8Config;
+    constexpr int STAGES = Cfg::STAGES, SLOTS = Cfg::SLOTS, CL = 2;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem =
+        reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFF);  // codes landed (this CTA's)
+    uint64_t *empty = full + STAGES;                                     // codes read by both converter sets
+    uint64_t *ready = empty + STAGES;                                    // (leader's) a slot expanded in both CTAs
+    uint64_t *freed = ready + SLOTS;                                     // a slot read by the MMA
+    uint64_t *tfull = freed + SLOTS;
+    uint64_t *tempty = tfull + 2;
+    uint64_t *mma_done = tempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();  // 0: leader
+    const int cluster = blockIdx.x / CL, nclusters = gridDim.x / CL;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 8);
+        }
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&ready[s], CL * 4);
+            mbar_init(&freed[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&tfull[b], 1);
+            mbar_init(&tempty[b], CL * 8);
+        }
+        mbar_init(mma_done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX32);
+        tma_prefetch_desc(&tmX16);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
+        tmem_relinquish_pair();
+    }
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    grid_dep_wait();
+    grid_dep_launch();
+    const GroupTable table = group_table_build(reinterpret_cast<int *>(smem + Cfg::TABLE_OFF), args.offsets, args.G,
+                                               args.T, threadIdx.x, Cfg::THREADS, RowTilesOf{args.most});
+    const uint32_t tmem_base = *tmem_slot;
+    const uint32_t ready0_leader = mapa_shared(smem_u32(&ready[0]), 0);
+    const uint32_t tempty0_leader = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t abort_local = smem_u32(const_cast<int *>(abort_flag));
+    const long long tiles = static_cast<long long>(table.first[args.G]) * args.tiles_f;
+    const int num_kb = (args.K + Cfg::BK - 1) / Cfg::BK;
+
+    if (warp < Cfg::CONV_WARP0) {
+        regs_decrease<40>();
+        if (warp == 0 && lane == 0) {
+            // ------------------------------------------------ TMA producer --
+            uint32_t stage = 0, phase = 0;
+            bool ok = true, issued = false;
+            const uint64_t keep = l2_policy_evict_last();
+            for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
+                const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
+                const int f = t.f0 + static_cast<int>(rank) * 128, bnh = t.bn >> 1;
+                const int r0 = t.r0 + static_cast<int>(rank) * bnh;
+                for (int kb = 0; kb < num_kb; ++kb) {
+                    if (!pair_wait<CL>(&empty[stage], phase ^ 1u, abort_flag, args.status, abort_local, rank)) {
+                        ok = false;
+                        break;
+                    }
+                    issued = true;
+                    unsigned char *sW = smem + stage * Cfg::STAGE_BYTES, *sX = sW + Cfg::W_BYTES;
+                    const int k = kb * Cfg::BK;
+                    mbar_arrive_expect_tx(&full[stage], Cfg::W_BYTES + bnh * 128);
+                    tma_load_3d_hint(sW, &tmW, &full[stage], k, f, t.g, keep);
+                    int r = 0;
+                    for (; r + 32 <= bnh; r += 32)
+                        tma_load_3d_hint(sX + r * 128, &tmX32, &full[stage], k, r0 + r, 0, keep);
+                    for (; r < bnh; r += 16)
+                        tma_load_3d_hint(sX + r * 128, &tmX16, &full[stage], k, r0 + r, 0, keep);
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (*abort_flag && issued) {
+                // Unwinding: loads in flight complete within microseconds; give
+                // them time to land before this CTA's shared memory is released.
+                const unsigned long long t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 200000ull) sleep_ns(10000);
+            }
+        } else if (warp == 1 && lane == 0 && rank == 0) {
+            // --------------------------------------------------- MMA issuer --
+            uint32_t half = 0;   // halves issued: slot half % 4, its use half / 4
+            uint32_t local = 0;  // accumulators filled
+            bool ok = true, issued = false;
+            for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
+                const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
+                const uint32_t idesc = mma_idesc(TcTraits<kDtF16>::kFmt, TcTraits<kDtF16>::kFmt, 256, t.bn);
+                for (int h = 0; ok && h < 2 * num_kb; h += Cfg::CHUNK_HALVES) {
+                    const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
+                    ++local;
+                    ok = pair_wait<CL>(&tempty[acc], acc_phase ^ 1u, abort_flag, args.status, abort_local, rank);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
+                    const int end = min(2 * num_kb, h + Cfg::CHUNK_HALVES);
+                    for (int i = h; i < end; ++i, ++half) {
+                        const uint32_t slot = half % SLOTS;
+                        ok = pair_wait_acquire<CL>(&ready[slot], (half / SLOTS) & 1u, abort_flag, args.status,
+                                                   abort_local, rank);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint32_t x_addr = smem_u32(smem + Cfg::SLOT_OFF + slot * Cfg::SLOT_BYTES);
+                        const uint32_t w_tmem = tmem_base + Cfg::W_SLOT + slot * Cfg::W_SLOT_COLS;
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            tc_mma_pair_f16_tmem_a(d_tmem, w_tmem + ks * 8, sw128_desc(x_addr + ks * 32, 16u, 1024u),
+                                                   idesc, (i != h || ks != 0) ? 1u : 0u);
+                        issued = true;
+                        tc_commit_pair(&freed[slot], 0x3);
+                    }
+                    if (ok) tc_commit_pair(&tfull[acc], 0x3);
+                }
+            }
+            if (*abort_flag && issued) {
+                tc_commit_pair(mma_done, 1u);
+                mbar_drain_wait(mma_done, 0, 100000000ull);
+            }
+        }
+    } else if (warp < Cfg::EPI_WARP0) {
+        // ----------------------------------------------------- converters --
+        regs_decrease<64>();
+        const int quad = warp & 3, hk = (warp - Cfg::CONV_WARP0) >> 2;
+        const int wr = quad * 32 + lane;  // this thread's row of W
+        uint32_t stage = 0, phase = 0, half = hk;
+        bool ok = true;
+        for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
+            const int bnh = row_tile(table, tile, args.tiles_f, args.K).bn >> 1;
+            for (int kb = 0; kb < num_kb; ++kb, half += 2) {
+                const uint32_t slot = half % SLOTS;
+                bool got = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
+                got = got && pair_wait<CL>(&freed[slot], ((half / SLOTS) & 1u) ^ 1u, abort_flag, args.status,
+                                           abort_local, rank);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const unsigned char *sW = smem + stage * Cfg::STAGE_BYTES, *sX = sW + Cfg::W_BYTES;
+                unsigned char *xs = smem + Cfg::SLOT_OFF + slot * Cfg::SLOT_BYTES;
+                const uint32_t w_tmem = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + Cfg::W_SLOT +
+                                        slot * Cfg::W_SLOT_COLS;
+                // this row's 64 codes: 16-byte unit u of a row sits at u ^ (row % 8)
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    uint32_t out[16];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const int u = hk * 4 + p * 2 + i;
+                        const uint4 c = *reinterpret_cast<const uint4 *>(sW + wr * 128 + ((u ^ (wr & 7)) << 4));
+                        expand4(c.x, out[8 * i], out[8 * i + 1]);
+                        expand4(c.y, out[8 * i + 2], out[8 * i + 3]);
+                        expand4(c.z, out[8 * i + 4], out[8 * i + 5]);
+                        expand4(c.w, out[8 * i + 6], out[8 * i + 7]);
+                    }
+                    tmem_st_x16(w_tmem + p * 16, out);
+                }
+                // 16 codes of each row of X: unit hk * 4 + quad in, units 2 quad and 2 quad + 1 out
+                for (int r = lane; r < bnh; r += 32) {
+                    const int sw = r & 7;
+                    const uint4 c = *reinterpret_cast<const uint4 *>(sX + r * 128 + (((hk * 4 + quad) ^ sw) << 4));
+                    uint4 a, b;
+                    expand4(c.x, a.x, a.y);
+                    expand4(c.y, a.z, a.w);
+                    expand4(c.z, b.x, b.y);
+                    expand4(c.w, b.z, b.w);
+                    *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad) ^ sw) << 4)) = a;
+                    *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad + 1) ^ sw) << 4)) = b;
+                }
+                tmem_st_wait();
+                fence_proxy_async_smem();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_remote_release(ready0_leader + 8u * slot);
+                    mbar_arrive(&empty[stage]);
+                }
+                if (++stage == STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------- epilogue --
+        regs_increase<152>();
+        using OutT = typename Elem<OUT>::T;
+        const int quad = warp & 3, side = (warp - Cfg::EPI_WARP0) >> 2;
+        const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi, args.pairs};
+        constexpr int MC = kI8TileRows / 64;  // most 32-column chunks of a warp
+        uint32_t local = 0;
+        bool ok = true;
+        for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
+            const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
+            const int chunks = t.bn >> 5;
+            const int c_begin = side ? (chunks + 1) >> 1 : 0, nch = (side ? chunks : (chunks + 1) >> 1) - c_begin;
+            int sum[MC][32];
+#pragma unroll
+            for (int c = 0; c < MC; ++c)
+#pragma unroll
+                for (int j = 0; j < 32; ++j) sum[c][j] = 0;
+            for (int h = 0; h < 2 * num_kb; h += Cfg::CHUNK_HALVES) {
+                const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
+                ++local;
+                const bool got = pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank);
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::ACC_STRIDE +
+                                       c_begin * 32;
+#pragma unroll
+                for (int c = 0; c < MC; ++c) {
+                    if (c < nch) {
+                        uint32_t raw[32];
+                        __syncwarp();
+                        tmem_ld_issue(t_row + c * 32, raw);
+                        tmem_ld_wait(raw);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) sum[c][j] += __float2int_rn(__uint_as_float(raw[j]));
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
+            }
+            if (!ok) break;
+            const int f = t.f0 + static_cast<int>(rank) * 128 + quad * 32 + lane;
+            const long long gf = static_cast<long long>(t.g) * args.F + f;
+            const bool f_ok = f < args.F;
+            const float bias = args.epi != kEpiNone && f_ok ? args.bias[gf] : 0.0f;
+            const float cs = args.col_scale != nullptr && f_ok ? args.col_scale[gf] : 1.0f;
+            OutT *out = static_cast<OutT *>(args.C) + t.r0 * args.ldc + f;
+#pragma unroll
+            for (int c = 0; c < MC; ++c) {
+                if (c < nch) {
+                    const int row = (c_begin + c) * 32;
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __int2float_rn(sum[c][j]);
+                    store_chunk_t<OUT>(v, out + row * args.ldc, args.F - f, t.nr - row,
+                                       args.row_scale != nullptr ? args.row_scale + t.r0 + row : nullptr, cs, bias, e);
+                }
+            }
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync_all();  // no CTA leaves while its peer may still signal into it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, Cfg::TMEM_COLS);
+    }
+}
+
+template <int OUT>
+cudaError_t launch_i8_tc_out(const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
+                             const GtcArgs &args, int clusters, cudaStream_t stream) {
+    auto kern = i8_tc_kernel<OUT>;
+    cudaError_t err =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, I8Config::smem_bytes(kMaxGroups));
+    if (err != cudaSuccess) return err;
+    // The register trade below the launch's total holds for this build only.
+    cudaFuncAttributes fa;
+    if ((err = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return err;
+    if (fa.numRegs != I8Config::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * clusters, 1, 1);
+    cfg.blockDim = dim3(I8Config::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = I8Config::smem_bytes(args.G);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx32, tx16, args);
+}
+
+}  // namespace
+
+cudaError_t launch_i8_tc(int out, const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
+                         const GtcArgs &args, int clusters, cudaStream_t stream) {
+    if (out == kDtF32) return launch_i8_tc_out<kDtF32>(tw, tx32, tx16, args, clusters, stream);
+    if (out == kDtF16) return launch_i8_tc_out<kDtF16>(tw, tx32, tx16, args, clusters, stream);
+    if (out == kDtBF16) return launch_i8_tc_out<kDtBF16>(tw, tx32, tx16, args, clusters, stream);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gb300

@@ -75,6 +75,43 @@ __device__ __forceinline__ int group_of(const GroupTable &t, int tile) {
     return lo;
 }
 
+// ------------------------------------------------------------- row tiles --
+// The tensor-core kernels give a group of n rows ceil(n / most) tiles of one
+// common width, a multiple of 32 (`most` is one too).
+struct RowTilesOf {
+    int most;
+    __device__ __forceinline__ int operator()(int rows) const { return (rows + most - 1) / most; }
+};
+
+__device__ __forceinline__ int tile_width(int n, int tiles) {
+    const int per = (n + tiles - 1) / tiles;
+    return (per + 31) & ~31;
+}
+
+struct GroupedTile {
+    int g;          // group
+    int f0;         // first column of C (256 of them)
+    int r0, nr;     // first row of C (gradient: of its index m) and how many this tile stores
+    int bn;         // MMA columns, nr rounded up to 32
+    int k0, nk;     // gradient: first row summed and how many; forward: 0 and K
+};
+
+// Tile `tile` of a forward product: a row tile's column tiles follow one another.
+__device__ __forceinline__ GroupedTile row_tile(const GroupTable &t, long long tile, int tiles_f, int K) {
+    GroupedTile o;
+    const int rt = static_cast<int>(tile / tiles_f);
+    o.f0 = static_cast<int>(tile - static_cast<long long>(rt) * tiles_f) * 256;
+    o.g = group_of(t, rt);
+    const int lo = t.lo[o.g], n = t.hi[o.g] - lo, nt = t.first[o.g + 1] - t.first[o.g];
+    const int w = tile_width(n, nt);
+    o.r0 = lo + (rt - t.first[o.g]) * w;
+    o.nr = min(w, lo + n - o.r0);
+    o.bn = (o.nr + 31) & ~31;
+    o.k0 = 0;
+    o.nk = K;
+    return o;
+}
+
 // One output: z = alpha * scale * acc (+ beta * C) (+ bias), activation, cast.
 // The accurate activation forms for every output type: the cheap ones are
 // within 4e-4 |z|, which shows where the activation's value is far below |z|.

@@ -171,6 +171,8 @@ struct GtcArgs {
     int epi;
     int pairs;                      // 16-bit C: base and pitch allow 32-bit stores of two columns
     uint32_t a_mn;                  // forward: the weights are contiguous along F
+    const float *col_scale;         // integer product: G x F, NULL: 1
+    int most;                       // integer product: widest row tile (a multiple of 32)
     unsigned int *status;
 };
 
@@ -180,6 +182,11 @@ struct GtcArgs {
 //   Gradient: ta = (F, T), tb = (R, T), boxes of 64 x 64; tb16 unused.  All 3-D, 128-byte swizzle.
 cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const CUtensorMap &ta, const CUtensorMap &tb,
                               const CUtensorMap &tb16, const GtcArgs &args, int clusters, cudaStream_t stream);
+//   8-bit integer products on the tensor cores, `clusters` SM pairs.  tw = weight codes (K, F, G) in boxes of
+//   128 x 128 bytes, tx32 / tx16 = row codes (K, T) in boxes of 128 x 32 and 128 x 16; 128-byte swizzle.
+cudaError_t launch_i8_tc(int out, const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
+                         const GtcArgs &args, int clusters, cudaStream_t stream);
+constexpr int kI8TileRows = 192;    // its widest row tile
 //   grouped products on the CUDA cores, any strides (ab: F32, F16, BF16 or kDtI8), `grid` blocks:
 cudaError_t launch_grouped_simt(int ab, int out, const GroupedArgs &args, int grid, cudaStream_t stream);
 cudaError_t launch_wgrad_simt(int ab, int out, const WgradArgs &args, int grid, cudaStream_t stream);

@@ -568,6 +568,27 @@ __device__ __forceinline__ void tc_mma_pair(uint32_t d_tmem, uint64_t a_desc, ui
     }
 }
 
+// tc_mma_f16_tmem_a for a CTA pair: each CTA's tensor memory holds its own 128 rows of A.
+__device__ __forceinline__ void tc_mma_pair_f16_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                                       uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Registers per thread of the executing warpgroup from here on (all four of
+// its warps execute it).
+template <int N>
+__device__ __forceinline__ void regs_decrease() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_increase() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // Arrive on the mbarrier at `bar`'s offset in every CTA of `cta_mask` once all
 // pair MMAs issued so far by this thread have completed.
 // tc_mma_bs for a CTA pair (M = 256 across the two CTAs), issued by the leader.
