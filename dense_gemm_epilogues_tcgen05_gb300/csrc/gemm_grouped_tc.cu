@@ -232,8 +232,9 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                 for (int kb = 0; kb < num_kb; ++kb) {
                     ok = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
                     if (WG && ok && (kb + 1) * BK > t.nk) {
-                        ok = pair_wait_acquire<CL>(&fixed[stage], (fixed_parity >> stage) & 1u, abort_flag,
-                                                   args.status, abort_local, rank);
+                        ok = pair_wait<CL>(&fixed[stage], (fixed_parity >> stage) & 1u, abort_flag, args.status,
+                                           abort_local, rank);
+                        smem_acquire_cluster();
                         fixed_parity ^= 1u << stage;
                     }
                     if (!ok) break;
@@ -281,8 +282,9 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                         for (int i = lane; i < (BK - valid) * 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
+                    smem_release_cluster();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote_release(fixed0_leader + 8u * s);
+                    if (lane == 0) mbar_arrive_remote_relaxed(fixed0_leader + 8u * s);
                 }
                 stage = (stage + num_kb) % STAGES;
             }

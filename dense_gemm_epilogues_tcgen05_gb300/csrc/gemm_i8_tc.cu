@@ -40,6 +40,8 @@
 // of W (codes in, codes out) and 768 bytes per row of X (codes in and out,
 // 16-bit in and out) against the MMA's 8 clocks per row, 1.08 of the
 // 128 B/clk at 192 columns (1.25 at 128) -- and the weights' bytes at small M.
+#include <algorithm>
+
 #include "gemm_tcgen05.cuh"
 #include "grouped.cuh"
 
@@ -48,23 +50,31 @@ namespace gb300 {
 namespace {
 
 struct I8Config {
-    static constexpr int BK = 128, STAGES = 5, SLOTS = 4;
-    static constexpr int X_ROWS = kI8TileRows / 2;                 // rows of X per CTA
-    static constexpr int W_BYTES = 128 * BK, X_BYTES = X_ROWS * BK, STAGE_BYTES = W_BYTES + X_BYTES;
-    static constexpr int SLOT_BYTES = X_ROWS * 128;                // X's 64 k in 16 bits
-    static constexpr int CHUNK_HALVES = 1024 / 64;                 // 64-k halves summed in fp32
-    static constexpr int ACC_STRIDE = kI8TileRows, W_SLOT = 2 * ACC_STRIDE, W_SLOT_COLS = 32, TMEM_COLS = 512;
+    static constexpr int BK = 128, MAX_STAGES = 8, MAX_SLOTS = 12;
+    static constexpr int W_BYTES = 128 * BK;
+    static constexpr int CHUNK_HALVES = 1024 / 64;  // 64-k halves summed in fp32
+    static constexpr int W_SLOT_COLS = 32, TMEM_COLS = 512;
     static constexpr int CONV_WARP0 = 4, EPI_WARP0 = 12, THREADS = 640;
     static constexpr int LAUNCH_REGS = 96;
-    static constexpr int SLOT_OFF = STAGES * STAGE_BYTES, BAR_OFF = SLOT_OFF + SLOTS * SLOT_BYTES, BAR_BYTES = 256;
-    static constexpr int TABLE_OFF = BAR_OFF + BAR_BYTES;
-    static_assert(STAGE_BYTES % 1024 == 0 && W_BYTES % 1024 == 0 && SLOT_BYTES % 1024 == 0, "swizzle atoms aligned");
-    static_assert(W_SLOT + SLOTS * W_SLOT_COLS <= TMEM_COLS, "W slots fit beside the accumulators");
-    static_assert((2 * STAGES + 2 * SLOTS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
-    static int smem_bytes(int G) { return 1024 + TABLE_OFF + (group_table_bytes(G) + 15) / 16 * 16; }
+    static constexpr int BAR_BYTES = 512, SMEM_MAX = 232448;
+    static_assert((2 * MAX_STAGES + 2 * MAX_SLOTS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
+    // after up to 1023 bytes of alignment: [stages][slots][barriers][group table]
+    static int fixed_bytes(int G) { return 1024 + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16; }
 };
-static_assert(1024 + I8Config::TABLE_OFF + group_table_bytes(kMaxGroups) <= 232448, "fits the shared memory");
-static_assert(1024 + I8Config::TABLE_OFF > 232448 / 2, "one CTA per SM: a pair allocates all 512 TMEM columns");
+
+// What follows from the widest row tile `most` and the group count: most / 2
+// rows of X per CTA; tensor memory beside the two accumulators holds slots of
+// expanded W, with as many of X in shared memory; the rest of shared memory
+// holds stages of codes.
+struct I8Shape {
+    int stage_bytes, slot_bytes, slots, stages;
+    __host__ __device__ __forceinline__ I8Shape(int most, int stages_) : stages(stages_) {
+        stage_bytes = I8Config::W_BYTES + most / 2 * I8Config::BK;
+        slot_bytes = most / 2 * 128;  // 64 k in 16 bits
+        const int cols = (I8Config::TMEM_COLS - 2 * most) / I8Config::W_SLOT_COLS;
+        slots = cols < I8Config::MAX_SLOTS ? cols & ~1 : I8Config::MAX_SLOTS;
+    }
+};
 
 // Four codes to two pairs of binary16.
 __device__ __forceinline__ void expand4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
@@ -82,15 +92,18 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX32,
                  const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ GtcArgs args) {
     using Cfg = I8Config;
-    constexpr int STAGES = Cfg::STAGES, SLOTS = Cfg::SLOTS, CL = 2;
+    constexpr int CL = 2;
+    const I8Shape sh(args.most, args.stages);
+    const uint32_t slots = sh.slots, stages = sh.stages;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFF);  // codes landed (this CTA's)
-    uint64_t *empty = full + STAGES;                                     // codes read by both converter sets
-    uint64_t *ready = empty + STAGES;                                    // (leader's) a slot expanded in both CTAs
-    uint64_t *freed = ready + SLOTS;                                     // a slot read by the MMA
-    uint64_t *tfull = freed + SLOTS;
+    unsigned char *slot_base = smem + stages * sh.stage_bytes;
+    uint64_t *full = reinterpret_cast<uint64_t *>(slot_base + slots * sh.slot_bytes);  // codes landed
+    uint64_t *empty = full + Cfg::MAX_STAGES;   // codes read by both converter sets
+    uint64_t *ready = empty + Cfg::MAX_STAGES;  // (leader's) a slot expanded in both CTAs
+    uint64_t *freed = ready + Cfg::MAX_SLOTS;   // a slot read by the MMA
+    uint64_t *tfull = freed + Cfg::MAX_SLOTS;
     uint64_t *tempty = tfull + 2;
     uint64_t *mma_done = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
@@ -101,11 +114,11 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
     const int cluster = blockIdx.x / CL, nclusters = gridDim.x / CL;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < Cfg::MAX_STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 8);
         }
-        for (int s = 0; s < SLOTS; ++s) {
+        for (int s = 0; s < Cfg::MAX_SLOTS; ++s) {
             mbar_init(&ready[s], CL * 4);
             mbar_init(&freed[s], 1);
         }
@@ -130,10 +143,11 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
     tc_fence_after();
     grid_dep_wait();
     grid_dep_launch();
-    const GroupTable table = group_table_build(reinterpret_cast<int *>(smem + Cfg::TABLE_OFF), args.offsets, args.G,
+    const GroupTable table = group_table_build(reinterpret_cast<int *>(reinterpret_cast<unsigned char *>(full) + Cfg::BAR_BYTES), args.offsets, args.G,
                                                args.T, threadIdx.x, Cfg::THREADS, RowTilesOf{args.most});
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t ready0_leader = mapa_shared(smem_u32(&ready[0]), 0);
+    const uint32_t acc_stride = args.most, w_slot0 = tmem_base + 2 * acc_stride;
     const uint32_t tempty0_leader = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t abort_local = smem_u32(const_cast<int *>(abort_flag));
     const long long tiles = static_cast<long long>(table.first[args.G]) * args.tiles_f;
@@ -156,7 +170,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                         break;
                     }
                     issued = true;
-                    unsigned char *sW = smem + stage * Cfg::STAGE_BYTES, *sX = sW + Cfg::W_BYTES;
+                    unsigned char *sW = smem + stage * sh.stage_bytes, *sX = sW + Cfg::W_BYTES;
                     const int k = kb * Cfg::BK;
                     mbar_arrive_expect_tx(&full[stage], Cfg::W_BYTES + bnh * 128);
                     tma_load_3d_hint(sW, &tmW, &full[stage], k, f, t.g, keep);
@@ -165,7 +179,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                         tma_load_3d_hint(sX + r * 128, &tmX32, &full[stage], k, r0 + r, 0, keep);
                     for (; r < bnh; r += 16)
                         tma_load_3d_hint(sX + r * 128, &tmX16, &full[stage], k, r0 + r, 0, keep);
-                    if (++stage == STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -177,9 +191,13 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                 const unsigned long long t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 200000ull) sleep_ns(10000);
             }
-        } else if (warp == 1 && lane == 0 && rank == 0) {
+        } else if (warp == 1 && rank == 0) {
             // --------------------------------------------------- MMA issuer --
-            uint32_t half = 0;   // halves issued: slot half % 4, its use half / 4
+            // The whole warp walks the loop and one elected lane issues, so that
+            // addresses and descriptors stay in uniform registers: the issuing
+            // thread's own time per 64 k has to stay below the MMAs' (384 clocks
+            // at 192 columns).
+            uint32_t slot = 0, slot_phase = 0;
             uint32_t local = 0;  // accumulators filled
             bool ok = true, issued = false;
             for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
@@ -189,30 +207,38 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                     const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
                     ++local;
                     ok = pair_wait<CL>(&tempty[acc], acc_phase ^ 1u, abort_flag, args.status, abort_local, rank);
+                    if (!__all_sync(0xffffffffu, ok)) ok = false;
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
+                    const uint32_t d_tmem = tmem_base + acc * acc_stride;
                     const int end = min(2 * num_kb, h + Cfg::CHUNK_HALVES);
-                    for (int i = h; i < end; ++i, ++half) {
-                        const uint32_t slot = half % SLOTS;
-                        ok = pair_wait_acquire<CL>(&ready[slot], (half / SLOTS) & 1u, abort_flag, args.status,
-                                                   abort_local, rank);
+                    for (int i = h; i < end; ++i) {
+                        ok = pair_wait<CL>(&ready[slot], slot_phase, abort_flag, args.status, abort_local, rank);
+                        if (!__all_sync(0xffffffffu, ok)) ok = false;
                         if (!ok) break;
+                        smem_acquire_cluster();
                         tc_fence_after();
-                        const uint32_t x_addr = smem_u32(smem + Cfg::SLOT_OFF + slot * Cfg::SLOT_BYTES);
-                        const uint32_t w_tmem = tmem_base + Cfg::W_SLOT + slot * Cfg::W_SLOT_COLS;
+                        const uint64_t bd = sw128_desc(smem_u32(slot_base) + slot * sh.slot_bytes, 16u, 1024u);
+                        const uint32_t w_tmem = w_slot0 + slot * Cfg::W_SLOT_COLS;
+                        if (elect_one()) {
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            tc_mma_pair_f16_tmem_a(d_tmem, w_tmem + ks * 8, sw128_desc(x_addr + ks * 32, 16u, 1024u),
-                                                   idesc, (i != h || ks != 0) ? 1u : 0u);
+                            for (int ks = 0; ks < 4; ++ks)  // 16 k: 8 columns of W, 32 bytes of X's rows
+                                tc_mma_pair_f16_tmem_a(d_tmem, w_tmem + ks * 8, bd + 2 * ks, idesc,
+                                                       (i != h || ks != 0) ? 1u : 0u);
+                            tc_commit_pair(&freed[slot], 0x3);
+                            if (i + 1 == end) tc_commit_pair(&tfull[acc], 0x3);
+                        }
                         issued = true;
-                        tc_commit_pair(&freed[slot], 0x3);
+                        __syncwarp();
+                        if (++slot == slots) {
+                            slot = 0;
+                            slot_phase ^= 1u;
+                        }
                     }
-                    if (ok) tc_commit_pair(&tfull[acc], 0x3);
                 }
             }
             if (*abort_flag && issued) {
-                tc_commit_pair(mma_done, 1u);
+                if (elect_one()) tc_commit_pair(mma_done, 1u);
                 mbar_drain_wait(mma_done, 0, 100000000ull);
             }
         }
@@ -221,32 +247,43 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
         regs_decrease<64>();
         const int quad = warp & 3, hk = (warp - Cfg::CONV_WARP0) >> 2;
         const int wr = quad * 32 + lane;  // this thread's row of W
-        uint32_t stage = 0, phase = 0, half = hk;
+        constexpr int XR = kI8TileRows / 64;  // rows of X per thread
+        uint32_t stage = 0, phase = 0, slot = hk, slot_phase = 0;
         bool ok = true;
         for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
             const int bnh = row_tile(table, tile, args.tiles_f, args.K).bn >> 1;
-            for (int kb = 0; kb < num_kb; ++kb, half += 2) {
-                const uint32_t slot = half % SLOTS;
+            for (int kb = 0; kb < num_kb; ++kb) {
                 bool got = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
-                got = got && pair_wait<CL>(&freed[slot], ((half / SLOTS) & 1u) ^ 1u, abort_flag, args.status,
-                                           abort_local, rank);
+                const unsigned char *sW = smem + stage * sh.stage_bytes, *sX = sW + Cfg::W_BYTES;
+                uint4 w[4], x[XR];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = *reinterpret_cast<const uint4 *>(sW + wr * 128 + (((hk * 4 + i) ^ (wr & 7)) << 4));
+#pragma unroll
+                for (int i = 0; i < XR; ++i)
+                    if (lane + 32 * i < bnh)
+                        x[i] = *reinterpret_cast<const uint4 *>(sX + (lane + 32 * i) * 128 +
+                                                                (((hk * 4 + quad) ^ (lane & 7)) << 4));
+                got = got &&
+                      pair_wait<CL>(&freed[slot], slot_phase ^ 1u, abort_flag, args.status, abort_local, rank);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[stage]);  // every lane has read its codes
                 tc_fence_after();
-                const unsigned char *sW = smem + stage * Cfg::STAGE_BYTES, *sX = sW + Cfg::W_BYTES;
-                unsigned char *xs = smem + Cfg::SLOT_OFF + slot * Cfg::SLOT_BYTES;
-                const uint32_t w_tmem = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + Cfg::W_SLOT +
-                                        slot * Cfg::W_SLOT_COLS;
-                // this row's 64 codes: 16-byte unit u of a row sits at u ^ (row % 8)
+                unsigned char *xs = slot_base + slot * sh.slot_bytes;
+                const uint32_t w_tmem =
+                    w_slot0 + (static_cast<uint32_t>(quad * 32) << 16) + slot * Cfg::W_SLOT_COLS;
+                // codes to binary16: this row's 64 of W (16-byte unit u of a row sits
+                // at u ^ (row % 8)) to 32 columns of tensor memory
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     uint32_t out[16];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const int u = hk * 4 + p * 2 + i;
-                        const uint4 c = *reinterpret_cast<const uint4 *>(sW + wr * 128 + ((u ^ (wr & 7)) << 4));
+                        const uint4 c = w[2 * p + i];
                         expand4(c.x, out[8 * i], out[8 * i + 1]);
                         expand4(c.y, out[8 * i + 2], out[8 * i + 3]);
                         expand4(c.z, out[8 * i + 4], out[8 * i + 5]);
@@ -255,26 +292,30 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                     tmem_st_x16(w_tmem + p * 16, out);
                 }
                 // 16 codes of each row of X: unit hk * 4 + quad in, units 2 quad and 2 quad + 1 out
-                for (int r = lane; r < bnh; r += 32) {
-                    const int sw = r & 7;
-                    const uint4 c = *reinterpret_cast<const uint4 *>(sX + r * 128 + (((hk * 4 + quad) ^ sw) << 4));
-                    uint4 a, b;
-                    expand4(c.x, a.x, a.y);
-                    expand4(c.y, a.z, a.w);
-                    expand4(c.z, b.x, b.y);
-                    expand4(c.w, b.z, b.w);
-                    *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad) ^ sw) << 4)) = a;
-                    *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad + 1) ^ sw) << 4)) = b;
+#pragma unroll
+                for (int i = 0; i < XR; ++i) {
+                    const int r = lane + 32 * i;
+                    if (r < bnh) {
+                        uint4 a, b;
+                        expand4(x[i].x, a.x, a.y);
+                        expand4(x[i].y, a.z, a.w);
+                        expand4(x[i].z, b.x, b.y);
+                        expand4(x[i].w, b.z, b.w);
+                        *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad) ^ (lane & 7)) << 4)) = a;
+                        *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad + 1) ^ (lane & 7)) << 4)) = b;
+                    }
                 }
                 tmem_st_wait();
                 fence_proxy_async_smem();
+                smem_release_cluster();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive_remote_release(ready0_leader + 8u * slot);
-                    mbar_arrive(&empty[stage]);
+                if (lane == 0) mbar_arrive_remote_relaxed(ready0_leader + 8u * slot);
+                if ((slot += 2) >= slots) {
+                    slot -= slots;
+                    slot_phase ^= 1u;
                 }
-                if (++stage == STAGES) {
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -307,7 +348,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::ACC_STRIDE +
+                const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * acc_stride +
                                        c_begin * 32;
 #pragma unroll
                 for (int c = 0; c < MC; ++c) {
@@ -356,19 +397,26 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
 
 template <int OUT>
 cudaError_t launch_i8_tc_out(const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
-                             const GtcArgs &args, int clusters, cudaStream_t stream) {
+                             const GtcArgs &a, int clusters, cudaStream_t stream) {
     auto kern = i8_tc_kernel<OUT>;
     cudaError_t err =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, I8Config::smem_bytes(kMaxGroups));
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, I8Config::SMEM_MAX);
     if (err != cudaSuccess) return err;
-    // The register trade below the launch's total holds for this build only.
+    // The register trade adds up for this launch count only.
     cudaFuncAttributes fa;
     if ((err = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return err;
     if (fa.numRegs != I8Config::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
+    GtcArgs args = a;
+    I8Shape sh(args.most, 0);
+    const int data = I8Config::SMEM_MAX - I8Config::fixed_bytes(args.G) - sh.slots * sh.slot_bytes;
+    args.stages = std::min(I8Config::MAX_STAGES, data / sh.stage_bytes);
+    if (args.most < 32 || args.most > kI8TileRows || args.most % 32 != 0 || args.stages < 2)
+        return cudaErrorInvalidValue;
+    const int smem = I8Config::fixed_bytes(args.G) + sh.slots * sh.slot_bytes + args.stages * sh.stage_bytes;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters, 1, 1);
     cfg.blockDim = dim3(I8Config::THREADS, 1, 1);
-    cfg.dynamicSmemBytes = I8Config::smem_bytes(args.G);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

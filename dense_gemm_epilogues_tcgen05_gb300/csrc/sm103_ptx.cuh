@@ -449,24 +449,27 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// The same with release at cluster scope: for an arrive that hands ordinary
-// shared-memory writes (not tensor memory) to a thread of the other CTA, which
-// waits with mbar_wait_cluster.
-__device__ __forceinline__ void mbar_arrive_remote_release(uint32_t cluster_addr) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+// Handing ordinary writes of this CTA's shared memory to a thread of the other
+// CTA (which then lets the tensor cores read them): each writer orders its
+// writes at cluster scope with smem_release_cluster and the arrive is relaxed;
+// the waiter follows its wait with smem_acquire_cluster.  The fences are
+// restricted to shared memory: an arrive with release at cluster scope also
+// waits for global memory, about 1000 cycles on GB300.
+__device__ __forceinline__ void smem_release_cluster() {
+    asm volatile("fence.release.sync_restrict::shared::cta.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void smem_acquire_cluster() {
+    asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory");
+}
+__device__ __forceinline__ void mbar_arrive_remote_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
-// One try of a wait that acquires at cluster scope.
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar_addr, uint32_t parity) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar_addr), "r"(parity), "r"(kWaitSuspendNs)
-        : "memory");
-    return ok != 0;
+// True in exactly one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void st_shared_cluster_u32(uint32_t cluster_addr, uint32_t v) {
@@ -640,14 +643,6 @@ __device__ __forceinline__ bool pair_wait(uint64_t *bar, uint32_t parity, volati
     if (mbar_wait_bounded(bar, parity, abort_flag, status)) return true;
     raise_abort_others<CL>(abort_local, rank);
     return false;
-}
-
-// pair_wait for a phase completed by mbar_arrive_remote_release: acquires at cluster scope.
-template <int CL>
-__device__ __forceinline__ bool pair_wait_acquire(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                                  unsigned int *status, uint32_t abort_local, uint32_t rank) {
-    if (!pair_wait<CL>(bar, parity, abort_flag, status, abort_local, rank)) return false;
-    return mbar_try_wait_cluster(smem_u32(bar), parity);  // complete already: returns at once
 }
 
 // ------------------------------------------- flags between clusters (gpu) --
