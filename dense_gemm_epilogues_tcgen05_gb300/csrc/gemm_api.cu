@@ -1359,6 +1359,20 @@ static int pair_clusters(const DeviceState *dev, int64_t tiles, gemm_launch_info
     return clusters;
 }
 
+// Widest row tile of the 8-bit integer kernel.  192 rows share one expansion of W best (8192 x 4096 x 4096 on
+// GB300: 246 us at 192, 277 at 160, 313 at 128, 430 at 64); where a group has few rows W's expansion is all
+// the time there is, and 64 leaves tensor memory for ten slots of it instead of four (64 experts x 64 rows,
+// 2048 x 4096: 88 us against 91).
+static int i8_most_rows(int64_t G, int64_t M) { return M <= 64 || M <= 16 * G ? 64 : kI8TileRows; }
+
+// Whether a call runs on the streaming kernel for few rows.
+static bool i8_few_rows(int64_t G, int64_t M) { return M <= 8 || M <= 2 * G; }
+
+// Rows that 16-byte loads can read: base and, with more than one row, pitch.
+static bool aligned16(const void *p, int64_t rows, int64_t pitch) {
+    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows == 1 || pitch % 16 == 0);
+}
+
 // The product behind gemm_grouped, gemm_i8 and gemm_i8_grouped (ab: a gemm_dtype_t or kDtI8), arguments checked.
 static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, DeviceState *dev, cudaStream_t s) {
     gemm_launch_info_t info = {};
@@ -1391,6 +1405,11 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
                               ? GEMM_OK : GEMM_ERR_CUDA, info);
         }
     }
+    if (args.K > 0 && ab == kDtI8 && i8_few_rows(args.G, args.M) && aligned16(args.A, args.M, args.sam) &&
+        aligned16(args.B, args.N, args.sbn) && (args.G == 1 || args.sbg % 16 == 0)) {
+        info.path = GEMM_PATH_SIMT;
+        return record(launch_i8_gemv(cd, args, dev->num_sms, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
+    }
     if (args.K > 0 && ab == kDtI8 && tma_ok(args.A, args.M, 1, args.sam, 1) && tma_ok(args.B, args.N, 1, args.sbn, 1) &&
         group_stride_ok(args.G, args.sbg, 1)) {
         CUtensorMap tw, tx32, tx16;
@@ -1406,7 +1425,7 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
         t.bias = args.bias; t.row_scale = args.row_scale; t.col_scale = args.col_scale;
         t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
         t.pairs = pair_stores(args.C, args.ldc, 0);
-        t.most = kI8TileRows;
+        t.most = i8_most_rows(args.G, args.M);
         t.status = args.status;
         const int64_t row_tiles = args.M / t.most + std::min(args.G, args.M);
         const int clusters = pair_clusters(dev, row_tiles * t.tiles_f, &info);

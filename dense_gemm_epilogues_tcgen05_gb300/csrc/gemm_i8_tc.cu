@@ -19,22 +19,22 @@
 //                 128 k (bytes) deep, into a ring of five 28 KB stages of codes,
 //                 on this CTA's own barriers;
 //   warp 1        MMA issuer (leader CTA only);
-//   warps 4-11    converters, two sets of four; set h takes the 64-k half h of
-//                 every stage.  A thread expands one row of W into tensor
+//   warps 4-19    converters, four sets of four; a set takes one 64-k half of
+//                 every other stage.  A thread expands one row of W into tensor
 //                 memory (the MMA's first operand: 32 columns of two values, so
 //                 expanded W never crosses shared memory), and a warp one
 //                 16-byte column of each row of X into a swizzled 16-bit tile;
-//                 four slots of each;
-//   warps 12-19   epilogue: two per 32-lane quadrant, half of the columns each;
+//                 four to ten slots of each;
+//   warps 20-27   epilogue: two per 32-lane quadrant, half of the columns each;
 //                 96 integer sums per thread, then store_chunk_t.
 //
 // A code becomes binary16 by a byte permute into the mantissa of 1024 (the sign
 // bit flipped first: 1024 + 128 + code) and one subtraction of 1152: five
 // instructions for four codes, all exact.
 //
-// Registers: 20 warps launch with 96 each; the warpgroups then trade them (40
-// for the issuers, 64 for each converter set, 152 for each epilogue set: 472
-// of the 480 that five warps of a sub-partition launched with).
+// Registers: 28 warps launch with 72 each; the warpgroups then trade them (32
+// for the issuers, 48 for each converter set, 136 for each epilogue set: 496 of
+// the 504 that seven warps of a sub-partition launched with).
 //
 // Bound: at large sizes shared-memory bandwidth -- per 128 k a CTA moves 32 KB
 // of W (codes in, codes out) and 768 bytes per row of X (codes in and out,
@@ -54,8 +54,11 @@ struct I8Config {
     static constexpr int W_BYTES = 128 * BK;
     static constexpr int CHUNK_HALVES = 1024 / 64;  // 64-k halves summed in fp32
     static constexpr int W_SLOT_COLS = 32, TMEM_COLS = 512;
-    static constexpr int CONV_WARP0 = 4, EPI_WARP0 = 12, THREADS = 640;
-    static constexpr int LAUNCH_REGS = 96;
+    static constexpr int SETS = 4;                  // converter sets of four warps
+    static constexpr int CONV_WARP0 = 4, EPI_WARP0 = CONV_WARP0 + 4 * SETS, THREADS = 32 * (EPI_WARP0 + 8);
+    // registers per thread: at launch, then the issuers', the converters', the epilogue's
+    static constexpr int LAUNCH_REGS = 72, ISSUE_REGS = 32, CONV_REGS = 48, EPI_REGS = 136;
+    static_assert(ISSUE_REGS + SETS * CONV_REGS + 2 * EPI_REGS <= (SETS + 3) * LAUNCH_REGS, "the trade adds up");
     static constexpr int BAR_BYTES = 512, SMEM_MAX = 232448;
     static_assert((2 * MAX_STAGES + 2 * MAX_SLOTS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
     // after up to 1023 bytes of alignment: [stages][slots][barriers][group table]
@@ -68,12 +71,20 @@ struct I8Config {
 // holds stages of codes.
 struct I8Shape {
     int stage_bytes, slot_bytes, slots, stages;
-    __host__ __device__ __forceinline__ I8Shape(int most, int stages_) : stages(stages_) {
+    __host__ __device__ I8Shape(int most, int stages_) : stages(stages_) {
         stage_bytes = I8Config::W_BYTES + most / 2 * I8Config::BK;
         slot_bytes = most / 2 * 128;  // 64 k in 16 bits
         const int cols = (I8Config::TMEM_COLS - 2 * most) / I8Config::W_SLOT_COLS;
-        slots = cols < I8Config::MAX_SLOTS ? cols & ~1 : I8Config::MAX_SLOTS;
+        // Two sets can skip uses of a stage and of a slot, and a parity wait is
+        // only right within one use.  A set at half h has had half h - 4 accepted,
+        // so the issuer has consumed every half up to h - 4 - slots: that covers
+        // the slot's use before the last (slots >= 4) and the stage's use before
+        // this one (2 stages >= slots + 5).
+        slots = cols < I8Config::MAX_SLOTS ? cols : I8Config::MAX_SLOTS;
+        if (slots > 2 * stages - 5) slots = 2 * stages - 5;
+        slots &= ~1;  // a stage's two halves are announced together
     }
+    int bytes() const { return slots * slot_bytes + stages * stage_bytes; }
 };
 
 // Four codes to two pairs of binary16.
@@ -101,7 +112,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
     unsigned char *slot_base = smem + stages * sh.stage_bytes;
     uint64_t *full = reinterpret_cast<uint64_t *>(slot_base + slots * sh.slot_bytes);  // codes landed
     uint64_t *empty = full + Cfg::MAX_STAGES;   // codes read by both converter sets
-    uint64_t *ready = empty + Cfg::MAX_STAGES;  // (leader's) a slot expanded in both CTAs
+    uint64_t *ready = empty + Cfg::MAX_STAGES;  // (leader's) two slots, one stage, expanded in both CTAs
     uint64_t *freed = ready + Cfg::MAX_SLOTS;   // a slot read by the MMA
     uint64_t *tfull = freed + Cfg::MAX_SLOTS;
     uint64_t *tempty = tfull + 2;
@@ -119,7 +130,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
             mbar_init(&empty[s], 8);
         }
         for (int s = 0; s < Cfg::MAX_SLOTS; ++s) {
-            mbar_init(&ready[s], CL * 4);
+            mbar_init(&ready[s], CL * 8);
             mbar_init(&freed[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -154,7 +165,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
     const int num_kb = (args.K + Cfg::BK - 1) / Cfg::BK;
 
     if (warp < Cfg::CONV_WARP0) {
-        regs_decrease<40>();
+        regs_decrease<Cfg::ISSUE_REGS>();
         if (warp == 0 && lane == 0) {
             // ------------------------------------------------ TMA producer --
             uint32_t stage = 0, phase = 0;
@@ -199,7 +210,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
             // at 192 columns).
             uint32_t slot = 0, slot_phase = 0;
             uint32_t local = 0;  // accumulators filled
-            bool ok = true, issued = false;
+            bool ok = true, issued = false, is_ready = false;
             for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
                 const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
                 const uint32_t idesc = mma_idesc(TcTraits<kDtF16>::kFmt, TcTraits<kDtF16>::kFmt, 256, t.bn);
@@ -212,13 +223,21 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                     tc_fence_after();
                     const uint32_t d_tmem = tmem_base + acc * acc_stride;
                     const int end = min(2 * num_kb, h + Cfg::CHUNK_HALVES);
-                    for (int i = h; i < end; ++i) {
-                        ok = pair_wait<CL>(&ready[slot], slot_phase, abort_flag, args.status, abort_local, rank);
-                        if (!__all_sync(0xffffffffu, ok)) ok = false;
-                        if (!ok) break;
+                    for (int i = h; i < end; i += 2) {
+                        if (!is_ready) {
+                            ok = pair_wait<CL>(&ready[slot >> 1], slot_phase, abort_flag, args.status, abort_local,
+                                               rank);
+                            if (!__all_sync(0xffffffffu, ok)) ok = false;
+                            if (!ok) break;
+                        }
                         smem_acquire_cluster();
                         tc_fence_after();
+                        // ask for the next two slots now: the answer comes while these MMAs issue
+                        const uint32_t next = slot + 2 == slots ? 0u : slot + 2;
+                        const uint32_t next_phase = next == 0 ? slot_phase ^ 1u : slot_phase;
+                        const bool next_ready = mbar_test_wait(smem_u32(&ready[next >> 1]), next_phase);
                         const uint64_t bd = sw128_desc(smem_u32(slot_base) + slot * sh.slot_bytes, 16u, 1024u);
+                        const uint64_t bd2 = bd + (sh.slot_bytes >> 4);
                         const uint32_t w_tmem = w_slot0 + slot * Cfg::W_SLOT_COLS;
                         if (elect_one()) {
 #pragma unroll
@@ -226,14 +245,17 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                                 tc_mma_pair_f16_tmem_a(d_tmem, w_tmem + ks * 8, bd + 2 * ks, idesc,
                                                        (i != h || ks != 0) ? 1u : 0u);
                             tc_commit_pair(&freed[slot], 0x3);
-                            if (i + 1 == end) tc_commit_pair(&tfull[acc], 0x3);
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                tc_mma_pair_f16_tmem_a(d_tmem, w_tmem + Cfg::W_SLOT_COLS + ks * 8, bd2 + 2 * ks,
+                                                       idesc, 1u);
+                            tc_commit_pair(&freed[slot + 1], 0x3);
+                            if (i + 2 == end) tc_commit_pair(&tfull[acc], 0x3);
                         }
                         issued = true;
-                        __syncwarp();
-                        if (++slot == slots) {
-                            slot = 0;
-                            slot_phase ^= 1u;
-                        }
+                        is_ready = __all_sync(0xffffffffu, next_ready);
+                        slot = next;
+                        slot_phase = next_phase;
                     }
                 }
             }
@@ -244,65 +266,65 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
         }
     } else if (warp < Cfg::EPI_WARP0) {
         // ----------------------------------------------------- converters --
-        regs_decrease<64>();
-        const int quad = warp & 3, hk = (warp - Cfg::CONV_WARP0) >> 2;
+        regs_decrease<Cfg::CONV_REGS>();
+        const int quad = warp & 3, set = (warp - Cfg::CONV_WARP0) >> 2, hk = set & 1;
+        constexpr int step = Cfg::SETS / 2;  // stages from one turn to the next
         const int wr = quad * 32 + lane;  // this thread's row of W
-        constexpr int XR = kI8TileRows / 64;  // rows of X per thread
-        uint32_t stage = 0, phase = 0, slot = hk, slot_phase = 0;
+        int kb = set >> 1;                // stage of the tile, numbered on through all tiles
+        uint32_t stage = kb, phase = 0, slot = 2 * kb + hk, slot_phase = 0;
         bool ok = true;
-        for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
+        for (long long tile = cluster; ok && tile < tiles; tile += nclusters, kb -= num_kb) {
             const int bnh = row_tile(table, tile, args.tiles_f, args.K).bn >> 1;
-            for (int kb = 0; kb < num_kb; ++kb) {
+            for (; kb < num_kb; kb += step) {
                 bool got = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
                 const unsigned char *sW = smem + stage * sh.stage_bytes, *sX = sW + Cfg::W_BYTES;
-                uint4 w[4], x[XR];
+                uint4 c[4];
+                // this row's 64 codes: 16-byte unit u of a row sits at u ^ (row % 8)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    w[i] = *reinterpret_cast<const uint4 *>(sW + wr * 128 + (((hk * 4 + i) ^ (wr & 7)) << 4));
-#pragma unroll
-                for (int i = 0; i < XR; ++i)
-                    if (lane + 32 * i < bnh)
-                        x[i] = *reinterpret_cast<const uint4 *>(sX + (lane + 32 * i) * 128 +
-                                                                (((hk * 4 + quad) ^ (lane & 7)) << 4));
+                    c[i] = *reinterpret_cast<const uint4 *>(sW + wr * 128 + (((hk * 4 + i) ^ (wr & 7)) << 4));
                 got = got &&
                       pair_wait<CL>(&freed[slot], slot_phase ^ 1u, abort_flag, args.status, abort_local, rank);
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
                     break;
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[stage]);  // every lane has read its codes
                 tc_fence_after();
-                unsigned char *xs = slot_base + slot * sh.slot_bytes;
+                // to 32 columns of tensor memory
                 const uint32_t w_tmem =
                     w_slot0 + (static_cast<uint32_t>(quad * 32) << 16) + slot * Cfg::W_SLOT_COLS;
-                // codes to binary16: this row's 64 of W (16-byte unit u of a row sits
-                // at u ^ (row % 8)) to 32 columns of tensor memory
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     uint32_t out[16];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const uint4 c = w[2 * p + i];
-                        expand4(c.x, out[8 * i], out[8 * i + 1]);
-                        expand4(c.y, out[8 * i + 2], out[8 * i + 3]);
-                        expand4(c.z, out[8 * i + 4], out[8 * i + 5]);
-                        expand4(c.w, out[8 * i + 6], out[8 * i + 7]);
+                        expand4(c[2 * p + i].x, out[8 * i], out[8 * i + 1]);
+                        expand4(c[2 * p + i].y, out[8 * i + 2], out[8 * i + 3]);
+                        expand4(c[2 * p + i].z, out[8 * i + 4], out[8 * i + 5]);
+                        expand4(c[2 * p + i].w, out[8 * i + 6], out[8 * i + 7]);
                     }
                     tmem_st_x16(w_tmem + p * 16, out);
                 }
                 // 16 codes of each row of X: unit hk * 4 + quad in, units 2 quad and 2 quad + 1 out
+                unsigned char *xs = slot_base + slot * sh.slot_bytes;
+                constexpr int XR = kI8TileRows / 64;  // most rows per thread
+                const int sw = lane & 7;
+#pragma unroll
+                for (int i = 0; i < XR; ++i)
+                    if (lane + 32 * i < bnh)
+                        c[i] = *reinterpret_cast<const uint4 *>(sX + (lane + 32 * i) * 128 +
+                                                                (((hk * 4 + quad) ^ sw) << 4));
 #pragma unroll
                 for (int i = 0; i < XR; ++i) {
                     const int r = lane + 32 * i;
                     if (r < bnh) {
                         uint4 a, b;
-                        expand4(x[i].x, a.x, a.y);
-                        expand4(x[i].y, a.z, a.w);
-                        expand4(x[i].z, b.x, b.y);
-                        expand4(x[i].w, b.z, b.w);
-                        *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad) ^ (lane & 7)) << 4)) = a;
-                        *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad + 1) ^ (lane & 7)) << 4)) = b;
+                        expand4(c[i].x, a.x, a.y);
+                        expand4(c[i].y, a.z, a.w);
+                        expand4(c[i].z, b.x, b.y);
+                        expand4(c[i].w, b.z, b.w);
+                        *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad) ^ sw) << 4)) = a;
+                        *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad + 1) ^ sw) << 4)) = b;
                     }
                 }
                 tmem_st_wait();
@@ -310,20 +332,23 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                 smem_release_cluster();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_remote_relaxed(ready0_leader + 8u * slot);
-                if ((slot += 2) >= slots) {
+                if (lane == 0) {
+                    mbar_arrive_remote_relaxed(ready0_leader + 8u * (slot >> 1));
+                    mbar_arrive(&empty[stage]);
+                }
+                if ((slot += 2 * step) >= slots) {
                     slot -= slots;
                     slot_phase ^= 1u;
                 }
-                if (++stage == stages) {
-                    stage = 0;
+                if ((stage += step) >= stages) {
+                    stage -= stages;
                     phase ^= 1u;
                 }
             }
         }
     } else {
         // ------------------------------------------------------- epilogue --
-        regs_increase<152>();
+        regs_increase<Cfg::EPI_REGS>();
         using OutT = typename Elem<OUT>::T;
         const int quad = warp & 3, side = (warp - Cfg::EPI_WARP0) >> 2;
         const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi, args.pairs};
@@ -353,12 +378,15 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < MC; ++c) {
                     if (c < nch) {
-                        uint32_t raw[32];
-                        __syncwarp();
-                        tmem_ld_issue(t_row + c * 32, raw);
-                        tmem_ld_wait(raw);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) sum[c][j] += __float2int_rn(__uint_as_float(raw[j]));
+                        for (int p = 0; p < 2; ++p) {
+                            uint32_t raw[16];
+                            __syncwarp();
+                            tmem_ld_x16(t_row + c * 32 + p * 16, raw);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                sum[c][16 * p + j] += __float2int_rn(__uint_as_float(raw[j]));
+                        }
                     }
                 }
                 tc_fence_before();
@@ -407,12 +435,12 @@ cudaError_t launch_i8_tc_out(const CUtensorMap &tw, const CUtensorMap &tx32, con
     if ((err = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return err;
     if (fa.numRegs != I8Config::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
     GtcArgs args = a;
-    I8Shape sh(args.most, 0);
-    const int data = I8Config::SMEM_MAX - I8Config::fixed_bytes(args.G) - sh.slots * sh.slot_bytes;
-    args.stages = std::min(I8Config::MAX_STAGES, data / sh.stage_bytes);
-    if (args.most < 32 || args.most > kI8TileRows || args.most % 32 != 0 || args.stages < 2)
-        return cudaErrorInvalidValue;
-    const int smem = I8Config::fixed_bytes(args.G) + sh.slots * sh.slot_bytes + args.stages * sh.stage_bytes;
+    if (args.most < 32 || args.most > kI8TileRows || args.most % 32 != 0) return cudaErrorInvalidValue;
+    args.stages = I8Config::MAX_STAGES;
+    while (args.stages > 4 && I8Config::fixed_bytes(args.G) + I8Shape(args.most, args.stages).bytes() > I8Config::SMEM_MAX)
+        --args.stages;
+    const int smem = I8Config::fixed_bytes(args.G) + I8Shape(args.most, args.stages).bytes();
+    if (smem > I8Config::SMEM_MAX || smem <= I8Config::SMEM_MAX / 2) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters, 1, 1);
     cfg.blockDim = dim3(I8Config::THREADS, 1, 1);

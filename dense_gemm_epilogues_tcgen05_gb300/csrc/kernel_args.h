@@ -187,6 +187,8 @@ cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const CUtensorMap &ta
 //   128 x 128 bytes, tx32 / tx16 = row codes (K, T) in boxes of 128 x 32 and 128 x 16; 128-byte swizzle.
 cudaError_t launch_i8_tc(int out, const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
                          const GtcArgs &args, int clusters, cudaStream_t stream);
+//   8-bit integer products for few rows (16-byte aligned rows of codes):
+cudaError_t launch_i8_gemv(int out, const GroupedArgs &args, int sms, cudaStream_t stream);
 constexpr int kI8TileRows = 192;    // its widest row tile
 //   grouped products on the CUDA cores, any strides (ab: F32, F16, BF16 or kDtI8), `grid` blocks:
 cudaError_t launch_grouped_simt(int ab, int out, const GroupedArgs &args, int grid, cudaStream_t stream);
