@@ -1335,6 +1335,22 @@ static gemm_status_t encode_3d(CUtensorMap *map, int ab, const void *base, int64
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
+// Rows of 8-bit codes as (128, rows, whole boxes of 128 along K, groups), boxes of 128 x box_rows x boxes x 1:
+// several 128-byte columns of a row block by one load, each laid out as encode_3d's.
+static gemm_status_t encode_i8_boxes(CUtensorMap *map, const void *base, int64_t K, int64_t rows, int64_t row_stride,
+                                     int64_t groups, int64_t group_stride, uint32_t box_rows, uint32_t boxes) {
+    cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(K / 128),
+                          static_cast<cuuint64_t>(groups)};
+    cuuint64_t strides[3] = {rows == 1 ? 16 : static_cast<cuuint64_t>(row_stride), 128,
+                             groups == 1 ? 16 : static_cast<cuuint64_t>(group_stride)};
+    cuuint32_t box[4] = {128u, box_rows, boxes, 1u};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = driver_fns().encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides,
+                                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
 // Whether a stride between matrices can be a tensor map's: a multiple of 16 bytes (0: one matrix for all
 // groups, which the map then has once).
 static bool group_stride_ok(int64_t G, int64_t stride, int es) {
@@ -1365,12 +1381,11 @@ static int pair_clusters(const DeviceState *dev, int64_t tiles, gemm_launch_info
 // 2048 x 4096: 88 us against 91).
 static int i8_most_rows(int64_t G, int64_t M) { return M <= 64 || M <= 16 * G ? 64 : kI8TileRows; }
 
-// Whether a call runs on the streaming kernel for few rows.
-static bool i8_few_rows(int64_t G, int64_t M) { return M <= 8 || M <= 2 * G; }
-
-// Rows that 16-byte loads can read: base and, with more than one row, pitch.
-static bool aligned16(const void *p, int64_t rows, int64_t pitch) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (rows == 1 || pitch % 16 == 0);
+// Row tiles of the streaming kernel, in eights (0: the call has too many rows for it).
+static int i8_few_rows(int64_t G, int64_t M) {
+    if (M <= 8 || M <= 2 * G) return 1;
+    if (M <= 16 || M <= 4 * G) return 2;
+    return M <= 32 || M <= 8 * G ? 4 : 0;
 }
 
 // The product behind gemm_grouped, gemm_i8 and gemm_i8_grouped (ab: a gemm_dtype_t or kDtI8), arguments checked.
@@ -1405,13 +1420,29 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
                               ? GEMM_OK : GEMM_ERR_CUDA, info);
         }
     }
-    if (args.K > 0 && ab == kDtI8 && i8_few_rows(args.G, args.M) && aligned16(args.A, args.M, args.sam) &&
-        aligned16(args.B, args.N, args.sbn) && (args.G == 1 || args.sbg % 16 == 0)) {
-        info.path = GEMM_PATH_SIMT;
-        return record(launch_i8_gemv(cd, args, dev->num_sms, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
-    }
     if (args.K > 0 && ab == kDtI8 && tma_ok(args.A, args.M, 1, args.sam, 1) && tma_ok(args.B, args.N, 1, args.sbn, 1) &&
         group_stride_ok(args.G, args.sbg, 1)) {
+        if (const int nt = i8_few_rows(args.G, args.M)) {
+            GvMaps m;
+            gemm_status_t st;
+            const uint32_t wr = static_cast<uint32_t>(i8_gemv_w_rows(nt)), xr = 8u * nt;
+            if ((st = encode_3d(&m.w_tail, kDtI8, args.B, args.K, args.N, args.sbn, args.G, args.sbg, wr)) != GEMM_OK)
+                return st;
+            if ((st = encode_3d(&m.x_tail, kDtI8, args.A, args.K, args.M, args.sam, 1, 0, xr)) != GEMM_OK) return st;
+            m.w = m.w_tail;
+            m.x = m.x_tail;
+            if (args.K >= 128) {
+                const uint32_t boxes = static_cast<uint32_t>(i8_gemv_boxes(nt));
+                if ((st = encode_i8_boxes(&m.w, args.B, args.K, args.N, args.sbn, args.G, args.sbg, wr, boxes)) !=
+                    GEMM_OK)
+                    return st;
+                if ((st = encode_i8_boxes(&m.x, args.A, args.K, args.M, args.sam, 1, 0, xr, boxes)) != GEMM_OK)
+                    return st;
+            }
+            info.path = GEMM_PATH_SIMT;
+            return record(launch_i8_gemv(cd, nt, m, args, dev->num_sms, s) == cudaSuccess ? GEMM_OK
+                                                                                               : GEMM_ERR_CUDA, info);
+        }
         CUtensorMap tw, tx32, tx16;
         gemm_status_t st;
         if ((st = encode_3d(&tw, kDtI8, args.B, args.K, args.N, args.sbn, args.G, args.sbg, 128)) != GEMM_OK) return st;

@@ -87,17 +87,6 @@ struct I8Shape {
     int bytes() const { return slots * slot_bytes + stages * stage_bytes; }
 };
 
-// Four codes to two pairs of binary16.
-__device__ __forceinline__ void expand4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
-    const uint32_t u = codes ^ 0x80808080u;
-    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
-    lo = *reinterpret_cast<const uint32_t *>(&x);
-    hi = *reinterpret_cast<const uint32_t *>(&y);
-}
-
 template <int OUT>
 __global__ void __launch_bounds__(I8Config::THREADS, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX32,

@@ -196,6 +196,18 @@ __device__ __forceinline__ void store_chunk_t(float (&v)[32], typename Elem<OUT>
     }
 }
 
+// ------------------------------------------------------------ 8-bit codes --
+// Four codes to two pairs of binary16.
+__device__ __forceinline__ void expand4(uint32_t codes, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = codes ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));  // 1152
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+
 // ------------------------------------------------------------ operand types --
 template <int AB> struct SimtAcc { using T = float; };
 template <> struct SimtAcc<kDtI8> { using T = int; };
