@@ -1375,17 +1375,35 @@ static int pair_clusters(const DeviceState *dev, int64_t tiles, gemm_launch_info
     return clusters;
 }
 
-// Widest row tile of the 8-bit integer kernel.  192 rows share one expansion of W best (8192 x 4096 x 4096 on
-// GB300: 246 us at 192, 277 at 160, 313 at 128, 430 at 64); where a group has few rows W's expansion is all
-// the time there is, and 64 leaves tensor memory for ten slots of it instead of four (64 experts x 64 rows,
-// 2048 x 4096: 88 us against 91).
-static int i8_most_rows(int64_t G, int64_t M) { return M <= 64 || M <= 16 * G ? 64 : kI8TileRows; }
+// Widest row tile of the 8-bit integer kernel: 64, 128 or 192.  A 128-k stage of a tile of w rows takes about
+// 600 + 4 w clocks (8192 x 4096 x 4096 on GB300: 374 / 254 / 230 us at 64 / 128 / 192 rows), so wide tiles share
+// the expansion of W best, and narrow ones win where they fill the SM pairs (192 x 4096 x 4096: 20 / 23 / 29 us).
+// Groups' sizes are only known on the device: they are taken as equal.
+static int i8_most_rows(int64_t G, int64_t M, int64_t N, int pairs) {
+    const int64_t groups = std::min(G, M), rows = (M + groups - 1) / groups;
+    int best = 0;
+    int64_t best_cost = 0;
+    for (int most = kI8TileRows; most >= 64; most -= 64) {
+        const int64_t nt = (rows + most - 1) / most, width = ((rows + nt - 1) / nt + 31) / 32 * 32;
+        const int64_t tiles = groups * nt * ((N + 255) / 256);
+        const int64_t cost = (tiles + pairs - 1) / pairs * (600 + 4 * width);
+        if (best == 0 || cost < best_cost) {
+            best = most;
+            best_cost = cost;
+        }
+    }
+    return best;
+}
 
-// Row tiles of the streaming kernel, in eights (0: the call has too many rows for it).
-static int i8_few_rows(int64_t G, int64_t M) {
+// Row tiles of the streaming kernel for few rows, in eights; 0: the call runs on the pair kernel.  One and two
+// eights keep up with HBM whatever the size (16384^2 codes on GB300: 46 to 49 us up to 8 rows, 58 to 16, the
+// pair kernel 60); four are bound by their MMAs (32 rows: 86 us), but with few tiles the pair kernel leaves
+// most SMs idle (32 rows of 4096^2: 15 us against 19), so they run where its tiles would not fill the SM pairs.
+static int i8_few_rows(int64_t G, int64_t M, int64_t N) {
     if (M <= 8 || M <= 2 * G) return 1;
     if (M <= 16 || M <= 4 * G) return 2;
-    return M <= 32 || M <= 8 * G ? 4 : 0;
+    const int64_t row_tiles = G == 1 ? (M + 31) / 32 : M / 32 + std::min(G, M);
+    return row_tiles * ((N + 255) / 256) <= 50 ? 4 : 0;
 }
 
 // The product behind gemm_grouped, gemm_i8 and gemm_i8_grouped (ab: a gemm_dtype_t or kDtI8), arguments checked.
@@ -1422,7 +1440,7 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
     }
     if (args.K > 0 && ab == kDtI8 && tma_ok(args.A, args.M, 1, args.sam, 1) && tma_ok(args.B, args.N, 1, args.sbn, 1) &&
         group_stride_ok(args.G, args.sbg, 1)) {
-        if (const int nt = i8_few_rows(args.G, args.M)) {
+        if (const int nt = i8_few_rows(args.G, args.M, args.N)) {
             GvMaps m;
             gemm_status_t st;
             const uint32_t wr = static_cast<uint32_t>(i8_gemv_w_rows(nt)), xr = 8u * nt;
@@ -1456,7 +1474,7 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
         t.bias = args.bias; t.row_scale = args.row_scale; t.col_scale = args.col_scale;
         t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
         t.pairs = pair_stores(args.C, args.ldc, 0);
-        t.most = i8_most_rows(args.G, args.M);
+        t.most = i8_most_rows(args.G, args.M, args.N, dev->num_sms / 2);
         t.status = args.status;
         const int64_t row_tiles = args.M / t.most + std::min(args.G, args.M);
         const int clusters = pair_clusters(dev, row_tiles * t.tiles_f, &info);

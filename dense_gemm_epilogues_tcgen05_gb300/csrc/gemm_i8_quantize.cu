@@ -4,32 +4,105 @@
 //
 // so q * scale is the row to within scale / 2.  A row of zeros gets scale 0
 // and codes 0; a row that holds a NaN or an infinity gets a NaN scale (the
-// product's row shows it) and codes 0.  127 x is exact in fp32 for 16-bit
-// inputs and the quotient is correctly rounded: a 16-bit input's quotient that
-// is not a tie is further from one than that rounding, so codes of 16-bit
-// inputs are the exact quotient's.
+// product's row shows it) and codes 0.
 //
 // One block per row, one pass over memory: a thread keeps its (up to 8)
 // 16-byte pieces of the row in registers between the maximum and the rounding,
-// and reads what a longer row has beyond them again (from L2).
+// and reads what a longer row has beyond them again (from L2).  The maximum of
+// 16-bit values is taken on their bits, two per instruction: with the sign
+// cleared, they are ordered as integers, infinities and NaN last.
+//
+// The codes are those of the exact quotient.  x * (127 / max) is off by at most
+// 2^-23 of a quotient of at most 127, so by less than 2^-15: where it is further
+// than that from a tie its rounding is the quotient's, and only the other values
+// (one in 2^14) take the division.  There 127 x is exact for 16-bit inputs, the
+// division is correctly rounded, and a quotient of two 16-bit values that is not a
+// tie is further from one than that rounding.
+//
+// Bound: HBM (3 bytes per 16-bit value).
 #include "grouped.cuh"
 
 namespace gb300 {
 
 namespace {
 
-constexpr int kQThreads = 256, kQKeep = 8;
+constexpr int kQThreads = 256;
 
 // |x| as an ordered integer; infinities and NaN are the largest.
 __device__ __forceinline__ unsigned abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 // round_even(127 x / amax).  `shrink` is 1, or 2^-32 on both where 127 x could
 // overflow (exact; what it flushes is far below half a step).
-__device__ __forceinline__ int code_of(float x, float amax, float shrink) {
+__device__ __noinline__ int code_by_division(float x, float amax, float shrink) {
     return __float2int_rn(__fdiv_rn(127.0f * (x * shrink), amax * shrink));
 }
 
-template <int XT, bool VEC>
+struct QRow {
+    float amax, inv, shrink;
+    bool zero;  // codes 0 throughout
+    bool slow;  // 127 / amax is not a normal number: divide always
+};
+
+// The largest |x| of a 16-byte piece, as the bits of an fp32 value; 16-bit types
+// two at a time (the halves of `acc` are combined at the end).
+template <int XT>
+__device__ __forceinline__ void max16(const uint4 &u, unsigned &acc) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (XT == kDtF32)
+            acc = max(acc, w[i] & 0x7FFFFFFFu);
+        else
+            acc = __vmaxu2(acc, w[i] & 0x7FFF7FFFu);
+    }
+}
+
+template <int XT>
+__device__ __forceinline__ unsigned max_bits(unsigned acc) {
+    if constexpr (XT == kDtF32) return acc;
+    const unsigned m = max(acc & 0xFFFFu, acc >> 16);
+    if constexpr (XT == kDtBF16) return m << 16;
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+}
+
+// Codes of N values (N even, at most 8) into N bytes.  r + 1.5 * 2^23 holds
+// round_even(r) in its low bits, as a two's complement byte.
+template <int N>
+__device__ __forceinline__ void codes_of(const float (&f)[N], const QRow &row, uint32_t (&w)[N / 4]) {
+    constexpr float kMagic = 12582912.0f;
+    uint32_t t[N];
+    float worst = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+        const uint64_t r = f2_mul(f2_pack(f[j], f[j + 1]), f2_splat(row.inv));
+        const uint64_t s = f2_add(r, f2_splat(kMagic));
+        const uint64_t back = f2_add(s, f2_splat(-kMagic));
+        const uint64_t off = f2_fma(back, f2_splat(-1.0f), r);
+        float s0, s1, o0, o1;
+        f2_unpack(s, s0, s1);
+        f2_unpack(off, o0, o1);
+        t[j] = __float_as_uint(s0);
+        t[j + 1] = __float_as_uint(s1);
+        worst = fmaxf(worst, fmaxf(fabsf(o0), fabsf(o1)));
+    }
+    if (row.slow || worst > 0.5f - 0x1p-15f) {
+#pragma unroll 1
+        for (int j = 0; j < N; ++j) {
+            const uint32_t c = static_cast<uint32_t>(code_by_division(f[j], row.amax, row.shrink));
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i == j) t[i] = c;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+        const uint32_t lo = __byte_perm(t[4 * i], t[4 * i + 1], 0x0040), hi = __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040);
+        w[i] = row.zero ? 0u : __byte_perm(lo, hi, 0x5410);
+    }
+}
+
+// VEC: 16-byte loads of X and whole-word stores of Q; KEEP pieces per thread stay in registers.
+template <int XT, bool VEC, int KEEP>
 __global__ void __launch_bounds__(kQThreads) i8_quantize_kernel(long long K, const void *X, long long ldx,
                                                                 signed char *Q, long long ldq, float *scale) {
     using InT = typename Elem<XT>::T;
@@ -38,70 +111,62 @@ __global__ void __launch_bounds__(kQThreads) i8_quantize_kernel(long long K, con
     const long long row = blockIdx.x;
     const InT *x = static_cast<const InT *>(X) + row * ldx;
     signed char *q = Q + row * ldq;
-    const int tid = threadIdx.x;
-    unsigned m = 0u;
-    uint4 keep[kQKeep];
+    const int tid = threadIdx.x, n = blockDim.x;
+    const uint4 *xv = reinterpret_cast<const uint4 *>(x);
     const long long nvec = VEC ? K / PV : 0;
+    unsigned acc = 0u;
+    uint4 keep[KEEP];
     if constexpr (VEC) {
-        const uint4 *xv = reinterpret_cast<const uint4 *>(x);
 #pragma unroll
-        for (int i = 0; i < kQKeep; ++i) {
-            const long long v = tid + static_cast<long long>(i) * kQThreads;
+        for (int i = 0; i < KEEP; ++i) {
+            const long long v = tid + static_cast<long long>(i) * n;
             keep[i] = v < nvec ? __ldg(xv + v) : make_uint4(0, 0, 0, 0);
         }
 #pragma unroll
-        for (int i = 0; i < kQKeep; ++i) {
-            float f[PV];
-            Vec16<XT>::unpack(keep[i], f);
-#pragma unroll
-            for (int j = 0; j < PV; ++j) m = max(m, abs_bits(f[j]));
-        }
-        for (long long v = tid + static_cast<long long>(kQKeep) * kQThreads; v < nvec; v += kQThreads) {
-            float f[PV];
-            Vec16<XT>::unpack(__ldg(xv + v), f);
-#pragma unroll
-            for (int j = 0; j < PV; ++j) m = max(m, abs_bits(f[j]));
-        }
+        for (int i = 0; i < KEEP; ++i) max16<XT>(keep[i], acc);
+        for (long long v = tid + static_cast<long long>(KEEP) * n; v < nvec; v += n) max16<XT>(__ldg(xv + v), acc);
     }
-    for (long long k = nvec * PV + tid; k < K; k += kQThreads) m = max(m, abs_bits(Elem<XT>::load(x + k)));
+    unsigned m = max_bits<XT>(acc);
+    for (long long k = nvec * PV + tid; k < K; k += n) m = max(m, abs_bits(Elem<XT>::load(x + k)));
     m = __reduce_max_sync(0xffffffffu, m);
     if ((tid & 31) == 0) part[tid >> 5] = m;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kQThreads / 32; ++w) m = max(m, part[w]);
+    for (int w = 0; w < n >> 5; ++w) m = max(m, part[w]);
     const bool finite = m < 0x7F800000u;
-    const float amax = __uint_as_float(m);
-    if (tid == 0) scale[row] = finite ? __fdiv_rn(amax, 127.0f) : __uint_as_float(0x7FC00000u);
-    const bool zero = !finite || m == 0u;
-    const float shrink = amax >= 1.2676506e30f ? 2.3283064365386963e-10f : 1.0f;  // 2^100, 2^-32
+    QRow r;
+    r.amax = __uint_as_float(m);
+    r.zero = !finite || m == 0u;
+    r.slow = !(r.amax > 1e-30f && r.amax < 1e30f) && !r.zero;
+    r.shrink = r.amax >= 1.2676506e30f ? 2.3283064365386963e-10f : 1.0f;  // 2^100, 2^-32
+    r.inv = r.slow || r.zero ? 0.0f : __fdiv_rn(127.0f, r.amax);
+    if (tid == 0) scale[row] = finite ? __fdiv_rn(r.amax, 127.0f) : __uint_as_float(0x7FC00000u);
     if constexpr (VEC) {
-        const uint4 *xv = reinterpret_cast<const uint4 *>(x);
         auto store = [&](long long v, const uint4 &u) {
             float f[PV];
             Vec16<XT>::unpack(u, f);
             uint32_t w[PV / 4];
-#pragma unroll
-            for (int j = 0; j < PV / 4; ++j) {
-                w[j] = 0u;
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-                    w[j] |= (zero ? 0u : static_cast<uint32_t>(code_of(f[4 * j + b], amax, shrink)) & 0xFFu) << (8 * b);
-            }
+            codes_of<PV>(f, r, w);
             if constexpr (PV == 8)
                 *reinterpret_cast<uint2 *>(q + v * PV) = make_uint2(w[0], w[1]);
             else
                 *reinterpret_cast<uint32_t *>(q + v * PV) = w[0];
         };
 #pragma unroll
-        for (int i = 0; i < kQKeep; ++i) {
-            const long long v = tid + static_cast<long long>(i) * kQThreads;
+        for (int i = 0; i < KEEP; ++i) {
+            const long long v = tid + static_cast<long long>(i) * n;
             if (v < nvec) store(v, keep[i]);
         }
-        for (long long v = tid + static_cast<long long>(kQKeep) * kQThreads; v < nvec; v += kQThreads)
-            store(v, __ldg(xv + v));
+        for (long long v = tid + static_cast<long long>(KEEP) * n; v < nvec; v += n) store(v, __ldg(xv + v));
     }
-    for (long long k = nvec * PV + tid; k < K; k += kQThreads)
-        q[k] = static_cast<signed char>(zero ? 0 : code_of(Elem<XT>::load(x + k), amax, shrink));
+    for (long long k = nvec * PV + tid; k < K; k += n)
+        q[k] = static_cast<signed char>(r.zero ? 0 : code_by_division(Elem<XT>::load(x + k), r.amax, r.shrink));
+}
+
+template <int XT, int KEEP>
+cudaError_t quantize_keep(unsigned grid, int threads, long long K, const void *X, long long ldx, signed char *Q,
+                          long long ldq, float *scale, cudaStream_t s) {
+    i8_quantize_kernel<XT, true, KEEP><<<grid, threads, 0, s>>>(K, X, ldx, Q, ldq, scale);
+    return cudaGetLastError();
 }
 
 template <int XT>
@@ -111,9 +176,19 @@ cudaError_t quantize_xt(long long M, long long K, const void *X, long long ldx, 
     const bool vec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (M == 1 || ldx * es % 16 == 0) &&
                      (reinterpret_cast<uintptr_t>(Q) & 7u) == 0 && (M == 1 || ldq % 8 == 0);
     const unsigned grid = static_cast<unsigned>(M);
-    if (vec) i8_quantize_kernel<XT, true><<<grid, kQThreads, 0, s>>>(K, X, ldx, Q, ldq, scale);
-    else i8_quantize_kernel<XT, false><<<grid, kQThreads, 0, s>>>(K, X, ldx, Q, ldq, scale);
-    return cudaGetLastError();
+    if (!vec) {
+        i8_quantize_kernel<XT, false, 1><<<grid, kQThreads, 0, s>>>(K, X, ldx, Q, ldq, scale);
+        return cudaGetLastError();
+    }
+    // few pieces per thread while 256 threads hold the row, so that many rows are in flight per SM
+    const long long pieces = K / Vec16<XT>::kPerVec;
+    const int keep = pieces <= kQThreads ? 1 : pieces <= 2 * kQThreads ? 2 : pieces <= 4 * kQThreads ? 4 : 8;
+    const long long want = (pieces + keep - 1) / keep;
+    const int threads = want >= kQThreads ? kQThreads : static_cast<int>((want + 31) / 32 * 32 > 0 ? (want + 31) / 32 * 32 : 32);
+    if (keep == 1) return quantize_keep<XT, 1>(grid, threads, K, X, ldx, Q, ldq, scale, s);
+    if (keep == 2) return quantize_keep<XT, 2>(grid, threads, K, X, ldx, Q, ldq, scale, s);
+    if (keep == 4) return quantize_keep<XT, 4>(grid, threads, K, X, ldx, Q, ldq, scale, s);
+    return quantize_keep<XT, 8>(grid, threads, K, X, ldx, Q, ldq, scale, s);
 }
 
 }  // namespace

@@ -258,20 +258,25 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
         regs_decrease<Cfg::CONV_REGS>();
         const int quad = warp & 3, set = (warp - Cfg::CONV_WARP0) >> 2, hk = set & 1;
         constexpr int step = Cfg::SETS / 2;  // stages from one turn to the next
-        const int wr = quad * 32 + lane;  // this thread's row of W
-        int kb = set >> 1;                // stage of the tile, numbered on through all tiles
+        // 16-byte unit u of a row sits at u ^ (row % 8).  This thread reads units
+        // 4 hk .. 4 hk + 3 of row 32 quad + lane of W; of rows lane, lane + 32, ... of
+        // X it reads unit 4 hk + quad and writes units 2 quad and 2 quad + 1.
+        const uint32_t sw = lane & 7;
+        const uint32_t w_at = smem_u32(smem) + (quad * 32 + lane) * 128 + ((4 * hk ^ sw) << 4);
+        const uint32_t x_at = smem_u32(smem) + Cfg::W_BYTES + lane * 128 + (((4 * hk + quad) ^ sw) << 4);
+        const uint32_t xs_at = smem_u32(slot_base) + lane * 128 + ((2 * quad ^ sw) << 4);
+        const uint32_t w_tmem0 = w_slot0 + (static_cast<uint32_t>(quad * 32) << 16);
+        int kb = set >> 1;  // stage of the tile, numbered on through all tiles
         uint32_t stage = kb, phase = 0, slot = 2 * kb + hk, slot_phase = 0;
         bool ok = true;
         for (long long tile = cluster; ok && tile < tiles; tile += nclusters, kb -= num_kb) {
             const int bnh = row_tile(table, tile, args.tiles_f, args.K).bn >> 1;
             for (; kb < num_kb; kb += step) {
                 bool got = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
-                const unsigned char *sW = smem + stage * sh.stage_bytes, *sX = sW + Cfg::W_BYTES;
+                const uint32_t st = stage * sh.stage_bytes;
                 uint4 c[4];
-                // this row's 64 codes: 16-byte unit u of a row sits at u ^ (row % 8)
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    c[i] = *reinterpret_cast<const uint4 *>(sW + wr * 128 + (((hk * 4 + i) ^ (wr & 7)) << 4));
+                for (int i = 0; i < 4; ++i) c[i] = lds128((w_at + st) ^ (i << 4));
                 got = got &&
                       pair_wait<CL>(&freed[slot], slot_phase ^ 1u, abort_flag, args.status, abort_local, rank);
                 if (!__all_sync(0xffffffffu, got)) {
@@ -279,9 +284,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                // to 32 columns of tensor memory
-                const uint32_t w_tmem =
-                    w_slot0 + (static_cast<uint32_t>(quad * 32) << 16) + slot * Cfg::W_SLOT_COLS;
+                // this row's 64 codes to 32 columns of tensor memory
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
                     uint32_t out[16];
@@ -292,28 +295,25 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                         expand4(c[2 * p + i].z, out[8 * i + 4], out[8 * i + 5]);
                         expand4(c[2 * p + i].w, out[8 * i + 6], out[8 * i + 7]);
                     }
-                    tmem_st_x16(w_tmem + p * 16, out);
+                    tmem_st_x16(w_tmem0 + slot * Cfg::W_SLOT_COLS + p * 16, out);
                 }
-                // 16 codes of each row of X: unit hk * 4 + quad in, units 2 quad and 2 quad + 1 out
-                unsigned char *xs = slot_base + slot * sh.slot_bytes;
+                // 16 codes of each row of X; rows of a started 32 past the tile's hold what
+                // the stage held before, and no MMA reads what becomes of them
+                const uint32_t xs = xs_at + slot * sh.slot_bytes;
                 constexpr int XR = kI8TileRows / 64;  // most rows per thread
-                const int sw = lane & 7;
 #pragma unroll
                 for (int i = 0; i < XR; ++i)
-                    if (lane + 32 * i < bnh)
-                        c[i] = *reinterpret_cast<const uint4 *>(sX + (lane + 32 * i) * 128 +
-                                                                (((hk * 4 + quad) ^ sw) << 4));
+                    if (32 * i < bnh) c[i] = lds128(x_at + st + i * 32 * 128);
 #pragma unroll
                 for (int i = 0; i < XR; ++i) {
-                    const int r = lane + 32 * i;
-                    if (r < bnh) {
+                    if (32 * i < bnh) {
                         uint4 a, b;
                         expand4(c[i].x, a.x, a.y);
                         expand4(c[i].y, a.z, a.w);
                         expand4(c[i].z, b.x, b.y);
                         expand4(c[i].w, b.z, b.w);
-                        *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad) ^ sw) << 4)) = a;
-                        *reinterpret_cast<uint4 *>(xs + r * 128 + (((2 * quad + 1) ^ sw) << 4)) = b;
+                        sts128(xs + i * 32 * 128, a);
+                        sts128((xs ^ 16) + i * 32 * 128, b);
                     }
                 }
                 tmem_st_wait();
@@ -424,7 +424,7 @@ cudaError_t launch_i8_tc_out(const CUtensorMap &tw, const CUtensorMap &tx32, con
     if ((err = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return err;
     if (fa.numRegs != I8Config::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
     GtcArgs args = a;
-    if (args.most < 32 || args.most > kI8TileRows || args.most % 32 != 0) return cudaErrorInvalidValue;
+    if (args.most < 64 || args.most > kI8TileRows || args.most % 64 != 0) return cudaErrorInvalidValue;
     args.stages = I8Config::MAX_STAGES;
     while (args.stages > 4 && I8Config::fixed_bytes(args.G) + I8Shape(args.most, args.stages).bytes() > I8Config::SMEM_MAX)
         --args.stages;

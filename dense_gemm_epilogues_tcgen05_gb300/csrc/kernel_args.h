@@ -172,7 +172,7 @@ struct GtcArgs {
     int pairs;                      // 16-bit C: base and pitch allow 32-bit stores of two columns
     uint32_t a_mn;                  // forward: the weights are contiguous along F
     const float *col_scale;         // integer product: G x F, NULL: 1
-    int most;                       // integer product: widest row tile (a multiple of 32)
+    int most;                       // integer product: widest row tile (a multiple of 64)
     int stages;                     // integer product: set by its launcher
     unsigned int *status;
 };

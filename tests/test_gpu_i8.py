@@ -174,6 +174,30 @@ def test_quantize_ties_extremes_and_not_finite(cuda_lib):
     assert s[5] == 0 and not q[5].any()
 
 
+@pytest.mark.parametrize("dt", [F16, BF16], ids=NAMES.get)
+def test_quantize_near_ties(cuda_lib, dt):
+    """Every mantissa of the type against many maxima: quotients on and next to ties, both signs."""
+    g = cuda_lib
+    bits = 11 if dt == F16 else 8
+    mant = torch.arange(1 << (bits - 1), 1 << bits, dtype=torch.float64)
+    x = torch.cat([mant, -mant / 2, mant / 4, -mant / 64]) / (1 << bits)  # all below 1
+    rows = 64
+    peaks = 1 + torch.arange(rows, dtype=torch.float64) / rows * (1 - 2.0 ** -7)
+    t = torch.cat([x.expand(rows, -1), peaks[:, None]], 1).to(DT[dt])
+    M, K = t.shape
+    q = torch.empty(M, K, dtype=torch.int8, device="cuda")
+    s = torch.empty(M, device="cuda")
+    g.gemm_i8_quantize(M, K, dt, t.cuda(), K, q, K, s)
+    padded_x = torch.zeros(M, K + 7, dtype=DT[dt])
+    padded_x[:, :K] = t
+    ld = (K + 7) // 8 * 8
+    q2 = torch.empty(M, ld, dtype=torch.int8, device="cuda")
+    g.gemm_i8_quantize(M, K, dt, padded_x[:, :ld].contiguous().cuda(), ld, q2, ld, s)  # the vector path
+    want, _ = og.quantize_reference(t.double().numpy())
+    np.testing.assert_array_equal(q.cpu().numpy(), want)
+    np.testing.assert_array_equal(q2[:, :K].cpu().numpy(), want)
+
+
 def test_quantize_then_multiply(cuda_lib):
     """The two together: x W^T of quantised x and W within half a step of each."""
     g = cuda_lib
