@@ -190,9 +190,20 @@ def _ptr(x):
     raise TypeError(f"expected a torch.Tensor, an int address or None, got {type(x).__name__}")
 
 
+def _current_stream() -> int:
+    """Handle of PyTorch's current stream on the current device."""
+    return torch.cuda.current_stream().cuda_stream
+
+
+if hasattr(torch._C, "_cuda_getCurrentRawStream") and hasattr(torch._C, "_cuda_getDevice"):
+    def _current_stream() -> int:  # noqa: F811 (the same handle without building a Stream object: 0.2 us, not 2.9)
+        torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+
+
 def _stream(s):
     if s is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -47,6 +47,8 @@ struct GtcConfig {
     static constexpr int TMEM_COLS = 512, ACC_STRIDE = 256;
     static constexpr int BAR_OFF = STAGES * STAGE_BYTES, BAR_BYTES = 256;
     static constexpr int TABLE_OFF = BAR_OFF + BAR_BYTES;
+    // fp32 outputs: k-blocks summed in the tensor core's accumulator before the sum moves to registers
+    static constexpr int SEG = 8;
     static_assert((4 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
     static int smem_bytes(int G) { return 1024 + TABLE_OFF + (group_table_bytes(G) + 15) / 16 * 16; }
 };
@@ -92,6 +94,8 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                       const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ GtcArgs args) {
     using Cfg = GtcConfig;
     constexpr int BK = Cfg::BK, STAGES = Cfg::STAGES, CL = 2;
+    constexpr bool SEGS = OUT == kDtF32;
+    constexpr int SEG = SEGS ? Cfg::SEG : 1 << 30;  // k-blocks per accumulator
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -222,14 +226,20 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
             while (ok && it.next(t)) {
                 const int num_kb = (t.nk + BK - 1) / BK;
                 if (num_kb == 0) continue;  // a group without rows: the epilogue alone
-                const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
-                ++local;
-                if (!pair_wait<CL>(&tempty[acc], acc_phase ^ 1u, abort_flag, args.status, abort_local, rank)) break;
-                tc_fence_after();
-                const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
                 const uint32_t idesc = mma_idesc(TcTraits<AB>::kFmt, TcTraits<AB>::kFmt, 256, t.bn) | (a_mn << 15) |
                                        (b_mn << 16);
+                uint32_t acc = 0;
                 for (int kb = 0; kb < num_kb; ++kb) {
+                    const bool opens = SEGS ? kb % SEG == 0 : kb == 0;
+                    if (opens) {
+                        acc = local & 1;
+                        const uint32_t acc_phase = (local >> 1) & 1;
+                        ++local;
+                        ok = pair_wait<CL>(&tempty[acc], acc_phase ^ 1u, abort_flag, args.status, abort_local, rank);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
+                    const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
                     ok = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
                     if (WG && ok && (kb + 1) * BK > t.nk) {
                         ok = pair_wait<CL>(&fixed[stage], (fixed_parity >> stage) & 1u, abort_flag, args.status,
@@ -245,15 +255,15 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                     for (int ks = 0; ks < BK / 16; ++ks)
                         tc_mma_pair<kKindF16>(d_tmem, sw128_desc(a_addr + ks * a_kstep, a_lbo, 1024u),
                                               sw128_desc(b_addr + ks * b_kstep, b_lbo, 1024u), idesc,
-                                              (kb | ks) != 0 ? 1u : 0u);
+                                              !opens || ks != 0 ? 1u : 0u);
                     issued = true;
                     tc_commit_pair(&empty[stage], 0x3);
                     if (++stage == STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
+                    if (kb + 1 == num_kb || (SEGS && (kb + 1) % SEG == 0)) tc_commit_pair(&tfull[acc], 0x3);
                 }
-                if (ok) tc_commit_pair(&tfull[acc], 0x3);
             }
             if (*abort_flag && issued) {
                 tc_commit_pair(mma_done, 1u);
@@ -297,49 +307,94 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi, args.pairs};
         int local = 0;
         while (it.next(t)) {
-            const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
-            const bool have = t.nk > 0;
+            const int num_kb = (t.nk + BK - 1) / BK;
             const int f = t.f0 + static_cast<int>(rank) * 128 + quad * 32 + lane;
             const float bias = (args.epi != kEpiNone && f < args.F)
                                    ? args.bias[static_cast<long long>(t.g) * args.F + f] : 0.0f;
             OutT *c = static_cast<OutT *>(args.C) + (WG ? t.g * args.scg : 0ll) + t.r0 * args.ldc + f;
             const float *rs = args.row_scale != nullptr ? args.row_scale + t.r0 : nullptr;
-            if (have) {
-                ++local;
-                const bool got = pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank);
-                if (!__all_sync(0xffffffffu, got)) break;
-                tc_fence_after();
-            }
-            const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * Cfg::ACC_STRIDE;
             const int chunks = t.bn >> 5;
-            const int c_begin = half ? (chunks + 1) >> 1 : 0, c_end = half ? chunks : (chunks + 1) >> 1;
-#pragma unroll 1
-            for (int ch = c_begin; ch < c_end; ++ch) {
-                float v[32];
-                if (have) {
-                    uint32_t raw[32];
-                    __syncwarp();
-                    tmem_ld_issue(t_row + ch * 32, raw);
-                    tmem_ld_wait(raw);
+            const int c_begin = half ? (chunks + 1) >> 1 : 0, nch = (half ? chunks : (chunks + 1) >> 1) - c_begin;
+            const uint32_t t_quad = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c_begin * 32;
+            auto store = [&](float (&v)[32], int ch) {
+                const int row = (c_begin + ch) * 32;
+                store_chunk_t<OUT>(v, c + row * args.ldc, args.F - f, t.nr - row, rs != nullptr ? rs + row : nullptr,
+                                   1.0f, bias, e);
+            };
+            if constexpr (SEGS) {
+                // The tensor core's fp32 sums lose about half a unit in the last place per
+                // instruction, always towards zero; over a few hundred of them that is an
+                // error several times an fp32 sum's own (2048 rows: 1.4e-6 of the result).
+                // So every 512 k the accumulator is added into registers, rounded to nearest.
+                float sum[4][32];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
-                } else {
+                for (int ch = 0; ch < 4; ++ch)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
-                }
-                if (have && ch + 1 == c_end) {
-                    // the accumulator is in registers: free it before the stores
+                    for (int j = 0; j < 32; ++j) sum[ch][j] = 0.0f;
+                bool ok = true;
+                for (int kb = 0; kb < num_kb; kb += SEG) {
+                    const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
+                    ++local;
+                    const bool got = pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank);
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        if (ch < nch) {
+#pragma unroll
+                            for (int p = 0; p < 2; ++p) {
+                                uint32_t raw[16];
+                                __syncwarp();
+                                tmem_ld_x16(t_quad + acc * Cfg::ACC_STRIDE + ch * 32 + p * 16, raw);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) sum[ch][16 * p + j] += __uint_as_float(raw[j]);
+                            }
+                        }
+                    }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
                 }
-                store_chunk_t<OUT>(v, c + ch * 32 * args.ldc, args.F - f, t.nr - ch * 32,
-                                   rs != nullptr ? rs + ch * 32 : nullptr, 1.0f, bias, e);
-            }
-            if (have && c_begin == c_end) {  // a 32-column tile has no second half
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
+                if (!ok) break;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+                    if (ch < nch) store(sum[ch], ch);
+            } else {
+                const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
+                if (num_kb > 0) {
+                    ++local;
+                    const bool got = pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank);
+                    if (!__all_sync(0xffffffffu, got)) break;
+                    tc_fence_after();
+                }
+#pragma unroll 1
+                for (int ch = 0; ch < nch; ++ch) {
+                    float v[32];
+                    if (num_kb > 0) {
+                        uint32_t raw[32];
+                        __syncwarp();
+                        tmem_ld_issue(t_quad + acc * Cfg::ACC_STRIDE + ch * 32, raw);
+                        tmem_ld_wait(raw);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+                    }
+                    if (num_kb > 0 && ch + 1 == nch) {
+                        // the accumulator is in registers: free it before the stores
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
+                    }
+                    store(v, ch);
+                }
+                if (num_kb > 0 && nch == 0) {  // a 32-column tile has no second half
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
+                }
             }
         }
     }
