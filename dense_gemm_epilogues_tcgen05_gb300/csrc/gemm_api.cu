@@ -1362,6 +1362,28 @@ static int pair_stores(const void *C, int64_t ldc, int64_t group_stride) {
     return (reinterpret_cast<uintptr_t>(C) & 3u) == 0 && ldc % 2 == 0 && group_stride % 2 == 0;
 }
 
+// Map of C for the grouped kernels' stores, (columns, rows, groups); false (and the kernels store from registers)
+// where its base or pitches rule out TMA, or its rows do not end on 16 bytes (a TMA store clips there, and would
+// write into the padding).
+static bool encode_grouped_c(CUtensorMap *map, int cd, void *C, int64_t cols, int64_t rows, int64_t ldc,
+                             int64_t groups, int64_t group_stride) {
+    const int es = elem_bytes(cd);
+    const int64_t limit = int64_t(1) << 40;
+    if ((reinterpret_cast<uintptr_t>(C) & 15u) != 0 || cols * es % 16 != 0) return false;
+    if (rows > 1 && (ldc * es % 16 != 0 || ldc * es >= limit)) return false;
+    if (groups > 1 && (group_stride * es % 16 != 0 || group_stride * es >= limit)) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(groups)};
+    cuuint64_t strides[2] = {rows == 1 ? 16 : static_cast<cuuint64_t>(ldc) * es,
+                             groups == 1 ? 16 : static_cast<cuuint64_t>(group_stride) * es};
+    cuuint32_t box[3] = {32u, cd == GEMM_F32 ? 16u : 32u, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return driver_fns().encode(map, cd == GEMM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : tma_dtype(cd), 3, C, dims, strides,
+                               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                               cd == GEMM_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Record of a pair launch over at most `tiles` tiles; returns its clusters.
 static int pair_clusters(const DeviceState *dev, int64_t tiles, gemm_launch_info_t *info) {
     const int clusters = static_cast<int>(std::min<int64_t>(tiles, dev->num_sms / 2));
@@ -1414,7 +1436,7 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
         const bool n_major = !k_major && tma_ok(args.B, args.K, args.sbn, args.sbk, 2);
         if (tma_ok(args.A, args.M, args.sak, args.sam, 2) && (k_major || n_major) &&
             group_stride_ok(args.G, args.sbg, 2)) {
-            CUtensorMap ta, tb, tb16;
+            CUtensorMap ta, tb, tb16, tc;
             gemm_status_t st;
             st = k_major ? encode_3d(&ta, ab, args.B, args.K, args.N, args.sbn, args.G, args.sbg, 128)
                          : encode_3d(&ta, ab, args.B, args.N, args.K, args.sbk, args.G, args.sbg, 64);
@@ -1429,12 +1451,14 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
             t.bias = args.bias; t.row_scale = args.row_scale;
             t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
             t.pairs = pair_stores(args.C, args.ldc, 0);
+            t.c_tma = encode_grouped_c(&tc, cd, args.C, args.N, args.M, args.ldc, 1, 0);
+            if (!t.c_tma) tc = ta;  // not used
             t.a_mn = n_major ? 1u : 0u;
             t.status = args.status;
             // at most: every 256 rows a tile, and one more ragged tile per group that can have rows
             const int64_t row_tiles = args.M / 256 + std::min(args.G, args.M);
             const int clusters = pair_clusters(dev, row_tiles * t.tiles_f, &info);
-            return record(launch_grouped_tc(false, ab, cd, ta, tb, tb16, t, clusters, s) == cudaSuccess
+            return record(launch_grouped_tc(false, ab, cd, ta, tb, tb16, tc, t, clusters, s) == cudaSuccess
                               ? GEMM_OK : GEMM_ERR_CUDA, info);
         }
     }
@@ -1584,7 +1608,7 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
     if (a_sum != nullptr && launch_grouped_colsum(ab_dtype, a, s) != cudaSuccess) return GEMM_ERR_CUDA;
     gemm_launch_info_t info = {};
     if (product && es == 2 && tma_ok(A, T, a_stride_m, a_stride_r, 2) && tma_ok(D, T, d_stride_n, d_stride_r, 2)) {
-        CUtensorMap ta, tb;
+        CUtensorMap ta, tb, tc;
         if ((st = encode_3d(&ta, ab_dtype, D, N, T, d_stride_r, 1, 0, 64)) != GEMM_OK) return st;
         if ((st = encode_3d(&tb, ab_dtype, A, M, T, a_stride_r, 1, 0, 64)) != GEMM_OK) return st;
         GtcArgs t = {};
@@ -1595,9 +1619,11 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
         t.C = C; t.scg = c_stride_g; t.ldc = ldc;
         t.alpha = alpha; t.beta = beta; t.epi = kEpiNone;
         t.pairs = pair_stores(C, ldc, G > 1 ? c_stride_g : 0);
+        t.c_tma = encode_grouped_c(&tc, c_dtype, C, N, M, ldc, G, c_stride_g);
+        if (!t.c_tma) tc = ta;  // not used
         t.status = dev->status;
         const int clusters = pair_clusters(dev, G * t.tiles_f * t.tiles_r, &info);
-        return record(launch_grouped_tc(true, ab_dtype, c_dtype, ta, tb, tb, t, clusters, s) == cudaSuccess
+        return record(launch_grouped_tc(true, ab_dtype, c_dtype, ta, tb, tb, tc, t, clusters, s) == cudaSuccess
                           ? GEMM_OK : GEMM_ERR_CUDA, info);
     }
     info.path = product ? GEMM_PATH_SIMT : GEMM_PATH_EPILOGUE_ONLY;

@@ -18,7 +18,8 @@
 //
 //   warp 0       TMA producer: its own 128 rows of the MMA's first operand and
 //                its own half of the columns' operand, 64 deep, into a ring of
-//                six 32 KB stages, counted on the leader's barrier;
+//                six (five beside a large group table) 32 KB stages, counted on the
+//                leader's barrier;
 //   warp 1       MMA issuer (leader CTA only), two 256-column accumulators;
 //   warp 2       gradient only: the last k-block of a group reaches into the
 //                next group's rows (or past T).  They are zeroed in shared
@@ -40,20 +41,20 @@ namespace gb300 {
 namespace {
 
 struct GtcConfig {
-    static constexpr int BK = 64, STAGES = 6;
+    static constexpr int BK = 64, MAX_STAGES = 6;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI_WARP0 = 3, EPI_WARPS = 8;
     static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
     static constexpr int TMEM_COLS = 512, ACC_STRIDE = 256;
-    static constexpr int BAR_OFF = STAGES * STAGE_BYTES, BAR_BYTES = 256;
-    static constexpr int TABLE_OFF = BAR_OFF + BAR_BYTES;
+    static constexpr int BAR_BYTES = 256, BOX_BYTES = EPI_WARPS * 2 * kBoxBytes, SMEM_MAX = 232448;
     // fp32 outputs: k-blocks summed in the tensor core's accumulator before the sum moves to registers
     static constexpr int SEG = 8;
-    static_assert((4 * STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
-    static int smem_bytes(int G) { return 1024 + TABLE_OFF + (group_table_bytes(G) + 15) / 16 * 16; }
+    static_assert((4 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
+    // after up to 1023 bytes of alignment: [stages][boxes][barriers][group table]
+    static int fixed_bytes(int G) { return 1024 + BOX_BYTES + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16; }
 };
-static_assert(1024 + GtcConfig::TABLE_OFF + group_table_bytes(kMaxGroups) <= 232448, "fits the shared memory");
-static_assert(1024 + GtcConfig::TABLE_OFF > 232448 / 2, "one CTA per SM: a pair allocates all 512 TMEM columns");
+static_assert(1024 + GtcConfig::BOX_BYTES + GtcConfig::BAR_BYTES + group_table_bytes(kMaxGroups) +
+                      5 * GtcConfig::STAGE_BYTES <= GtcConfig::SMEM_MAX, "five stages always fit");
 
 // Walks this cluster's tiles.
 template <bool WG>
@@ -91,19 +92,22 @@ struct GtcIter {
 template <bool WG, int AB, int OUT>
 __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
     grouped_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ GtcArgs args) {
+                      const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmC,
+                      const __grid_constant__ GtcArgs args) {
     using Cfg = GtcConfig;
-    constexpr int BK = Cfg::BK, STAGES = Cfg::STAGES, CL = 2;
+    constexpr int BK = Cfg::BK, CL = 2;
+    const uint32_t stages = args.stages;
     constexpr bool SEGS = OUT == kDtF32;
     constexpr int SEG = SEGS ? Cfg::SEG : 1 << 30;  // k-blocks per accumulator
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + Cfg::BAR_OFF);
-    uint64_t *empty = full + STAGES;
-    uint64_t *landed = empty + STAGES;   // gradient, last k-blocks: this CTA's bytes have landed
-    uint64_t *fixed = landed + STAGES;   // (leader's) both CTAs have cleared the foreign rows
-    uint64_t *tfull = fixed + STAGES;
+    unsigned char *boxes = smem + stages * Cfg::STAGE_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(boxes + Cfg::BOX_BYTES);
+    uint64_t *empty = full + Cfg::MAX_STAGES;
+    uint64_t *landed = empty + Cfg::MAX_STAGES;   // gradient, last k-blocks: this CTA's bytes have landed
+    uint64_t *fixed = landed + Cfg::MAX_STAGES;   // (leader's) both CTAs have cleared the foreign rows
+    uint64_t *tfull = fixed + Cfg::MAX_STAGES;
     uint64_t *tempty = tfull + 2;
     uint64_t *mma_done = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
     const int cluster = blockIdx.x / CL, nclusters = gridDim.x / CL;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < STAGES; ++s) {
+        for (int s = 0; s < Cfg::MAX_STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 1);
             mbar_init(&landed[s], 1);
@@ -130,6 +134,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         tma_prefetch_desc(&tmA);
         tma_prefetch_desc(&tmB);
         if (!WG) tma_prefetch_desc(&tmB16);
+        if (args.c_tma) tma_prefetch_desc(&tmC);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
@@ -141,8 +146,9 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
     tc_fence_after();
     grid_dep_wait();
     grid_dep_launch();
-    const GroupTable table = group_table_build(reinterpret_cast<int *>(smem + Cfg::TABLE_OFF), args.offsets, args.G,
-                                               args.T, threadIdx.x, Cfg::THREADS, RowTilesOf{256});
+    const GroupTable table = group_table_build(
+        reinterpret_cast<int *>(reinterpret_cast<unsigned char *>(full) + Cfg::BAR_BYTES), args.offsets, args.G, args.T,
+        threadIdx.x, Cfg::THREADS, RowTilesOf{256});
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), 0);
     const uint32_t fixed0_leader = mapa_shared(smem_u32(&fixed[0]), 0);
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                                 tma_load_3d_pair(sB + r * 128, &tmB16, fbar, k, c0 + r, 0, keep);
                         }
                     }
-                    if (++stage == STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -258,7 +264,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                                               !opens || ks != 0 ? 1u : 0u);
                     issued = true;
                     tc_commit_pair(&empty[stage], 0x3);
-                    if (++stage == STAGES) {
+                    if (++stage == stages) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -279,7 +285,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                 const int num_kb = (t.nk + BK - 1) / BK;
                 const int valid = t.nk - (num_kb - 1) * BK;  // rows of the last k-block
                 if (num_kb > 0 && valid < BK) {
-                    const uint32_t s = (stage + num_kb - 1) % STAGES;
+                    const uint32_t s = (stage + num_kb - 1) % stages;
                     const bool got =
                         pair_wait<CL>(&landed[s], (parity >> s) & 1u, abort_flag, args.status, abort_local, rank);
                     if (!__all_sync(0xffffffffu, got)) break;
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote_relaxed(fixed0_leader + 8u * s);
                 }
-                stage = (stage + num_kb) % STAGES;
+                stage = (stage + num_kb) % stages;
             }
         }
     } else {
@@ -305,6 +311,8 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         const int quad = warp & 3;                      // TMEM lanes 32*quad ..
         const int half = (warp - Cfg::EPI_WARP0) >> 2;  // which half of the tile's columns
         const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi, args.pairs};
+        unsigned char *box = boxes + (warp - Cfg::EPI_WARP0) * 2 * kBoxBytes;
+        uint32_t turn = 0;
         int local = 0;
         while (it.next(t)) {
             const int num_kb = (t.nk + BK - 1) / BK;
@@ -318,8 +326,14 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
             const uint32_t t_quad = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c_begin * 32;
             auto store = [&](float (&v)[32], int ch) {
                 const int row = (c_begin + ch) * 32;
-                store_chunk_t<OUT>(v, c + row * args.ldc, args.F - f, t.nr - row, rs != nullptr ? rs + row : nullptr,
-                                   1.0f, bias, e);
+                OutT *c0 = c + row * args.ldc;
+                chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row, rs != nullptr ? rs + row : nullptr, 1.0f, bias, e);
+                if (args.c_tma && row + 32 <= t.nr) {
+                    if (f - lane < args.F)
+                        box_chunk_t<OUT>(v, &tmC, box, turn, f - lane, t.r0 + row, WG ? t.g : 0);
+                } else {
+                    store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, e);
+                }
             };
             if constexpr (SEGS) {
                 // The tensor core's fp32 sums lose about half a unit in the last place per
@@ -399,6 +413,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         }
     }
 
+    if (warp >= Cfg::EPI_WARP0 && lane == 0) bulk_wait<0>();  // stores in flight read this CTA's shared memory
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();  // no CTA leaves while its peer may still signal into it
@@ -409,12 +424,14 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
 }
 
 template <bool WG, int AB, int OUT>
-cudaError_t launch_gtc(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb16, const GtcArgs &args,
-                       int clusters, cudaStream_t stream) {
+cudaError_t launch_gtc(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb16, const CUtensorMap &tc,
+                       const GtcArgs &a, int clusters, cudaStream_t stream) {
     auto kern = grouped_tc_kernel<WG, AB, OUT>;
-    const int smem = GtcConfig::smem_bytes(args.G);
-    cudaError_t err =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GtcConfig::smem_bytes(kMaxGroups));
+    GtcArgs args = a;
+    args.stages = GtcConfig::MAX_STAGES;
+    if (GtcConfig::fixed_bytes(args.G) + args.stages * GtcConfig::STAGE_BYTES > GtcConfig::SMEM_MAX) --args.stages;
+    const int smem = GtcConfig::fixed_bytes(args.G) + args.stages * GtcConfig::STAGE_BYTES;
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, GtcConfig::SMEM_MAX);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * clusters, 1, 1);
@@ -430,28 +447,28 @@ cudaError_t launch_gtc(const CUtensorMap &ta, const CUtensorMap &tb, const CUten
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tb16, args);
+    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tb16, tc, args);
 }
 
 template <bool WG, int AB>
 cudaError_t launch_gtc_out(int out, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb16,
-                           const GtcArgs &args, int clusters, cudaStream_t stream) {
-    if (out == kDtF32) return launch_gtc<WG, AB, kDtF32>(ta, tb, tb16, args, clusters, stream);
-    if (out == kDtF16) return launch_gtc<WG, AB, kDtF16>(ta, tb, tb16, args, clusters, stream);
-    if (out == kDtBF16) return launch_gtc<WG, AB, kDtBF16>(ta, tb, tb16, args, clusters, stream);
+                           const CUtensorMap &tc, const GtcArgs &args, int clusters, cudaStream_t stream) {
+    if (out == kDtF32) return launch_gtc<WG, AB, kDtF32>(ta, tb, tb16, tc, args, clusters, stream);
+    if (out == kDtF16) return launch_gtc<WG, AB, kDtF16>(ta, tb, tb16, tc, args, clusters, stream);
+    if (out == kDtBF16) return launch_gtc<WG, AB, kDtBF16>(ta, tb, tb16, tc, args, clusters, stream);
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const CUtensorMap &ta, const CUtensorMap &tb,
-                              const CUtensorMap &tb16, const GtcArgs &args, int clusters, cudaStream_t stream) {
+                              const CUtensorMap &tb16, const CUtensorMap &tc, const GtcArgs &args, int clusters, cudaStream_t stream) {
     if (ab == kDtF16)
-        return wgrad ? launch_gtc_out<true, kDtF16>(out, ta, tb, tb16, args, clusters, stream)
-                     : launch_gtc_out<false, kDtF16>(out, ta, tb, tb16, args, clusters, stream);
+        return wgrad ? launch_gtc_out<true, kDtF16>(out, ta, tb, tb16, tc, args, clusters, stream)
+                     : launch_gtc_out<false, kDtF16>(out, ta, tb, tb16, tc, args, clusters, stream);
     if (ab == kDtBF16)
-        return wgrad ? launch_gtc_out<true, kDtBF16>(out, ta, tb, tb16, args, clusters, stream)
-                     : launch_gtc_out<false, kDtBF16>(out, ta, tb, tb16, args, clusters, stream);
+        return wgrad ? launch_gtc_out<true, kDtBF16>(out, ta, tb, tb16, tc, args, clusters, stream)
+                     : launch_gtc_out<false, kDtBF16>(out, ta, tb, tb16, tc, args, clusters, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -396,8 +396,10 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __int2float_rn(sum[c][j]);
-                    store_chunk_t<OUT>(v, out + row * args.ldc, args.F - f, t.nr - row,
-                                       args.row_scale != nullptr ? args.row_scale + t.r0 + row : nullptr, cs, bias, e);
+                    OutT *c0 = out + row * args.ldc;
+                    chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row,
+                                        args.row_scale != nullptr ? args.row_scale + t.r0 + row : nullptr, cs, bias, e);
+                    store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, e);
                 }
             }
         }

@@ -127,9 +127,12 @@ __device__ __forceinline__ float grouped_value(float acc, float scale, float bet
 // the weight gradient, its contiguous index) are the MMA's rows and lie in
 // tensor-memory lanes, the tokens are its columns -- so that a ragged group
 // costs columns in steps of 32, not rows in steps of 256.  A warp then holds
-// 32 consecutive columns of C in its lanes and 32 rows of C in its registers,
-// and one store instruction writes whole 64- or 128-byte runs of C's rows:
-// no staging through shared memory, and any row pitch.
+// 32 consecutive columns of C in its lanes and 32 rows of C in its registers.
+// Whole blocks of 32 rows go through shared memory as 2 KB boxes that TMA
+// stores; a group's last rows, which must not touch the next group's, and
+// outputs that TMA cannot write are stored from registers, 64 or 128 bytes of
+// a row per instruction.  (Storing everything from registers cost 98 of 679 us
+// for 32768 x 4096 x 4096, and 27 of 46 us for 24 gradients of 1000 x 1000.)
 struct StoreArgs {
     long long ldc;
     float alpha, beta;
@@ -138,14 +141,14 @@ struct StoreArgs {
 };
 
 // v: this lane's column at 32 consecutive rows, of which the first nrow are
-// stored (before any scale); c: element (row 0, this lane's column); the lane's
-// column is `left` columns before the end of C's rows (<= 0: outside).
-// row_scale: of row 0 on, or NULL; col_scale and bias: this lane's column's.
-// Warp-collective.
+// valid: sums on entry, outputs before the cast on return.  c: element (row 0,
+// this lane's column); the lane's column is `left` columns before the end of C's
+// rows (<= 0: outside).  row_scale: of row 0 on, or NULL; col_scale and bias:
+// this lane's column's.  Warp-collective.
 template <int OUT>
-__device__ __forceinline__ void store_chunk_t(float (&v)[32], typename Elem<OUT>::T *c, int left, int nrow,
-                                              const float *row_scale, float col_scale, float bias,
-                                              const StoreArgs &e) {
+__device__ __forceinline__ void chunk_values_t(float (&v)[32], const typename Elem<OUT>::T *c, int left, int nrow,
+                                               const float *row_scale, float col_scale, float bias,
+                                               const StoreArgs &e) {
     const int lane = threadIdx.x & 31;
     const bool f_ok = left > 0;
     const float a = e.alpha * col_scale;
@@ -167,6 +170,14 @@ __device__ __forceinline__ void store_chunk_t(float (&v)[32], typename Elem<OUT>
         for (int j = 0; j < 32; j += 2) f2_unpack(f2_add(f2_pack(v[j], v[j + 1]), b2), v[j], v[j + 1]);
         if (e.epi >= kEpiBiasGelu) activate_run<OUT, 32>(v, 0, e.epi, true);
     }
+}
+
+// The outputs v from registers.
+template <int OUT>
+__device__ __forceinline__ void store_chunk_t(const float (&v)[32], typename Elem<OUT>::T *c, int left, int nrow,
+                                              const StoreArgs &e) {
+    const int lane = threadIdx.x & 31;
+    const bool f_ok = left > 0;
     if constexpr (OUT != kDtF32) {
         if (e.pairs) {
             // Lanes 2p and 2p + 1 trade values so that each stores 32-bit words
@@ -193,6 +204,46 @@ __device__ __forceinline__ void store_chunk_t(float (&v)[32], typename Elem<OUT>
     for (int j = 0; j < 32; ++j) {
         if (f_ok && j < nrow) *c = Elem<OUT>::cvt(v[j]);
         c += e.ldc;
+    }
+}
+
+// All 32 rows of the outputs v through the warp's two 2 KB boxes: 16-bit outputs
+// as one box of 32 rows x 64 bytes, fp32 as two of 16 rows x 128 bytes (each
+// swizzled by its row's width).  Column x and row y of the first element, matrix
+// z; columns outside the tensor are not written.  The stores stay in flight; a
+// box is reused when its last store has read it.  Warp-collective.
+constexpr int kBoxBytes = 2048;
+
+template <int OUT>
+__device__ __forceinline__ void box_chunk_t(const float (&v)[32], const CUtensorMap *tm, unsigned char *boxes,
+                                            uint32_t &turn, int x, int y, int z) {
+    const int lane = threadIdx.x & 31;
+    constexpr int ROWS = OUT == kDtF32 ? 16 : 32;
+#pragma unroll
+    for (int h = 0; h < 32 / ROWS; ++h) {
+        unsigned char *box = boxes + (turn & 1) * kBoxBytes;
+        ++turn;
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+        if constexpr (OUT == kDtF32) {
+#pragma unroll
+            for (int r = 0; r < 16; ++r)  // 16-byte unit lane / 4 of row r at unit (lane / 4) ^ (r % 8)
+                *reinterpret_cast<float *>(box + r * 128 + ((lane * 4) ^ ((r & 7) << 4))) = v[16 * h + r];
+        } else {
+            const uint32_t odd = lane & 1u, col = (lane >> 1) * 4u;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
+                const uint32_t w = odd ? pack2_out<OUT>(got, v[2 * i + 1]) : pack2_out<OUT>(v[2 * i], got);
+                *reinterpret_cast<uint32_t *>(box + sw64_word((2 * i + odd) * 64u + col)) = w;
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_3d_hint(tm, box, x, y + h * ROWS, z, l2_policy_evict_first());
+            bulk_commit();
+        }
     }
 }
 

@@ -173,7 +173,8 @@ struct GtcArgs {
     uint32_t a_mn;                  // forward: the weights are contiguous along F
     const float *col_scale;         // integer product: G x F, NULL: 1
     int most;                       // integer product: widest row tile (a multiple of 64)
-    int stages;                     // integer product: set by its launcher
+    int stages;                     // set by the launcher
+    int c_tma;                      // C can be written by TMA (launch_grouped_tc's tc is valid)
     unsigned int *status;
 };
 
@@ -181,8 +182,10 @@ struct GtcArgs {
 //   grouped products on the tensor cores, `clusters` SM pairs.  Forward: ta = weights (K, F, G) in boxes
 //   of 64 x 128 (a_mn: (F, K, G) in 64 x 64), tb / tb16 = rows (K, T) in boxes of 64 x 64 and 64 x 16.
 //   Gradient: ta = (F, T), tb = (R, T), boxes of 64 x 64; tb16 unused.  All 3-D, 128-byte swizzle.
+//   tc = C (F, rows, G): 16-bit in boxes of 32 x 32 with 64-byte swizzle, fp32 in 32 x 16 with 128-byte swizzle.
 cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const CUtensorMap &ta, const CUtensorMap &tb,
-                              const CUtensorMap &tb16, const GtcArgs &args, int clusters, cudaStream_t stream);
+                              const CUtensorMap &tb16, const CUtensorMap &tc, const GtcArgs &args, int clusters,
+                              cudaStream_t stream);
 //   8-bit integer products on the tensor cores, `clusters` SM pairs.  tw = weight codes (K, F, G) in boxes of
 //   128 x 128 bytes, tx32 / tx16 = row codes (K, T) in boxes of 128 x 32 and 128 x 16; 128-byte swizzle.
 cudaError_t launch_i8_tc(int out, const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
