@@ -1335,18 +1335,23 @@ static gemm_status_t encode_3d(CUtensorMap *map, int ab, const void *base, int64
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
-// Rows of 8-bit codes as (128, rows, whole boxes of 128 along K, groups), boxes of 128 x box_rows x boxes x 1:
-// several 128-byte columns of a row block by one load, each laid out as encode_3d's.
-static gemm_status_t encode_i8_boxes(CUtensorMap *map, const void *base, int64_t K, int64_t rows, int64_t row_stride,
-                                     int64_t groups, int64_t group_stride, uint32_t box_rows, uint32_t boxes) {
-    cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(K / 128),
+// The contiguous index cut into whole blocks of 128 bytes: (block, rows, inner / block, groups), boxes of 128
+// bytes x box_rows x boxes x 1 -- several 128-byte columns of a row block by one load, each laid out as
+// encode_3d's.  A last part of a block is left out (zeros).
+static gemm_status_t encode_blocks(CUtensorMap *map, int ab, const void *base, int64_t inner, int64_t rows,
+                                   int64_t row_stride, int64_t groups, int64_t group_stride, uint32_t box_rows,
+                                   uint32_t boxes) {
+    const int es = ab == kDtI8 ? 1 : 2;
+    const cuuint64_t block = 128u / es;
+    cuuint64_t dims[4] = {block, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(inner) / block,
                           static_cast<cuuint64_t>(groups)};
-    cuuint64_t strides[3] = {rows == 1 ? 16 : static_cast<cuuint64_t>(row_stride), 128,
-                             groups == 1 ? 16 : static_cast<cuuint64_t>(group_stride)};
-    cuuint32_t box[4] = {128u, box_rows, boxes, 1u};
+    cuuint64_t strides[3] = {rows == 1 ? 16 : static_cast<cuuint64_t>(row_stride) * es, 128,
+                             groups == 1 ? 16 : static_cast<cuuint64_t>(group_stride) * es};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(block), box_rows, boxes, 1u};
     cuuint32_t estr[4] = {1, 1, 1, 1};
-    CUresult r = driver_fns().encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides,
-                                     box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    CUresult r = driver_fns().encode(map, ab == kDtI8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : tma_dtype(ab), 4,
+                                     const_cast<void *>(base), dims, strides, box, estr,
+                                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                      CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
 }
@@ -1436,13 +1441,16 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
         const bool n_major = !k_major && tma_ok(args.B, args.K, args.sbn, args.sbk, 2);
         if (tma_ok(args.A, args.M, args.sak, args.sam, 2) && (k_major || n_major) &&
             group_stride_ok(args.G, args.sbg, 2)) {
-            CUtensorMap ta, tb, tb16, tc;
+            GtcMaps m = {};
             gemm_status_t st;
-            st = k_major ? encode_3d(&ta, ab, args.B, args.K, args.N, args.sbn, args.G, args.sbg, 128)
-                         : encode_3d(&ta, ab, args.B, args.N, args.K, args.sbk, args.G, args.sbg, 64);
+            const bool whole = n_major && args.N % 64 == 0;
+            st = k_major ? encode_3d(&m.a, ab, args.B, args.K, args.N, args.sbn, args.G, args.sbg, 128)
+                 : whole ? encode_blocks(&m.a, ab, args.B, args.N, args.K, args.sbk, args.G, args.sbg, 64, 2)
+                         : encode_3d(&m.a, ab, args.B, args.N, args.K, args.sbk, args.G, args.sbg, 64);
             if (st != GEMM_OK) return st;
-            if ((st = encode_3d(&tb, ab, args.A, args.K, args.M, args.sam, 1, 0, 64)) != GEMM_OK) return st;
-            if ((st = encode_3d(&tb16, ab, args.A, args.K, args.M, args.sam, 1, 0, 16)) != GEMM_OK) return st;
+            for (uint32_t i = 0; i < 8; ++i)
+                if ((st = encode_3d(&m.b[i], ab, args.A, args.K, args.M, args.sam, 1, 0, 16 * (i + 1))) != GEMM_OK)
+                    return st;
             GtcArgs t = {};
             t.G = args.G; t.T = args.M; t.F = args.N; t.K = args.K;
             t.tiles_f = (args.N + 255) / 256;
@@ -1451,14 +1459,14 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
             t.bias = args.bias; t.row_scale = args.row_scale;
             t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
             t.pairs = pair_stores(args.C, args.ldc, 0);
-            t.c_tma = encode_grouped_c(&tc, cd, args.C, args.N, args.M, args.ldc, 1, 0);
-            if (!t.c_tma) tc = ta;  // not used
+            t.c_tma = encode_grouped_c(&m.c, cd, args.C, args.N, args.M, args.ldc, 1, 0);
+            t.a_whole = whole;
             t.a_mn = n_major ? 1u : 0u;
             t.status = args.status;
             // at most: every 256 rows a tile, and one more ragged tile per group that can have rows
             const int64_t row_tiles = args.M / 256 + std::min(args.G, args.M);
             const int clusters = pair_clusters(dev, row_tiles * t.tiles_f, &info);
-            return record(launch_grouped_tc(false, ab, cd, ta, tb, tb16, tc, t, clusters, s) == cudaSuccess
+            return record(launch_grouped_tc(false, ab, cd, m, t, clusters, s) == cudaSuccess
                               ? GEMM_OK : GEMM_ERR_CUDA, info);
         }
     }
@@ -1475,10 +1483,10 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
             m.x = m.x_tail;
             if (args.K >= 128) {
                 const uint32_t boxes = static_cast<uint32_t>(i8_gemv_boxes(nt));
-                if ((st = encode_i8_boxes(&m.w, args.B, args.K, args.N, args.sbn, args.G, args.sbg, wr, boxes)) !=
+                if ((st = encode_blocks(&m.w, kDtI8, args.B, args.K, args.N, args.sbn, args.G, args.sbg, wr, boxes)) !=
                     GEMM_OK)
                     return st;
-                if ((st = encode_i8_boxes(&m.x, args.A, args.K, args.M, args.sam, 1, 0, xr, boxes)) != GEMM_OK)
+                if ((st = encode_blocks(&m.x, kDtI8, args.A, args.K, args.M, args.sam, 1, 0, xr, boxes)) != GEMM_OK)
                     return st;
             }
             info.path = GEMM_PATH_SIMT;
@@ -1608,9 +1616,14 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
     if (a_sum != nullptr && launch_grouped_colsum(ab_dtype, a, s) != cudaSuccess) return GEMM_ERR_CUDA;
     gemm_launch_info_t info = {};
     if (product && es == 2 && tma_ok(A, T, a_stride_m, a_stride_r, 2) && tma_ok(D, T, d_stride_n, d_stride_r, 2)) {
-        CUtensorMap ta, tb, tc;
-        if ((st = encode_3d(&ta, ab_dtype, D, N, T, d_stride_r, 1, 0, 64)) != GEMM_OK) return st;
-        if ((st = encode_3d(&tb, ab_dtype, A, M, T, a_stride_r, 1, 0, 64)) != GEMM_OK) return st;
+        GtcMaps m = {};
+        const bool a_whole = N % 64 == 0, b_whole = M % 64 == 0;
+        st = a_whole ? encode_blocks(&m.a, ab_dtype, D, N, T, d_stride_r, 1, 0, 64, 2)
+                     : encode_3d(&m.a, ab_dtype, D, N, T, d_stride_r, 1, 0, 64);
+        if (st != GEMM_OK) return st;
+        for (uint32_t i = 0; i < 2 && b_whole; ++i)
+            if ((st = encode_blocks(&m.b[i], ab_dtype, A, M, T, a_stride_r, 1, 0, 64, i + 1)) != GEMM_OK) return st;
+        if ((st = encode_3d(&m.b[2], ab_dtype, A, M, T, a_stride_r, 1, 0, 64)) != GEMM_OK) return st;
         GtcArgs t = {};
         t.G = a.G; t.T = a.T; t.F = a.N; t.R = a.M;
         t.tiles_f = (a.N + 255) / 256;
@@ -1619,11 +1632,12 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
         t.C = C; t.scg = c_stride_g; t.ldc = ldc;
         t.alpha = alpha; t.beta = beta; t.epi = kEpiNone;
         t.pairs = pair_stores(C, ldc, G > 1 ? c_stride_g : 0);
-        t.c_tma = encode_grouped_c(&tc, c_dtype, C, N, M, ldc, G, c_stride_g);
-        if (!t.c_tma) tc = ta;  // not used
+        t.c_tma = encode_grouped_c(&m.c, c_dtype, C, N, M, ldc, G, c_stride_g);
+        t.a_whole = a_whole;
+        t.b_whole = b_whole;
         t.status = dev->status;
         const int clusters = pair_clusters(dev, G * t.tiles_f * t.tiles_r, &info);
-        return record(launch_grouped_tc(true, ab_dtype, c_dtype, ta, tb, tb, tc, t, clusters, s) == cudaSuccess
+        return record(launch_grouped_tc(true, ab_dtype, c_dtype, m, t, clusters, s) == cudaSuccess
                           ? GEMM_OK : GEMM_ERR_CUDA, info);
     }
     info.path = product ? GEMM_PATH_SIMT : GEMM_PATH_EPILOGUE_ONLY;

@@ -91,9 +91,7 @@ struct GtcIter {
 
 template <bool WG, int AB, int OUT>
 __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
-    grouped_tc_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                      const __grid_constant__ CUtensorMap tmB16, const __grid_constant__ CUtensorMap tmC,
-                      const __grid_constant__ GtcArgs args) {
+    grouped_tc_kernel(const __grid_constant__ GtcMaps maps, const __grid_constant__ GtcArgs args) {
     using Cfg = GtcConfig;
     constexpr int BK = Cfg::BK, CL = 2;
     const uint32_t stages = args.stages;
@@ -131,10 +129,9 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         mbar_init(mma_done, 1);
         *abort_flag = 0;
         fence_barrier_init();
-        tma_prefetch_desc(&tmA);
-        tma_prefetch_desc(&tmB);
-        if (!WG) tma_prefetch_desc(&tmB16);
-        if (args.c_tma) tma_prefetch_desc(&tmC);
+        tma_prefetch_desc(&maps.a);
+        tma_prefetch_desc(&maps.b[WG ? 2 : 7]);
+        if (args.c_tma) tma_prefetch_desc(&maps.c);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
@@ -168,6 +165,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                 const int bnh = t.bn >> 1;
                 const int c0 = t.r0 + static_cast<int>(rank) * bnh;  // first of this CTA's MMA columns
                 const int num_kb = (t.nk + BK - 1) / BK;
+                const bool b_whole = WG && args.b_whole && (c0 & 63) == 0;
                 const uint32_t bytes = Cfg::A_BYTES + (WG ? ((bnh + 63) >> 6) * 64u * 128u : bnh * 128u);
                 for (int kb = 0; kb < num_kb; ++kb) {
                     if (!pair_wait<CL>(&empty[stage], phase ^ 1u, abort_flag, args.status, abort_local, rank)) {
@@ -178,33 +176,41 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                     unsigned char *sA = smem + stage * Cfg::STAGE_BYTES;
                     unsigned char *sB = sA + Cfg::A_BYTES;
                     const int k = t.k0 + kb * BK;
+                    // One load per operand wherever a map allows: each takes the issuing
+                    // thread about 90 clocks, and a k-block's MMAs only 512.
                     if (WG && (kb + 1) * BK > t.nk) {
                         // reaches past the group: on this CTA's own barrier, for warp 2
                         if (rank == 0) mbar_arrive(&full[stage]);
                         mbar_arrive_expect_tx(&landed[stage], bytes);
-                        for (int j = 0; j < 2; ++j)
-                            tma_load_3d_hint(sA + j * 64 * 128, &tmA, &landed[stage], f + j * 64, k, 0, keep);
-                        for (int j = 0; j * 64 < bnh; ++j)
-                            tma_load_3d_hint(sB + j * 64 * 128, &tmB, &landed[stage], c0 + j * 64, k, 0, keep);
+                        if (args.a_whole)
+                            tma_load_4d_hint(sA, &maps.a, &landed[stage], 0, k, f >> 6, 0, keep);
+                        else
+                            for (int j = 0; j < 2; ++j)
+                                tma_load_3d_hint(sA + j * 64 * 128, &maps.a, &landed[stage], f + j * 64, k, 0, keep);
+                        if (b_whole)
+                            tma_load_4d_hint(sB, &maps.b[bnh > 64], &landed[stage], 0, k, c0 >> 6, 0, keep);
+                        else
+                            for (int j = 0; j * 64 < bnh; ++j)
+                                tma_load_3d_hint(sB + j * 64 * 128, &maps.b[2], &landed[stage], c0 + j * 64, k, 0,
+                                                 keep);
                     } else {
                         const uint32_t fbar = full0_leader + 8u * stage;
                         if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
-                        if (WG || args.a_mn) {
+                        if (!WG && !args.a_mn) {
+                            tma_load_3d_pair(sA, &maps.a, fbar, k, f, t.g, keep);
+                        } else if (args.a_whole) {
+                            tma_load_4d_pair(sA, &maps.a, fbar, 0, k, f >> 6, WG ? 0 : t.g, keep);
+                        } else {
                             for (int j = 0; j < 2; ++j)
-                                tma_load_3d_pair(sA + j * 64 * 128, &tmA, fbar, f + j * 64, k, WG ? 0 : t.g, keep);
-                        } else {
-                            tma_load_3d_pair(sA, &tmA, fbar, k, f, t.g, keep);
+                                tma_load_3d_pair(sA + j * 64 * 128, &maps.a, fbar, f + j * 64, k, WG ? 0 : t.g, keep);
                         }
-                        if (WG) {
-                            for (int j = 0; j * 64 < bnh; ++j)
-                                tma_load_3d_pair(sB + j * 64 * 128, &tmB, fbar, c0 + j * 64, k, 0, keep);
+                        if (!WG) {
+                            tma_load_3d_pair(sB, &maps.b[(bnh >> 4) - 1], fbar, k, c0, 0, keep);
+                        } else if (b_whole) {
+                            tma_load_4d_pair(sB, &maps.b[bnh > 64], fbar, 0, k, c0 >> 6, 0, keep);
                         } else {
-                            // boxes of 64 rows, then of 16
-                            int r = 0;
-                            for (; r + 64 <= bnh; r += 64)
-                                tma_load_3d_pair(sB + r * 128, &tmB, fbar, k, c0 + r, 0, keep);
-                            for (; r < bnh; r += 16)
-                                tma_load_3d_pair(sB + r * 128, &tmB16, fbar, k, c0 + r, 0, keep);
+                            for (int j = 0; j * 64 < bnh; ++j)
+                                tma_load_3d_pair(sB + j * 64 * 128, &maps.b[2], fbar, c0 + j * 64, k, 0, keep);
                         }
                     }
                     if (++stage == stages) {
@@ -330,7 +336,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                 chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row, rs != nullptr ? rs + row : nullptr, 1.0f, bias, e);
                 if (args.c_tma && row + 32 <= t.nr) {
                     if (f - lane < args.F)
-                        box_chunk_t<OUT>(v, &tmC, box, turn, f - lane, t.r0 + row, WG ? t.g : 0);
+                        box_chunk_t<OUT>(v, &maps.c, box, turn, f - lane, t.r0 + row, WG ? t.g : 0);
                 } else {
                     store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, e);
                 }
@@ -424,8 +430,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
 }
 
 template <bool WG, int AB, int OUT>
-cudaError_t launch_gtc(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb16, const CUtensorMap &tc,
-                       const GtcArgs &a, int clusters, cudaStream_t stream) {
+cudaError_t launch_gtc(const GtcMaps &maps, const GtcArgs &a, int clusters, cudaStream_t stream) {
     auto kern = grouped_tc_kernel<WG, AB, OUT>;
     GtcArgs args = a;
     args.stages = GtcConfig::MAX_STAGES;
@@ -447,28 +452,26 @@ cudaError_t launch_gtc(const CUtensorMap &ta, const CUtensorMap &tb, const CUten
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, ta, tb, tb16, tc, args);
+    return cudaLaunchKernelEx(&cfg, kern, maps, args);
 }
 
 template <bool WG, int AB>
-cudaError_t launch_gtc_out(int out, const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &tb16,
-                           const CUtensorMap &tc, const GtcArgs &args, int clusters, cudaStream_t stream) {
-    if (out == kDtF32) return launch_gtc<WG, AB, kDtF32>(ta, tb, tb16, tc, args, clusters, stream);
-    if (out == kDtF16) return launch_gtc<WG, AB, kDtF16>(ta, tb, tb16, tc, args, clusters, stream);
-    if (out == kDtBF16) return launch_gtc<WG, AB, kDtBF16>(ta, tb, tb16, tc, args, clusters, stream);
+cudaError_t launch_gtc_out(int out, const GtcMaps &maps, const GtcArgs &args, int clusters, cudaStream_t stream) {
+    if (out == kDtF32) return launch_gtc<WG, AB, kDtF32>(maps, args, clusters, stream);
+    if (out == kDtF16) return launch_gtc<WG, AB, kDtF16>(maps, args, clusters, stream);
+    if (out == kDtBF16) return launch_gtc<WG, AB, kDtBF16>(maps, args, clusters, stream);
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const CUtensorMap &ta, const CUtensorMap &tb,
-                              const CUtensorMap &tb16, const CUtensorMap &tc, const GtcArgs &args, int clusters, cudaStream_t stream) {
+cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const GtcMaps &maps, const GtcArgs &args, int clusters, cudaStream_t stream) {
     if (ab == kDtF16)
-        return wgrad ? launch_gtc_out<true, kDtF16>(out, ta, tb, tb16, tc, args, clusters, stream)
-                     : launch_gtc_out<false, kDtF16>(out, ta, tb, tb16, tc, args, clusters, stream);
+        return wgrad ? launch_gtc_out<true, kDtF16>(out, maps, args, clusters, stream)
+                     : launch_gtc_out<false, kDtF16>(out, maps, args, clusters, stream);
     if (ab == kDtBF16)
-        return wgrad ? launch_gtc_out<true, kDtBF16>(out, ta, tb, tb16, tc, args, clusters, stream)
-                     : launch_gtc_out<false, kDtBF16>(out, ta, tb, tb16, tc, args, clusters, stream);
+        return wgrad ? launch_gtc_out<true, kDtBF16>(out, maps, args, clusters, stream)
+                     : launch_gtc_out<false, kDtBF16>(out, maps, args, clusters, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -171,20 +171,26 @@ struct GtcArgs {
     int epi;
     int pairs;                      // 16-bit C: base and pitch allow 32-bit stores of two columns
     uint32_t a_mn;                  // forward: the weights are contiguous along F
+    int a_whole, b_whole;           // see launch_grouped_tc
     const float *col_scale;         // integer product: G x F, NULL: 1
     int most;                       // integer product: widest row tile (a multiple of 64)
     int stages;                     // set by the launcher
-    int c_tma;                      // C can be written by TMA (launch_grouped_tc's tc is valid)
+    int c_tma;                      // C can be written by TMA (launch_grouped_tc's c is valid)
     unsigned int *status;
 };
 
 // Launchers (each returns the launch's cudaError_t), defined by the kernel files.
-//   grouped products on the tensor cores, `clusters` SM pairs.  Forward: ta = weights (K, F, G) in boxes
-//   of 64 x 128 (a_mn: (F, K, G) in 64 x 64), tb / tb16 = rows (K, T) in boxes of 64 x 64 and 64 x 16.
-//   Gradient: ta = (F, T), tb = (R, T), boxes of 64 x 64; tb16 unused.  All 3-D, 128-byte swizzle.
-//   tc = C (F, rows, G): 16-bit in boxes of 32 x 32 with 64-byte swizzle, fp32 in 32 x 16 with 128-byte swizzle.
-cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const CUtensorMap &ta, const CUtensorMap &tb,
-                              const CUtensorMap &tb16, const CUtensorMap &tc, const GtcArgs &args, int clusters,
+//   grouped products on the tensor cores, `clusters` SM pairs.  Every load is one box of 64 (128 bytes) of the
+//   contiguous index, 128-byte swizzle:
+//     forward   a = weights (K, F, G) in boxes of 64 x 128; with a_mn (F, K, G) in 64 x 64, or with a_whole
+//               (64, K, F / 64, G) in 64 x 64 x 2.  b[i] = rows (K, T) in boxes of 64 x 16 (i + 1), i = 0 .. 7.
+//     gradient  a = (F, T) in 64 x 64, or with a_whole (64, T, F / 64) in 64 x 64 x 2.  b[2] = (R, T) in 64 x 64; with
+//               b_whole also b[0], b[1] = (64, T, R / 64) in 64 x 64 x 1 and x 2.
+//   c = C (F, rows, G) when args.c_tma: 16-bit in boxes of 32 x 32, 64-byte swizzle; fp32 in 32 x 16, 128-byte.
+struct GtcMaps {
+    CUtensorMap a, c, b[8];
+};
+cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const GtcMaps &maps, const GtcArgs &args, int clusters,
                               cudaStream_t stream);
 //   8-bit integer products on the tensor cores, `clusters` SM pairs.  tw = weight codes (K, F, G) in boxes of
 //   128 x 128 bytes, tx32 / tx16 = row codes (K, T) in boxes of 128 x 32 and 128 x 16; 128-byte swizzle.
