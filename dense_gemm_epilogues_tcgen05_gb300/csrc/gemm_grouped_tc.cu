@@ -227,13 +227,18 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
             }
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             // ---------------------------------------------------- MMA issuer --
+            // The whole warp walks the loop and one elected lane issues, so that
+            // addresses and descriptors stay in uniform registers, and the next stage
+            // is asked for before this one's MMAs issue: a k-block's MMAs take 512
+            // clocks, and the issuing thread's own time has to stay well below.
             const uint32_t a_mn = WG ? 1u : args.a_mn, b_mn = WG ? 1u : 0u;
-            const uint32_t a_lbo = a_mn ? 128u * BK : 16u, b_lbo = b_mn ? 128u * BK : 16u;
-            const uint32_t a_kstep = a_mn ? 128u * 16 : 32u, b_kstep = b_mn ? 128u * 16 : 32u;
+            const uint32_t a_kstep = (a_mn ? 128u * 16 : 32u) >> 4, b_kstep = (b_mn ? 128u * 16 : 32u) >> 4;
+            const uint64_t a_desc0 = sw128_desc(smem_u32(smem), a_mn ? 128u * BK : 16u, 1024u);
+            const uint64_t b_desc0 = sw128_desc(smem_u32(smem) + Cfg::A_BYTES, b_mn ? 128u * BK : 16u, 1024u);
             uint32_t stage = 0, phase = 0, fixed_parity = 0;
-            bool ok = true, issued = false;
+            bool ok = true, issued = false, is_full = false;
             int local = 0;
             while (ok && it.next(t)) {
                 const int num_kb = (t.nk + BK - 1) / BK;
@@ -248,37 +253,47 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                         const uint32_t acc_phase = (local >> 1) & 1;
                         ++local;
                         ok = pair_wait<CL>(&tempty[acc], acc_phase ^ 1u, abort_flag, args.status, abort_local, rank);
+                        ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
-                    ok = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
-                    if (WG && ok && (kb + 1) * BK > t.nk) {
+                    if (!is_full) {
+                        ok = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
+                    if (WG && (kb + 1) * BK > t.nk) {
                         ok = pair_wait<CL>(&fixed[stage], (fixed_parity >> stage) & 1u, abort_flag, args.status,
                                            abort_local, rank);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
                         smem_acquire_cluster();
                         fixed_parity ^= 1u << stage;
                     }
-                    if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a_addr = smem_u32(smem + stage * Cfg::STAGE_BYTES);
-                    const uint32_t b_addr = a_addr + Cfg::A_BYTES;
+                    const uint32_t next = stage + 1 == stages ? 0u : stage + 1;
+                    const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+                    const bool next_full = mbar_test_wait(smem_u32(&full[next]), next_phase);
+                    const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
+                    const uint32_t at = stage * (Cfg::STAGE_BYTES >> 4);  // addresses are in 16-byte units, below 2^14
+                    const uint64_t ad = a_desc0 + at, bd = b_desc0 + at;
+                    const bool closes = kb + 1 == num_kb || (SEGS && (kb + 1) % SEG == 0);
+                    if (elect_one()) {
 #pragma unroll
-                    for (int ks = 0; ks < BK / 16; ++ks)
-                        tc_mma_pair<kKindF16>(d_tmem, sw128_desc(a_addr + ks * a_kstep, a_lbo, 1024u),
-                                              sw128_desc(b_addr + ks * b_kstep, b_lbo, 1024u), idesc,
-                                              !opens || ks != 0 ? 1u : 0u);
-                    issued = true;
-                    tc_commit_pair(&empty[stage], 0x3);
-                    if (++stage == stages) {
-                        stage = 0;
-                        phase ^= 1u;
+                        for (uint32_t ks = 0; ks < BK / 16; ++ks)
+                            tc_mma_pair<kKindF16>(d_tmem, ad + ks * a_kstep, bd + ks * b_kstep, idesc,
+                                                  !opens || ks != 0 ? 1u : 0u);
+                        tc_commit_pair(&empty[stage], 0x3);
+                        if (closes) tc_commit_pair(&tfull[acc], 0x3);
                     }
-                    if (kb + 1 == num_kb || (SEGS && (kb + 1) % SEG == 0)) tc_commit_pair(&tfull[acc], 0x3);
+                    issued = true;
+                    is_full = __all_sync(0xffffffffu, next_full);
+                    stage = next;
+                    phase = next_phase;
                 }
             }
             if (*abort_flag && issued) {
-                tc_commit_pair(mma_done, 1u);
+                if (elect_one()) tc_commit_pair(mma_done, 1u);
                 mbar_drain_wait(mma_done, 0, 100000000ull);
             }
         }
