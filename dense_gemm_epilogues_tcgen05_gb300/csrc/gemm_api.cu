@@ -1613,7 +1613,6 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
     a.beta = beta;
     a.status = dev->status;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    if (a_sum != nullptr && launch_grouped_colsum(ab_dtype, a, s) != cudaSuccess) return GEMM_ERR_CUDA;
     gemm_launch_info_t info = {};
     if (product && es == 2 && tma_ok(A, T, a_stride_m, a_stride_r, 2) && tma_ok(D, T, d_stride_n, d_stride_r, 2)) {
         GtcMaps m = {};
@@ -1637,9 +1636,14 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
         t.b_whole = b_whole;
         t.status = dev->status;
         const int clusters = pair_clusters(dev, G * t.tiles_f * t.tiles_r, &info);
+        // the sums first: what they read of A the product then finds in L2
+        if (a_sum != nullptr && launch_grouped_colsum(ab_dtype, a, true, dev->num_sms, s) != cudaSuccess)
+            return GEMM_ERR_CUDA;
         return record(launch_grouped_tc(true, ab_dtype, c_dtype, m, t, clusters, s) == cudaSuccess
                           ? GEMM_OK : GEMM_ERR_CUDA, info);
     }
+    if (a_sum != nullptr && launch_grouped_colsum(ab_dtype, a, false, dev->num_sms, s) != cudaSuccess)
+        return GEMM_ERR_CUDA;
     info.path = product ? GEMM_PATH_SIMT : GEMM_PATH_EPILOGUE_ONLY;
     const int grid = simt_grid(dev, G * ((M + 63) / 64), (N + 63) / 64);
     return record(launch_wgrad_simt(ab_dtype, c_dtype, a, grid, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);

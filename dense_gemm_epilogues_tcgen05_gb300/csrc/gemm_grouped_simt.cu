@@ -160,6 +160,69 @@ __global__ void __launch_bounds__(256) grouped_colsum_kernel(const WgradArgs a) 
     }
 }
 
+// The same for 16-bit values contiguous along m in 16-byte aligned rows: a
+// block sums 64 columns of one group, 8 per thread by LANES row lanes, four
+// rows of each in flight; the lanes' sums meet in shared memory in a fixed order.
+template <int AB, int LANES>
+__global__ void __launch_bounds__(8 * LANES) grouped_colsum_vec_kernel(const WgradArgs a) {
+    __shared__ float part[LANES][64 + 8];
+    const int cv = threadIdx.x & 7, y = threadIdx.x >> 3;
+    const int g = blockIdx.y, m0 = blockIdx.x * 64, m = m0 + cv * 8;
+    grid_dep_launch();  // the product's kernel may set itself up meanwhile; it waits for this grid
+    const int lo = min(max(a.offsets[g], 0), a.T), hi = min(max(a.offsets[g + 1], lo), a.T);
+    float s[8] = {};
+    if (m + 8 <= a.M) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const typename Elem<AB>::T *>(a.A) + m);
+        const long long pitch = a.sar / 8;
+        int r = lo + y;
+        for (; hi - r > 3 * LANES; r += 4 * LANES) {
+            uint4 u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) u[i] = __ldg(src + (r + i * LANES) * pitch);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float f[8];
+                Vec16<AB>::unpack(u[i], f);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s[j] += f[j];
+            }
+        }
+        for (; r < hi; r += LANES) {
+            float f[8];
+            Vec16<AB>::unpack(__ldg(src + r * pitch), f);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[j] += f[j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            for (int r = lo + y; m + j < a.M && r < hi; r += LANES) s[j] += SimtLoad<AB>::load(a.A, r * a.sar + m + j);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[y][cv * 8 + j] = s[j];
+    __syncthreads();
+    const int c = threadIdx.x, col = m0 + c;
+    if (c < 64 && col < a.M) {
+        float sum = part[0][c];
+#pragma unroll
+        for (int i = 1; i < LANES; ++i) sum += part[i][c];
+        float *out = a.a_sum + static_cast<long long>(g) * a.M + col;
+        *out = a.beta != 0.0f ? fmaf(a.beta, *out, a.alpha * sum) : a.alpha * sum;
+    }
+}
+
+template <int AB>
+cudaError_t launch_colsum_vec(const WgradArgs &a, int sms, cudaStream_t s) {
+    const dim3 grid((a.M + 63) / 64, a.G);
+    // A block's time is its group's rows over its lanes, four loads at a time: many lanes for long groups, and
+    // where there are few blocks (16 groups of some 1000 rows x 2048 columns on GB300: 34 us with 32 lanes).
+    if (static_cast<long long>(grid.x) * grid.y < 2ll * sms || a.T / a.G >= 256)
+        grouped_colsum_vec_kernel<AB, 128><<<grid, 1024, 0, s>>>(a);
+    else
+        grouped_colsum_vec_kernel<AB, 32><<<grid, 256, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
 template <int AB>
 cudaError_t grouped_simt_out(int out, const GroupedArgs &a, int grid, cudaStream_t s) {
     if (out == kDtF32) grouped_simt_kernel<AB, kDtF32><<<grid, kGThreads, 0, s>>>(a);
@@ -195,7 +258,9 @@ cudaError_t launch_wgrad_simt(int ab, int out, const WgradArgs &a, int grid, cud
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_grouped_colsum(int ab, const WgradArgs &a, cudaStream_t s) {
+cudaError_t launch_grouped_colsum(int ab, const WgradArgs &a, bool vec, int sms, cudaStream_t s) {
+    if (vec && ab == kDtF16) return launch_colsum_vec<kDtF16>(a, sms, s);
+    if (vec && ab == kDtBF16) return launch_colsum_vec<kDtBF16>(a, sms, s);
     const dim3 grid((a.M + 31) / 32, a.G);
     if (ab == kDtF32) grouped_colsum_kernel<kDtF32><<<grid, 256, 0, s>>>(a);
     else if (ab == kDtF16) grouped_colsum_kernel<kDtF16><<<grid, 256, 0, s>>>(a);

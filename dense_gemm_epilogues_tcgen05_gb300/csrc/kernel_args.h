@@ -210,7 +210,8 @@ constexpr int kI8TileRows = 192;    // its widest row tile
 //   grouped products on the CUDA cores, any strides (ab: F32, F16, BF16 or kDtI8), `grid` blocks:
 cudaError_t launch_grouped_simt(int ab, int out, const GroupedArgs &args, int grid, cudaStream_t stream);
 cudaError_t launch_wgrad_simt(int ab, int out, const WgradArgs &args, int grid, cudaStream_t stream);
-cudaError_t launch_grouped_colsum(int ab, const WgradArgs &args, cudaStream_t stream);
+//   a_sum; vec: A's 16-bit values are contiguous along m in 16-byte aligned rows
+cudaError_t launch_grouped_colsum(int ab, const WgradArgs &args, bool vec, int sms, cudaStream_t stream);
 //   per-row 8-bit quantisation:
 cudaError_t launch_i8_quantize(int x_dtype, long long M, long long K, const void *X, long long ldx, signed char *Q,
                                long long ldq, float *scale, cudaStream_t stream);
