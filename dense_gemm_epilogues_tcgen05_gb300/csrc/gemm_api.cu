@@ -1715,7 +1715,7 @@ gemm_status_t gemm_i8_quantize(int64_t M, int64_t K, gemm_dtype_t x_dtype, const
     if ((st = check_range(X, extent_bytes(1, 0, M, ldx, K, 1, elem_bytes(x_dtype)))) != GEMM_OK) return st;
     if ((st = check_range(Q, extent_bytes(1, 0, M, ldq, K, 1, 1))) != GEMM_OK) return st;
     return launch_i8_quantize(x_dtype, M, K, X, ldx, reinterpret_cast<signed char *>(Q), ldq, scale,
-                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                              dev->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GEMM_OK
                : GEMM_ERR_CUDA;
 }

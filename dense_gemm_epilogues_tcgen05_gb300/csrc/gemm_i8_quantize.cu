@@ -6,18 +6,22 @@
 // and codes 0; a row that holds a NaN or an infinity gets a NaN scale (the
 // product's row shows it) and codes 0.
 //
-// One block per row, one pass over memory: a thread keeps its (up to 8)
-// 16-byte pieces of the row in registers between the maximum and the rounding,
-// and reads what a longer row has beyond them again (from L2).  The maximum of
+// One pass over memory: a thread keeps its (up to 8) 16-byte pieces of a row in
+// registers between the maximum and the rounding.  Many rows: persistent blocks,
+// which load the next row's pieces before they round a row's.  Few, very long or
+// unaligned rows: one block per row, which reads what a row has beyond the pieces
+// again (from L2).  The maximum of
 // 16-bit values is taken on their bits, two per instruction: with the sign
 // cleared, they are ordered as integers, infinities and NaN last.
 //
-// The codes are those of the exact quotient.  x * (127 / max) is off by at most
-// 2^-23 of a quotient of at most 127, so by less than 2^-15: where it is further
-// than that from a tie its rounding is the quotient's, and only the other values
-// (one in 2^14) take the division.  There 127 x is exact for 16-bit inputs, the
-// division is correctly rounded, and a quotient of two 16-bit values that is not a
-// tie is further from one than that rounding.
+// The codes are those of the exact quotient.  n = round(x * (127 / max)) is the
+// quotient's rounding or, within 2^-15 of a tie (the product is off by at most
+// 2^-23 of at most 127), a neighbour of it.  There the remainder 127 x - n max
+// decides: twice its size against max, and the even code where they are equal.
+// For 16-bit inputs 127 x is exact and the remainder of a quotient that is not a
+// tie differs from max / 2 by far more than the rounding of its fused
+// multiply-add.  (Ties are not rare: with x and max of few bits the quotients lie
+// on a coarse grid, and in rows of normal bf16 values most warps meet one.)
 //
 // Bound: HBM (3 bytes per 16-bit value).
 #include "grouped.cuh"
@@ -85,7 +89,7 @@ __device__ __forceinline__ void codes_of(const float (&f)[N], const QRow &row, u
         t[j + 1] = __float_as_uint(s1);
         worst = fmaxf(worst, fmaxf(fabsf(o0), fabsf(o1)));
     }
-    if (row.slow || worst > 0.5f - 0x1p-15f) {
+    if (row.slow) {
 #pragma unroll 1
         for (int j = 0; j < N; ++j) {
             const uint32_t c = static_cast<uint32_t>(code_by_division(f[j], row.amax, row.shrink));
@@ -93,12 +97,46 @@ __device__ __forceinline__ void codes_of(const float (&f)[N], const QRow &row, u
             for (int i = 0; i < N; ++i)
                 if (i == j) t[i] = c;
         }
+    } else if (worst > 0.5f - 0x1p-15f) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const float n = __uint_as_float(t[j]) - kMagic;
+            const float e = fmaf(-n, row.amax, 127.0f * f[j]), d = 2.0f * fabsf(e);
+            if (d > row.amax || (d == row.amax && (t[j] & 1u))) t[j] += e > 0.0f ? 1u : 0xFFFFFFFFu;
+        }
     }
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) {
         const uint32_t lo = __byte_perm(t[4 * i], t[4 * i + 1], 0x0040), hi = __byte_perm(t[4 * i + 2], t[4 * i + 3], 0x0040);
         w[i] = row.zero ? 0u : __byte_perm(lo, hi, 0x5410);
     }
+}
+
+// What a row's largest |x| (as bits) makes of it; one thread writes the scale.
+__device__ __forceinline__ QRow row_scale(unsigned m, float *scale, bool writes) {
+    const bool finite = m < 0x7F800000u;
+    QRow r;
+    r.amax = __uint_as_float(m);
+    r.zero = !finite || m == 0u;
+    r.slow = !(r.amax > 1e-30f && r.amax < 1e30f) && !r.zero;
+    r.shrink = r.amax >= 1.2676506e30f ? 2.3283064365386963e-10f : 1.0f;  // 2^100, 2^-32
+    r.inv = r.slow || r.zero ? 0.0f : __fdiv_rn(127.0f, r.amax);
+    if (writes) *scale = finite ? __fdiv_rn(r.amax, 127.0f) : __uint_as_float(0x7FC00000u);
+    return r;
+}
+
+// Codes of the 16-byte piece u, piece v of its row.
+template <int XT>
+__device__ __forceinline__ void store_codes(signed char *q, long long v, const uint4 &u, const QRow &r) {
+    constexpr int PV = Vec16<XT>::kPerVec;
+    float f[PV];
+    Vec16<XT>::unpack(u, f);
+    uint32_t w[PV / 4];
+    codes_of<PV>(f, r, w);
+    if constexpr (PV == 8)
+        *reinterpret_cast<uint2 *>(q + v * PV) = make_uint2(w[0], w[1]);
+    else
+        *reinterpret_cast<uint32_t *>(q + v * PV) = w[0];
 }
 
 // VEC: 16-byte loads of X and whole-word stores of Q; KEEP pieces per thread stay in registers.
@@ -132,46 +170,73 @@ __global__ void __launch_bounds__(kQThreads) i8_quantize_kernel(long long K, con
     if ((tid & 31) == 0) part[tid >> 5] = m;
     __syncthreads();
     for (int w = 0; w < n >> 5; ++w) m = max(m, part[w]);
-    const bool finite = m < 0x7F800000u;
-    QRow r;
-    r.amax = __uint_as_float(m);
-    r.zero = !finite || m == 0u;
-    r.slow = !(r.amax > 1e-30f && r.amax < 1e30f) && !r.zero;
-    r.shrink = r.amax >= 1.2676506e30f ? 2.3283064365386963e-10f : 1.0f;  // 2^100, 2^-32
-    r.inv = r.slow || r.zero ? 0.0f : __fdiv_rn(127.0f, r.amax);
-    if (tid == 0) scale[row] = finite ? __fdiv_rn(r.amax, 127.0f) : __uint_as_float(0x7FC00000u);
+    const QRow r = row_scale(m, scale + row, tid == 0);
     if constexpr (VEC) {
-        auto store = [&](long long v, const uint4 &u) {
-            float f[PV];
-            Vec16<XT>::unpack(u, f);
-            uint32_t w[PV / 4];
-            codes_of<PV>(f, r, w);
-            if constexpr (PV == 8)
-                *reinterpret_cast<uint2 *>(q + v * PV) = make_uint2(w[0], w[1]);
-            else
-                *reinterpret_cast<uint32_t *>(q + v * PV) = w[0];
-        };
 #pragma unroll
         for (int i = 0; i < KEEP; ++i) {
             const long long v = tid + static_cast<long long>(i) * n;
-            if (v < nvec) store(v, keep[i]);
+            if (v < nvec) store_codes<XT>(q, v, keep[i], r);
         }
-        for (long long v = tid + static_cast<long long>(KEEP) * n; v < nvec; v += n) store(v, __ldg(xv + v));
+        for (long long v = tid + static_cast<long long>(KEEP) * n; v < nvec; v += n)
+            store_codes<XT>(q, v, __ldg(xv + v), r);
     }
     for (long long k = nvec * PV + tid; k < K; k += n)
         q[k] = static_cast<signed char>(r.zero ? 0 : code_by_division(Elem<XT>::load(x + k), r.amax, r.shrink));
 }
 
+// Persistent form for many rows of `pieces` 16-byte pieces, at most KEEP
+// blockDim.x: the next row's pieces are on their way while a row is rounded.
 template <int XT, int KEEP>
-cudaError_t quantize_keep(unsigned grid, int threads, long long K, const void *X, long long ldx, signed char *Q,
-                          long long ldq, float *scale, cudaStream_t s) {
-    i8_quantize_kernel<XT, true, KEEP><<<grid, threads, 0, s>>>(K, X, ldx, Q, ldq, scale);
+__global__ void __launch_bounds__(kQThreads, KEEP <= 4 ? 4 : 3)
+    i8_quantize_rows_kernel(long long M, int pieces, const void *X, long long ldx, signed char *Q, long long ldq,
+                            float *scale) {
+    __shared__ unsigned part[2][kQThreads / 32];
+    const int tid = threadIdx.x, n = blockDim.x;
+    const uint4 *x = static_cast<const uint4 *>(X);
+    const long long pitch = ldx * static_cast<long long>(sizeof(typename Elem<XT>::T)) / 16;
+    uint4 cur[KEEP], nxt[KEEP];
+#pragma unroll
+    for (int i = 0; i < KEEP; ++i)
+        nxt[i] = tid + i * n < pieces ? __ldg(x + blockIdx.x * pitch + tid + i * n) : make_uint4(0, 0, 0, 0);
+    int flip = 0;
+    for (long long row = blockIdx.x; row < M; row += gridDim.x, flip ^= 1) {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) cur[i] = nxt[i];
+        const long long ahead = row + gridDim.x;
+        if (ahead < M) {
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i)
+                if (tid + i * n < pieces) nxt[i] = __ldg(x + ahead * pitch + tid + i * n);
+        }
+        unsigned acc = 0u;
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) max16<XT>(cur[i], acc);
+        unsigned m = __reduce_max_sync(0xffffffffu, max_bits<XT>(acc));
+        if ((tid & 31) == 0) part[flip][tid >> 5] = m;
+        __syncthreads();  // the other half of `part` is free: all have read it before this row's barrier
+        for (int w = 0; w < n >> 5; ++w) m = max(m, part[flip][w]);
+        const QRow r = row_scale(m, scale + row, tid == 0);
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i)
+            if (tid + i * n < pieces) store_codes<XT>(Q + row * ldq, tid + i * n, cur[i], r);
+    }
+}
+
+template <int XT, int KEEP>
+cudaError_t quantize_keep(long long M, int threads, long long K, const void *X, long long ldx, signed char *Q,
+                          long long ldq, float *scale, int sms, cudaStream_t s) {
+    const long long pieces = K / Vec16<XT>::kPerVec, blocks = 4ll * sms * (kQThreads / threads);
+    if (K % Vec16<XT>::kPerVec == 0 && pieces > 0 && pieces <= static_cast<long long>(KEEP) * threads && M >= 2 * blocks)
+        i8_quantize_rows_kernel<XT, KEEP><<<static_cast<unsigned>(blocks), threads, 0, s>>>(
+            M, static_cast<int>(pieces), X, ldx, Q, ldq, scale);
+    else
+        i8_quantize_kernel<XT, true, KEEP><<<static_cast<unsigned>(M), threads, 0, s>>>(K, X, ldx, Q, ldq, scale);
     return cudaGetLastError();
 }
 
 template <int XT>
 cudaError_t quantize_xt(long long M, long long K, const void *X, long long ldx, signed char *Q, long long ldq,
-                        float *scale, cudaStream_t s) {
+                        float *scale, int sms, cudaStream_t s) {
     const int es = static_cast<int>(sizeof(typename Elem<XT>::T));
     const bool vec = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (M == 1 || ldx * es % 16 == 0) &&
                      (reinterpret_cast<uintptr_t>(Q) & 7u) == 0 && (M == 1 || ldq % 8 == 0);
@@ -185,19 +250,19 @@ cudaError_t quantize_xt(long long M, long long K, const void *X, long long ldx, 
     const int keep = pieces <= kQThreads ? 1 : pieces <= 2 * kQThreads ? 2 : pieces <= 4 * kQThreads ? 4 : 8;
     const long long want = (pieces + keep - 1) / keep;
     const int threads = want >= kQThreads ? kQThreads : static_cast<int>((want + 31) / 32 * 32 > 0 ? (want + 31) / 32 * 32 : 32);
-    if (keep == 1) return quantize_keep<XT, 1>(grid, threads, K, X, ldx, Q, ldq, scale, s);
-    if (keep == 2) return quantize_keep<XT, 2>(grid, threads, K, X, ldx, Q, ldq, scale, s);
-    if (keep == 4) return quantize_keep<XT, 4>(grid, threads, K, X, ldx, Q, ldq, scale, s);
-    return quantize_keep<XT, 8>(grid, threads, K, X, ldx, Q, ldq, scale, s);
+    if (keep == 1) return quantize_keep<XT, 1>(M, threads, K, X, ldx, Q, ldq, scale, sms, s);
+    if (keep == 2) return quantize_keep<XT, 2>(M, threads, K, X, ldx, Q, ldq, scale, sms, s);
+    if (keep == 4) return quantize_keep<XT, 4>(M, threads, K, X, ldx, Q, ldq, scale, sms, s);
+    return quantize_keep<XT, 8>(M, threads, K, X, ldx, Q, ldq, scale, sms, s);
 }
 
 }  // namespace
 
 cudaError_t launch_i8_quantize(int x_dtype, long long M, long long K, const void *X, long long ldx, signed char *Q,
-                               long long ldq, float *scale, cudaStream_t s) {
-    if (x_dtype == kDtF32) return quantize_xt<kDtF32>(M, K, X, ldx, Q, ldq, scale, s);
-    if (x_dtype == kDtF16) return quantize_xt<kDtF16>(M, K, X, ldx, Q, ldq, scale, s);
-    if (x_dtype == kDtBF16) return quantize_xt<kDtBF16>(M, K, X, ldx, Q, ldq, scale, s);
+                               long long ldq, float *scale, int sms, cudaStream_t s) {
+    if (x_dtype == kDtF32) return quantize_xt<kDtF32>(M, K, X, ldx, Q, ldq, scale, sms, s);
+    if (x_dtype == kDtF16) return quantize_xt<kDtF16>(M, K, X, ldx, Q, ldq, scale, sms, s);
+    if (x_dtype == kDtBF16) return quantize_xt<kDtBF16>(M, K, X, ldx, Q, ldq, scale, sms, s);
     return cudaErrorInvalidValue;
 }
 

@@ -214,7 +214,7 @@ cudaError_t launch_wgrad_simt(int ab, int out, const WgradArgs &args, int grid, 
 cudaError_t launch_grouped_colsum(int ab, const WgradArgs &args, bool vec, int sms, cudaStream_t stream);
 //   per-row 8-bit quantisation:
 cudaError_t launch_i8_quantize(int x_dtype, long long M, long long K, const void *X, long long ldx, signed char *Q,
-                               long long ldq, float *scale, cudaStream_t stream);
+                               long long ldq, float *scale, int sms, cudaStream_t stream);
 //   one-SM tcgen05 kernel, `bn` = 256 or 128, `grid` CTAs:
 cudaError_t launch_tcgen05_f16(int out, int bn, const CUtensorMap &, const CUtensorMap &, const TcArgs &, int grid,
                                cudaStream_t);
