@@ -1362,11 +1362,6 @@ static bool group_stride_ok(int64_t G, int64_t stride, int es) {
     return G == 1 || (stride > 0 && stride * es % 16 == 0 && stride * es < (int64_t(1) << 40));
 }
 
-// 16-bit outputs stored two columns at a time: even pitch, 4-byte aligned base.
-static int pair_stores(const void *C, int64_t ldc, int64_t group_stride) {
-    return (reinterpret_cast<uintptr_t>(C) & 3u) == 0 && ldc % 2 == 0 && group_stride % 2 == 0;
-}
-
 // Map of C for the grouped kernels' stores, (columns, rows, groups); false (and the kernels store from registers)
 // where its base or pitches rule out TMA, or its rows do not end on 16 bytes (a TMA store clips there, and would
 // write into the padding).
@@ -1458,7 +1453,6 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
             t.C = args.C; t.ldc = args.ldc;
             t.bias = args.bias; t.row_scale = args.row_scale;
             t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
-            t.pairs = pair_stores(args.C, args.ldc, 0);
             t.c_tma = encode_grouped_c(&m.c, cd, args.C, args.N, args.M, args.ldc, 1, 0);
             t.a_whole = whole;
             t.a_mn = n_major ? 1u : 0u;
@@ -1505,13 +1499,14 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
         t.C = args.C; t.ldc = args.ldc;
         t.bias = args.bias; t.row_scale = args.row_scale; t.col_scale = args.col_scale;
         t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
-        t.pairs = pair_stores(args.C, args.ldc, 0);
+        CUtensorMap tc = tw;
+        t.c_tma = encode_grouped_c(&tc, cd, args.C, args.N, args.M, args.ldc, 1, 0);
         t.most = i8_most_rows(args.G, args.M, args.N, dev->num_sms / 2);
         t.status = args.status;
         const int64_t row_tiles = args.M / t.most + std::min(args.G, args.M);
         const int clusters = pair_clusters(dev, row_tiles * t.tiles_f, &info);
         info.bn = t.most;
-        return record(launch_i8_tc(cd, tw, tx32, tx16, t, clusters, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
+        return record(launch_i8_tc(cd, tw, tx32, tx16, tc, t, clusters, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
     }
     info.path = args.K == 0 ? GEMM_PATH_EPILOGUE_ONLY : GEMM_PATH_SIMT;
     const int grid = simt_grid(dev, (args.M + 63) / 64 + args.G, (args.N + 63) / 64);
@@ -1630,7 +1625,6 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
         t.offsets = offsets;
         t.C = C; t.scg = c_stride_g; t.ldc = ldc;
         t.alpha = alpha; t.beta = beta; t.epi = kEpiNone;
-        t.pairs = pair_stores(C, ldc, G > 1 ? c_stride_g : 0);
         t.c_tma = encode_grouped_c(&m.c, c_dtype, C, N, M, ldc, G, c_stride_g);
         t.a_whole = a_whole;
         t.b_whole = b_whole;

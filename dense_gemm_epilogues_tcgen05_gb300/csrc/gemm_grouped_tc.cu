@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         using OutT = typename Elem<OUT>::T;
         const int quad = warp & 3;                      // TMEM lanes 32*quad ..
         const int half = (warp - Cfg::EPI_WARP0) >> 2;  // which half of the tile's columns
-        const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi, args.pairs};
+        const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi};
         unsigned char *box = boxes + (warp - Cfg::EPI_WARP0) * 2 * kBoxBytes;
         uint32_t turn = 0;
         int local = 0;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                     if (f - lane < args.F)
                         box_chunk_t<OUT>(v, &maps.c, box, turn, f - lane, t.r0 + row, WG ? t.g : 0);
                 } else {
-                    store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, e);
+                    store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
                 }
             };
             if constexpr (SEGS) {

@@ -26,7 +26,7 @@
 //                 16-byte column of each row of X into a swizzled 16-bit tile;
 //                 four to ten slots of each;
 //   warps 20-27   epilogue: two per 32-lane quadrant, half of the columns each;
-//                 96 integer sums per thread, then store_chunk_t.
+//                 96 integer sums per thread, then as in gemm_grouped_tc.cu.
 //
 // A code becomes binary16 by a byte permute into the mantissa of 1024 (the sign
 // bit flipped first: 1024 + 128 + code) and one subtraction of 1152: five
@@ -61,8 +61,9 @@ struct I8Config {
     static_assert(ISSUE_REGS + SETS * CONV_REGS + 2 * EPI_REGS <= (SETS + 3) * LAUNCH_REGS, "the trade adds up");
     static constexpr int BAR_BYTES = 512, SMEM_MAX = 232448;
     static_assert((2 * MAX_STAGES + 2 * MAX_SLOTS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
-    // after up to 1023 bytes of alignment: [stages][slots][barriers][group table]
-    static int fixed_bytes(int G) { return 1024 + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16; }
+    // after up to 1023 bytes of alignment: [stages][slots][boxes][barriers][group table]
+    static constexpr int OUT_BYTES = 8 * 2 * kBoxBytes;
+    static int fixed_bytes(int G) { return 1024 + OUT_BYTES + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16; }
 };
 
 // What follows from the widest row tile `most` and the group count: most / 2
@@ -90,7 +91,8 @@ struct I8Shape {
 template <int OUT>
 __global__ void __launch_bounds__(I8Config::THREADS, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX32,
-                 const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ GtcArgs args) {
+                 const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ CUtensorMap tmC,
+                 const __grid_constant__ GtcArgs args) {
     using Cfg = I8Config;
     constexpr int CL = 2;
     const I8Shape sh(args.most, args.stages);
@@ -99,7 +101,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char *slot_base = smem + stages * sh.stage_bytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(slot_base + slots * sh.slot_bytes);  // codes landed
+    uint64_t *full = reinterpret_cast<uint64_t *>(slot_base + slots * sh.slot_bytes + Cfg::OUT_BYTES);  // codes landed
     uint64_t *empty = full + Cfg::MAX_STAGES;   // codes read by both converter sets
     uint64_t *ready = empty + Cfg::MAX_STAGES;  // (leader's) two slots, one stage, expanded in both CTAs
     uint64_t *freed = ready + Cfg::MAX_SLOTS;   // a slot read by the MMA
@@ -132,6 +134,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX32);
         tma_prefetch_desc(&tmX16);
+        if (args.c_tma) tma_prefetch_desc(&tmC);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
@@ -340,30 +343,73 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
         regs_increase<Cfg::EPI_REGS>();
         using OutT = typename Elem<OUT>::T;
         const int quad = warp & 3, side = (warp - Cfg::EPI_WARP0) >> 2;
-        const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi, args.pairs};
+        const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi};
+        unsigned char *box = slot_base + slots * sh.slot_bytes + (warp - Cfg::EPI_WARP0) * 2 * kBoxBytes;
         constexpr int MC = kI8TileRows / 64;  // most 32-column chunks of a warp
-        uint32_t local = 0;
+        uint32_t local = 0, turn = 0;
         bool ok = true;
         for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
             const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
             const int chunks = t.bn >> 5;
             const int c_begin = side ? (chunks + 1) >> 1 : 0, nch = (side ? chunks : (chunks + 1) >> 1) - c_begin;
+            const int f = t.f0 + static_cast<int>(rank) * 128 + quad * 32 + lane;
+            const long long gf = static_cast<long long>(t.g) * args.F + f;
+            const bool f_ok = f < args.F;
+            const float bias = args.epi != kEpiNone && f_ok ? args.bias[gf] : 0.0f;
+            const float cs = args.col_scale != nullptr && f_ok ? args.col_scale[gf] : 1.0f;
+            OutT *out = static_cast<OutT *>(args.C) + t.r0 * args.ldc + f;
+            const uint32_t t_quad = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c_begin * 32;
+            auto store = [&](float (&v)[32], int c) {
+                const int row = (c_begin + c) * 32;
+                OutT *c0 = out + row * args.ldc;
+                chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row,
+                                    args.row_scale != nullptr ? args.row_scale + t.r0 + row : nullptr, cs, bias, e);
+                if (args.c_tma && row + 32 <= t.nr) {
+                    if (f - lane < args.F) box_chunk_t<OUT>(v, &tmC, box, turn, f - lane, t.r0 + row, 0);
+                } else {
+                    store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
+                }
+            };
+            auto accumulator = [&](uint32_t &acc) {  // the next one; false when the kernel gives up
+                acc = local & 1;
+                const uint32_t acc_phase = (local >> 1) & 1;
+                ++local;
+                ok = __all_sync(0xffffffffu,
+                                pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank));
+                if (ok) tc_fence_after();
+                return ok;
+            };
+            auto release = [&](uint32_t acc) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
+            };
+            uint32_t acc;
+            if (2 * num_kb <= Cfg::CHUNK_HALVES) {
+                // one accumulator holds the whole sum, exact in fp32
+                if (!accumulator(acc)) break;
+#pragma unroll 1
+                for (int c = 0; c < nch; ++c) {
+                    uint32_t raw[32];
+                    __syncwarp();
+                    tmem_ld_issue(t_quad + acc * acc_stride + c * 32, raw);
+                    tmem_ld_wait(raw);
+                    if (c + 1 == nch) release(acc);
+                    float v[32];
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]);
+                    store(v, c);
+                }
+                if (nch == 0) release(acc);
+                continue;
+            }
             int sum[MC][32];
 #pragma unroll
             for (int c = 0; c < MC; ++c)
 #pragma unroll
                 for (int j = 0; j < 32; ++j) sum[c][j] = 0;
             for (int h = 0; h < 2 * num_kb; h += Cfg::CHUNK_HALVES) {
-                const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
-                ++local;
-                const bool got = pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank);
-                if (!__all_sync(0xffffffffu, got)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + acc * acc_stride +
-                                       c_begin * 32;
+                if (!accumulator(acc)) break;
 #pragma unroll
                 for (int c = 0; c < MC; ++c) {
                     if (c < nch) {
@@ -371,40 +417,29 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                         for (int p = 0; p < 2; ++p) {
                             uint32_t raw[16];
                             __syncwarp();
-                            tmem_ld_x16(t_row + c * 32 + p * 16, raw);
+                            tmem_ld_x16(t_quad + acc * acc_stride + c * 32 + p * 16, raw);
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
                                 sum[c][16 * p + j] += __float2int_rn(__uint_as_float(raw[j]));
                         }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
+                release(acc);
             }
             if (!ok) break;
-            const int f = t.f0 + static_cast<int>(rank) * 128 + quad * 32 + lane;
-            const long long gf = static_cast<long long>(t.g) * args.F + f;
-            const bool f_ok = f < args.F;
-            const float bias = args.epi != kEpiNone && f_ok ? args.bias[gf] : 0.0f;
-            const float cs = args.col_scale != nullptr && f_ok ? args.col_scale[gf] : 1.0f;
-            OutT *out = static_cast<OutT *>(args.C) + t.r0 * args.ldc + f;
 #pragma unroll
             for (int c = 0; c < MC; ++c) {
                 if (c < nch) {
-                    const int row = (c_begin + c) * 32;
                     float v[32];
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = __int2float_rn(sum[c][j]);
-                    OutT *c0 = out + row * args.ldc;
-                    chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row,
-                                        args.row_scale != nullptr ? args.row_scale + t.r0 + row : nullptr, cs, bias, e);
-                    store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, e);
+                    store(v, c);
                 }
             }
         }
     }
 
+    if (warp >= Cfg::EPI_WARP0 && lane == 0) bulk_wait<0>();  // stores in flight read this CTA's shared memory
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();  // no CTA leaves while its peer may still signal into it
@@ -416,7 +451,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
 
 template <int OUT>
 cudaError_t launch_i8_tc_out(const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
-                             const GtcArgs &a, int clusters, cudaStream_t stream) {
+                             const CUtensorMap &tc, const GtcArgs &a, int clusters, cudaStream_t stream) {
     auto kern = i8_tc_kernel<OUT>;
     cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, I8Config::SMEM_MAX);
@@ -446,16 +481,16 @@ cudaError_t launch_i8_tc_out(const CUtensorMap &tw, const CUtensorMap &tx32, con
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx32, tx16, args);
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx32, tx16, tc, args);
 }
 
 }  // namespace
 
 cudaError_t launch_i8_tc(int out, const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
-                         const GtcArgs &args, int clusters, cudaStream_t stream) {
-    if (out == kDtF32) return launch_i8_tc_out<kDtF32>(tw, tx32, tx16, args, clusters, stream);
-    if (out == kDtF16) return launch_i8_tc_out<kDtF16>(tw, tx32, tx16, args, clusters, stream);
-    if (out == kDtBF16) return launch_i8_tc_out<kDtBF16>(tw, tx32, tx16, args, clusters, stream);
+                         const CUtensorMap &tc, const GtcArgs &args, int clusters, cudaStream_t stream) {
+    if (out == kDtF32) return launch_i8_tc_out<kDtF32>(tw, tx32, tx16, tc, args, clusters, stream);
+    if (out == kDtF16) return launch_i8_tc_out<kDtF16>(tw, tx32, tx16, tc, args, clusters, stream);
+    if (out == kDtBF16) return launch_i8_tc_out<kDtBF16>(tw, tx32, tx16, tc, args, clusters, stream);
     return cudaErrorInvalidValue;
 }
 

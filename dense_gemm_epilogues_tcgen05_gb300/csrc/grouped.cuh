@@ -130,14 +130,15 @@ __device__ __forceinline__ float grouped_value(float acc, float scale, float bet
 // 32 consecutive columns of C in its lanes and 32 rows of C in its registers.
 // Whole blocks of 32 rows go through shared memory as 2 KB boxes that TMA
 // stores; a group's last rows, which must not touch the next group's, and
-// outputs that TMA cannot write are stored from registers, 64 or 128 bytes of
-// a row per instruction.  (Storing everything from registers cost 98 of 679 us
-// for 32768 x 4096 x 4096, and 27 of 46 us for 24 gradients of 1000 x 1000.)
+// outputs that TMA cannot write are stored from registers, 64 or 128 bytes of a
+// row per instruction.  27270 x 6304 fp16 outputs of a product 320 deep on GB300:
+// boxes 124 us (6 to 7 clocks per box row), registers 150 us; pairing lanes for
+// 32-bit stores 195 us, four warps joining their columns in shared memory for
+// 16-byte stores 153 us (248 where rows are only 4-byte aligned).
 struct StoreArgs {
     long long ldc;
     float alpha, beta;
     int epi;
-    int pairs;  // 16-bit output: base and pitch allow 32-bit stores of two columns
 };
 
 // v: this lane's column at 32 consecutive rows, of which the first nrow are
@@ -172,38 +173,15 @@ __device__ __forceinline__ void chunk_values_t(float (&v)[32], const typename El
     }
 }
 
-// The outputs v from registers.
+// The outputs v from registers: 32 columns of a row per instruction.
 template <int OUT>
 __device__ __forceinline__ void store_chunk_t(const float (&v)[32], typename Elem<OUT>::T *c, int left, int nrow,
-                                              const StoreArgs &e) {
-    const int lane = threadIdx.x & 31;
-    const bool f_ok = left > 0;
-    if constexpr (OUT != kDtF32) {
-        if (e.pairs) {
-            // Lanes 2p and 2p + 1 trade values so that each stores 32-bit words
-            // (columns 2p, 2p + 1) of every other row: two rows per instruction.
-            const int odd = lane & 1;
-            const int pair_left = left + odd;  // columns from 2p on
-            typename Elem<OUT>::T *cw = c - odd + odd * e.ldc;  // column 2p, row `odd`
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
-                const float lo = odd ? got : v[2 * i], hi = odd ? v[2 * i + 1] : got;
-                if (2 * i + odd < nrow) {
-                    if (pair_left > 1)
-                        *reinterpret_cast<uint32_t *>(cw) = pack2_out<OUT>(lo, hi);
-                    else if (pair_left == 1)
-                        *cw = Elem<OUT>::cvt(lo);
-                }
-                cw += 2 * e.ldc;
-            }
-            return;
-        }
-    }
+                                              long long ldc) {
+    if (left <= 0) return;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-        if (f_ok && j < nrow) *c = Elem<OUT>::cvt(v[j]);
-        c += e.ldc;
+        if (j < nrow) *c = Elem<OUT>::cvt(v[j]);
+        c += ldc;
     }
 }
 

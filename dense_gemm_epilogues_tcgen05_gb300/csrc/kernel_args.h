@@ -169,13 +169,12 @@ struct GtcArgs {
     const float *bias, *row_scale;  // G x F, T; NULL when absent
     float alpha, beta;
     int epi;
-    int pairs;                      // 16-bit C: base and pitch allow 32-bit stores of two columns
     uint32_t a_mn;                  // forward: the weights are contiguous along F
     int a_whole, b_whole;           // see launch_grouped_tc
     const float *col_scale;         // integer product: G x F, NULL: 1
     int most;                       // integer product: widest row tile (a multiple of 64)
     int stages;                     // set by the launcher
-    int c_tma;                      // C can be written by TMA (launch_grouped_tc's c is valid)
+    int c_tma;                      // C can be written by TMA (the map of C is valid)
     unsigned int *status;
 };
 
@@ -193,9 +192,10 @@ struct GtcMaps {
 cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const GtcMaps &maps, const GtcArgs &args, int clusters,
                               cudaStream_t stream);
 //   8-bit integer products on the tensor cores, `clusters` SM pairs.  tw = weight codes (K, F, G) in boxes of
-//   128 x 128 bytes, tx32 / tx16 = row codes (K, T) in boxes of 128 x 32 and 128 x 16; 128-byte swizzle.
+//   128 x 128 bytes, tx32 / tx16 = row codes (K, T) in boxes of 128 x 32 and 128 x 16; 128-byte swizzle; tc = C
+//   as launch_grouped_tc's c.
 cudaError_t launch_i8_tc(int out, const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
-                         const GtcArgs &args, int clusters, cudaStream_t stream);
+                         const CUtensorMap &tc, const GtcArgs &args, int clusters, cudaStream_t stream);
 //   8-bit integer products for few rows, tiles of 8 nt rows (nt 1, 2 or 4).  A stage is i8_gemv_boxes(nt) boxes
 //   of 128 k; the maps w and x see the codes as (128, rows, K / 128, G) and load a stage at once, w_tail and
 //   x_tail as (K, rows, G) for the stage in which K ends inside a box.  Box rows: i8_gemv_w_rows(nt), 8 nt.
