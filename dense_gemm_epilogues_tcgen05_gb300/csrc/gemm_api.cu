@@ -1421,11 +1421,31 @@ static int i8_most_rows(int64_t G, int64_t M, int64_t N, int pairs) {
 // eights keep up with HBM whatever the size (16384^2 codes on GB300: 46 to 49 us up to 8 rows, 58 to 16, the
 // pair kernel 60); four are bound by their MMAs (32 rows: 86 us), but with few tiles the pair kernel leaves
 // most SMs idle (32 rows of 4096^2: 15 us against 19), so they run where its tiles would not fill the SM pairs.
-static int i8_few_rows(int64_t G, int64_t M, int64_t N) {
+static int few_rows(int64_t G, int64_t M, int64_t N) {
     if (M <= 8 || M <= 2 * G) return 1;
     if (M <= 16 || M <= 4 * G) return 2;
     const int64_t row_tiles = G == 1 ? (M + 31) / 32 : M / 32 + std::min(G, M);
     return row_tiles * ((N + 255) / 256) <= 50 ? 4 : 0;
+}
+
+static gemm_status_t few_rows_launch(const GroupedArgs &args, int ab, int cd, int nt, DeviceState *dev,
+                                     cudaStream_t s) {
+    GvMaps m;
+    gemm_status_t st;
+    const uint32_t wr = static_cast<uint32_t>(few_rows_w_rows(nt)), xr = 8u * nt;
+    if ((st = encode_3d(&m.w_tail, ab, args.B, args.K, args.N, args.sbn, args.G, args.sbg, wr)) != GEMM_OK) return st;
+    if ((st = encode_3d(&m.x_tail, ab, args.A, args.K, args.M, args.sam, 1, 0, xr)) != GEMM_OK) return st;
+    m.w = m.w_tail;
+    m.x = m.x_tail;
+    if (args.K >= (ab == kDtI8 ? 128 : 64)) {
+        const uint32_t boxes = static_cast<uint32_t>(few_rows_boxes(nt));
+        if ((st = encode_blocks(&m.w, ab, args.B, args.K, args.N, args.sbn, args.G, args.sbg, wr, boxes)) != GEMM_OK)
+            return st;
+        if ((st = encode_blocks(&m.x, ab, args.A, args.K, args.M, args.sam, 1, 0, xr, boxes)) != GEMM_OK) return st;
+    }
+    gemm_launch_info_t info = {};
+    info.path = GEMM_PATH_SIMT;
+    return record(launch_few_rows(ab, cd, nt, m, args, dev->num_sms, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
 }
 
 // The product behind gemm_grouped, gemm_i8 and gemm_i8_grouped (ab: a gemm_dtype_t or kDtI8), arguments checked.
@@ -1436,6 +1456,10 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
         const bool n_major = !k_major && tma_ok(args.B, args.K, args.sbn, args.sbk, 2);
         if (tma_ok(args.A, args.M, args.sak, args.sam, 2) && (k_major || n_major) &&
             group_stride_ok(args.G, args.sbg, 2)) {
+            // With tiles for all SM pairs the pair kernel streams weights as fast (6.4 TB/s) whatever the rows.
+            const int64_t tiles = (args.M / 256 + std::min(args.G, args.M)) * ((args.N + 255) / 256);
+            const int nt = k_major && tiles < dev->num_sms / 2 ? few_rows(args.G, args.M, args.N) : 0;
+            if (nt != 0) return few_rows_launch(args, ab, cd, nt, dev, s);
             GtcMaps m = {};
             gemm_status_t st;
             const bool whole = n_major && args.N % 64 == 0;
@@ -1466,27 +1490,7 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
     }
     if (args.K > 0 && ab == kDtI8 && tma_ok(args.A, args.M, 1, args.sam, 1) && tma_ok(args.B, args.N, 1, args.sbn, 1) &&
         group_stride_ok(args.G, args.sbg, 1)) {
-        if (const int nt = i8_few_rows(args.G, args.M, args.N)) {
-            GvMaps m;
-            gemm_status_t st;
-            const uint32_t wr = static_cast<uint32_t>(i8_gemv_w_rows(nt)), xr = 8u * nt;
-            if ((st = encode_3d(&m.w_tail, kDtI8, args.B, args.K, args.N, args.sbn, args.G, args.sbg, wr)) != GEMM_OK)
-                return st;
-            if ((st = encode_3d(&m.x_tail, kDtI8, args.A, args.K, args.M, args.sam, 1, 0, xr)) != GEMM_OK) return st;
-            m.w = m.w_tail;
-            m.x = m.x_tail;
-            if (args.K >= 128) {
-                const uint32_t boxes = static_cast<uint32_t>(i8_gemv_boxes(nt));
-                if ((st = encode_blocks(&m.w, kDtI8, args.B, args.K, args.N, args.sbn, args.G, args.sbg, wr, boxes)) !=
-                    GEMM_OK)
-                    return st;
-                if ((st = encode_blocks(&m.x, kDtI8, args.A, args.K, args.M, args.sam, 1, 0, xr, boxes)) != GEMM_OK)
-                    return st;
-            }
-            info.path = GEMM_PATH_SIMT;
-            return record(launch_i8_gemv(cd, nt, m, args, dev->num_sms, s) == cudaSuccess ? GEMM_OK
-                                                                                               : GEMM_ERR_CUDA, info);
-        }
+        if (const int nt = few_rows(args.G, args.M, args.N)) return few_rows_launch(args, ab, cd, nt, dev, s);
         CUtensorMap tw, tx32, tx16;
         gemm_status_t st;
         if ((st = encode_3d(&tw, kDtI8, args.B, args.K, args.N, args.sbn, args.G, args.sbg, 128)) != GEMM_OK) return st;

@@ -1,26 +1,30 @@
-// gemm_i8_gemv.cu -- 8-bit integer products for few rows (decoding): the
-// weights stream once through shared memory and everything else hides behind
-// that.
+// gemm_few_rows.cu -- products for few rows (decoding), 16-bit values or 8-bit
+// integers, dense or grouped: the weights stream once through shared memory and
+// everything else hides behind that.
 //
 // One persistent block per SM walks tiles of 16 RG rows of W (output channels)
 // by 8 NT rows of X of one group.  A producer thread keeps a ring of about
-// 200 KB of TMA loads in flight across tiles -- a stage is KS boxes of 128 k of
-// the W rows and of the X rows, one load each -- and warp (i, j) multiplies W row group i,
-// box j; the KS partial sums of an output meet in shared memory at the end of a
-// tile.  The integer sum is exact, so the result does not depend on the split.
+// 200 KB of TMA loads in flight across tiles -- a stage is KS boxes of 128 bytes
+// of k of the W rows and of the X rows, one load each -- and in each of two teams,
+// which take every other stage, warp (i, j) multiplies W row group i, box j; the
+// partial sums of an output meet in shared memory at the end of a tile, in a
+// fixed order.
 //
-// Up to four rows: dot products of four codes (dp4a).  More: mma.sync m16n8k16 on
-// the codes expanded to binary16, fp32 sums moved into integers every 1024 k as in
-// gemm_i8_tc.cu (mma.sync's own 8-bit integer kind takes about 20 clocks per SM
-// for 16 x 8 x 32 on GB300, as long as HBM takes to bring its 512 codes of W).
+// 16-bit values: mma.sync m16n8k16 with fp32 sums.  8-bit integers, up to four
+// rows: dot products of four codes (dp4a); up to eight: mma.sync m16n8k32 on the
+// codes; more: m16n8k16 on the codes expanded to binary16, fp32 sums moved into
+// integers every 1024 k as in gemm_i8_tc.cu (the integer kind takes about 20
+// clocks per SM for 16 x 8 x 32 on GB300, as long as HBM takes to bring its 512
+// codes of W, so it does for eight rows and not for sixteen).  Integer sums are
+// exact, so those results do not depend on the path.
 //
 // The sum over k does not care which k an MMA's slot holds as long as both
 // operands agree, so lane (g, t) = (lane / 4, lane % 4) reads whole 16-byte units
-// 2t and 2t + 1 of rows g and g + 8 of W and of rows g of X, and feeds each word
-// to one MMA.  Unit u of row r sits at u ^ (r % 8) (128-byte swizzle), which puts
-// the eight units that a quarter-warp reads into different banks.  Rows and k
-// outside the matrices arrive as zeros; rows of X that belong to the next group
-// are other columns of the MMA and are not stored.
+// 2t and 2t + 1 of rows g and g + 8 of W and of rows g of X, and feeds their words
+// to the MMAs in order.  Unit u of row r sits at u ^ (r % 8) (128-byte swizzle),
+// which puts the eight units that a quarter-warp reads into different banks.
+// Rows and k outside the matrices arrive as zeros; rows of X that belong to the
+// next group are other columns of the MMA and are not stored.
 //
 // Bound: HBM, by the weights' bytes.
 #include "grouped.cuh"
@@ -57,12 +61,20 @@ __device__ __forceinline__ void mma_s8(int (&d)[4], uint32_t a0, uint32_t a1, ui
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                        uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+template <int AB>
+__device__ __forceinline__ void mma_16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                       uint32_t b1) {
+    if constexpr (AB == kDtF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+            "{%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ int dot16(const uint4 &a, const uint4 &b, int c) {
@@ -86,20 +98,22 @@ __device__ __forceinline__ GvTile gv_tile(const GroupTable &t, long long tile, i
     return o;
 }
 
-template <int OUT, int NT>
+template <int AB, int OUT, int NT>
 __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
-    i8_gemv_kernel(const __grid_constant__ GvMaps maps, const __grid_constant__ GroupedArgs a) {
+    few_rows_kernel(const __grid_constant__ GvMaps maps, const __grid_constant__ GroupedArgs a) {
     using Cfg = GvConfig<NT>;
     using OutT = typename Elem<OUT>::T;
+    using SumT = typename SimtAcc<AB>::T;  // 32-bit integers or fp32
     constexpr int STAGES = Cfg::STAGES, KS = Cfg::KS, X_ROWS = Cfg::X_ROWS;
+    constexpr int BOX_K = AB == kDtI8 ? 128 : 64;  // elements in 128 bytes
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + STAGES * Cfg::STAGE_BYTES);
     uint64_t *empty = full + STAGES;
     volatile int *abort_flag = reinterpret_cast<volatile int *>(empty + STAGES);
-    int *part = reinterpret_cast<int *>(reinterpret_cast<unsigned char *>(full) + Cfg::BAR_BYTES);
-    int *table_mem = part + Cfg::PART_INTS;
+    SumT *part = reinterpret_cast<SumT *>(reinterpret_cast<unsigned char *>(full) + Cfg::BAR_BYTES);
+    int *table_mem = reinterpret_cast<int *>(part + Cfg::PART_INTS);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
@@ -118,7 +132,7 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
         group_table_build(table_mem, a.offsets, a.G, a.M, threadIdx.x, Cfg::THREADS, RowTilesOf{X_ROWS});
     const int tiles_n = (a.N + Cfg::W_ROWS - 1) / Cfg::W_ROWS;
     const long long tiles = static_cast<long long>(t.first[a.G]) * tiles_n;
-    const int turns = (a.K + 128 * KS - 1) / (128 * KS);  // stages per tile
+    const int turns = (a.K + BOX_K * KS - 1) / (BOX_K * KS);  // stages per tile
 
     if (warp == Cfg::WARPS) {
         if (lane == 0) {
@@ -137,13 +151,13 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
                     armed |= 1u << stage;
                     armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
                     unsigned char *st = smem + stage * Cfg::STAGE_BYTES;
-                    if (a.K % 128 == 0 || (i + 1) * KS * 128 <= a.K) {
-                        // whole boxes of 128 k, those past K as zeros
+                    if (a.K % BOX_K == 0 || (i + 1) * KS * BOX_K <= a.K) {
+                        // whole boxes, those past K as zeros
                         tma_load_4d_hint(st, &maps.w, &full[stage], 0, o.n0, i * KS, o.g, once);
                         tma_load_4d_hint(st + Cfg::X_OFF, &maps.x, &full[stage], 0, o.r0, i * KS, 0, keep);
                     } else {
                         for (int j = 0; j < KS; ++j) {
-                            const int k = (i * KS + j) * 128;
+                            const int k = (i * KS + j) * BOX_K;
                             tma_load_3d_hint(st + j * Cfg::W_BOX, &maps.w_tail, &full[stage], k, o.n0, o.g, once);
                             tma_load_3d_hint(st + Cfg::X_OFF + j * Cfg::X_BOX, &maps.x_tail, &full[stage], k, o.r0, 0,
                                              keep);
@@ -192,7 +206,29 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
             }
             return true;
         };
-        if (NT == 1 && o.nr <= kGvDotRows) {
+        if constexpr (AB != kDtI8) {
+            float d[NT][4] = {};
+            for (int i = first; i < turns; i += Cfg::TEAMS) {
+                const bool go = turn([&](const uint4 (&p)[2], const uint4 (&q)[2], const unsigned char *x) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const uint4 v = *reinterpret_cast<const uint4 *>(x + (n * 8 + g8) * 128 +
+                                                                             (((2 * t4 + u) ^ g8) << 4));
+                            mma_16<AB>(d[n], p[u].x, q[u].x, p[u].y, q[u].y, v.x, v.y);
+                            mma_16<AB>(d[n], p[u].z, q[u].z, p[u].w, q[u].w, v.z, v.w);
+                        }
+                });
+                if (!go) break;
+            }
+            // rows of W g8, g8 + 8; rows of X 2 t4, 2 t4 + 1 of each eight
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    part[(warp * X_ROWS + n * 8 + 2 * t4 + (i & 1)) * 16 + g8 + (i >> 1) * 8] = d[n][i];
+        } else if (NT == 1 && o.nr <= kGvDotRows) {
             int d[kGvDotRows][2] = {};
             for (int i = first; i < turns; i += Cfg::TEAMS) {
                 const bool go = turn([&](const uint4 (&p)[2], const uint4 (&q)[2], const unsigned char *x) {
@@ -259,7 +295,7 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
                             for (int j = 0; j < 4; ++j) {
                                 uint32_t lo, hi;
                                 expand4(vw[j], lo, hi);
-                                mma_f16(d[n], pl[j], ql[j], ph[j], qh[j], lo, hi);
+                                mma_16<kDtF16>(d[n], pl[j], ql[j], ph[j], qh[j], lo, hi);
                             }
                         }
                     }
@@ -286,7 +322,7 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
         for (int i = threadIdx.x; ok && i < Cfg::W_ROWS * X_ROWS; i += 32 * Cfg::WARPS) {
             const int r = i / Cfg::W_ROWS, in = i % Cfg::W_ROWS, n = o.n0 + in;
             if (r >= o.nr || n >= a.N) continue;
-            int sum = 0;
+            SumT sum = 0;
 #pragma unroll
             for (int j = 0; j < Cfg::TEAMS * KS; ++j)
                 sum += part[((j / KS * Cfg::TEAM + (in >> 4) * KS + j % KS) * X_ROWS + r) * 16 + (in & 15)];
@@ -305,10 +341,10 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
     }
 }
 
-template <int OUT, int NT>
-cudaError_t launch_gemv_cfg(const GvMaps &maps, const GroupedArgs &a, int sms, cudaStream_t s) {
+template <int AB, int OUT, int NT>
+cudaError_t launch_few_cfg(const GvMaps &maps, const GroupedArgs &a, int sms, cudaStream_t s) {
     using Cfg = GvConfig<NT>;
-    auto kern = i8_gemv_kernel<OUT, NT>;
+    auto kern = few_rows_kernel<AB, OUT, NT>;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM);
     if (err != cudaSuccess) return err;
     const long long row_tiles = a.M / Cfg::X_ROWS + (a.M < a.G ? a.M : a.G);
@@ -326,24 +362,32 @@ cudaError_t launch_gemv_cfg(const GvMaps &maps, const GroupedArgs &a, int sms, c
     return cudaLaunchKernelEx(&cfg, kern, maps, a);
 }
 
-template <int OUT>
-cudaError_t launch_gemv_out(int nt, const GvMaps &maps, const GroupedArgs &a, int sms, cudaStream_t s) {
-    if (nt == 1) return launch_gemv_cfg<OUT, 1>(maps, a, sms, s);
-    if (nt == 2) return launch_gemv_cfg<OUT, 2>(maps, a, sms, s);
-    if (nt == 4) return launch_gemv_cfg<OUT, 4>(maps, a, sms, s);
+template <int AB, int OUT>
+cudaError_t launch_few_nt(int nt, const GvMaps &maps, const GroupedArgs &a, int sms, cudaStream_t s) {
+    if (nt == 1) return launch_few_cfg<AB, OUT, 1>(maps, a, sms, s);
+    if (nt == 2) return launch_few_cfg<AB, OUT, 2>(maps, a, sms, s);
+    if (nt == 4) return launch_few_cfg<AB, OUT, 4>(maps, a, sms, s);
+    return cudaErrorInvalidValue;
+}
+
+template <int AB>
+cudaError_t launch_few_out(int out, int nt, const GvMaps &maps, const GroupedArgs &a, int sms, cudaStream_t s) {
+    if (out == kDtF32) return launch_few_nt<AB, kDtF32>(nt, maps, a, sms, s);
+    if (out == kDtF16) return launch_few_nt<AB, kDtF16>(nt, maps, a, sms, s);
+    if (out == kDtBF16) return launch_few_nt<AB, kDtBF16>(nt, maps, a, sms, s);
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-int i8_gemv_w_rows(int nt) { return nt <= 2 ? GvConfig<1>::W_ROWS : GvConfig<4>::W_ROWS; }
-int i8_gemv_boxes(int nt) { return nt <= 2 ? GvConfig<1>::KS : GvConfig<4>::KS; }
+int few_rows_w_rows(int nt) { return nt <= 2 ? GvConfig<1>::W_ROWS : GvConfig<4>::W_ROWS; }
+int few_rows_boxes(int nt) { return nt <= 2 ? GvConfig<1>::KS : GvConfig<4>::KS; }
 
-cudaError_t launch_i8_gemv(int out, int nt, const GvMaps &maps, const GroupedArgs &a,
-                           int sms, cudaStream_t s) {
-    if (out == kDtF32) return launch_gemv_out<kDtF32>(nt, maps, a, sms, s);
-    if (out == kDtF16) return launch_gemv_out<kDtF16>(nt, maps, a, sms, s);
-    if (out == kDtBF16) return launch_gemv_out<kDtBF16>(nt, maps, a, sms, s);
+cudaError_t launch_few_rows(int ab, int out, int nt, const GvMaps &maps, const GroupedArgs &a, int sms,
+                            cudaStream_t s) {
+    if (ab == kDtI8) return launch_few_out<kDtI8>(out, nt, maps, a, sms, s);
+    if (ab == kDtF16) return launch_few_out<kDtF16>(out, nt, maps, a, sms, s);
+    if (ab == kDtBF16) return launch_few_out<kDtBF16>(out, nt, maps, a, sms, s);
     return cudaErrorInvalidValue;
 }
 

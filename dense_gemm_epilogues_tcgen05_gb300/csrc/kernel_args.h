@@ -196,16 +196,17 @@ cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const GtcMaps &maps, 
 //   as launch_grouped_tc's c.
 cudaError_t launch_i8_tc(int out, const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
                          const CUtensorMap &tc, const GtcArgs &args, int clusters, cudaStream_t stream);
-//   8-bit integer products for few rows, tiles of 8 nt rows (nt 1, 2 or 4).  A stage is i8_gemv_boxes(nt) boxes
-//   of 128 k; the maps w and x see the codes as (128, rows, K / 128, G) and load a stage at once, w_tail and
-//   x_tail as (K, rows, G) for the stage in which K ends inside a box.  Box rows: i8_gemv_w_rows(nt), 8 nt.
+//   products for few rows (ab: F16, BF16 or kDtI8; weights contiguous along K), tiles of 8 nt rows (nt 1, 2 or 4).
+//   A stage is few_rows_boxes(nt) boxes of 128 bytes of k; the maps w and x see the operands as (128 bytes, rows,
+//   whole boxes along K, G) and load a stage at once, w_tail and x_tail as (K, rows, G) for the stage in which K
+//   ends inside a box.  Box rows: few_rows_w_rows(nt), 8 nt.
 struct GvMaps {
     CUtensorMap w, x, w_tail, x_tail;
 };
-cudaError_t launch_i8_gemv(int out, int nt, const GvMaps &maps, const GroupedArgs &args, int sms,
-                           cudaStream_t stream);
-int i8_gemv_w_rows(int nt);
-int i8_gemv_boxes(int nt);
+cudaError_t launch_few_rows(int ab, int out, int nt, const GvMaps &maps, const GroupedArgs &args, int sms,
+                            cudaStream_t stream);
+int few_rows_w_rows(int nt);
+int few_rows_boxes(int nt);
 constexpr int kI8TileRows = 192;    // its widest row tile
 //   grouped products on the CUDA cores, any strides (ab: F32, F16, BF16 or kDtI8), `grid` blocks:
 cudaError_t launch_grouped_simt(int ab, int out, const GroupedArgs &args, int grid, cudaStream_t stream);

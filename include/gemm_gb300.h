@@ -75,7 +75,9 @@ typedef enum {
     GEMM_ERR_TIMEOUT = 6        /* a device-side wait gave up (reported by gemm_device_status) */
 } gemm_status_t;
 
-/* Which kernel family a call runs on (see gemm_query_path).  fp32 inputs report
+/* Which kernel family a call runs on (see gemm_query_path).  The grouped and 8-bit products report TCGEN05 for
+ * their tcgen05 kernels, EPILOGUE_ONLY without a product, and SIMT for every other kernel (few rows: mma.sync and
+ * dot products; any strides: multiply-adds).  fp32 inputs report
  * GEMM_PATH_SIMT, the path without a workspace; given a workspace of
  * gemm_workspace_size() bytes they run as 3xTF32 on the tensor cores. */
 typedef enum {
@@ -653,8 +655,9 @@ gemm_status_t gemm_device_status(gemm_stream_t stream);
  *                  Not read when K == 0 or alpha == 0 (the product term is 0).
  * F16 / BF16 inputs run on the tensor cores when A is contiguous along k, B
  * along k or j, both bases are 16-byte aligned and the other strides multiples
- * of 16 bytes; anything else on the CUDA cores.  The activations take the
- * forms of fp32 outputs whatever c_dtype.  C must not overlap the inputs.
+ * of 16 bytes; anything else on the CUDA cores.  Outputs are stored fastest
+ * with a 16-byte aligned C, pitch and N * element size.  The activations take
+ * the forms of fp32 outputs whatever c_dtype.  C must not overlap the inputs.
  * Asynchronous on `stream`; errors as gemm(), GEMM_ERR_MISALIGNED for an
  * offsets array that is not 4-byte aligned.
  */

@@ -126,6 +126,32 @@ def test_integer_exact(cuda_lib, split, N, K, trans, ab):
     np.testing.assert_array_equal(got, want)
 
 
+@pytest.mark.parametrize("split", ["ragged", "tiles", "many"])
+@pytest.mark.parametrize("N,K", [(1500, 72), (1513, 840)], ids=str)
+@pytest.mark.parametrize("trans", [False, True], ids=["nk", "kn"])
+@pytest.mark.parametrize("out", [F32, BF16], ids=NAMES.get)
+def test_integer_exact_on_the_pair_kernel(cuda_lib, split, N, K, trans, out):
+    """Enough column tiles that no call takes the kernel for few rows; bf16 outputs are the rounded sums."""
+    got, want, _, path = run_grouped(cuda_lib, SPLITS[split], N, K, BF16, out, integer=True, trans=trans, seed=N + K,
+                                     first=3, after=5, ldc_pad=4 - N % 4)
+    assert path == cuda_lib.PATH_TCGEN05
+    if out == BF16:
+        want = torch.from_numpy(want).bfloat16().double().numpy()
+    np.testing.assert_array_equal(got, want)
+
+
+@pytest.mark.parametrize("rows", [1, 7, 8, 9, 16, 17, 33, 64])
+@pytest.mark.parametrize("N,K", [(1, 64), (33, 8), (200, 1000), (517, 4160)], ids=str)
+@pytest.mark.parametrize("ab", [F16, BF16], ids=NAMES.get)
+def test_few_rows(cuda_lib, rows, N, K, ab):
+    """One group, and the rows split unevenly over three."""
+    for sizes in ([rows], [rows // 2, 0, rows - rows // 2]):
+        got, want, _, _ = run_grouped(cuda_lib, sizes, N, K, ab, F32, integer=True, seed=rows + N, first=1, after=2)
+        np.testing.assert_array_equal(got, want)
+    got, want, D, _ = run_grouped(cuda_lib, [rows], N, K, ab, ab, epi=4, alpha=0.5, beta=0.25, row_scale=True, seed=K)
+    check(got, want, D, ab)
+
+
 @pytest.mark.parametrize("out", [F32, F16, BF16], ids=NAMES.get)
 @pytest.mark.parametrize("epi", range(6))
 @pytest.mark.parametrize("ab", [F16, BF16], ids=NAMES.get)
