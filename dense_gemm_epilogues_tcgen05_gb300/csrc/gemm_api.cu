@@ -1362,28 +1362,6 @@ static bool group_stride_ok(int64_t G, int64_t stride, int es) {
     return G == 1 || (stride > 0 && stride * es % 16 == 0 && stride * es < (int64_t(1) << 40));
 }
 
-// Map of C for the grouped kernels' stores, (columns, rows, groups); false (and the kernels store from registers)
-// where its base or pitches rule out TMA, or its rows do not end on 16 bytes (a TMA store clips there, and would
-// write into the padding).
-static bool encode_grouped_c(CUtensorMap *map, int cd, void *C, int64_t cols, int64_t rows, int64_t ldc,
-                             int64_t groups, int64_t group_stride) {
-    const int es = elem_bytes(cd);
-    const int64_t limit = int64_t(1) << 40;
-    if ((reinterpret_cast<uintptr_t>(C) & 15u) != 0 || cols * es % 16 != 0) return false;
-    if (rows > 1 && (ldc * es % 16 != 0 || ldc * es >= limit)) return false;
-    if (groups > 1 && (group_stride * es % 16 != 0 || group_stride * es >= limit)) return false;
-    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
-                          static_cast<cuuint64_t>(groups)};
-    cuuint64_t strides[2] = {rows == 1 ? 16 : static_cast<cuuint64_t>(ldc) * es,
-                             groups == 1 ? 16 : static_cast<cuuint64_t>(group_stride) * es};
-    cuuint32_t box[3] = {32u, cd == GEMM_F32 ? 16u : 32u, 1u};
-    cuuint32_t estr[3] = {1, 1, 1};
-    return driver_fns().encode(map, cd == GEMM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : tma_dtype(cd), 3, C, dims, strides,
-                               box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                               cd == GEMM_F32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // Record of a pair launch over at most `tiles` tiles; returns its clusters.
 static int pair_clusters(const DeviceState *dev, int64_t tiles, gemm_launch_info_t *info) {
     const int clusters = static_cast<int>(std::min<int64_t>(tiles, dev->num_sms / 2));
@@ -1477,7 +1455,6 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
             t.C = args.C; t.ldc = args.ldc;
             t.bias = args.bias; t.row_scale = args.row_scale;
             t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
-            t.c_tma = encode_grouped_c(&m.c, cd, args.C, args.N, args.M, args.ldc, 1, 0);
             t.a_whole = whole;
             t.a_mn = n_major ? 1u : 0u;
             t.status = args.status;
@@ -1503,14 +1480,12 @@ static gemm_status_t grouped_launch(const GroupedArgs &args, int ab, int cd, Dev
         t.C = args.C; t.ldc = args.ldc;
         t.bias = args.bias; t.row_scale = args.row_scale; t.col_scale = args.col_scale;
         t.alpha = args.alpha; t.beta = args.beta; t.epi = args.epilogue;
-        CUtensorMap tc = tw;
-        t.c_tma = encode_grouped_c(&tc, cd, args.C, args.N, args.M, args.ldc, 1, 0);
         t.most = i8_most_rows(args.G, args.M, args.N, dev->num_sms / 2);
         t.status = args.status;
         const int64_t row_tiles = args.M / t.most + std::min(args.G, args.M);
         const int clusters = pair_clusters(dev, row_tiles * t.tiles_f, &info);
         info.bn = t.most;
-        return record(launch_i8_tc(cd, tw, tx32, tx16, tc, t, clusters, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
+        return record(launch_i8_tc(cd, tw, tx32, tx16, t, clusters, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
     }
     info.path = args.K == 0 ? GEMM_PATH_EPILOGUE_ONLY : GEMM_PATH_SIMT;
     const int grid = simt_grid(dev, (args.M + 63) / 64 + args.G, (args.N + 63) / 64);
@@ -1629,7 +1604,6 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
         t.offsets = offsets;
         t.C = C; t.scg = c_stride_g; t.ldc = ldc;
         t.alpha = alpha; t.beta = beta; t.epi = kEpiNone;
-        t.c_tma = encode_grouped_c(&m.c, c_dtype, C, N, M, ldc, G, c_stride_g);
         t.a_whole = a_whole;
         t.b_whole = b_whole;
         t.status = dev->status;

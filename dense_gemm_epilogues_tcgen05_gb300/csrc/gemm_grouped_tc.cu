@@ -18,8 +18,8 @@
 //
 //   warp 0       TMA producer: its own 128 rows of the MMA's first operand and
 //                its own half of the columns' operand, 64 deep, into a ring of
-//                six (five beside a large group table) 32 KB stages, counted on the
-//                leader's barrier;
+//                seven (six beside a large group table) 32 KB stages, counted on
+//                the leader's barrier;
 //   warp 1       MMA issuer (leader CTA only), two 256-column accumulators;
 //   warp 2       gradient only: the last k-block of a group reaches into the
 //                next group's rows (or past T).  They are zeroed in shared
@@ -41,20 +41,20 @@ namespace gb300 {
 namespace {
 
 struct GtcConfig {
-    static constexpr int BK = 64, MAX_STAGES = 6;
+    static constexpr int BK = 64, MAX_STAGES = 7;
     static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int EPI_WARP0 = 3, EPI_WARPS = 8;
     static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
     static constexpr int TMEM_COLS = 512, ACC_STRIDE = 256;
-    static constexpr int BAR_BYTES = 256, BOX_BYTES = EPI_WARPS * 2 * kBoxBytes, SMEM_MAX = 232448;
+    static constexpr int BAR_BYTES = 320, SMEM_MAX = 232448;
     // fp32 outputs: k-blocks summed in the tensor core's accumulator before the sum moves to registers
     static constexpr int SEG = 8;
     static_assert((4 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
-    // after up to 1023 bytes of alignment: [stages][boxes][barriers][group table]
-    static int fixed_bytes(int G) { return 1024 + BOX_BYTES + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16; }
+    // after up to 1023 bytes of alignment: [stages][barriers][group table]
+    static int fixed_bytes(int G) { return 1024 + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16; }
 };
-static_assert(1024 + GtcConfig::BOX_BYTES + GtcConfig::BAR_BYTES + group_table_bytes(kMaxGroups) +
-                      5 * GtcConfig::STAGE_BYTES <= GtcConfig::SMEM_MAX, "five stages always fit");
+static_assert(1024 + GtcConfig::BAR_BYTES + group_table_bytes(kMaxGroups) + 6 * GtcConfig::STAGE_BYTES <=
+                  GtcConfig::SMEM_MAX, "six stages always fit");
 
 // Walks this cluster's tiles.
 template <bool WG>
@@ -100,8 +100,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char *boxes = smem + stages * Cfg::STAGE_BYTES;
-    uint64_t *full = reinterpret_cast<uint64_t *>(boxes + Cfg::BOX_BYTES);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + stages * Cfg::STAGE_BYTES);
     uint64_t *empty = full + Cfg::MAX_STAGES;
     uint64_t *landed = empty + Cfg::MAX_STAGES;   // gradient, last k-blocks: this CTA's bytes have landed
     uint64_t *fixed = landed + Cfg::MAX_STAGES;   // (leader's) both CTAs have cleared the foreign rows
@@ -131,7 +130,6 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         fence_barrier_init();
         tma_prefetch_desc(&maps.a);
         tma_prefetch_desc(&maps.b[WG ? 2 : 7]);
-        if (args.c_tma) tma_prefetch_desc(&maps.c);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
@@ -332,8 +330,6 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         const int quad = warp & 3;                      // TMEM lanes 32*quad ..
         const int half = (warp - Cfg::EPI_WARP0) >> 2;  // which half of the tile's columns
         const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi};
-        unsigned char *box = boxes + (warp - Cfg::EPI_WARP0) * 2 * kBoxBytes;
-        uint32_t turn = 0;
         int local = 0;
         while (it.next(t)) {
             const int num_kb = (t.nk + BK - 1) / BK;
@@ -349,12 +345,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                 const int row = (c_begin + ch) * 32;
                 OutT *c0 = c + row * args.ldc;
                 chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row, rs != nullptr ? rs + row : nullptr, 1.0f, bias, e);
-                if (args.c_tma && row + 32 <= t.nr) {
-                    if (f - lane < args.F)
-                        box_chunk_t<OUT>(v, &maps.c, box, turn, f - lane, t.r0 + row, WG ? t.g : 0);
-                } else {
-                    store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
-                }
+                store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
             };
             if constexpr (SEGS) {
                 // The tensor core's fp32 sums lose about half a unit in the last place per
@@ -434,7 +425,6 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         }
     }
 
-    if (warp >= Cfg::EPI_WARP0 && lane == 0) bulk_wait<0>();  // stores in flight read this CTA's shared memory
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();  // no CTA leaves while its peer may still signal into it

@@ -61,9 +61,8 @@ struct I8Config {
     static_assert(ISSUE_REGS + SETS * CONV_REGS + 2 * EPI_REGS <= (SETS + 3) * LAUNCH_REGS, "the trade adds up");
     static constexpr int BAR_BYTES = 512, SMEM_MAX = 232448;
     static_assert((2 * MAX_STAGES + 2 * MAX_SLOTS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
-    // after up to 1023 bytes of alignment: [stages][slots][boxes][barriers][group table]
-    static constexpr int OUT_BYTES = 8 * 2 * kBoxBytes;
-    static int fixed_bytes(int G) { return 1024 + OUT_BYTES + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16; }
+    // after up to 1023 bytes of alignment: [stages][slots][barriers][group table]
+    static int fixed_bytes(int G) { return 1024 + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16; }
 };
 
 // What follows from the widest row tile `most` and the group count: most / 2
@@ -91,8 +90,7 @@ struct I8Shape {
 template <int OUT>
 __global__ void __launch_bounds__(I8Config::THREADS, 1)
     i8_tc_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX32,
-                 const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ CUtensorMap tmC,
-                 const __grid_constant__ GtcArgs args) {
+                 const __grid_constant__ CUtensorMap tmX16, const __grid_constant__ GtcArgs args) {
     using Cfg = I8Config;
     constexpr int CL = 2;
     const I8Shape sh(args.most, args.stages);
@@ -101,7 +99,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char *slot_base = smem + stages * sh.stage_bytes;
-    uint64_t *full = reinterpret_cast<uint64_t *>(slot_base + slots * sh.slot_bytes + Cfg::OUT_BYTES);  // codes landed
+    uint64_t *full = reinterpret_cast<uint64_t *>(slot_base + slots * sh.slot_bytes);  // codes landed
     uint64_t *empty = full + Cfg::MAX_STAGES;   // codes read by both converter sets
     uint64_t *ready = empty + Cfg::MAX_STAGES;  // (leader's) two slots, one stage, expanded in both CTAs
     uint64_t *freed = ready + Cfg::MAX_SLOTS;   // a slot read by the MMA
@@ -134,7 +132,6 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
         tma_prefetch_desc(&tmW);
         tma_prefetch_desc(&tmX32);
         tma_prefetch_desc(&tmX16);
-        if (args.c_tma) tma_prefetch_desc(&tmC);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, Cfg::TMEM_COLS);
@@ -344,9 +341,8 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
         using OutT = typename Elem<OUT>::T;
         const int quad = warp & 3, side = (warp - Cfg::EPI_WARP0) >> 2;
         const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi};
-        unsigned char *box = slot_base + slots * sh.slot_bytes + (warp - Cfg::EPI_WARP0) * 2 * kBoxBytes;
         constexpr int MC = kI8TileRows / 64;  // most 32-column chunks of a warp
-        uint32_t local = 0, turn = 0;
+        uint32_t local = 0;
         bool ok = true;
         for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
             const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
@@ -364,11 +360,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                 OutT *c0 = out + row * args.ldc;
                 chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row,
                                     args.row_scale != nullptr ? args.row_scale + t.r0 + row : nullptr, cs, bias, e);
-                if (args.c_tma && row + 32 <= t.nr) {
-                    if (f - lane < args.F) box_chunk_t<OUT>(v, &tmC, box, turn, f - lane, t.r0 + row, 0);
-                } else {
-                    store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
-                }
+                store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
             };
             auto accumulator = [&](uint32_t &acc) {  // the next one; false when the kernel gives up
                 acc = local & 1;
@@ -439,7 +431,6 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
         }
     }
 
-    if (warp >= Cfg::EPI_WARP0 && lane == 0) bulk_wait<0>();  // stores in flight read this CTA's shared memory
     __syncwarp();
     tc_fence_before();
     cluster_sync_all();  // no CTA leaves while its peer may still signal into it
@@ -451,7 +442,7 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
 
 template <int OUT>
 cudaError_t launch_i8_tc_out(const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
-                             const CUtensorMap &tc, const GtcArgs &a, int clusters, cudaStream_t stream) {
+                             const GtcArgs &a, int clusters, cudaStream_t stream) {
     auto kern = i8_tc_kernel<OUT>;
     cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, I8Config::SMEM_MAX);
@@ -481,16 +472,16 @@ cudaError_t launch_i8_tc_out(const CUtensorMap &tw, const CUtensorMap &tx32, con
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kern, tw, tx32, tx16, tc, args);
+    return cudaLaunchKernelEx(&cfg, kern, tw, tx32, tx16, args);
 }
 
 }  // namespace
 
 cudaError_t launch_i8_tc(int out, const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
-                         const CUtensorMap &tc, const GtcArgs &args, int clusters, cudaStream_t stream) {
-    if (out == kDtF32) return launch_i8_tc_out<kDtF32>(tw, tx32, tx16, tc, args, clusters, stream);
-    if (out == kDtF16) return launch_i8_tc_out<kDtF16>(tw, tx32, tx16, tc, args, clusters, stream);
-    if (out == kDtBF16) return launch_i8_tc_out<kDtBF16>(tw, tx32, tx16, tc, args, clusters, stream);
+                         const GtcArgs &args, int clusters, cudaStream_t stream) {
+    if (out == kDtF32) return launch_i8_tc_out<kDtF32>(tw, tx32, tx16, args, clusters, stream);
+    if (out == kDtF16) return launch_i8_tc_out<kDtF16>(tw, tx32, tx16, args, clusters, stream);
+    if (out == kDtBF16) return launch_i8_tc_out<kDtBF16>(tw, tx32, tx16, args, clusters, stream);
     return cudaErrorInvalidValue;
 }
 

@@ -127,14 +127,13 @@ __device__ __forceinline__ float grouped_value(float acc, float scale, float bet
 // the weight gradient, its contiguous index) are the MMA's rows and lie in
 // tensor-memory lanes, the tokens are its columns -- so that a ragged group
 // costs columns in steps of 32, not rows in steps of 256.  A warp then holds
-// 32 consecutive columns of C in its lanes and 32 rows of C in its registers.
-// Whole blocks of 32 rows go through shared memory as 2 KB boxes that TMA
-// stores; a group's last rows, which must not touch the next group's, and
-// outputs that TMA cannot write are stored from registers, 64 or 128 bytes of a
-// row per instruction.  27270 x 6304 fp16 outputs of a product 320 deep on GB300:
-// boxes 124 us (6 to 7 clocks per box row), registers 150 us; pairing lanes for
-// 32-bit stores 195 us, four warps joining their columns in shared memory for
-// 16-byte stores 153 us (248 where rows are only 4-byte aligned).
+// 32 consecutive columns of C in its lanes and 32 rows of C in its registers,
+// and each store instruction writes 32 columns of a row, 64 or 128 bytes: no
+// staging, any pitch and alignment, and a group's last rows need no other path.
+// (27270 x 6304 fp16 outputs of a product 320 deep on GB300: 106 us; through
+// shared memory as TMA boxes of 32 rows x 64 bytes 113 us, at 6 to 7 clocks per
+// box row; pairing lanes for 32-bit stores 195 us; four warps joining their
+// columns in shared memory for 16-byte stores 153 us.)
 struct StoreArgs {
     long long ldc;
     float alpha, beta;
@@ -182,46 +181,6 @@ __device__ __forceinline__ void store_chunk_t(const float (&v)[32], typename Ele
     for (int j = 0; j < 32; ++j) {
         if (j < nrow) *c = Elem<OUT>::cvt(v[j]);
         c += ldc;
-    }
-}
-
-// All 32 rows of the outputs v through the warp's two 2 KB boxes: 16-bit outputs
-// as one box of 32 rows x 64 bytes, fp32 as two of 16 rows x 128 bytes (each
-// swizzled by its row's width).  Column x and row y of the first element, matrix
-// z; columns outside the tensor are not written.  The stores stay in flight; a
-// box is reused when its last store has read it.  Warp-collective.
-constexpr int kBoxBytes = 2048;
-
-template <int OUT>
-__device__ __forceinline__ void box_chunk_t(const float (&v)[32], const CUtensorMap *tm, unsigned char *boxes,
-                                            uint32_t &turn, int x, int y, int z) {
-    const int lane = threadIdx.x & 31;
-    constexpr int ROWS = OUT == kDtF32 ? 16 : 32;
-#pragma unroll
-    for (int h = 0; h < 32 / ROWS; ++h) {
-        unsigned char *box = boxes + (turn & 1) * kBoxBytes;
-        ++turn;
-        if (lane == 0) bulk_wait_read<1>();
-        __syncwarp();
-        if constexpr (OUT == kDtF32) {
-#pragma unroll
-            for (int r = 0; r < 16; ++r)  // 16-byte unit lane / 4 of row r at unit (lane / 4) ^ (r % 8)
-                *reinterpret_cast<float *>(box + r * 128 + ((lane * 4) ^ ((r & 7) << 4))) = v[16 * h + r];
-        } else {
-            const uint32_t odd = lane & 1u, col = (lane >> 1) * 4u;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float got = __shfl_xor_sync(0xffffffffu, odd ? v[2 * i] : v[2 * i + 1], 1);
-                const uint32_t w = odd ? pack2_out<OUT>(got, v[2 * i + 1]) : pack2_out<OUT>(v[2 * i], got);
-                *reinterpret_cast<uint32_t *>(box + sw64_word((2 * i + odd) * 64u + col)) = w;
-            }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tma_store_3d_hint(tm, box, x, y + h * ROWS, z, l2_policy_evict_first());
-            bulk_commit();
-        }
     }
 }
 

@@ -174,7 +174,6 @@ struct GtcArgs {
     const float *col_scale;         // integer product: G x F, NULL: 1
     int most;                       // integer product: widest row tile (a multiple of 64)
     int stages;                     // set by the launcher
-    int c_tma;                      // C can be written by TMA (the map of C is valid)
     unsigned int *status;
 };
 
@@ -185,17 +184,15 @@ struct GtcArgs {
 //               (64, K, F / 64, G) in 64 x 64 x 2.  b[i] = rows (K, T) in boxes of 64 x 16 (i + 1), i = 0 .. 7.
 //     gradient  a = (F, T) in 64 x 64, or with a_whole (64, T, F / 64) in 64 x 64 x 2.  b[2] = (R, T) in 64 x 64; with
 //               b_whole also b[0], b[1] = (64, T, R / 64) in 64 x 64 x 1 and x 2.
-//   c = C (F, rows, G) when args.c_tma: 16-bit in boxes of 32 x 32, 64-byte swizzle; fp32 in 32 x 16, 128-byte.
 struct GtcMaps {
-    CUtensorMap a, c, b[8];
+    CUtensorMap a, b[8];
 };
 cudaError_t launch_grouped_tc(bool wgrad, int ab, int out, const GtcMaps &maps, const GtcArgs &args, int clusters,
                               cudaStream_t stream);
 //   8-bit integer products on the tensor cores, `clusters` SM pairs.  tw = weight codes (K, F, G) in boxes of
-//   128 x 128 bytes, tx32 / tx16 = row codes (K, T) in boxes of 128 x 32 and 128 x 16; 128-byte swizzle; tc = C
-//   as launch_grouped_tc's c.
+//   128 x 128 bytes, tx32 / tx16 = row codes (K, T) in boxes of 128 x 32 and 128 x 16; 128-byte swizzle.
 cudaError_t launch_i8_tc(int out, const CUtensorMap &tw, const CUtensorMap &tx32, const CUtensorMap &tx16,
-                         const CUtensorMap &tc, const GtcArgs &args, int clusters, cudaStream_t stream);
+                         const GtcArgs &args, int clusters, cudaStream_t stream);
 //   products for few rows (ab: F16, BF16 or kDtI8; weights contiguous along K), tiles of 8 nt rows (nt 1, 2 or 4).
 //   A stage is few_rows_boxes(nt) boxes of 128 bytes of k; the maps w and x see the operands as (128 bytes, rows,
 //   whole boxes along K, G) and load a stage at once, w_tail and x_tail as (K, rows, G) for the stage in which K

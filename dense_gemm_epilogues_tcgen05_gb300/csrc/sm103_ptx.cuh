@@ -180,15 +180,6 @@ __device__ __forceinline__ void tma_store_2d_hint(const CUtensorMap *map, const 
                  : "memory");
 }
 
-// The 3-D form with an L2 eviction policy.
-__device__ __forceinline__ void tma_store_3d_hint(const CUtensorMap *map, const void *smem_src, int32_t x, int32_t y,
-                                                  int32_t z, uint64_t policy) {
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group.L2::cache_hint [%0, {%2, %3, %4}], [%1], %5;" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(smem_u32(smem_src)), "r"(x), "r"(y), "r"(z), "l"(policy)
-                 : "memory");
-}
-
 // 16-byte store to global memory, cached in L2 only, with an L2 eviction policy.
 __device__ __forceinline__ void st_global_cg_v4_hint(float *p, const float4 &v, uint64_t policy) {
     asm volatile("st.global.cg.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "f"(v.x), "f"(v.y),

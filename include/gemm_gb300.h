@@ -655,9 +655,8 @@ gemm_status_t gemm_device_status(gemm_stream_t stream);
  *                  Not read when K == 0 or alpha == 0 (the product term is 0).
  * F16 / BF16 inputs run on the tensor cores when A is contiguous along k, B
  * along k or j, both bases are 16-byte aligned and the other strides multiples
- * of 16 bytes; anything else on the CUDA cores.  Outputs are stored fastest
- * with a 16-byte aligned C, pitch and N * element size.  The activations take
- * the forms of fp32 outputs whatever c_dtype.  C must not overlap the inputs.
+ * of 16 bytes; anything else on the CUDA cores.  The activations take the
+ * forms of fp32 outputs whatever c_dtype.  C must not overlap the inputs.
  * Asynchronous on `stream`; errors as gemm(), GEMM_ERR_MISALIGNED for an
  * offsets array that is not 4-byte aligned.
  */
