@@ -26,7 +26,11 @@
 // Rows and k outside the matrices arrive as zeros; rows of X that belong to the
 // next group are other columns of the MMA and are not stored.
 //
-// Bound: HBM, by the weights' bytes.
+// Bound: HBM, by the weights' bytes.  GB300: one row of 16384 x 16384 codes 46 us
+// (5.9 TB/s), 16 rows 58 us, 64 experts x 64 rows 2048 x 4096 59 us (6.5 TB/s); two
+// experts of 4096 x 4096 fp16, 4 rows, 13 us.  One load per stage and operand instead
+// of four was worth 20 %: the issuing thread was the bound.  32 rows of 8-bit codes:
+// 87 us, by their MMAs.
 #include "grouped.cuh"
 
 namespace gb300 {

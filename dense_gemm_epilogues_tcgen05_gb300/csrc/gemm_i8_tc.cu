@@ -16,7 +16,7 @@
 // 256 rows are the MMA's rows, up to 192 rows of X its columns.  Per CTA:
 //
 //   warp 0        TMA producer: 128 rows of W and half of the tile's rows of X,
-//                 128 k (bytes) deep, into a ring of five 28 KB stages of codes,
+//                 128 k (bytes) deep, into a ring of 28 KB stages of codes (as many as fit),
 //                 on this CTA's own barriers;
 //   warp 1        MMA issuer (leader CTA only);
 //   warps 4-19    converters, four sets of four; a set takes one 64-k half of
@@ -36,10 +36,14 @@
 // for the issuers, 48 for each converter set, 136 for each epilogue set: 496 of
 // the 504 that seven warps of a sub-partition launched with).
 //
-// Bound: at large sizes shared-memory bandwidth -- per 128 k a CTA moves 32 KB
-// of W (codes in, codes out) and 768 bytes per row of X (codes in and out,
-// 16-bit in and out) against the MMA's 8 clocks per row, 1.08 of the
-// 128 B/clk at 192 columns (1.25 at 128) -- and the weights' bytes at small M.
+// Bound and measured (GB300, 8192 x 4096 x 4096 codes, bias and GELU, bf16 out):
+// 210 us, 1.31 PFLOP/s.  A build that took 216 us showed the tensor pipe busy 49 %
+// and the issue slots 53 % of the time.  Shared memory would allow 1.08 of the MMAs'
+// time at 192 columns: per 128 k a CTA moves 32 KB of W and 768 bytes per row of X
+// against the MMA's 8 clocks per row.  On the way: arrives with release at cluster
+// scope 372 us, fences restricted to shared memory 241 us; outputs of one accumulator
+// straight from fp32 228 -> 217 us; outputs stored from registers and one more stage
+// of codes 217 -> 210 us.
 #include <algorithm>
 
 #include "gemm_tcgen05.cuh"
