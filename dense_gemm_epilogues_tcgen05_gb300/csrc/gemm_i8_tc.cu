@@ -37,8 +37,8 @@
 // the 504 that seven warps of a sub-partition launched with).
 //
 // Bound and measured (GB300, 8192 x 4096 x 4096 codes, bias and GELU, bf16 out):
-// 210 us, 1.31 PFLOP/s.  A build that took 216 us showed the tensor pipe busy 49 %
-// and the issue slots 53 % of the time.  Shared memory would allow 1.08 of the MMAs'
+// 210 us, 1.31 PFLOP/s.  The tensor pipe is busy 51 % and the issue slots 52 % of
+// the time.  Shared memory would allow 1.08 of the MMAs'
 // time at 192 columns: per 128 k a CTA moves 32 KB of W and 768 bytes per row of X
 // against the MMA's 8 clocks per row.  On the way: arrives with release at cluster
 // scope 372 us, fences restricted to shared memory 241 us; outputs of one accumulator
