@@ -211,7 +211,11 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
             return true;
         };
         if constexpr (AB != kDtI8) {
-            float d[NT][4] = {};
+            // The MMA cuts off what falls below its fp32 sum's last place, always towards
+            // zero, so every 512 k (8 stages of 64) that sum is added into another, rounded
+            // to nearest, as in gemm_grouped_tc.cu.
+            float sum[NT][4] = {}, d[NT][4] = {};
+            int since = 0;
             for (int i = first; i < turns; i += Cfg::TEAMS) {
                 const bool go = turn([&](const uint4 (&p)[2], const uint4 (&q)[2], const unsigned char *x) {
 #pragma unroll
@@ -225,13 +229,22 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
                         }
                 });
                 if (!go) break;
+                if ((++since & 7) == 0 || i + Cfg::TEAMS >= turns) {
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            sum[n][j] += d[n][j];
+                            d[n][j] = 0.0f;
+                        }
+                }
             }
             // rows of W g8, g8 + 8; rows of X 2 t4, 2 t4 + 1 of each eight
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    part[(warp * X_ROWS + n * 8 + 2 * t4 + (i & 1)) * 16 + g8 + (i >> 1) * 8] = d[n][i];
+                    part[(warp * X_ROWS + n * 8 + 2 * t4 + (i & 1)) * 16 + g8 + (i >> 1) * 8] = sum[n][i];
         } else if (NT == 1 && o.nr <= kGvDotRows) {
             int d[kGvDotRows][2] = {};
             for (int i = first; i < turns; i += Cfg::TEAMS) {

@@ -52,7 +52,7 @@ struct GtcConfig {
     static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
     static constexpr int TMEM_COLS = 512, ACC_STRIDE = 256;
     static constexpr int BAR_BYTES = 320, SMEM_MAX = 232448;
-    // fp32 outputs: k-blocks summed in the tensor core's accumulator before the sum moves to registers
+    // k-blocks summed in the tensor core's accumulator before the sum moves to registers
     static constexpr int SEG = 8;
     static_assert((4 * MAX_STAGES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
     // after up to 1023 bytes of alignment: [stages][barriers][group table]
@@ -100,8 +100,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
     using Cfg = GtcConfig;
     constexpr int BK = Cfg::BK, CL = 2;
     const uint32_t stages = args.stages;
-    constexpr bool SEGS = OUT == kDtF32;
-    constexpr int SEG = SEGS ? Cfg::SEG : 1 << 30;  // k-blocks per accumulator
+    constexpr int SEG = !WG || OUT == kDtF32 ? Cfg::SEG : 1 << 30;  // k-blocks per accumulator
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -250,7 +249,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                                        (b_mn << 16);
                 uint32_t acc = 0;
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    const bool opens = SEGS ? kb % SEG == 0 : kb == 0;
+                    const bool opens = kb % SEG == 0;
                     if (opens) {
                         acc = local & 1;
                         const uint32_t acc_phase = (local >> 1) & 1;
@@ -280,7 +279,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                     const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
                     const uint32_t at = stage * (Cfg::STAGE_BYTES >> 4);  // addresses are in 16-byte units, below 2^14
                     const uint64_t ad = a_desc0 + at, bd = b_desc0 + at;
-                    const bool closes = kb + 1 == num_kb || (SEGS && (kb + 1) % SEG == 0);
+                    const bool closes = kb + 1 == num_kb || (kb + 1) % SEG == 0;
                     if (elect_one()) {
 #pragma unroll
                         for (uint32_t ks = 0; ks < BK / 16; ++ks)
@@ -352,11 +351,13 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                 chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row, rs != nullptr ? rs + row : nullptr, 1.0f, bias, e);
                 store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
             };
-            if constexpr (SEGS) {
+            if (num_kb > SEG) {
                 // The tensor core's fp32 sums lose about half a unit in the last place per
                 // instruction, always towards zero; over a few hundred of them that is an
-                // error several times an fp32 sum's own (2048 rows: 1.4e-6 of the result).
-                // So every 512 k the accumulator is added into registers, rounded to nearest.
+                // error several times an fp32 sum's own (2048 rows: 1.4e-6 of the result; in a
+                // bf16 row gradient 4096 deep it made 0.23 % of the outputs miss the nearest
+                // bf16, where plain fp32 sums miss 0.04 %).  So every 512 k the accumulator is
+                // added into registers, rounded to nearest.
                 float sum[4][32];
 #pragma unroll
                 for (int ch = 0; ch < 4; ++ch)
