@@ -321,9 +321,11 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                         for (int i = lane; i < (BK - valid) * 8; i += 32) row[i] = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
-                    smem_release_cluster();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_remote_relaxed(fixed0_leader + 8u * s);
+                    if (lane == 0) {
+                        smem_release_cluster();
+                        mbar_arrive_remote_relaxed(fixed0_leader + 8u * s);
+                    }
                 }
                 stage = (stage + num_kb) % stages;
             }

@@ -322,10 +322,10 @@ __global__ void __launch_bounds__(I8Config::THREADS, 1)
                 }
                 tmem_st_wait();
                 fence_proxy_async_smem();
-                smem_release_cluster();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) {
+                    smem_release_cluster();
                     mbar_arrive_remote_relaxed(ready0_leader + 8u * (slot >> 1));
                     mbar_arrive(&empty[stage]);
                 }

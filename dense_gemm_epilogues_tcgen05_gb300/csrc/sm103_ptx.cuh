@@ -488,9 +488,11 @@ __device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
 }
 
 // Handing ordinary writes of this CTA's shared memory to a thread of the other
-// CTA (which then lets the tensor cores read them): each writer orders its
-// writes at cluster scope with smem_release_cluster and the arrive is relaxed;
-// the waiter follows its wait with smem_acquire_cluster.  The fences are
+// CTA (which then lets the tensor cores read them): the writers meet (a warp by
+// __syncwarp), then the thread that arrives orders all their writes at cluster
+// scope with smem_release_cluster -- after they met, or the fence would cover
+// its own writes alone -- and its arrive is relaxed; the waiter follows its wait
+// with smem_acquire_cluster.  The fences are
 // restricted to shared memory: an arrive with release at cluster scope also
 // waits for global memory, about 1000 cycles on GB300.
 __device__ __forceinline__ void smem_release_cluster() {
