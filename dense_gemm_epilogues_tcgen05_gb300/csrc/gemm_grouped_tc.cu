@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
     using Cfg = GtcConfig;
     constexpr int BK = Cfg::BK, CL = 2;
     const uint32_t stages = args.stages;
-    constexpr int SEG = !WG || OUT == kDtF32 ? Cfg::SEG : 1 << 30;  // k-blocks per accumulator
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -249,7 +248,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                                        (b_mn << 16);
                 uint32_t acc = 0;
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    const bool opens = kb % SEG == 0;
+                    const bool opens = kb % Cfg::SEG == 0;
                     if (opens) {
                         acc = local & 1;
                         const uint32_t acc_phase = (local >> 1) & 1;
@@ -279,7 +278,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                     const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
                     const uint32_t at = stage * (Cfg::STAGE_BYTES >> 4);  // addresses are in 16-byte units, below 2^14
                     const uint64_t ad = a_desc0 + at, bd = b_desc0 + at;
-                    const bool closes = kb + 1 == num_kb || (kb + 1) % SEG == 0;
+                    const bool closes = kb + 1 == num_kb || (kb + 1) % Cfg::SEG == 0;
                     if (elect_one()) {
 #pragma unroll
                         for (uint32_t ks = 0; ks < BK / 16; ++ks)
@@ -335,15 +334,16 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
         using OutT = typename Elem<OUT>::T;
         const int quad = warp & 3;                      // TMEM lanes 32*quad ..
         const int half = (warp - Cfg::EPI_WARP0) >> 2;  // which half of the tile's columns
-        const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi};
+        // (a gradient has no activation: known here, their code stays out of its kernels)
+        const StoreArgs e{args.ldc, args.alpha, args.beta, WG ? static_cast<int>(kEpiNone) : args.epi};
         int local = 0;
         while (it.next(t)) {
             const int num_kb = (t.nk + BK - 1) / BK;
             const int f = t.f0 + static_cast<int>(rank) * 128 + quad * 32 + lane;
-            const float bias = (args.epi != kEpiNone && f < args.F)
+            const float bias = (e.epi != kEpiNone && f < args.F)
                                    ? args.bias[static_cast<long long>(t.g) * args.F + f] : 0.0f;
             OutT *c = static_cast<OutT *>(args.C) + (WG ? t.g * args.scg : 0ll) + t.r0 * args.ldc + f;
-            const float *rs = args.row_scale != nullptr ? args.row_scale + t.r0 : nullptr;
+            const float *rs = !WG && args.row_scale != nullptr ? args.row_scale + t.r0 : nullptr;
             const int chunks = t.bn >> 5;
             const int c_begin = half ? (chunks + 1) >> 1 : 0, nch = (half ? chunks : (chunks + 1) >> 1) - c_begin;
             const uint32_t t_quad = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c_begin * 32;
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
                 chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row, rs != nullptr ? rs + row : nullptr, 1.0f, bias, e);
                 store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
             };
-            if (num_kb > SEG) {
+            if (num_kb > Cfg::SEG) {
                 // The tensor core's fp32 sums lose about half a unit in the last place per
                 // instruction, always towards zero; over a few hundred of them that is an
                 // error several times an fp32 sum's own (2048 rows: 1.4e-6 of the result; in a
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(GtcConfig::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) sum[ch][j] = 0.0f;
                 bool ok = true;
-                for (int kb = 0; kb < num_kb; kb += SEG) {
+                for (int kb = 0; kb < num_kb; kb += Cfg::SEG) {
                     const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
                     ++local;
                     const bool got = pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank);

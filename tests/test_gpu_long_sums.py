@@ -73,3 +73,21 @@ def test_few_rows(cuda_lib, ab, out, rows):
     g.gemm_grouped(1, rows, N, K, ab, off, A, K, 1, B, N * K, 1, K, C, N, out, 1.0, beta, None, 0)
     assert g.gemm_last_launch()["path"] == g.PATH_SIMT and g.gemm_device_status() == 0
     check(C, want, total, K, out)
+
+
+@pytest.mark.parametrize("out", [F32, F16, BF16], ids=NAMES.get)
+@pytest.mark.parametrize("ab", [F16, BF16], ids=NAMES.get)
+def test_weight_gradient(cuda_lib, ab, out):
+    g = cuda_lib
+    rng = np.random.default_rng(ab)
+    sizes, M, N = [700, 16384, 0, 9001], 72, 104
+    G, T = len(sizes), sum(sizes)
+    off = offsets_of(sizes)
+    A, Av = positive(rng, (T, M), ab)
+    D, Dv = positive(rng, (T, N), ab)
+    total = np.stack([Av[off[e]:off[e + 1]].T @ Dv[off[e]:off[e + 1]] for e in range(G)])
+    C, beta, want = output(total, out)
+    g.gemm_grouped_wgrad(G, T, M, N, ab, torch.from_numpy(off).int().cuda(), A, M, 1, D, N, 1, C, M * N, N, out, 1.0,
+                         beta)
+    assert g.gemm_last_launch()["path"] == g.PATH_TCGEN05 and g.gemm_device_status() == 0
+    check(C, want, total, max(sizes), out)
