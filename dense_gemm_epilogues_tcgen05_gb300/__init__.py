@@ -29,6 +29,7 @@ __all__ = [
     "Q4_AUTO", "Q4_FFMA", "Q4_MMA", "gemm_set_q4_kernel",
     "gemm_ex", "gemm_get_tuning", "MX_E4M3", "MX_E2M1", "gemm_mx", "gemm_mx_workspace_size",
     "gemm_grouped", "gemm_grouped_wgrad", "gemm_i8", "gemm_i8_grouped", "gemm_i8_quantize", "MAX_GROUPS", "I8_MAX_K",
+    "GROUPED_MAX_EXTENT",
     "gemm_set_tile_policy", "gemm_query_tile", "gemm_set_schedule", "gemm_builtin_scratch", "gemm_wait_selftest",
     "gemm_device_status", "gemm_status_string", "gemm_version", "LIB_PATH", "lib",
 ]
@@ -55,6 +56,7 @@ Q4_DEQUANT_ROWS = 384  # GEMM_Q4_DEQUANT_ROWS: from this many rows of x gemm_q4_
 # gemm_q4_kernel_t
 Q4_AUTO, Q4_FFMA, Q4_MMA = 0, 1, 2
 MAX_GROUPS = 1024    # GEMM_MAX_GROUPS: groups (experts) of one grouped call
+GROUPED_MAX_EXTENT = 2147482624  # GEMM_GROUPED_MAX_EXTENT: largest M, N, K, T of a grouped or 8-bit product
 I8_MAX_K = 131071    # GEMM_I8_MAX_K: longest sum of the 8-bit integer products
 # gemm_mx_elem_t
 MX_E4M3, MX_E2M1 = 0, 1

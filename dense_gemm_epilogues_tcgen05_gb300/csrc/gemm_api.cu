@@ -1284,6 +1284,11 @@ gemm_status_t gemm_mx(int64_t M, int64_t N, int64_t K, gemm_mx_elem_t elem, cons
 
 // ------------------------------------------------- grouped and 8-bit products --
 
+// Largest M, N, K and T of the grouped and 8-bit products: their kernels hold indexes in 32 bits and round them up
+// to tiles, at most 512 wide.
+constexpr int64_t kGroupedMaxExtent = GEMM_GROUPED_MAX_EXTENT;
+static_assert(kGroupedMaxExtent + 1023 <= INT32_MAX, "rounding up stays in 32 bits");
+
 // Blocks of a CUDA-core grouped kernel: at most eight per SM, never more than its tiles could be.
 static int simt_grid(const DeviceState *dev, int64_t row_tiles, int64_t col_tiles) {
     const int64_t cap = static_cast<int64_t>(dev->num_sms) * 8;
@@ -1312,7 +1317,8 @@ static gemm_status_t grouped_rules(int64_t G, int64_t M, int64_t N, int64_t K, c
         *noop = true;
         return GEMM_OK;
     }
-    if (G > GEMM_MAX_GROUPS || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (G > GEMM_MAX_GROUPS || M > kGroupedMaxExtent || N > kGroupedMaxExtent || K > kGroupedMaxExtent)
+        return GEMM_ERR_UNSUPPORTED;
     if (C == nullptr || ldc < N) return GEMM_ERR_INVALID_ARG;
     if (epi != GEMM_EPI_NONE && bias == nullptr) return GEMM_ERR_INVALID_ARG;
     return GEMM_OK;
@@ -1549,7 +1555,8 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
     if (ab_dtype == GEMM_E4M3 || c_dtype == GEMM_E4M3 || (ab_dtype == GEMM_F32 && c_dtype != GEMM_F32))
         return GEMM_ERR_UNSUPPORTED;
     if (G == 0 || M == 0 || N == 0) return record(GEMM_OK, gemm_launch_info_t{});
-    if (G > GEMM_MAX_GROUPS || T > INT32_MAX || M > INT32_MAX || N > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
+    if (G > GEMM_MAX_GROUPS || T > kGroupedMaxExtent || M > kGroupedMaxExtent || N > kGroupedMaxExtent)
+        return GEMM_ERR_UNSUPPORTED;
     if (offsets == nullptr || C == nullptr || ldc < N) return GEMM_ERR_INVALID_ARG;
     // groups of C must not overlap: they are written
     if (G > 1 && (c_stride_g < 0 || extent_bytes(1, 0, M, ldc, N, 1, 1) > static_cast<size_t>(c_stride_g)))

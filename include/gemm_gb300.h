@@ -633,8 +633,12 @@ gemm_status_t gemm_device_status(gemm_stream_t stream);
  *                  offsets[G] on are not touched.  Values outside these rules
  *                  are clamped to [0, M] (no access leaves the arrays), with
  *                  unspecified results.  At most GEMM_MAX_GROUPS groups.
+ *
+ * M, N, K (and T) of these and of the 8-bit products are at most
+ * GEMM_GROUPED_MAX_EXTENT; larger ones are GEMM_ERR_UNSUPPORTED.
  */
 #define GEMM_MAX_GROUPS 1024
+#define GEMM_GROUPED_MAX_EXTENT 2147482624 /* 2^31 - 1024 */
 
 /*
  * gemm_grouped -- for every row r of group g and every column j:
