@@ -352,9 +352,9 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
             const float cin = a.beta != 0.0f ? Elem<OUT>::load(c) : 0.0f;
             *c = Elem<OUT>::cvt(grouped_value<OUT>(static_cast<float>(sum), s, a.beta, cin, bias, a.epilogue));
         }
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * Cfg::WARPS) : "memory");
         first = (first + turns) & 1;
-        if (*abort_flag) break;  // written before the barrier by whoever gave up: all consumers see it
+        // The producer may give up between two consumers' looks at the flag: they leave together or not at all.
+        if (barrier_any<1, 32 * Cfg::WARPS>(*abort_flag != 0)) break;
     }
 }
 

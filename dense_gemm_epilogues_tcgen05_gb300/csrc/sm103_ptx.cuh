@@ -119,6 +119,24 @@ __device__ __forceinline__ bool mbar_drain_wait(uint64_t *bar, uint32_t parity, 
     return true;
 }
 
+// Named barrier ID over the N threads that take part, which also tells every one
+// of them whether any brought `vote`: a decision that all of them share.  A flag
+// that a thread outside the barrier may raise at any time is no such decision --
+// read by each for itself, some would leave and the others wait for them.
+template <int ID, int N>
+__device__ __forceinline__ bool barrier_any(bool vote) {
+    uint32_t any;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, %2, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(any)
+        : "r"(static_cast<uint32_t>(vote)), "n"(ID), "n"(N)
+        : "memory");
+    return any != 0;
+}
+
 // --------------------------------------------------------------------- TMA --
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map) {
