@@ -65,7 +65,8 @@ template <> struct Elem<kDtE4M3> {
 // inside the normalised tolerances, whose scale is at least |z|.  The
 // reciprocal and 2^x are the hardware approximations (rcp.approx, ex2.approx,
 // relative error ~2^-22).  gelu_erf and gelu_erf2 perform the same operations
-// in the same order, so a value gets the same result from either.
+// in the same order, but the compiler contracts gelu_erf's 1 - q with the
+// product q: the two can differ by the rounding of q (2^-25 of |z|).
 namespace gelu_c {
 constexpr float kRsqrt2 = 0.70710678118654752440f;
 constexpr float kP = 0.3275911f;
@@ -329,7 +330,8 @@ __device__ __forceinline__ float activate_one(float z, int epi, bool precise) {
 // The activation of v[off] .. v[off + CNT - 1] (CNT even): one branch on the
 // epilogue for the whole run, then the chosen activation straight through --
 // a branch per element (indirect, for a switch) cost more than ReLU itself.
-// Values get exactly what activate_one gives them.
+// Values get what activate_one gives them (erf-GELU in its accurate form: to
+// the rounding that gelu_erf names).
 template <int OUT, int CNT>
 __device__ __forceinline__ void activate_run(float (&v)[32], int off, int epi, bool precise) {
     const bool kLow = kCheapActivation<OUT> && !precise;

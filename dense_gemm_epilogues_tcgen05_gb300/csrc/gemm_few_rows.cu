@@ -344,9 +344,8 @@ __global__ void __launch_bounds__(GvConfig<NT>::THREADS, 1)
             for (int j = 0; j < Cfg::TEAMS * KS; ++j)
                 sum += part[((j / KS * Cfg::TEAM + (in >> 4) * KS + j % KS) * X_ROWS + r) * 16 + (in & 15)];
             const long long gn = static_cast<long long>(o.g) * a.N + n;
-            float s = a.alpha;
-            if (a.col_scale != nullptr) s *= a.col_scale[gn];
-            if (a.row_scale != nullptr) s *= a.row_scale[o.r0 + r];
+            const float s = product_factor(a.alpha, a.col_scale != nullptr ? a.col_scale + gn : nullptr,
+                                           a.row_scale != nullptr ? a.row_scale + o.r0 + r : nullptr);
             OutT *c = static_cast<OutT *>(a.C) + (o.r0 + r) * a.ldc + n;
             const float bias = a.epilogue != kEpiNone ? a.bias[gn] : 0.0f;
             const float cin = a.beta != 0.0f ? Elem<OUT>::load(c) : 0.0f;

@@ -85,13 +85,13 @@ __global__ void __launch_bounds__(kGThreads) grouped_simt_kernel(const GroupedAr
             const int r = ty + 16 * i;
             if (r >= rows) continue;
             OutT *c = static_cast<OutT *>(a.C) + (r0 + r) * a.ldc + n0;
-            const float rs = a.alpha * (a.row_scale != nullptr ? a.row_scale[r0 + r] : 1.0f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const int n = tx + 16 * j;
                 if (n >= cols) continue;
                 const long long col = static_cast<long long>(g) * a.N + n0 + n;
-                const float s = a.col_scale != nullptr ? rs * a.col_scale[col] : rs;
+                const float s = product_factor(a.alpha, a.col_scale != nullptr ? a.col_scale + col : nullptr,
+                                               a.row_scale != nullptr ? a.row_scale + r0 + r : nullptr);
                 const float b = a.epilogue != kEpiNone ? a.bias[col] : 0.0f;
                 const float cin = a.beta != 0.0f ? Elem<OUT>::load(c + n) : 0.0f;
                 // no k (K == 0, alpha == 0): the scales are not read into the result

@@ -112,14 +112,31 @@ __device__ __forceinline__ GroupedTile row_tile(const GroupTable &t, long long t
     return o;
 }
 
-// One output: z = alpha * scale * acc (+ beta * C) (+ bias), activation, cast.
+// The factor of a product's sum, (alpha * column's) * row's: one order in every
+// kernel, so that an output does not depend on which of them computed it.
+__device__ __forceinline__ float product_factor(float alpha, const float *col_scale, const float *row_scale) {
+    float s = alpha;
+    if (col_scale != nullptr) s = __fmul_rn(s, *col_scale);
+    if (row_scale != nullptr) s = __fmul_rn(s, *row_scale);
+    return s;
+}
+
+// One output: z = scale * acc (+ beta * C) (+ bias), activation; a rounding each,
+// as chunk_values_t has them (no product contracted into the addition).
 // The accurate activation forms for every output type: the cheap ones are
 // within 4e-4 |z|, which shows where the activation's value is far below |z|.
 template <int OUT>
 __device__ __forceinline__ float grouped_value(float acc, float scale, float beta, float c_in, float bias, int epi) {
-    float z = acc * scale;
+    float z = __fmul_rn(acc, scale);
     if (beta != 0.0f) z = fmaf(beta, c_in, z);
-    return activate_one<OUT>(z + bias, epi, true);
+    if (epi != kEpiNone) z = __fadd_rn(z, bias);
+    if (epi == kEpiBiasGelu) {
+        // the form of chunk_values_t: the compiler contracts gelu_erf's 1 - q with the product q
+        float unused = 0.0f;
+        gelu_erf2(z, unused);
+        return z;
+    }
+    return activate_one<OUT>(z, epi, true);
 }
 
 // ------------------------------------------------- transposed accumulators --
