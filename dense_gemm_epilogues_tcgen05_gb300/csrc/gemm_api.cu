@@ -14,6 +14,7 @@
 #include <atomic>
 #include <cstdint>
 #include <cstring>
+#include <initializer_list>
 #include <iterator>
 #include <mutex>
 
@@ -1306,6 +1307,18 @@ static size_t extent_bytes(int64_t n0, int64_t s0, int64_t n1, int64_t s1, int64
     return static_cast<size_t>(last >= kMost ? kMost : std::min(kMost, (last + 1) * Wide(es)));
 }
 
+// Whether every given array starts at a multiple of its element's bytes (NULL always does): the kernels read and
+// write whole elements.
+struct ElemArray {
+    const void *p;
+    int bytes;
+};
+static bool elements_aligned(std::initializer_list<ElemArray> arrays) {
+    for (const ElemArray &a : arrays)
+        if (reinterpret_cast<uintptr_t>(a.p) % a.bytes != 0) return false;
+    return true;
+}
+
 // Argument rules that every grouped call shares.  Sets *noop where there is nothing to do.
 static gemm_status_t grouped_rules(int64_t G, int64_t M, int64_t N, int64_t K, const void *C, int64_t ldc, int cd,
                                    const float *bias, int epi, bool *noop) {
@@ -1510,17 +1523,19 @@ gemm_status_t gemm_grouped(int64_t G, int64_t M, int64_t N, int64_t K, gemm_dtyp
     if (ab_dtype == GEMM_E4M3 || (ab_dtype == GEMM_F32 && c_dtype != GEMM_F32)) return GEMM_ERR_UNSUPPORTED;
     if (noop) return record(GEMM_OK, gemm_launch_info_t{});
     if (offsets == nullptr) return GEMM_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(offsets) & 3u) != 0) return GEMM_ERR_MISALIGNED;
     const bool product = K > 0 && alpha != 0.0f;
     if (product) {
         if (A == nullptr || B == nullptr) return GEMM_ERR_INVALID_ARG;
         if (a_stride_m < 0 || a_stride_k < 0 || b_stride_g < 0 || b_stride_k < 0 || b_stride_n < 0)
             return GEMM_ERR_INVALID_ARG;
     }
+    const int es = elem_bytes(ab_dtype);
+    if (!elements_aligned({{offsets, 4}, {C, elem_bytes(c_dtype)}, {epilogue != GEMM_EPI_NONE ? bias : nullptr, 4}}) ||
+        (product && !elements_aligned({{A, es}, {B, es}, {row_scale, 4}})))
+        return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    const int es = elem_bytes(ab_dtype);
     if ((st = check_range(offsets, static_cast<size_t>(G + 1) * 4)) != GEMM_OK) return st;
     if ((st = check_range(C, extent_bytes(1, 0, M, ldc, N, 1, elem_bytes(c_dtype)))) != GEMM_OK) return st;
     if (epilogue != GEMM_EPI_NONE && (st = check_range(bias, static_cast<size_t>(G) * N * 4)) != GEMM_OK) return st;
@@ -1561,18 +1576,18 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
     // groups of C must not overlap: they are written
     if (G > 1 && (c_stride_g < 0 || extent_bytes(1, 0, M, ldc, N, 1, 1) > static_cast<size_t>(c_stride_g)))
         return GEMM_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(offsets) & 3u) != 0 || (reinterpret_cast<uintptr_t>(a_sum) & 3u) != 0)
-        return GEMM_ERR_MISALIGNED;
     const bool product = T > 0 && alpha != 0.0f;
     if (product) {
         if (A == nullptr || D == nullptr) return GEMM_ERR_INVALID_ARG;
         if (a_stride_r < 0 || a_stride_m < 0 || d_stride_r < 0 || d_stride_n < 0) return GEMM_ERR_INVALID_ARG;
     }
+    const int es = elem_bytes(ab_dtype), ces = elem_bytes(c_dtype);
+    if (!elements_aligned({{offsets, 4}, {a_sum, 4}, {C, ces}}) || (product && !elements_aligned({{A, es}, {D, es}})))
+        return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
     DeviceState *dev = nullptr;
     gemm_status_t st;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    const int es = elem_bytes(ab_dtype), ces = elem_bytes(c_dtype);
     if ((st = check_range(offsets, static_cast<size_t>(G + 1) * 4)) != GEMM_OK) return st;
     if ((st = check_range(C, extent_bytes(G, G > 1 ? c_stride_g : 0, M, ldc, N, 1, ces))) != GEMM_OK) return st;
     if (a_sum != nullptr && (st = check_range(a_sum, static_cast<size_t>(G) * M * 4)) != GEMM_OK) return st;
@@ -1638,9 +1653,11 @@ gemm_status_t gemm_i8_grouped(int64_t G, int64_t M, int64_t N, int64_t K, const 
     if (noop) return record(GEMM_OK, gemm_launch_info_t{});
     if (K > GEMM_I8_MAX_K) return GEMM_ERR_UNSUPPORTED;
     if (offsets == nullptr && G != 1) return GEMM_ERR_INVALID_ARG;
-    if ((reinterpret_cast<uintptr_t>(offsets) & 3u) != 0) return GEMM_ERR_MISALIGNED;
     const bool product = K > 0 && alpha != 0.0f;
     if (product && (X == nullptr || W == nullptr || ldx < K || ldw < K || w_stride_g < 0)) return GEMM_ERR_INVALID_ARG;
+    if (!elements_aligned({{offsets, 4}, {C, elem_bytes(c_dtype)}, {epilogue != GEMM_EPI_NONE ? bias : nullptr, 4}}) ||
+        (product && !elements_aligned({{x_scale, 4}, {w_scale, 4}})))
+        return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
@@ -1686,6 +1703,7 @@ gemm_status_t gemm_i8_quantize(int64_t M, int64_t K, gemm_dtype_t x_dtype, const
     if (M > INT32_MAX || K > INT32_MAX) return GEMM_ERR_UNSUPPORTED;
     if (scale == nullptr || (K > 0 && (X == nullptr || Q == nullptr))) return GEMM_ERR_INVALID_ARG;
     if (ldx < K || ldq < K) return GEMM_ERR_INVALID_ARG;
+    if (!elements_aligned({{K > 0 ? X : nullptr, elem_bytes(x_dtype)}, {scale, 4}})) return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
     DeviceState *dev = nullptr;
     gemm_status_t st;

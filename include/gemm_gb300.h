@@ -69,7 +69,7 @@ typedef enum {
     GEMM_OK = 0,
     GEMM_ERR_INVALID_ARG = 1,   /* negative size, ldc < N, bad enum, NULL where a buffer is needed */
     GEMM_ERR_UNSUPPORTED = 2,   /* dtype combination the library does not implement */
-    GEMM_ERR_MISALIGNED = 3,    /* reserved: every stride/alignment has a path, so not returned today */
+    GEMM_ERR_MISALIGNED = 3,    /* an array not aligned as its entry point needs (gemm() itself never returns it) */
     GEMM_ERR_WORKSPACE = 4,     /* workspace missing or smaller than gemm_workspace_size() */
     GEMM_ERR_CUDA = 5,          /* a CUDA runtime/driver call failed (launch, attribute, tensor map) */
     GEMM_ERR_TIMEOUT = 6        /* a device-side wait gave up (reported by gemm_device_status) */
@@ -662,7 +662,8 @@ gemm_status_t gemm_device_status(gemm_stream_t stream);
  * of 16 bytes; anything else on the CUDA cores.  The activations take the
  * forms of fp32 outputs whatever c_dtype.  C must not overlap the inputs.
  * Asynchronous on `stream`; errors as gemm(), GEMM_ERR_MISALIGNED for an
- * offsets array that is not 4-byte aligned.
+ * array that is read or written and does not start at a multiple of its
+ * element's size.
  */
 gemm_status_t gemm_grouped(int64_t G, int64_t M, int64_t N, int64_t K, gemm_dtype_t ab_dtype, const int32_t *offsets,
                            const void *A, int64_t a_stride_m, int64_t a_stride_k, const void *B, int64_t b_stride_g,
@@ -711,7 +712,8 @@ gemm_status_t gemm_grouped_wgrad(int64_t G, int64_t T, int64_t M, int64_t N, gem
  *                  M or on the kernel that a call runs.  It is rounded to fp32
  *                  once, scaled, and rounded to c_dtype (F32, F16 or BF16).
  *   bias           fp32[N]; C, ldc, alpha, beta, epilogue as in gemm().
- * Any alignment; 16-byte aligned bases and pitches run on the fast kernels.
+ * Any alignment of the codes; 16-byte aligned bases and pitches run on the
+ * fast kernels.  The other arrays as in gemm_grouped.
  *
  * gemm_i8_grouped -- the same, grouped by expert: rows of group g use W[g] =
  * W + g*w_stride_g, w_scale[g] and bias[g] (fp32[G x N] each); offsets as in
@@ -733,7 +735,8 @@ gemm_status_t gemm_i8_grouped(int64_t G, int64_t M, int64_t N, int64_t K, const 
  *
  * A row of zeros (or K == 0) gets scale 0 and codes 0.  A row that holds a NaN
  * or an infinity gets a NaN scale, so that the product's row shows it, and
- * codes 0.  Columns K..ldq-1 of Q are not written.
+ * codes 0.  Columns K..ldq-1 of Q are not written.  X and scale start at a
+ * multiple of their element's size (else GEMM_ERR_MISALIGNED).
  */
 gemm_status_t gemm_i8_quantize(int64_t M, int64_t K, gemm_dtype_t x_dtype, const void *X, int64_t ldx, int8_t *Q,
                                int64_t ldq, float *scale, gemm_stream_t stream);
