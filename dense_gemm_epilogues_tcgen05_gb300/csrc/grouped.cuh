@@ -25,25 +25,39 @@ __host__ __device__ constexpr int group_table_bytes(int G) { return 4 * (3 * G +
 
 // Fill the table (every thread of the block calls this; `n` threads, a
 // multiple of 32).  tiles_of(rows) is the number of row tiles of a group.
-// Offsets are clamped to [0, M] and to be non-decreasing inside a group, so
-// whatever the array holds, no row outside 0 .. M-1 is ever touched.
+// Offsets are clamped to [0, M], and where one is below an earlier one it is
+// raised to that, so whatever the array holds, no row outside 0 .. M-1 is ever
+// touched, no row belongs to two groups, and the tiles of all groups together
+// are no more than M rows and G groups can have (first[G] stays in 32 bits).
 // offsets == NULL: one group of all M rows.
 template <typename F>
 __device__ __forceinline__ GroupTable group_table_build(int *smem, const int *offsets, int G, int M, int tid, int n,
                                                         F tiles_of) {
     GroupTable t{smem, smem + G + 1, smem + 2 * G + 1, G};
+    bool falls = false;
     for (int g = tid; g < G; g += n) {
         int lo = 0, hi = M;
         if (offsets != nullptr) {
             lo = min(max(__ldg(offsets + g), 0), M);
-            hi = min(max(__ldg(offsets + g + 1), lo), M);
+            hi = min(max(__ldg(offsets + g + 1), 0), M);
+            falls = falls || hi < lo;
         }
         t.lo[g] = lo;
         t.hi[g] = hi;
-        t.first[g + 1] = tiles_of(hi - lo);
+        t.first[g + 1] = tiles_of(max(hi - lo, 0));
     }
     if (tid == 0) t.first[0] = 0;
-    __syncthreads();
+    if (__syncthreads_or(falls)) {  // offsets that are not non-decreasing
+        if (tid == 0) {
+            int end = 0;
+            for (int g = 0; g < G; ++g) {
+                t.lo[g] = end = max(end, t.lo[g]);
+                t.hi[g] = end = max(end, t.hi[g]);
+                t.first[g + 1] = tiles_of(t.hi[g] - t.lo[g]);
+            }
+        }
+        __syncthreads();
+    }
     if (tid < 32) {
         int base = 0;
         for (int g0 = 0; g0 < G; g0 += 32) {

@@ -631,8 +631,10 @@ gemm_status_t gemm_device_status(gemm_stream_t stream);
  *                  M.  The host never reads it: a router's counts need no copy
  *                  back.  Groups may be empty; rows below offsets[0] or from
  *                  offsets[G] on are not touched.  Values outside these rules
- *                  are clamped to [0, M] (no access leaves the arrays), with
- *                  unspecified results.  At most GEMM_MAX_GROUPS groups.
+ *                  are clamped to [0, M], one below an earlier one to that
+ *                  (no access leaves the arrays and no row of C is written
+ *                  twice), with unspecified results.  At most
+ *                  GEMM_MAX_GROUPS groups.
  *
  * M, N, K (and T) of these and of the 8-bit products are at most
  * GEMM_GROUPED_MAX_EXTENT; larger ones are GEMM_ERR_UNSUPPORTED.
