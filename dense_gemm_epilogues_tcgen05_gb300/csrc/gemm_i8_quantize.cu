@@ -18,9 +18,10 @@
 // quotient's rounding or, within 2^-15 of a tie (the product is off by at most
 // 2^-23 of at most 127), a neighbour of it.  There the remainder 127 x - n max
 // decides: twice its size against max, and the even code where they are equal.
-// For 16-bit inputs 127 x is exact and the remainder of a quotient that is not a
-// tie differs from max / 2 by far more than the rounding of its fused
-// multiply-add.  (Ties are not rare: with x and max of few bits the quotients lie
+// Next to a tie the fused multiply-add gives the remainder exactly (both terms
+// are multiples of max's last place, or n is 0), and so does the subtraction of
+// max; 127 x is exact for 16-bit inputs, and what its rounding cut off an fp32
+// input's is added last.  (Ties are not rare: with x and max of few bits the quotients lie
 // on a coarse grid, and in rows of normal bf16 values most warps meet one.)
 //
 // Bound: HBM (3 bytes per 16-bit value): 16384 x 8192 bf16 80 us on GB300, 5.0 TB/s,
@@ -37,17 +38,33 @@ constexpr int kQThreads = 256;
 // |x| as an ordered integer; infinities and NaN are the largest.
 __device__ __forceinline__ unsigned abs_bits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
-// round_even(127 x / amax).  `shrink` is 1, or 2^-32 on both where 127 x could
-// overflow (exact; what it flushes is far below half a step).
-__device__ __noinline__ int code_by_division(float x, float amax, float shrink) {
-    return __float2int_rn(__fdiv_rn(127.0f * (x * shrink), amax * shrink));
+struct QRow {
+    float amax, inv;  // the row's maximum times pre, and 127 over that
+    float pre;        // 1, or the power of two that brings a very small or large maximum near 1: its values
+                      // are multiplied by it (exact where a code other than 0 can come of it)
+    bool zero;        // codes 0 throughout
+};
+
+// What to add to the code n (odd or even) of x, at most one off, for
+// round_even(127 x / amax); x and amax with `pre`.
+template <int XT>
+__device__ __forceinline__ int step_to_nearest(float x, float n, bool odd, float amax) {
+    const float p = 127.0f * x, e = fmaf(-n, amax, p);
+    float d = 2.0f * fabsf(e) - amax;
+    if constexpr (XT == kDtF32) {
+        const float cut = fmaf(127.0f, x, -p);
+        d = fmaf(e > 0.0f ? 2.0f : -2.0f, cut, d);
+    }
+    return d > 0.0f || (d == 0.0f && odd) ? (e > 0.0f ? 1 : -1) : 0;
 }
 
-struct QRow {
-    float amax, inv, shrink;
-    bool zero;  // codes 0 throughout
-    bool slow;  // 127 / amax is not a normal number: divide always
-};
+// The code of one value.
+template <int XT>
+__device__ __forceinline__ int code_of(float x, const QRow &row) {
+    x *= row.pre;
+    const int n = __float2int_rn(x * row.inv);
+    return row.zero ? 0 : n + step_to_nearest<XT>(x, static_cast<float>(n), (n & 1) != 0, row.amax);
+}
 
 // The largest |x| of a 16-byte piece, as the bits of an fp32 value; 16-bit types
 // two at a time (the halves of `acc` are combined at the end).
@@ -73,9 +90,13 @@ __device__ __forceinline__ unsigned max_bits(unsigned acc) {
 
 // Codes of N values (N even, at most 8) into N bytes.  r + 1.5 * 2^23 holds
 // round_even(r) in its low bits, as a two's complement byte.
-template <int N>
-__device__ __forceinline__ void codes_of(const float (&f)[N], const QRow &row, uint32_t (&w)[N / 4]) {
+template <int XT, int N>
+__device__ __forceinline__ void codes_of(float (&f)[N], const QRow &row, uint32_t (&w)[N / 4]) {
     constexpr float kMagic = 12582912.0f;
+    if (row.pre != 1.0f) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) f[j] *= row.pre;
+    }
     uint32_t t[N];
     float worst = 0.0f;
 #pragma unroll
@@ -91,20 +112,11 @@ __device__ __forceinline__ void codes_of(const float (&f)[N], const QRow &row, u
         t[j + 1] = __float_as_uint(s1);
         worst = fmaxf(worst, fmaxf(fabsf(o0), fabsf(o1)));
     }
-    if (row.slow) {
-#pragma unroll 1
-        for (int j = 0; j < N; ++j) {
-            const uint32_t c = static_cast<uint32_t>(code_by_division(f[j], row.amax, row.shrink));
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-                if (i == j) t[i] = c;
-        }
-    } else if (worst > 0.5f - 0x1p-15f) {
+    if (worst > 0.5f - 0x1p-15f) {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
             const float n = __uint_as_float(t[j]) - kMagic;
-            const float e = fmaf(-n, row.amax, 127.0f * f[j]), d = 2.0f * fabsf(e);
-            if (d > row.amax || (d == row.amax && (t[j] & 1u))) t[j] += e > 0.0f ? 1u : 0xFFFFFFFFu;
+            t[j] += static_cast<uint32_t>(step_to_nearest<XT>(f[j], n, (t[j] & 1u) != 0, row.amax));
         }
     }
 #pragma unroll
@@ -118,12 +130,12 @@ __device__ __forceinline__ void codes_of(const float (&f)[N], const QRow &row, u
 __device__ __forceinline__ QRow row_scale(unsigned m, float *scale, bool writes) {
     const bool finite = m < 0x7F800000u;
     QRow r;
-    r.amax = __uint_as_float(m);
+    const float amax = __uint_as_float(m);
     r.zero = !finite || m == 0u;
-    r.slow = !(r.amax > 1e-30f && r.amax < 1e30f) && !r.zero;
-    r.shrink = r.amax >= 1.2676506e30f ? 2.3283064365386963e-10f : 1.0f;  // 2^100, 2^-32
-    r.inv = r.slow || r.zero ? 0.0f : __fdiv_rn(127.0f, r.amax);
-    if (writes) *scale = finite ? __fdiv_rn(r.amax, 127.0f) : __uint_as_float(0x7FC00000u);
+    r.pre = r.zero || (amax > 1e-30f && amax < 1e30f) ? 1.0f : amax < 1.0f ? 0x1p64f : 0x1p-64f;
+    r.amax = amax * r.pre;
+    r.inv = r.zero ? 0.0f : __fdiv_rn(127.0f, r.amax);
+    if (writes) *scale = finite ? __fdiv_rn(amax, 127.0f) : __uint_as_float(0x7FC00000u);
     return r;
 }
 
@@ -134,7 +146,7 @@ __device__ __forceinline__ void store_codes(signed char *q, long long v, const u
     float f[PV];
     Vec16<XT>::unpack(u, f);
     uint32_t w[PV / 4];
-    codes_of<PV>(f, r, w);
+    codes_of<XT, PV>(f, r, w);
     if constexpr (PV == 8)
         *reinterpret_cast<uint2 *>(q + v * PV) = make_uint2(w[0], w[1]);
     else
@@ -183,7 +195,7 @@ __global__ void __launch_bounds__(kQThreads) i8_quantize_kernel(long long K, con
             store_codes<XT>(q, v, __ldg(xv + v), r);
     }
     for (long long k = nvec * PV + tid; k < K; k += n)
-        q[k] = static_cast<signed char>(r.zero ? 0 : code_by_division(Elem<XT>::load(x + k), r.amax, r.shrink));
+        q[k] = static_cast<signed char>(code_of<XT>(Elem<XT>::load(x + k), r));
 }
 
 // Persistent form for many rows of `pieces` 16-byte pieces, at most KEEP
