@@ -282,15 +282,23 @@ gemm_status_t encode_operand(CUtensorMap *map, int ab, const void *base, const O
     return encode_2d(map, ab, base, mn, k, s_k, swz, swz);
 }
 
+// Can C (M x N, row pitch ldc) be written by TMA boxes?  Its base and pitch as
+// TMA needs them, and rows of whole 16 bytes: a store clips a box at the end of
+// the rows in steps of 16 bytes, and would write into what follows a row's last
+// element there.
+bool c_tma_ok(const void *C, int64_t N, int64_t ldc, int es) {
+    const int64_t pitch = ldc * es;
+    return (reinterpret_cast<uintptr_t>(C) & 15u) == 0 && pitch % 16 == 0 && pitch > 0 &&
+           pitch < (int64_t(1) << 40) && N * es % 16 == 0;
+}
+
 // Map of the output C (N x M, row pitch ldc) for the pair kernel's staged
 // epilogue: boxes of 32 rows x 64 bytes with the 64-byte swizzle.  Returns
-// false (and the kernel stores C directly) when C's base or row pitch rules
-// out TMA.
+// false (and the kernel stores C directly) when c_tma_ok does.
 bool encode_c(CUtensorMap *map, int cd, void *C, int64_t M, int64_t N, int64_t ldc) {
     const int es = elem_bytes(cd);
     const int64_t pitch = ldc * es;
-    if ((reinterpret_cast<uintptr_t>(C) & 15u) != 0 || pitch % 16 != 0 || pitch <= 0 || pitch >= (int64_t(1) << 40))
-        return false;
+    if (!c_tma_ok(C, N, ldc, es)) return false;
     const CUtensorMapDataType dt = cd == GEMM_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : cd == GEMM_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
                                                     : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;

@@ -227,8 +227,8 @@ gemm_status_t gemm_set_schedule(gemm_schedule_t schedule);
  * N-contiguous (B stored K x N row-major) keeps the tensor pipe measurably
  * less busy than a K-contiguous one (79.5 % vs 86.5 % of cycles, bf16
  * 8192^3), so AUTO transposes exactly that case for fp16 / bf16 inputs: A
- * K-contiguous, B N-contiguous, 16-bit output, C base and pitch usable by
- * TMA (fp8 inputs measured no faster transposed and keep the given order).
+ * K-contiguous, B N-contiguous, 16-bit output, C base, pitch and row length
+ * usable by TMA (multiples of 16 bytes; fp8 inputs measured no faster transposed and keep the given order).
  * The result is the same product; only the summation order inside fp32
  * accumulation may differ.
  */
