@@ -13,6 +13,7 @@ import argparse
 import concurrent.futures as cf
 import hashlib
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -30,6 +31,21 @@ NVCC_FLAGS = ARCH_FLAGS + [
     "-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
     "-Xcompiler", "-fPIC", "-Xptxas", "-v", "-DNDEBUG",
 ]
+
+
+# Kernels whose warpgroups trade registers (setmaxnreg): the trade adds up for this count at launch and no other,
+# and a sum above what the block was launched with would wait for ever.
+LAUNCH_REGISTERS = {"i8_tc_kernel": 72}
+
+
+def check_registers(report: str) -> None:
+    """Raise unless the compiler gave every kernel of LAUNCH_REGISTERS the count that its source is written for."""
+    for name, want in LAUNCH_REGISTERS.items():
+        got = [int(m.group(1)) for part in report.split("Compiling entry function")[1:]
+               if name in part.split("'")[1] for m in [re.search(r"Used (\d+) registers", part)] if m]
+        if not got or any(r != want for r in got):
+            raise RuntimeError(f"{name}: compiled to {sorted(set(got)) or 'no'} registers, written for {want}; its "
+                               f"source's LAUNCH_REGS and register trade need to follow this compiler")
 
 
 def _nvcc() -> str:
@@ -94,6 +110,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             logs.append(log)
     with open(os.path.join(BUILD_DIR, "ptxas_report.txt"), "w") as f:
         f.write("\n".join(logs))
+    check_registers("\n".join(logs))
     tmp = LIB_PATH + ".tmp"
     cmd = [nvcc] + ARCH_FLAGS + ["-shared", "-o", tmp] + sorted(objs) + [
         "-cudart", "shared", "-Xlinker", "-rpath,$ORIGIN:/usr/local/cuda/lib64"]

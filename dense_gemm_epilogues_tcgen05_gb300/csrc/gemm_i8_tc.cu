@@ -451,7 +451,8 @@ cudaError_t launch_i8_tc_out(const CUtensorMap &tw, const CUtensorMap &tx32, con
     cudaError_t err =
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, I8Config::SMEM_MAX);
     if (err != cudaSuccess) return err;
-    // The register trade adds up for this launch count only.
+    // The register trade adds up for this launch count only.  The build holds the compiler to it; a library
+    // built past that check refuses here, where the kernel would wait for registers for ever.
     cudaFuncAttributes fa;
     if ((err = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return err;
     if (fa.numRegs != I8Config::LAUNCH_REGS) return cudaErrorInvalidKernelImage;
