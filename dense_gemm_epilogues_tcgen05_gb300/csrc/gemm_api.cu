@@ -1450,6 +1450,8 @@ static gemm_status_t few_rows_launch(const GroupedArgs &args, int ab, int cd, in
     }
     gemm_launch_info_t info = {};
     info.path = GEMM_PATH_SIMT;
+    info.kind = 3;
+    info.bn = 8 * nt;
     return record(launch_few_rows(ab, cd, nt, m, args, dev->num_sms, s) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA, info);
 }
 

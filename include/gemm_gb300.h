@@ -332,8 +332,9 @@ gemm_status_t gemm_query_tile(int64_t M, int64_t N, int64_t K, gemm_dtype_t ab_d
  */
 typedef struct {
     int path;          /* gemm_path_t of the kernel family launched (NOOP when nothing was) */
-    int kind;          /* tcgen05 path: 1 one SM per tile, 2 a pair of SMs per tile; else 0 */
-    int bn;            /* tcgen05 path: tile width in columns of the MMA's output */
+    int kind;          /* tcgen05 path: 1 one SM per tile, 2 a pair of SMs per tile; SIMT path of the grouped
+                          and 8-bit products: 3 their streaming kernel for few rows; else 0 */
+    int bn;            /* tcgen05 path: tile width in columns of the MMA's output; kind 3: rows of a tile */
     int transposed;    /* 1 when the pair kernel ran C^T = B^T A^T */
     int cluster_ctas;  /* CTAs per cluster: 1 (one-SM kernel), 2 (one pair) or 4 (two pairs sharing A) */
     int grid_ctas;     /* CTAs of the tcgen05 GEMM kernel (0 on the other paths) */
