@@ -1425,7 +1425,11 @@ static int i8_most_rows(int64_t G, int64_t M, int64_t N, int pairs) {
 // Row tiles of the streaming kernel for few rows, in eights; 0: the call runs on the pair kernel.  One and two
 // eights keep up with HBM whatever the size (16384^2 codes on GB300: 46 to 49 us up to 8 rows, 58 to 16, the
 // pair kernel 60); four are bound by their MMAs (32 rows: 86 us), but with few tiles the pair kernel leaves
-// most SMs idle (32 rows of 4096^2: 15 us against 19), so they run where its tiles would not fill the SM pairs.
+// most SMs idle, so they run where its tiles would not fill the SM pairs.  Both sides, 8-bit, flushed L2: 12 rows of
+// 4096^2 12 us against the pair kernel's 25, 32 rows 20 / 25, 128 x 2048 x 8192 29 / 37; next to the limit either may
+// win: 96 rows of 4096^2 (48 tiles) 31 / 25, 200 x 1536 x 4096 (42) 29 / 25, 24 x 16384 x 4096 (64, the pair's) 32 / 29.
+// Groups are taken as equal, since the host does not know them.  256 rows over 128 experts of 2048 x 4096: 172 us
+// against 223; all of them at one expert: 51 against 29, still below what the call may take.
 static int few_rows(int64_t G, int64_t M, int64_t N) {
     if (M <= 8 || M <= 2 * G) return 1;
     if (M <= 16 || M <= 4 * G) return 2;

@@ -10,7 +10,7 @@
 // partial sums of an output meet in shared memory at the end of a tile, in a
 // fixed order.
 //
-// 16-bit values: mma.sync m16n8k16 with fp32 sums.  8-bit integers, up to four
+// 16-bit values: mma.sync m16n8k16 with fp32 sums, joined every 512 k.  8-bit integers, up to four
 // rows: dot products of four codes (dp4a); up to eight: mma.sync m16n8k32 on the
 // codes; more: m16n8k16 on the codes expanded to binary16, fp32 sums moved into
 // integers every 1024 k as in gemm_i8_tc.cu (the integer kind takes about 20

@@ -32,10 +32,10 @@
 //
 // Bound and measured (GB300): small groups by the weights' bytes, each expert's
 // read once per 256 of its rows and from L2 after the first (64 experts x 4096 rows,
-// 2048 x 4096 fp16: 170 us, 6.6 TB/s of the 1.12 GB); large ones by the tensor pipe
-// (32 experts, 32768 rows, 4096 x 4096 bf16, row gradient: 732 us,
-// 1.50 PFLOP/s); the gradient by the tensor pipe and its output's
-// bytes together (16 experts, 16384 rows, 2048 x 4096, fp32 out: 210 us, 59 % tensor pipe,
+// 2048 x 4096 fp16: 173 us, 6.5 TB/s of the 1.12 GB); large ones by the tensor pipe
+// (32 experts, 32768 rows, 4096 x 4096 bf16, row gradient: 748 us,
+// 1.47 PFLOP/s; 3 % faster without the fp32 sums in registers); the gradient by the tensor pipe and its output's
+// bytes together (16 experts, 16384 rows, 2048 x 4096, fp32 out: 201 us, 61 % tensor pipe,
 // 738 MB), and by its tiles' fixed costs when groups are small (24 gradients of
 // 1000 x 1000 over 777 rows: 25 us with the bias sums).
 #include "gemm_tcgen05.cuh"

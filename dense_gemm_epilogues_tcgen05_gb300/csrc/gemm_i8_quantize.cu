@@ -21,12 +21,13 @@
 // Next to a tie the fused multiply-add gives the remainder exactly (both terms
 // are multiples of max's last place, or n is 0), and so does the subtraction of
 // max; 127 x is exact for 16-bit inputs, and what its rounding cut off an fp32
-// input's is added last.  (Ties are not rare: with x and max of few bits the quotients lie
-// on a coarse grid, and in rows of normal bf16 values most warps meet one.)
+// input's is added last.  (Ties are not rare: with x and max of few bits the
+// quotients lie on a coarse grid, and in rows of normal bf16 values most warps meet one.)
 //
-// Bound: HBM (3 bytes per 16-bit value): 16384 x 8192 bf16 80 us on GB300, 5.0 TB/s,
-// with 61 % of the issue slots used (a block per row without the prefetch 103 us;
-// a division per value 194 us).
+// Bound: HBM (3 bytes per 16-bit value): 16384 x 8192 bf16 68 us on GB300, 5.9 TB/s,
+// with 67 % of the issue slots used (with a division kept for extreme rows, and the
+// stack it needs, 80 us; a block per row without the prefetch 103 us; a division per
+// value 194 us).
 #include "grouped.cuh"
 
 namespace gb300 {

@@ -37,13 +37,13 @@
 // the 504 that seven warps of a sub-partition launched with).
 //
 // Bound and measured (GB300, 8192 x 4096 x 4096 codes, bias and GELU, bf16 out):
-// 210 us, 1.31 PFLOP/s.  The tensor pipe is busy 51 % and the issue slots 52 % of
-// the time.  Shared memory would allow 1.08 of the MMAs'
+// 212 us, 1.30 PFLOP/s.  The tensor pipe is busy 50 % and the issue slots 52 % of
+// the time, so neither is the bound; no counter names the latency that is.  Shared memory would allow 1.08 of the MMAs'
 // time at 192 columns: per 128 k a CTA moves 32 KB of W and 768 bytes per row of X
 // against the MMA's 8 clocks per row.  On the way: arrives with release at cluster
 // scope 372 us, fences restricted to shared memory 241 us; outputs of one accumulator
 // straight from fp32 228 -> 217 us; outputs stored from registers and one more stage
-// of codes 217 -> 210 us.
+// of codes 217 -> 210 us; the fence behind the warp's meeting 210 -> 212 us (other boxes).
 #include <algorithm>
 
 #include "gemm_tcgen05.cuh"
