@@ -29,7 +29,10 @@ __all__ = [
     "Q4_AUTO", "Q4_FFMA", "Q4_MMA", "gemm_set_q4_kernel",
     "gemm_ex", "gemm_get_tuning", "MX_E4M3", "MX_E2M1", "gemm_mx", "gemm_mx_workspace_size",
     "gemm_grouped", "gemm_grouped_wgrad", "gemm_i8", "gemm_i8_grouped", "gemm_i8_quantize", "MAX_GROUPS", "I8_MAX_K",
-    "GROUPED_MAX_EXTENT",
+    "GROUPED_MAX_EXTENT", "gemm_mx_quantize", "gemm_mx_dequantize", "gemm_mx_grouped",
+    "SCORE_SOFTMAX", "SCORE_SIGMOID", "ROUTE_MAX_TOP", "ROUTE_MAX_GROUPS", "ROUTE_MAX_PAIRS", "ROWS_MAX_D",
+    "gemm_route", "gemm_route_grad", "gemm_route_rows", "gemm_route_rows_workspace_size",
+    "gemm_rows_gather", "gemm_rows_combine", "gemm_rows_combine_grad",
     "gemm_set_tile_policy", "gemm_query_tile", "gemm_set_schedule", "gemm_builtin_scratch", "gemm_wait_selftest",
     "gemm_device_status", "gemm_status_string", "gemm_version", "LIB_PATH", "lib",
 ]
@@ -60,6 +63,12 @@ GROUPED_MAX_EXTENT = 2147482624  # GEMM_GROUPED_MAX_EXTENT: largest M, N, K, T o
 I8_MAX_K = 131071    # GEMM_I8_MAX_K: longest sum of the 8-bit integer products
 # gemm_mx_elem_t
 MX_E4M3, MX_E2M1 = 0, 1
+# gemm_score_t
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+ROUTE_MAX_TOP = 32           # GEMM_ROUTE_MAX_TOP: experts of one token
+ROUTE_MAX_GROUPS = 32        # GEMM_ROUTE_MAX_GROUPS: groups of experts of one router
+ROUTE_MAX_PAIRS = 1 << 30    # GEMM_ROUTE_MAX_PAIRS: (token, slot) pairs of one call
+ROWS_MAX_D = 1 << 23         # GEMM_ROWS_MAX_D: columns of the rows that are moved
 # gemm_status_t
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT = range(7)
 
@@ -166,6 +175,28 @@ lib.gemm_i8_grouped.argtypes = [_i64, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp
                                 _f32, _f32, _vp, _int, _vp]
 lib.gemm_i8_quantize.restype = _int
 lib.gemm_i8_quantize.argtypes = [_i64, _i64, _int, _vp, _i64, _vp, _i64, _vp, _vp]
+lib.gemm_mx_quantize.restype = _int
+lib.gemm_mx_quantize.argtypes = [_i64, _i64, _int, _int, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+lib.gemm_mx_dequantize.restype = _int
+lib.gemm_mx_dequantize.argtypes = [_i64, _i64, _int, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp]
+lib.gemm_mx_grouped.restype = _int
+lib.gemm_mx_grouped.argtypes = [_i64, _i64, _i64, _i64, _int, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _i64,
+                                _i64, _vp, _i64, _int, _f32, _f32, _vp, _int, _vp, _vp]
+lib.gemm_route.restype = _int
+lib.gemm_route.argtypes = [_i64, _i64, _i64, _int, _vp, _i64, _vp, _int, _i64, _i64, _i64, _int, _f32, _vp, _vp, _vp]
+lib.gemm_route_grad.restype = _int
+lib.gemm_route_grad.argtypes = [_i64, _i64, _i64, _int, _vp, _i64, _int, _int, _f32, _vp, _vp, _vp, _i64, _vp]
+lib.gemm_route_rows.restype = _int
+lib.gemm_route_rows.argtypes = [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+lib.gemm_route_rows_workspace_size.restype = _sz
+lib.gemm_route_rows_workspace_size.argtypes = [_i64, _i64, _i64]
+lib.gemm_rows_gather.restype = _int
+lib.gemm_rows_gather.argtypes = [_i64, _i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64, _vp]
+lib.gemm_rows_combine.restype = _int
+lib.gemm_rows_combine.argtypes = [_i64, _i64, _i64, _i64, _int, _vp, _i64, _vp, _vp, _f32, _int, _vp, _i64, _vp]
+lib.gemm_rows_combine_grad.restype = _int
+lib.gemm_rows_combine_grad.argtypes = [_i64, _i64, _i64, _i64, _int, _vp, _i64, _int, _vp, _i64, _vp, _vp, _vp, _i64,
+                                       _vp, _vp]
 lib.gemm_device_status.restype = _int
 lib.gemm_device_status.argtypes = [_vp]
 lib.gemm_status_string.restype = ctypes.c_char_p
@@ -401,6 +432,86 @@ def gemm_i8_quantize(M, K, x_dtype, X, ldx, Q, ldq, scale, stream=None) -> int:
     """Rows of X to 8-bit codes Q = round(127 x / max|x|) and scale = max|x| / 127 (fp32, one per row)."""
     st = lib.gemm_i8_quantize(M, K, x_dtype, _ptr(X), ldx, _ptr(Q), ldq, _ptr(scale), _stream(stream))
     return _check(st, "gemm_i8_quantize")
+
+
+def gemm_mx_quantize(M, K, elem, x_dtype, X, ldx, Q, ldq, scale, lds, source=None, top=1, rows_x=None,
+                     stream=None) -> int:
+    """Rows of X to block-scaled codes Q (MX_E4M3 / MX_E2M1, pitch ldq elements) and E8M0 scales (one per 32 k,
+    pitch lds bytes).  With ``source`` (int32 device array of M) row i is row source[i] // top of X, which has
+    rows_x rows (M without a source); rows whose source is none stay as they were."""
+    st = lib.gemm_mx_quantize(M, K, elem, x_dtype, _ptr(X), ldx, M if rows_x is None else rows_x, _ptr(source), top,
+                              _ptr(Q), ldq, _ptr(scale), lds, _stream(stream))
+    return _check(st, "gemm_mx_quantize")
+
+
+def gemm_mx_dequantize(M, K, elem, Q, ldq, scale, lds, y_dtype, Y, ldy, stream=None) -> int:
+    """Y = Q * 2^(scale - 127) as F32, F16 or BF16 rows (pitch ldy)."""
+    st = lib.gemm_mx_dequantize(M, K, elem, _ptr(Q), ldq, _ptr(scale), lds, y_dtype, _ptr(Y), ldy, _stream(stream))
+    return _check(st, "gemm_mx_dequantize")
+
+
+def gemm_mx_grouped(G, M, N, K, elem, offsets, X, ldx, x_scale, ldxs, W, w_stride_g, ldw, w_scale, ws_stride_g, ldws,
+                    C, ldc, c_dtype, alpha, beta, bias, epilogue, row_scale=None, stream=None) -> int:
+    """gemm_grouped over block-scaled codes (MX_E4M3 / MX_E2M1): X M x K, W G x N x K, strides of codes in elements
+    and of scales in bytes; see include/gemm_gb300.h."""
+    st = lib.gemm_mx_grouped(G, M, N, K, elem, _ptr(offsets), _ptr(X), ldx, _ptr(x_scale), ldxs, _ptr(W), w_stride_g,
+                             ldw, _ptr(w_scale), ws_stride_g, ldws, _ptr(C), ldc, c_dtype, alpha, beta, _ptr(bias),
+                             epilogue, _ptr(row_scale), _stream(stream))
+    return _check(st, "gemm_mx_grouped")
+
+
+def gemm_route(T, E, top, l_dtype, logits, ldl, expert, weight, bias=None, score=SCORE_SOFTMAX, groups=1, top_groups=1,
+               group_sum=1, renormalise=True, scale=1.0, stream=None) -> int:
+    """Experts (int32, T x top) and weights (fp32, T x top) of T tokens from a router's logits (T x ldl): softmax or
+    sigmoid scores (SCORE_*), a bias that moves the choice alone, the top_groups worthiest of ``groups`` groups of
+    experts, weights renormalised over the chosen ones and times ``scale``.  Slots without an expert: -1, 0."""
+    st = lib.gemm_route(T, E, top, l_dtype, _ptr(logits), ldl, _ptr(bias), score, groups, top_groups, group_sum,
+                        int(renormalise), scale, _ptr(expert), _ptr(weight), _stream(stream))
+    return _check(st, "gemm_route")
+
+
+def gemm_route_grad(T, E, top, l_dtype, logits, ldl, expert, dweight, dlogits, ldd, score=SCORE_SOFTMAX,
+                    renormalise=True, scale=1.0, stream=None) -> int:
+    """Gradient of gemm_route's weights by its logits (dlogits: T x ldd of l_dtype), the choice held fixed."""
+    st = lib.gemm_route_grad(T, E, top, l_dtype, _ptr(logits), ldl, score, int(renormalise), scale, _ptr(expert),
+                             _ptr(dweight), _ptr(dlogits), ldd, _stream(stream))
+    return _check(st, "gemm_route_grad")
+
+
+def gemm_route_rows(T, top, E, expert, offsets, row, source, workspace=None, workspace_bytes=0, stream=None) -> int:
+    """The T x top pairs sorted by expert: offsets (E + 1) for the grouped products, the row of each pair (or None)
+    and the pair of each row (T * top), -1 where there is none; all int32."""
+    st = lib.gemm_route_rows(T, top, E, _ptr(expert), _ptr(offsets), _ptr(row), _ptr(source), _ptr(workspace),
+                             workspace_bytes, _stream(stream))
+    return _check(st, "gemm_route_rows")
+
+
+def gemm_route_rows_workspace_size(T, top, E) -> int:
+    """Bytes of workspace gemm_route_rows needs (0 for few pairs)."""
+    return int(lib.gemm_route_rows_workspace_size(T, top, E))
+
+
+def gemm_rows_gather(R, D, T, top, dtype, X, ldx, source, weight, Y, ldy, stream=None) -> int:
+    """Y[r] = weight[source[r]] * X[source[r] // top] (weight None: a copy): tokens' rows into expert order."""
+    st = lib.gemm_rows_gather(R, D, T, top, dtype, _ptr(X), ldx, _ptr(source), _ptr(weight), _ptr(Y), ldy,
+                              _stream(stream))
+    return _check(st, "gemm_rows_gather")
+
+
+def gemm_rows_combine(T, top, D, R, y_dtype, Y, ldy, row, weight, beta, out_dtype, Out, ldo, stream=None) -> int:
+    """Out[t] = sum over slots of weight[t][s] * Y[row[t][s]] + beta * Out[t] (weight None: 1)."""
+    st = lib.gemm_rows_combine(T, top, D, R, y_dtype, _ptr(Y), ldy, _ptr(row), _ptr(weight), beta, out_dtype, _ptr(Out),
+                               ldo, _stream(stream))
+    return _check(st, "gemm_rows_combine")
+
+
+def gemm_rows_combine_grad(T, top, D, R, d_dtype, dOut, ldd, y_dtype, Y, ldy, row, weight, dY, lddy, dweight=None,
+                           stream=None) -> int:
+    """Gradients of gemm_rows_combine: dY[row[t][s]] = weight[t][s] * dOut[t] and dweight[t][s] = dOut[t] . Y[row]
+    (either may be None)."""
+    st = lib.gemm_rows_combine_grad(T, top, D, R, d_dtype, _ptr(dOut), ldd, y_dtype, _ptr(Y), ldy, _ptr(row),
+                                    _ptr(weight), _ptr(dY), lddy, _ptr(dweight), _stream(stream))
+    return _check(st, "gemm_rows_combine_grad")
 
 
 def gemm_last_launch() -> dict:

@@ -1731,6 +1731,392 @@ gemm_status_t gemm_i8_quantize(int64_t M, int64_t K, gemm_dtype_t x_dtype, const
                : GEMM_ERR_CUDA;
 }
 
+// ------------------------------------------- block-scaled rows and experts --
+
+static bool mx_elem_ok(int elem) { return elem == GEMM_MX_E4M3 || elem == GEMM_MX_E2M1; }
+static bool value_dtype(int dt) { return dt == GEMM_F32 || dt == GEMM_F16 || dt == GEMM_BF16; }
+
+// Rules that quantisation and its inverse share: M rows of K values (V, pitch ldv, type dt) and of codes and scales.
+static gemm_status_t mx_rows_rules(int64_t M, int64_t K, int elem, int dt, const void *V, int64_t ldv, const void *Q,
+                                   int64_t ldq, const uint8_t *scale, int64_t lds, bool *noop) {
+    *noop = false;
+    if (M < 0 || K < 0 || !mx_elem_ok(elem) || !valid_dtype(dt)) return GEMM_ERR_INVALID_ARG;
+    if (!value_dtype(dt)) return GEMM_ERR_UNSUPPORTED;
+    if (K % 32 != 0) return GEMM_ERR_INVALID_ARG;
+    if (M == 0 || K == 0) {
+        *noop = true;
+        return GEMM_OK;
+    }
+    if (M > kGroupedMaxExtent || K > kGroupedMaxExtent || M > (int64_t(1) << 43) / K) return GEMM_ERR_UNSUPPORTED;
+    if (V == nullptr || Q == nullptr || scale == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (ldv < K || ldq < K || lds < K / 32 || (elem == GEMM_MX_E2M1 && ldq % 2 != 0)) return GEMM_ERR_INVALID_ARG;
+    return GEMM_OK;
+}
+
+// Whether rows of `pitch` bytes all start at multiples of n bytes.
+static bool rows_at(const void *p, int64_t rows, int64_t pitch, int n) {
+    return reinterpret_cast<uintptr_t>(p) % n == 0 && (rows == 1 || pitch % n == 0);
+}
+
+gemm_status_t gemm_mx_quantize(int64_t M, int64_t K, gemm_mx_elem_t elem, gemm_dtype_t x_dtype, const void *X,
+                               int64_t ldx, int64_t rows_x, const int32_t *source, int64_t top, void *Q, int64_t ldq,
+                               uint8_t *scale, int64_t lds, gemm_stream_t stream) {
+    bool noop;
+    gemm_status_t st = mx_rows_rules(M, K, elem, x_dtype, X, ldx, Q, ldq, scale, lds, &noop);
+    if (st != GEMM_OK) return st;
+    if (rows_x < 0 || (source == nullptr ? rows_x < M : top < 1)) return GEMM_ERR_INVALID_ARG;
+    if (noop || rows_x == 0) return GEMM_OK;
+    if (rows_x > kGroupedMaxExtent || (source != nullptr && top > INT32_MAX)) return GEMM_ERR_UNSUPPORTED;
+    const int es = elem_bytes(x_dtype), per_byte = elem == GEMM_MX_E2M1 ? 2 : 1;
+    if (!elements_aligned({{X, es}, {source, 4}})) return GEMM_ERR_MISALIGNED;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if ((st = check_range(X, extent_bytes(1, 0, rows_x, ldx, K, 1, es))) != GEMM_OK) return st;
+    if (source != nullptr && (st = check_range(source, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
+    if ((st = check_range(Q, extent_bytes(1, 0, M, ldq / per_byte, K / per_byte, 1, 1))) != GEMM_OK) return st;
+    if ((st = check_range(scale, extent_bytes(1, 0, M, lds, K / 32, 1, 1))) != GEMM_OK) return st;
+    MxQuantArgs a = {};
+    a.M = static_cast<int>(M);
+    a.K = static_cast<int>(K);
+    a.X = X; a.ldx = ldx; a.rows_x = rows_x;
+    a.source = source;
+    a.top = source != nullptr ? static_cast<int>(top) : 1;
+    a.Q = static_cast<unsigned char *>(Q); a.q_pitch = ldq / per_byte;
+    a.scale = scale; a.s_pitch = lds;
+    return launch_mx_quantize(elem, x_dtype, a, rows_at(X, rows_x, ldx * es, 16),
+                              rows_at(Q, M, a.q_pitch, 8 / per_byte), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status_t gemm_mx_dequantize(int64_t M, int64_t K, gemm_mx_elem_t elem, const void *Q, int64_t ldq,
+                                 const uint8_t *scale, int64_t lds, gemm_dtype_t y_dtype, void *Y, int64_t ldy,
+                                 gemm_stream_t stream) {
+    bool noop;
+    gemm_status_t st = mx_rows_rules(M, K, elem, y_dtype, Y, ldy, Q, ldq, scale, lds, &noop);
+    if (st != GEMM_OK || noop) return st;
+    const int es = elem_bytes(y_dtype), per_byte = elem == GEMM_MX_E2M1 ? 2 : 1;
+    if (!elements_aligned({{Y, es}})) return GEMM_ERR_MISALIGNED;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if ((st = check_range(Y, extent_bytes(1, 0, M, ldy, K, 1, es))) != GEMM_OK) return st;
+    if ((st = check_range(Q, extent_bytes(1, 0, M, ldq / per_byte, K / per_byte, 1, 1))) != GEMM_OK) return st;
+    if ((st = check_range(scale, extent_bytes(1, 0, M, lds, K / 32, 1, 1))) != GEMM_OK) return st;
+    MxQuantArgs a = {};
+    a.M = static_cast<int>(M);
+    a.K = static_cast<int>(K);
+    a.Q = static_cast<unsigned char *>(const_cast<void *>(Q)); a.q_pitch = ldq / per_byte;
+    a.scale = const_cast<uint8_t *>(scale); a.s_pitch = lds;
+    a.Y = Y; a.ldy = ldy;
+    return launch_mx_dequantize(elem, y_dtype, a, rows_at(Q, M, a.q_pitch, 8 / per_byte), rows_at(Y, M, ldy * es, 16),
+                                reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// 3-D map of scales (blocks, rows, groups), boxes of 16 x box_rows x 1 bytes, no swizzle, zero fill.
+static gemm_status_t encode_scales(CUtensorMap *map, const uint8_t *base, int64_t blocks, int64_t rows, int64_t pitch,
+                                   int64_t groups, int64_t stride, uint32_t box_rows, int dims_n) {
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(blocks), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(groups)};
+    cuuint64_t strides[2] = {rows == 1 ? 16 : static_cast<cuuint64_t>(pitch),
+                             groups == 1 ? 16 : static_cast<cuuint64_t>(stride)};
+    cuuint32_t box[3] = {16, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = driver_fns().encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, static_cast<cuuint32_t>(dims_n),
+                                     const_cast<uint8_t *>(base), dims, strides, box, estr,
+                                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                                     CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status_t gemm_mx_grouped(int64_t G, int64_t M, int64_t N, int64_t K, gemm_mx_elem_t elem, const int32_t *offsets,
+                              const void *X, int64_t ldx, const uint8_t *x_scale, int64_t ldxs, const void *W,
+                              int64_t w_stride_g, int64_t ldw, const uint8_t *w_scale, int64_t ws_stride_g,
+                              int64_t ldws, void *C, int64_t ldc, gemm_dtype_t c_dtype, float alpha, float beta,
+                              const float *bias, gemm_epilogue_t epilogue, const float *row_scale,
+                              gemm_stream_t stream) {
+    bool noop;
+    gemm_status_t st = grouped_rules(G, M, N, K, C, ldc, c_dtype, bias, epilogue, &noop);
+    if (st != GEMM_OK) return st;
+    if (!mx_elem_ok(elem) || K % 32 != 0) return GEMM_ERR_INVALID_ARG;
+    if (noop) return record(GEMM_OK, gemm_launch_info_t{});
+    if (offsets == nullptr && G != 1) return GEMM_ERR_INVALID_ARG;
+    const bool product = K > 0 && alpha != 0.0f;
+    const int64_t per_byte = elem == GEMM_MX_E2M1 ? 2 : 1, blocks = K / 32, k_bytes = K / per_byte;
+    if (product) {
+        if (X == nullptr || W == nullptr || x_scale == nullptr || w_scale == nullptr) return GEMM_ERR_INVALID_ARG;
+        if (ldx < K || ldw < K || ldxs < blocks || ldws < blocks || w_stride_g < 0 || ws_stride_g < 0)
+            return GEMM_ERR_INVALID_ARG;
+        if (ldx % per_byte != 0 || ldw % per_byte != 0 || w_stride_g % per_byte != 0) return GEMM_ERR_INVALID_ARG;
+        if (G > 1 && (w_stride_g == 0 || ws_stride_g == 0)) return GEMM_ERR_INVALID_ARG;
+    }
+    const int64_t x_pitch = ldx / per_byte, w_pitch = ldw / per_byte, w_stride = w_stride_g / per_byte;
+    if (!elements_aligned({{offsets, 4}, {C, elem_bytes(c_dtype)}, {epilogue != GEMM_EPI_NONE ? bias : nullptr, 4}}) ||
+        (product && !elements_aligned({{row_scale, 4}})))
+        return GEMM_ERR_MISALIGNED;
+    if (product && (!tma_ok(X, M, 1, x_pitch, 1) || !tma_ok(W, N, 1, w_pitch, 1) || !tma_ok(x_scale, M, 1, ldxs, 1) ||
+                    !tma_ok(w_scale, N, 1, ldws, 1) || !group_stride_ok(G, w_stride, 1) ||
+                    !group_stride_ok(G, ws_stride_g, 1)))
+        return GEMM_ERR_MISALIGNED;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if (offsets != nullptr && (st = check_range(offsets, static_cast<size_t>(G + 1) * 4)) != GEMM_OK) return st;
+    if ((st = check_range(C, extent_bytes(1, 0, M, ldc, N, 1, elem_bytes(c_dtype)))) != GEMM_OK) return st;
+    if (epilogue != GEMM_EPI_NONE && (st = check_range(bias, static_cast<size_t>(G) * N * 4)) != GEMM_OK) return st;
+    GtcArgs t = {};
+    MxgMaps m = {};
+    if (product) {
+        if ((st = check_range(X, extent_bytes(1, 0, M, x_pitch, k_bytes, 1, 1))) != GEMM_OK) return st;
+        if ((st = check_range(x_scale, extent_bytes(1, 0, M, ldxs, blocks, 1, 1))) != GEMM_OK) return st;
+        if ((st = check_range(W, extent_bytes(G, w_stride, N, w_pitch, k_bytes, 1, 1))) != GEMM_OK) return st;
+        if ((st = check_range(w_scale, extent_bytes(G, ws_stride_g, N, ldws, blocks, 1, 1))) != GEMM_OK) return st;
+        if (row_scale != nullptr && (st = check_range(row_scale, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
+        if ((st = encode_3d(&m.w, kDtI8, W, k_bytes, N, w_pitch, G, w_stride, 128)) != GEMM_OK) return st;
+        for (uint32_t i = 0; i < kMxgMost / 32; ++i)
+            if ((st = encode_3d(&m.x[i], kDtI8, X, k_bytes, M, x_pitch, 1, 0, 16 * (i + 1))) != GEMM_OK) return st;
+        if ((st = encode_scales(&m.ws, w_scale, blocks, N, ldws, G, ws_stride_g, 128, 3)) != GEMM_OK) return st;
+        for (uint32_t i = 0; i < 4; ++i)
+            if ((st = encode_scales(&m.xs[i], x_scale, blocks, M, ldxs, 1, 0, 32u << i, 2)) != GEMM_OK) return st;
+        t.row_scale = row_scale;
+    }
+    t.G = static_cast<int>(G); t.T = static_cast<int>(M); t.F = static_cast<int>(N);
+    t.K = product ? static_cast<int>(K) : 0;
+    t.tiles_f = static_cast<int>((N + 255) / 256);
+    t.offsets = offsets;
+    t.C = C; t.ldc = ldc;
+    t.bias = bias;
+    t.alpha = alpha; t.beta = beta; t.epi = epilogue;
+    t.most = kMxgMost;
+    t.status = dev->status;
+    gemm_launch_info_t info = {};
+    const int64_t row_tiles = M / t.most + std::min(G, M);  // at most: every full tile, and one more for a group's rest
+    const int clusters = pair_clusters(dev, row_tiles * t.tiles_f, &info);
+    info.bn = t.most;
+    if (!product) info.path = GEMM_PATH_EPILOGUE_ONLY;
+    return record(launch_mx_grouped(elem, c_dtype, m, t, clusters, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+                      ? GEMM_OK : GEMM_ERR_CUDA, info);
+}
+
+// ----------------------------------------------------------------- routing --
+
+gemm_status_t gemm_route(int64_t T, int64_t E, int64_t top, gemm_dtype_t l_dtype, const void *logits, int64_t ldl,
+                         const float *bias, gemm_score_t score, int64_t groups, int64_t top_groups, int64_t group_sum,
+                         int renormalise, float scale, int32_t *expert, float *weight, gemm_stream_t stream) {
+    if (T < 0 || E < 1 || top < 1 || groups < 1 || !valid_dtype(l_dtype)) return GEMM_ERR_INVALID_ARG;
+    if (score != GEMM_SCORE_SOFTMAX && score != GEMM_SCORE_SIGMOID) return GEMM_ERR_INVALID_ARG;
+    if (E % groups != 0 || (groups > 1 && (top_groups < 1 || top_groups > groups || group_sum < 1 || group_sum > 2)))
+        return GEMM_ERR_INVALID_ARG;
+    if (!value_dtype(l_dtype) || E > GEMM_MAX_GROUPS || top > kRouteMaxTop || groups > kRouteMaxGroups)
+        return GEMM_ERR_UNSUPPORTED;
+    if (T == 0) return GEMM_OK;
+    if (T > GEMM_ROUTE_MAX_PAIRS / top) return GEMM_ERR_UNSUPPORTED;
+    if (logits == nullptr || expert == nullptr || weight == nullptr || ldl < E) return GEMM_ERR_INVALID_ARG;
+    const int es = elem_bytes(l_dtype);
+    if (!elements_aligned({{logits, es}, {bias, 4}, {expert, 4}, {weight, 4}})) return GEMM_ERR_MISALIGNED;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    gemm_status_t st;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if ((st = check_range(logits, extent_bytes(1, 0, T, ldl, E, 1, es))) != GEMM_OK) return st;
+    if (bias != nullptr && (st = check_range(bias, static_cast<size_t>(E) * 4)) != GEMM_OK) return st;
+    if ((st = check_range(expert, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if ((st = check_range(weight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    RouteArgs a = {};
+    a.T = T;
+    a.E = static_cast<int>(E); a.top = static_cast<int>(top);
+    a.logits = logits; a.ldl = ldl;
+    a.bias = bias;
+    a.score = score;
+    a.groups = static_cast<int>(groups);
+    a.top_groups = static_cast<int>(top_groups);
+    a.group_sum = groups > 1 ? static_cast<int>(group_sum) : 1;
+    a.renorm = renormalise != 0;
+    a.by_logit = bias == nullptr && a.group_sum == 1;
+    a.vec = rows_at(logits, T, ldl * es, 16) && E % (16 / es) == 0;
+    a.scale = scale;
+    a.expert = expert; a.weight = weight;
+    return launch_route(l_dtype, a, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status_t gemm_route_grad(int64_t T, int64_t E, int64_t top, gemm_dtype_t l_dtype, const void *logits, int64_t ldl,
+                              gemm_score_t score, int renormalise, float scale, const int32_t *expert,
+                              const float *dweight, void *dlogits, int64_t ldd, gemm_stream_t stream) {
+    if (T < 0 || E < 1 || top < 1 || !valid_dtype(l_dtype)) return GEMM_ERR_INVALID_ARG;
+    if (score != GEMM_SCORE_SOFTMAX && score != GEMM_SCORE_SIGMOID) return GEMM_ERR_INVALID_ARG;
+    if (!value_dtype(l_dtype) || E > GEMM_MAX_GROUPS || top > kRouteMaxTop) return GEMM_ERR_UNSUPPORTED;
+    if (T == 0) return GEMM_OK;
+    if (T > GEMM_ROUTE_MAX_PAIRS / top) return GEMM_ERR_UNSUPPORTED;
+    if (logits == nullptr || expert == nullptr || dweight == nullptr || dlogits == nullptr || ldl < E || ldd < E)
+        return GEMM_ERR_INVALID_ARG;
+    const int es = elem_bytes(l_dtype);
+    if (!elements_aligned({{logits, es}, {dlogits, es}, {expert, 4}, {dweight, 4}})) return GEMM_ERR_MISALIGNED;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    gemm_status_t st;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if ((st = check_range(logits, extent_bytes(1, 0, T, ldl, E, 1, es))) != GEMM_OK) return st;
+    if ((st = check_range(dlogits, extent_bytes(1, 0, T, ldd, E, 1, es))) != GEMM_OK) return st;
+    if ((st = check_range(expert, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if ((st = check_range(dweight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    RouteGradArgs a = {};
+    a.T = T;
+    a.E = static_cast<int>(E); a.top = static_cast<int>(top);
+    a.logits = logits; a.ldl = ldl;
+    a.score = score;
+    a.renorm = renormalise != 0;
+    a.vec = rows_at(logits, T, ldl * es, 16) && E % (16 / es) == 0;
+    a.vec_out = rows_at(dlogits, T, ldd * es, 16) && E % (16 / es) == 0;
+    a.scale = scale;
+    a.expert = expert; a.dweight = dweight;
+    a.dlogits = dlogits; a.ldd = ldd;
+    return launch_route_grad(l_dtype, a, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+size_t gemm_route_rows_workspace_size(int64_t T, int64_t top, int64_t E) {
+    if (T <= 0 || top <= 0 || E <= 0 || E > GEMM_MAX_GROUPS || T > GEMM_ROUTE_MAX_PAIRS / top) return 0;
+    const int chunks = route_rows_chunks(T * top);
+    return chunks > 1 ? static_cast<size_t>(chunks) * E * 4 : 0;
+}
+
+gemm_status_t gemm_route_rows(int64_t T, int64_t top, int64_t E, const int32_t *expert, int32_t *offsets, int32_t *row,
+                              int32_t *source, void *workspace, size_t workspace_bytes, gemm_stream_t stream) {
+    if (T < 0 || top < 1 || E < 1 || offsets == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (E > GEMM_MAX_GROUPS || T > GEMM_ROUTE_MAX_PAIRS / top) return GEMM_ERR_UNSUPPORTED;
+    if (T > 0 && (expert == nullptr || source == nullptr)) return GEMM_ERR_INVALID_ARG;
+    if (!elements_aligned({{expert, 4}, {offsets, 4}, {row, 4}, {source, 4}})) return GEMM_ERR_MISALIGNED;
+    const size_t need = gemm_route_rows_workspace_size(T, top, E), pairs = static_cast<size_t>(T) * top * 4;
+    if (need > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 15u) != 0 ||
+                     workspace_bytes < need))
+        return GEMM_ERR_WORKSPACE;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    gemm_status_t st;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if ((st = check_range(offsets, static_cast<size_t>(E + 1) * 4)) != GEMM_OK) return st;
+    if ((st = check_range(expert, pairs)) != GEMM_OK) return st;
+    if ((st = check_range(source, pairs)) != GEMM_OK) return st;
+    if (row != nullptr && (st = check_range(row, pairs)) != GEMM_OK) return st;
+    if ((st = check_range(workspace, need)) != GEMM_OK) return st;
+    RouteRowsArgs a = {};
+    a.P = static_cast<int>(T * top); a.E = static_cast<int>(E);
+    a.expert = expert; a.offsets = offsets; a.row = row; a.source = source;
+    a.counts = static_cast<int *>(workspace);
+    return launch_route_rows(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+// ---------------------------------------------------------- rows of experts --
+
+// Sizes that the three calls share; *noop where there is nothing to do.
+static gemm_status_t rows_rules(int64_t T, int64_t top, int64_t D, int64_t R, int t1, int t2, bool *noop) {
+    *noop = false;
+    if (T < 0 || top < 1 || D < 0 || R < 0 || !valid_dtype(t1) || !valid_dtype(t2)) return GEMM_ERR_INVALID_ARG;
+    if (!value_dtype(t1) || !value_dtype(t2)) return GEMM_ERR_UNSUPPORTED;
+    if (T > GEMM_ROUTE_MAX_PAIRS / top || R > kGroupedMaxExtent || D > GEMM_ROWS_MAX_D) return GEMM_ERR_UNSUPPORTED;
+    *noop = D == 0;
+    return GEMM_OK;
+}
+
+gemm_status_t gemm_rows_gather(int64_t R, int64_t D, int64_t T, int64_t top, gemm_dtype_t dtype, const void *X,
+                               int64_t ldx, const int32_t *source, const float *weight, void *Y, int64_t ldy,
+                               gemm_stream_t stream) {
+    bool noop;
+    gemm_status_t st = rows_rules(T, top, D, R, dtype, dtype, &noop);
+    if (st != GEMM_OK) return st;
+    if (noop || R == 0 || T == 0) return GEMM_OK;
+    if (X == nullptr || Y == nullptr || source == nullptr || ldx < D || ldy < D) return GEMM_ERR_INVALID_ARG;
+    const int es = elem_bytes(dtype);
+    if (!elements_aligned({{X, es}, {Y, es}, {source, 4}, {weight, 4}})) return GEMM_ERR_MISALIGNED;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if ((st = check_range(X, extent_bytes(1, 0, T, ldx, D, 1, es))) != GEMM_OK) return st;
+    if ((st = check_range(Y, extent_bytes(1, 0, R, ldy, D, 1, es))) != GEMM_OK) return st;
+    if ((st = check_range(source, static_cast<size_t>(R) * 4)) != GEMM_OK) return st;
+    if (weight != nullptr && (st = check_range(weight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    RowsArgs a = {};
+    a.T = T; a.R = R; a.top = static_cast<int>(top); a.D = static_cast<int>(D);
+    a.X = const_cast<void *>(X); a.ldx = ldx;
+    a.Y = Y; a.ldy = ldy;
+    a.source = source; a.weight = weight;
+    const bool vec = rows_at(X, T, ldx * es, 16) && rows_at(Y, R, ldy * es, 16) && D * es % 16 == 0;
+    return launch_rows_gather(dtype, a, vec, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status_t gemm_rows_combine(int64_t T, int64_t top, int64_t D, int64_t R, gemm_dtype_t y_dtype, const void *Y,
+                                int64_t ldy, const int32_t *row, const float *weight, float beta,
+                                gemm_dtype_t out_dtype, void *Out, int64_t ldo, gemm_stream_t stream) {
+    bool noop;
+    gemm_status_t st = rows_rules(T, top, D, R, y_dtype, out_dtype, &noop);
+    if (st != GEMM_OK) return st;
+    if (y_dtype != out_dtype && y_dtype != GEMM_F32 && out_dtype != GEMM_F32) return GEMM_ERR_UNSUPPORTED;
+    if (noop || T == 0) return GEMM_OK;
+    if (Out == nullptr || row == nullptr || ldo < D || (R > 0 && (Y == nullptr || ldy < D))) return GEMM_ERR_INVALID_ARG;
+    const int es = elem_bytes(y_dtype), os = elem_bytes(out_dtype);
+    if (!elements_aligned({{R > 0 ? Y : nullptr, es}, {Out, os}, {row, 4}, {weight, 4}})) return GEMM_ERR_MISALIGNED;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if ((st = check_range(Y, extent_bytes(1, 0, R, ldy, D, 1, es))) != GEMM_OK) return st;
+    if ((st = check_range(Out, extent_bytes(1, 0, T, ldo, D, 1, os))) != GEMM_OK) return st;
+    if ((st = check_range(row, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if (weight != nullptr && (st = check_range(weight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    RowsArgs a = {};
+    a.T = T; a.R = R; a.top = static_cast<int>(top); a.D = static_cast<int>(D);
+    a.X = Out; a.ldx = ldo;
+    a.Y = const_cast<void *>(Y); a.ldy = ldy;
+    a.row = row; a.weight = weight; a.beta = beta;
+    const bool vec = (R == 0 || rows_at(Y, R, ldy * es, 16)) && rows_at(Out, T, ldo * os, 16) && D * es % 16 == 0 &&
+                     D * os % 8 == 0;
+    return launch_rows_combine(y_dtype, out_dtype, a, vec, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
+gemm_status_t gemm_rows_combine_grad(int64_t T, int64_t top, int64_t D, int64_t R, gemm_dtype_t d_dtype,
+                                     const void *dOut, int64_t ldd, gemm_dtype_t y_dtype, const void *Y, int64_t ldy,
+                                     const int32_t *row, const float *weight, void *dY, int64_t lddy, float *dweight,
+                                     gemm_stream_t stream) {
+    bool noop;
+    gemm_status_t st = rows_rules(T, top, D, R, d_dtype, y_dtype, &noop);
+    if (st != GEMM_OK) return st;
+    if (d_dtype != y_dtype && d_dtype != GEMM_F32) return GEMM_ERR_UNSUPPORTED;
+    if (T == 0 || (dY == nullptr && dweight == nullptr) || (noop && dweight == nullptr)) return GEMM_OK;
+    const bool reads_y = R > 0 && D > 0 && dweight != nullptr, writes = R > 0 && D > 0 && dY != nullptr;
+    if (row == nullptr || (D > 0 && (dOut == nullptr || ldd < D)) || (reads_y && (Y == nullptr || ldy < D)) ||
+        (writes && lddy < D))
+        return GEMM_ERR_INVALID_ARG;
+    const int ds = elem_bytes(d_dtype), es = elem_bytes(y_dtype);
+    if (!elements_aligned({{D > 0 ? dOut : nullptr, ds}, {reads_y ? Y : nullptr, es}, {writes ? dY : nullptr, es},
+                           {row, 4}, {weight, 4}, {dweight, 4}}))
+        return GEMM_ERR_MISALIGNED;
+    if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    DeviceState *dev = nullptr;
+    if ((st = device_state(&dev)) != GEMM_OK) return st;
+    if ((st = check_range(dOut, extent_bytes(1, 0, T, ldd, D, 1, ds))) != GEMM_OK) return st;
+    if (reads_y && (st = check_range(Y, extent_bytes(1, 0, R, ldy, D, 1, es))) != GEMM_OK) return st;
+    if (writes && (st = check_range(dY, extent_bytes(1, 0, R, lddy, D, 1, es))) != GEMM_OK) return st;
+    const size_t pairs = static_cast<size_t>(T) * top * 4;
+    if ((st = check_range(row, pairs)) != GEMM_OK) return st;
+    if (weight != nullptr && (st = check_range(weight, pairs)) != GEMM_OK) return st;
+    if (dweight != nullptr && (st = check_range(dweight, pairs)) != GEMM_OK) return st;
+    RowsArgs a = {};
+    a.T = T; a.R = R; a.top = static_cast<int>(top); a.D = static_cast<int>(D);
+    a.X = const_cast<void *>(dOut); a.ldx = ldd;
+    a.Y = const_cast<void *>(Y); a.ldy = ldy;
+    a.row = row; a.weight = weight;
+    a.dY = writes ? dY : nullptr; a.lddy = lddy;
+    a.dweight = dweight;
+    const int widest = std::min(ds, es);  // 16 bytes of the narrower type hold the most values
+    const bool vec = (D == 0 || rows_at(dOut, T, ldd * ds, 16)) && (!reads_y || rows_at(Y, R, ldy * es, 16)) &&
+                     (!writes || rows_at(dY, R, lddy * es, 16)) && D * widest % 16 == 0;
+    return launch_rows_combine_grad(d_dtype, y_dtype, a, vec, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMM_OK : GEMM_ERR_CUDA;
+}
+
 gemm_status_t gemm_wait_selftest(const unsigned int *never_set, uint64_t limit_ns, gemm_stream_t stream) {
     if (never_set == nullptr || limit_ns == 0 || limit_ns > 1000000000ull) return GEMM_ERR_INVALID_ARG;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;

@@ -1,0 +1,403 @@
+// gemm_rows.cu -- the rows of a mixture of experts: the (token, expert) pairs
+// sorted by expert, rows copied from token order into that order, the weighted
+// sum back, and the gradients of both.
+//
+// A pair is p = t top + s (token t, slot s).  `row` holds each pair's place in
+// expert order and `source` each place's pair; -1: none (a slot without an
+// expert, a place behind the last pair).
+#include "epilogue.cuh"
+#include "kernel_args.h"
+
+namespace gb300 {
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+// ------------------------------------------------------------------ sorting --
+// A counting sort in which nothing depends on the order of atomics: pairs of one
+// expert stay in their order.  Many pairs: a first kernel counts each chunk's
+// experts, the second gives every chunk its own place in each expert's range and
+// its warps theirs, and each pair the number of equal ones before it in its warp
+// (match).  Few pairs: the second kernel alone, one block.
+
+constexpr int kCountThreads = 256;
+
+__global__ void __launch_bounds__(kCountThreads) route_count_kernel(const __grid_constant__ RouteRowsArgs a) {
+    extern __shared__ int counts[];
+    for (int e = threadIdx.x; e < a.E; e += kCountThreads) counts[e] = 0;
+    __syncthreads();
+    const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.P);
+    for (int p = begin + static_cast<int>(threadIdx.x); p < end; p += kCountThreads) {
+        const int e = __ldg(a.expert + p);
+        if (static_cast<unsigned>(e) < static_cast<unsigned>(a.E)) atomicAdd(&counts[e], 1);
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < a.E; e += kCountThreads)
+        a.counts[static_cast<long long>(blockIdx.x) * a.E + e] = counts[e];
+}
+
+// Pairs begin .. end - 1 of one warp, 32 at a time: f(pair, expert, lanes of the same expert), expert -1 where there
+// is none.
+template <typename F>
+__device__ __forceinline__ void warp_pairs(const RouteRowsArgs &a, int begin, int end, F f) {
+    const int lane = threadIdx.x & 31;
+    for (int p0 = begin; p0 < end; p0 += 32) {
+        const int p = p0 + lane;
+        int e = p < end ? __ldg(a.expert + p) : -1;
+        if (static_cast<unsigned>(e) >= static_cast<unsigned>(a.E)) e = -1;
+        f(p, e, __match_any_sync(kAll, e));
+    }
+}
+
+__global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant__ RouteRowsArgs a) {
+    extern __shared__ int smem[];
+    const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int *first = smem;              // E + 1: pairs of the experts before
+    int *own = smem + a.E + 1;      // warps x E: counts, then places
+    for (int i = threadIdx.x; i < warps * a.E; i += blockDim.x) own[i] = 0;
+    __syncthreads();
+    const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.P);
+    const int per = (a.chunk + warps * 32 - 1) / (warps * 32) * 32;  // pairs of a warp
+    const int w0 = min(begin + warp * per, end), w1 = min(w0 + per, end);
+    int *mine = own + warp * a.E;
+    warp_pairs(a, w0, w1, [&](int, int e, unsigned same) {
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    });
+    __syncthreads();
+    // every expert's total, and what lies before this chunk
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        int before = 0, total = 0;
+        if (gridDim.x > 1) {
+            for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
+                const int n = __ldg(a.counts + static_cast<long long>(c) * a.E + e);
+                before += c < static_cast<int>(blockIdx.x) ? n : 0;
+                total += n;
+            }
+        } else {
+            for (int w = 0; w < warps; ++w) total += own[w * a.E + e];
+        }
+        int at = before;
+        for (int w = 0; w < warps; ++w) {
+            const int n = own[w * a.E + e];
+            own[w * a.E + e] = at;
+            at += n;
+        }
+        first[e + 1] = total;
+    }
+    if (threadIdx.x == 0) first[0] = 0;
+    __syncthreads();
+    if (warp == 0) {
+        int base = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            const int e = e0 + lane;
+            int v = e < a.E ? first[e + 1] : 0;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(kAll, v, d);
+                if (lane >= d) v += o;
+            }
+            if (e < a.E) first[e + 1] = base + v;
+            base += __shfl_sync(kAll, v, 31);
+        }
+    }
+    __syncthreads();
+    if (blockIdx.x == 0)
+        for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.offsets[e] = first[e];
+    warp_pairs(a, w0, w1, [&](int p, int e, unsigned same) {
+        int at = -1;
+        if (e >= 0) {
+            at = first[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
+            a.source[at] = p;
+        }
+        if (p < w1 && a.row != nullptr) a.row[p] = at;
+        __syncwarp();
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    });
+    // the places behind the last pair
+    for (int r = first[a.E] + static_cast<int>(blockIdx.x * blockDim.x + threadIdx.x); r < a.P;
+         r += static_cast<int>(gridDim.x * blockDim.x))
+        a.source[r] = -1;
+}
+
+// ----------------------------------------------------------------- movement --
+// All three are bound by HBM; what they read and write, they do in 16-byte
+// pieces where bases and pitches allow.  Sums run in fp32 in the order of the
+// slots.
+
+constexpr int kMoveThreads = 256;
+
+// A piece of a row: 16 bytes (V) or one element.
+template <int DT, bool V> struct Piece {
+    static constexpr int N = Vec16<DT>::kPerVec;
+    static __device__ __forceinline__ void load(const void *row, long long i, float (&f)[N]) {
+        Vec16<DT>::unpack(__ldg(static_cast<const uint4 *>(row) + i), f);
+    }
+    static __device__ __forceinline__ void store(void *row, long long i, const float (&f)[N]) {
+        static_cast<uint4 *>(row)[i] = Vec16<DT>::pack(f);
+    }
+};
+template <int DT> struct Piece<DT, false> {
+    static constexpr int N = 1;
+    using T = typename Elem<DT>::T;
+    static __device__ __forceinline__ void load(const void *row, long long i, float (&f)[1]) {
+        f[0] = Elem<DT>::load(static_cast<const T *>(row) + i);
+    }
+    static __device__ __forceinline__ void store(void *row, long long i, const float (&f)[1]) {
+        static_cast<T *>(row)[i] = Elem<DT>::cvt(f[0]);
+    }
+};
+
+template <int DT>
+__device__ __forceinline__ const char *row_at(const void *base, long long row, long long ld) {
+    return static_cast<const char *>(base) + row * ld * static_cast<long long>(sizeof(typename Elem<DT>::T));
+}
+template <int DT>
+__device__ __forceinline__ char *row_at(void *base, long long row, long long ld) {
+    return static_cast<char *>(base) + row * ld * static_cast<long long>(sizeof(typename Elem<DT>::T));
+}
+
+// Y[r] = w[source[r]] X[source[r] / top]; places without a pair stay as they are.
+template <int DT, bool V>
+__global__ void __launch_bounds__(kMoveThreads) rows_gather_kernel(const __grid_constant__ RowsArgs a) {
+    using P = Piece<DT, V>;
+    const int pieces = a.D / P::N, tid = threadIdx.x;
+    for (long long r = blockIdx.x; r < a.R; r += gridDim.x) {
+        const int p = __ldg(a.source + r);
+        if (static_cast<unsigned>(p) >= static_cast<unsigned>(a.T) * static_cast<unsigned>(a.top)) continue;
+        const float w = a.weight != nullptr ? __ldg(a.weight + p) : 1.0f;
+        const void *x = row_at<DT>(a.X, p / a.top, a.ldx);
+        void *y = row_at<DT>(a.Y, r, a.ldy);
+#pragma unroll 4
+        for (int i = tid; i < pieces; i += kMoveThreads) {
+            float f[P::N];
+            P::load(x, i, f);
+            if (a.weight != nullptr) {
+#pragma unroll
+                for (int j = 0; j < P::N; ++j) f[j] *= w;
+            }
+            P::store(y, i, f);
+        }
+    }
+}
+
+constexpr int kSlots = 8;  // rows in flight per piece
+
+// Out[t] = sum_s w[t][s] Y[row[t][s]] + beta Out[t]; slots without a row add nothing.
+template <int YT, int OT, bool V>
+__global__ void __launch_bounds__(kMoveThreads) rows_combine_kernel(const __grid_constant__ RowsArgs a) {
+    using P = Piece<YT, V>;
+    using O = Piece<OT, V>;
+    constexpr int OV = P::N / O::N;  // pieces of the output per piece of Y: 1, 2, or 0 for half a piece
+    const int pieces = a.D / P::N;
+    const long long t = blockIdx.x;
+    const int i = blockIdx.y * kMoveThreads + threadIdx.x;
+    if (i >= pieces) return;
+    float acc[P::N];
+    char *out = row_at<OT>(a.X, t, a.ldx) + static_cast<long long>(i) * P::N * sizeof(typename Elem<OT>::T);
+#pragma unroll
+    for (int j = 0; j < P::N; ++j) acc[j] = 0.0f;
+    for (int s0 = 0; s0 < a.top; s0 += kSlots) {
+        int r[kSlots];
+        float w[kSlots], f[kSlots][P::N];
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+            r[s] = s0 + s < a.top ? __ldg(a.row + t * a.top + s0 + s) : -1;
+            if (static_cast<unsigned>(r[s]) >= static_cast<unsigned>(a.R)) r[s] = -1;
+            w[s] = a.weight != nullptr && r[s] >= 0 ? __ldg(a.weight + t * a.top + s0 + s) : 1.0f;
+        }
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+            if (r[s] >= 0) P::load(row_at<YT>(a.Y, r[s], a.ldy), i, f[s]);
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s)
+            if (r[s] >= 0) {
+#pragma unroll
+                for (int j = 0; j < P::N; ++j) acc[j] = fmaf(w[s], f[s][j], acc[j]);
+            }
+    }
+    if constexpr (!V) {
+        if (a.beta != 0.0f) acc[0] = fmaf(a.beta, Elem<OT>::load(reinterpret_cast<typename Elem<OT>::T *>(out)), acc[0]);
+        *reinterpret_cast<typename Elem<OT>::T *>(out) = Elem<OT>::cvt(acc[0]);
+    } else if constexpr (OV >= 1) {
+#pragma unroll
+        for (int v = 0; v < OV; ++v) {
+            float o[O::N];
+            if (a.beta != 0.0f) {
+                Vec16<OT>::unpack(reinterpret_cast<const uint4 *>(out)[v], o);
+#pragma unroll
+                for (int j = 0; j < O::N; ++j) acc[v * O::N + j] = fmaf(a.beta, o[j], acc[v * O::N + j]);
+            }
+#pragma unroll
+            for (int j = 0; j < O::N; ++j) o[j] = acc[v * O::N + j];
+            O::store(out, v, o);
+        }
+    } else {  // fp32 rows to 16 bits: four values, 8 bytes
+        using T = typename Elem<OT>::T;
+        T *o = reinterpret_cast<T *>(out);
+        if (a.beta != 0.0f) {
+#pragma unroll
+            for (int j = 0; j < P::N; ++j) acc[j] = fmaf(a.beta, Elem<OT>::load(o + j), acc[j]);
+        }
+        T four[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) four[j] = Elem<OT>::cvt(acc[j]);
+        *reinterpret_cast<uint2 *>(o) = *reinterpret_cast<const uint2 *>(four);
+    }
+}
+
+// dY[row] = w dOut[t], dweight[t][s] = dOut[t] . Y[row]; slots without a row: dweight 0.
+template <int DT, int YT, bool V>
+__global__ void __launch_bounds__(kMoveThreads) rows_combine_grad_kernel(const __grid_constant__ RowsArgs a) {
+    using P = Piece<DT, V>;
+    using Q = Piece<YT, V>;
+    // the widest piece of the two is the step: HV of P, YV of Q
+    constexpr int N = P::N > Q::N ? P::N : Q::N, HV = N / P::N, YV = N / Q::N;
+    __shared__ float part[kMoveThreads / 32][kSlots];
+    const int steps = a.D / N, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
+    const long long t = blockIdx.x;
+    const void *d = row_at<DT>(a.X, t, a.ldx);
+    for (int s0 = 0; s0 < a.top; s0 += kSlots) {
+        int r[kSlots];
+        float w[kSlots], dot[kSlots];
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) {
+            r[s] = s0 + s < a.top ? __ldg(a.row + t * a.top + s0 + s) : -1;
+            if (static_cast<unsigned>(r[s]) >= static_cast<unsigned>(a.R)) r[s] = -1;
+            w[s] = a.weight != nullptr && r[s] >= 0 ? __ldg(a.weight + t * a.top + s0 + s) : 1.0f;
+            dot[s] = 0.0f;
+        }
+        for (int i = tid; i < steps; i += n) {
+            float g[N];
+#pragma unroll
+            for (int v = 0; v < HV; ++v) {
+                float h[P::N];
+                P::load(d, static_cast<long long>(i) * HV + v, h);
+#pragma unroll
+                for (int j = 0; j < P::N; ++j) g[v * P::N + j] = h[j];
+            }
+            if (a.dweight != nullptr) {
+                float y[kSlots][Q::N];
+#pragma unroll
+                for (int v = 0; v < YV; ++v) {
+#pragma unroll
+                    for (int s = 0; s < kSlots; ++s)
+                        if (r[s] >= 0) Q::load(row_at<YT>(a.Y, r[s], a.ldy), static_cast<long long>(i) * YV + v, y[s]);
+#pragma unroll
+                    for (int s = 0; s < kSlots; ++s)
+                        if (r[s] >= 0) {
+#pragma unroll
+                            for (int j = 0; j < Q::N; ++j) dot[s] = fmaf(g[v * Q::N + j], y[s][j], dot[s]);
+                        }
+                }
+            }
+            if (a.dY != nullptr) {
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s)
+                    if (r[s] >= 0) {
+#pragma unroll
+                        for (int v = 0; v < YV; ++v) {
+                            float o[Q::N];
+#pragma unroll
+                            for (int j = 0; j < Q::N; ++j) o[j] = w[s] * g[v * Q::N + j];
+                            Q::store(row_at<YT>(a.dY, r[s], a.lddy), static_cast<long long>(i) * YV + v, o);
+                        }
+                    }
+            }
+        }
+        if (a.dweight != nullptr) {
+#pragma unroll
+            for (int s = 0; s < kSlots; ++s) {
+                float v = dot[s];
+#pragma unroll
+                for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(kAll, v, k);
+                if (lane == 0) part[warp][s] = v;
+            }
+            __syncthreads();
+            if (tid < kSlots && s0 + tid < a.top) {
+                float v = 0.0f;
+                for (int k = 0; k < n >> 5; ++k) v += part[k][tid];
+                a.dweight[t * a.top + s0 + tid] = v;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+template <int YT, int OT>
+cudaError_t launch_combine(const RowsArgs &a, bool vec, cudaStream_t s) {
+    const int pieces = vec ? a.D / Vec16<YT>::kPerVec : a.D;
+    const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>((pieces + kMoveThreads - 1) / kMoveThreads));
+    if (vec)
+        rows_combine_kernel<YT, OT, true><<<grid, kMoveThreads, 0, s>>>(a);
+    else
+        rows_combine_kernel<YT, OT, false><<<grid, kMoveThreads, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+template <int DT, int YT>
+cudaError_t launch_grad(const RowsArgs &a, bool vec, cudaStream_t s) {
+    const int per = vec ? (Vec16<DT>::kPerVec > Vec16<YT>::kPerVec ? Vec16<DT>::kPerVec : Vec16<YT>::kPerVec) : 1;
+    const int want = (a.D / per + 31) / 32 * 32, n = want < 32 ? 32 : want < kMoveThreads ? want : kMoveThreads;
+    if (vec)
+        rows_combine_grad_kernel<DT, YT, true><<<static_cast<unsigned>(a.T), n, 0, s>>>(a);
+    else
+        rows_combine_grad_kernel<DT, YT, false><<<static_cast<unsigned>(a.T), n, 0, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_route_rows(const RouteRowsArgs &in, cudaStream_t s) {
+    RouteRowsArgs a = in;
+    const int chunks = route_rows_chunks(a.P);
+    a.chunk = static_cast<int>(((static_cast<long long>(a.P) + chunks - 1) / chunks + 31) / 32 * 32);
+    // as many warps as 32 KB of counts allow, and as there are pairs for
+    const int most = 8192 / a.E < 32 ? 8192 / a.E : 32, want = (a.chunk + 31) / 32;
+    const int warps = want < 1 ? 1 : want < most ? want : most;
+    if (chunks > 1) route_count_kernel<<<chunks, kCountThreads, a.E * 4, s>>>(a);
+    route_rows_kernel<<<chunks, 32 * warps, (a.E + 1 + warps * a.E) * 4, s>>>(a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_rows_gather(int dtype, const RowsArgs &a, bool vec, int sms, cudaStream_t s) {
+    const long long most = 32ll * sms;
+    const unsigned grid = static_cast<unsigned>(a.R < most ? a.R : most);
+#define GB300_GATHER(DT)                                                                \
+    if (dtype == DT) {                                                                  \
+        if (vec)                                                                        \
+            rows_gather_kernel<DT, true><<<grid, kMoveThreads, 0, s>>>(a);              \
+        else                                                                            \
+            rows_gather_kernel<DT, false><<<grid, kMoveThreads, 0, s>>>(a);             \
+        return cudaGetLastError();                                                      \
+    }
+    GB300_GATHER(kDtF32)
+    GB300_GATHER(kDtF16)
+    GB300_GATHER(kDtBF16)
+#undef GB300_GATHER
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_rows_combine(int y_dtype, int out_dtype, const RowsArgs &a, bool vec, cudaStream_t s) {
+    if (y_dtype == kDtF32 && out_dtype == kDtF32) return launch_combine<kDtF32, kDtF32>(a, vec, s);
+    if (y_dtype == kDtF32 && out_dtype == kDtF16) return launch_combine<kDtF32, kDtF16>(a, vec, s);
+    if (y_dtype == kDtF32 && out_dtype == kDtBF16) return launch_combine<kDtF32, kDtBF16>(a, vec, s);
+    if (y_dtype == kDtF16 && out_dtype == kDtF32) return launch_combine<kDtF16, kDtF32>(a, vec, s);
+    if (y_dtype == kDtF16 && out_dtype == kDtF16) return launch_combine<kDtF16, kDtF16>(a, vec, s);
+    if (y_dtype == kDtBF16 && out_dtype == kDtF32) return launch_combine<kDtBF16, kDtF32>(a, vec, s);
+    if (y_dtype == kDtBF16 && out_dtype == kDtBF16) return launch_combine<kDtBF16, kDtBF16>(a, vec, s);
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_rows_combine_grad(int d_dtype, int y_dtype, const RowsArgs &a, bool vec, cudaStream_t s) {
+    if (d_dtype == kDtF32 && y_dtype == kDtF32) return launch_grad<kDtF32, kDtF32>(a, vec, s);
+    if (d_dtype == kDtF32 && y_dtype == kDtF16) return launch_grad<kDtF32, kDtF16>(a, vec, s);
+    if (d_dtype == kDtF32 && y_dtype == kDtBF16) return launch_grad<kDtF32, kDtBF16>(a, vec, s);
+    if (d_dtype == kDtF16 && y_dtype == kDtF16) return launch_grad<kDtF16, kDtF16>(a, vec, s);
+    if (d_dtype == kDtBF16 && y_dtype == kDtBF16) return launch_grad<kDtBF16, kDtBF16>(a, vec, s);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gb300

@@ -177,6 +177,80 @@ struct GtcArgs {
     unsigned int *status;
 };
 
+// Routing to experts (gemm_route.cu).
+enum : int { kScoreSoftmax = 0, kScoreSigmoid = 1 };
+constexpr int kRouteMaxTop = 32;    // experts of a token: one lane each
+constexpr int kRouteMaxGroups = 32; // groups of experts: one lane each
+struct RouteArgs {
+    long long T;
+    int E, top;
+    const void *logits;
+    long long ldl;
+    const float *bias;              // E, NULL: 0
+    int score, groups, top_groups, group_sum;
+    bool renorm;
+    bool by_logit;                  // the selection scores have the logits' order
+    bool vec;                       // 16-byte loads of whole rows
+    float scale;
+    int *expert;                    // T x top
+    float *weight;
+    int group_size, group_lanes, stage;  // set by the launcher: experts of a group; lanes of one, 0: through
+                                         // shared memory, `stage` values per warp
+};
+struct RouteGradArgs {
+    long long T;
+    int E, top;
+    const void *logits;
+    long long ldl;
+    int score;
+    bool renorm, vec, vec_out;
+    float scale;
+    const int *expert;
+    const float *dweight;
+    void *dlogits;
+    long long ldd;
+};
+
+// Pairs sorted by expert (gemm_rows.cu).  P = T top; counts: chunks x E, unused by one chunk.
+struct RouteRowsArgs {
+    int P, E;
+    const int *expert;
+    int *offsets, *row, *source, *counts;
+    int chunk;                      // set by the launcher: pairs of a block
+};
+// Blocks of a sort: one up to 4096 pairs, where its own launch is all that a second one would save.
+constexpr int route_rows_chunks(long long P) {
+    return P <= 4096 ? 1 : P >= 144ll * 1024 ? 144 : static_cast<int>((P + 1023) / 1024);
+}
+
+// Movement of rows (gemm_rows.cu): X token order (R: rows of Y), Y expert order.  The output of a combination is X
+// (without const), its incoming gradient X and dY.
+struct RowsArgs {
+    long long T, R;
+    int top, D;
+    void *X, *Y;
+    long long ldx, ldy;
+    const int *source, *row;
+    const float *weight;            // T x top, NULL: 1
+    float beta;
+    void *dY;
+    long long lddy;
+    float *dweight;
+};
+
+// Rows to block-scaled numbers and back (gemm_mx_quantize.cu); pitches of codes and scales in bytes.
+struct MxQuantArgs {
+    int M, K;
+    const void *X;
+    long long ldx, rows_x;
+    const int *source;              // M, NULL: row i of X
+    int top;
+    unsigned char *Q, *scale;
+    long long q_pitch, s_pitch;
+    void *Y;
+    long long ldy;
+};
+
 // Launchers (each returns the launch's cudaError_t), defined by the kernel files.
 //   grouped products on the tensor cores, `clusters` SM pairs.  Every load is one box of 64 (128 bytes) of the
 //   contiguous index, 128-byte swizzle:
@@ -266,6 +340,27 @@ cudaError_t launch_mx_pair(int elem, int out, const CUtensorMap &ta, const CUten
                            const CUtensorMap &tsb, const MxArgs &args, int clusters, cudaStream_t stream);
 cudaError_t launch_mx_sf_pack(const unsigned char *src, long long rows, long long blocks, unsigned char *dst,
                               long long row_blocks, long long kc_count, cudaStream_t stream);
+// Block-scaled product grouped by expert, `clusters` SM pairs, tiles of args.most rows at most.  Operands as bytes:
+// w = (K, F, G) in boxes of 128 x 128, x[i] = (K, T) in boxes of 128 x 16 (i + 1), 128-byte swizzle; their scales
+// ws = (K / 32, F, G) in boxes of 16 x 128 and xs[i] = (K / 32, T) in boxes of 16 x (32 << i), not swizzled.
+constexpr int kMxgMost = 224;       // its widest row tile: two accumulators and the scales in tensor memory
+struct MxgMaps {
+    CUtensorMap w, x[kMxgMost / 32], ws, xs[4];
+};
+cudaError_t launch_mx_grouped(int elem, int out, const MxgMaps &maps, const GtcArgs &args, int clusters,
+                              cudaStream_t stream);
+//   rows to block-scaled numbers (x_vec: 16-byte reads of X; q_vec: 8 values' codes written at once) and back:
+cudaError_t launch_mx_quantize(int elem, int x_dtype, const MxQuantArgs &args, bool x_vec, bool q_vec,
+                               cudaStream_t stream);
+cudaError_t launch_mx_dequantize(int elem, int y_dtype, const MxQuantArgs &args, bool q_vec, bool y_vec,
+                                 cudaStream_t stream);
+//   routing and its gradient, the sort by expert, the movement of rows (vec: 16-byte pieces):
+cudaError_t launch_route(int l_dtype, const RouteArgs &args, int sms, cudaStream_t stream);
+cudaError_t launch_route_grad(int l_dtype, const RouteGradArgs &args, int sms, cudaStream_t stream);
+cudaError_t launch_route_rows(const RouteRowsArgs &args, cudaStream_t stream);
+cudaError_t launch_rows_gather(int dtype, const RowsArgs &args, bool vec, int sms, cudaStream_t stream);
+cudaError_t launch_rows_combine(int y_dtype, int out_dtype, const RowsArgs &args, bool vec, cudaStream_t stream);
+cudaError_t launch_rows_combine_grad(int d_dtype, int y_dtype, const RowsArgs &args, bool vec, cudaStream_t stream);
 cudaError_t launch_wait_selftest(const unsigned int *never_set, unsigned long long limit_ns, unsigned int *status,
                                  cudaStream_t stream);
 

@@ -745,6 +745,154 @@ gemm_status_t gemm_i8_quantize(int64_t M, int64_t K, gemm_dtype_t x_dtype, const
                                int64_t ldq, float *scale, gemm_stream_t stream);
 
 /*
+ * Block-scaled rows and products for experts: the formats of gemm_mx (a shared
+ * power of two per 32 k, E4M3 or E2M1 elements), with a pitch for the scales.
+ *
+ * gemm_mx_quantize -- M rows of K values (K a multiple of 32) to codes and scales:
+ *
+ *     scale[i][b] = clamp(floor(log2 max |x|) - emax + 127, 0, 254), the maximum over x[i][32 b .. 32 b + 31]
+ *     Q[i][k]     = round_even(x[i][k] * 2^(127 - scale)), saturated
+ *
+ * with emax 2 (E2M1, largest 6) or 8 (E4M3, largest 448).  A block of zeros gets
+ * scale 0, one that holds a NaN or an infinity 0xFF (NaN) and elements 0.
+ *   X, x_dtype     F32, F16 or BF16, rows_x rows, pitch ldx >= K.
+ *   source         int32[M] on the device, or NULL.  Row i is row source[i] / top
+ *                  of X (as gemm_route_rows has it); where that is none of X's
+ *                  rows (source[i] < 0, or past the last), row i of Q and its
+ *                  scales are left as they were.  NULL: row i of X (rows_x >= M,
+ *                  top not used).
+ *   Q, ldq         M rows of pitch ldq elements (even for E2M1), as gemm_mx's A.
+ *   scale, lds     M rows of K/32 codes, pitch lds bytes.
+ * Any alignment of bytes; 16-byte aligned rows of X are read faster, and gemm_mx_grouped
+ * wants pitches of Q and scale of whole 16 bytes.
+ *
+ * gemm_mx_dequantize -- Y[i][k] = cast(Q[i][k] * 2^(scale - 127)) as F32, F16 or
+ * BF16 (exact before the cast); e.g. weights for gemm_grouped's gradients.
+ */
+gemm_status_t gemm_mx_quantize(int64_t M, int64_t K, gemm_mx_elem_t elem, gemm_dtype_t x_dtype, const void *X,
+                               int64_t ldx, int64_t rows_x, const int32_t *source, int64_t top, void *Q, int64_t ldq,
+                               uint8_t *scale, int64_t lds, gemm_stream_t stream);
+gemm_status_t gemm_mx_dequantize(int64_t M, int64_t K, gemm_mx_elem_t elem, const void *Q, int64_t ldq,
+                                 const uint8_t *scale, int64_t lds, gemm_dtype_t y_dtype, void *Y, int64_t ldy,
+                                 gemm_stream_t stream);
+
+/*
+ * gemm_mx_grouped -- gemm_grouped over block-scaled codes: for every row r of group
+ * g and every column j,
+ *
+ *     C[r][j] = cast(act(alpha * row_scale[r] * sum_k x[r][k] w[g][j][k] + beta * C[r][j] + bias[g][j]))
+ *
+ *   X, ldx         M rows of K elements; x_scale: their scales, pitch ldxs bytes.
+ *   W, ldw         G matrices of N rows of K elements, w_stride_g elements apart;
+ *                  w_scale: theirs, pitch ldws, ws_stride_g bytes apart.
+ *   K              a multiple of 32.  Bases are 16-byte aligned, pitches and strides
+ *                  multiples of 16 bytes (those of a single row or matrix are not
+ *                  used), else GEMM_ERR_MISALIGNED; with G > 1 the strides between
+ *                  matrices are positive.
+ *   offsets        as in gemm_grouped; NULL with G == 1: one group of all rows.
+ *   C, bias, row_scale, epilogue, alpha, beta: as in gemm_grouped.  K == 0 or
+ *                  alpha == 0 reads neither operands, scales nor row_scale.
+ * No workspace.  fp32 sums; errors as gemm_grouped.
+ */
+gemm_status_t gemm_mx_grouped(int64_t G, int64_t M, int64_t N, int64_t K, gemm_mx_elem_t elem, const int32_t *offsets,
+                              const void *X, int64_t ldx, const uint8_t *x_scale, int64_t ldxs, const void *W,
+                              int64_t w_stride_g, int64_t ldw, const uint8_t *w_scale, int64_t ws_stride_g,
+                              int64_t ldws, void *C, int64_t ldc, gemm_dtype_t c_dtype, float alpha, float beta,
+                              const float *bias, gemm_epilogue_t epilogue, const float *row_scale,
+                              gemm_stream_t stream);
+
+/*
+ * Routing: a router's logits to each token's experts, in the form that the
+ * grouped products take.
+ *
+ * gemm_route -- for T tokens and E experts (at most GEMM_MAX_GROUPS), the `top` (at
+ * most GEMM_ROUTE_MAX_TOP) chosen ones of each token and their weights:
+ *
+ *     s = softmax(logits over all experts) or sigmoid(logits),  sel = s + bias
+ *     a group's worth is the sum of the group_sum (1 or 2) highest sel of its E / groups
+ *     experts; experts outside the top_groups worthiest groups are not chosen
+ *     expert[t] = those of the `top` highest sel, the highest first
+ *     weight[t] = scale * s, or renormalised scale * s / (sum of the chosen s)
+ *
+ * Equal ones go to the lower index (expert, group).  The choice is made as by
+ * 64-bit scores; without a bias and with group_sum 1, by the logits, whose order
+ * the scores have.  An expert whose logit or bias is -infinity or NaN, or whose
+ * group has no available expert, is not available; logits of +infinity count as the
+ * largest finite number.  Where fewer than `top` are left, the other slots get
+ * expert -1 and weight 0, which the calls below leave out.
+ *   logits, ldl    T x E, pitch ldl, F32, F16 or BF16.
+ *   bias           fp32[E] or NULL.  It moves the choice, not the weights.
+ *   groups         1 (no limit; top_groups and group_sum are not used) .. GEMM_ROUTE_MAX_GROUPS,
+ *                  a divisor of E; 1 <= top_groups <= groups.
+ *   expert, weight int32 and fp32, T x top, contiguous.
+ *
+ * gemm_route_grad -- dlogits (T x E, pitch ldd, l_dtype; every element written) for
+ * the weights' gradient dweight, the choice held fixed.  Takes the logits, score,
+ * renormalise and scale of the forward call and its `expert`; slots whose expert is
+ * outside 0 .. E-1 are left out.  The bias has no gradient.
+ */
+#define GEMM_ROUTE_MAX_TOP 32
+#define GEMM_ROUTE_MAX_GROUPS 32
+typedef enum { GEMM_SCORE_SOFTMAX = 0, GEMM_SCORE_SIGMOID = 1 } gemm_score_t;
+gemm_status_t gemm_route(int64_t T, int64_t E, int64_t top, gemm_dtype_t l_dtype, const void *logits, int64_t ldl,
+                         const float *bias, gemm_score_t score, int64_t groups, int64_t top_groups, int64_t group_sum,
+                         int renormalise, float scale, int32_t *expert, float *weight, gemm_stream_t stream);
+gemm_status_t gemm_route_grad(int64_t T, int64_t E, int64_t top, gemm_dtype_t l_dtype, const void *logits, int64_t ldl,
+                              gemm_score_t score, int renormalise, float scale, const int32_t *expert,
+                              const float *dweight, void *dlogits, int64_t ldd, gemm_stream_t stream);
+
+/*
+ * gemm_route_rows -- the T x top pairs p = t * top + slot, sorted by expert: pairs
+ * of one expert keep their order, so the same call gives the same rows.
+ *   offsets        int32[E + 1]: what gemm_grouped and gemm_mx_grouped take.
+ *   row            int32[T * top]: the row of each pair, -1 where expert is outside
+ *                  0 .. E-1 (or NULL: not wanted).
+ *   source         int32[T * top]: the pair of each row, -1 behind the last row.
+ *   workspace      device scratch, 16-byte aligned, gemm_route_rows_workspace_size()
+ *                  bytes (0 for few pairs: may be NULL).  Calls sharing it must not
+ *                  overlap; no initialisation needed.
+ * T * top is at most GEMM_ROUTE_MAX_PAIRS in this and the calls below.
+ */
+#define GEMM_ROUTE_MAX_PAIRS 1073741824 /* 2^30 */
+gemm_status_t gemm_route_rows(int64_t T, int64_t top, int64_t E, const int32_t *expert, int32_t *offsets, int32_t *row,
+                              int32_t *source, void *workspace, size_t workspace_bytes, gemm_stream_t stream);
+size_t gemm_route_rows_workspace_size(int64_t T, int64_t top, int64_t E);
+
+/*
+ * Rows between token order (X: T rows) and expert order (Y: R rows) of D columns.
+ * Indexes outside their arrays are left out; sums run in fp32 in the slots' order.
+ *
+ * gemm_rows_gather -- Y[r] = weight[source[r]] * X[source[r] / top] (weight NULL:
+ * 1, a copy); rows whose source is none stay as they were.  Also the gradient of a
+ * combination's rows.
+ *
+ * gemm_rows_combine -- Out[t] = cast(sum over slots of weight[t][s] * Y[row[t][s]]
+ * + beta * Out[t]) (weight NULL: 1; slots without a row add nothing; Out unread for
+ * beta == 0).  With weight NULL also the gradient of a gather.  Out is F32 or of
+ * Y's type, or F16 / BF16 from F32 rows.
+ *
+ * gemm_rows_combine_grad -- dY[row[t][s]] = cast(weight[t][s] * dOut[t]) in Y's type
+ * and dweight[t][s] = dOut[t] . Y[row[t][s]] (fp32; 0 without a row).  Either may
+ * be NULL (not wanted; Y is not read without dweight).  dOut is F32 or of Y's type.
+ * No row may be named twice, as gemm_route_rows names none; rows of dY that are not
+ * named stay as they were.
+ *
+ * D <= GEMM_ROWS_MAX_D.  Bases and pitches of 16 bytes and D of whole 16-byte pieces
+ * run fastest; any others work.  The output must not overlap the inputs.
+ */
+#define GEMM_ROWS_MAX_D 8388608 /* 2^23 */
+gemm_status_t gemm_rows_gather(int64_t R, int64_t D, int64_t T, int64_t top, gemm_dtype_t dtype, const void *X,
+                               int64_t ldx, const int32_t *source, const float *weight, void *Y, int64_t ldy,
+                               gemm_stream_t stream);
+gemm_status_t gemm_rows_combine(int64_t T, int64_t top, int64_t D, int64_t R, gemm_dtype_t y_dtype, const void *Y,
+                                int64_t ldy, const int32_t *row, const float *weight, float beta,
+                                gemm_dtype_t out_dtype, void *Out, int64_t ldo, gemm_stream_t stream);
+gemm_status_t gemm_rows_combine_grad(int64_t T, int64_t top, int64_t D, int64_t R, gemm_dtype_t d_dtype,
+                                     const void *dOut, int64_t ldd, gemm_dtype_t y_dtype, const void *Y, int64_t ldy,
+                                     const int32_t *row, const float *weight, void *dY, int64_t lddy, float *dweight,
+                                     gemm_stream_t stream);
+
+/*
  * gemm_wait_selftest -- exercise the bounded waits the GEMM kernels rely on
  * instead of hanging.  Enqueues on `stream` a one-warp kernel that waits on an
  * mbarrier nobody arrives at and then on *never_set (a device word the caller
