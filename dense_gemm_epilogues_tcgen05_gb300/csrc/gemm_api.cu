@@ -199,6 +199,16 @@ gemm_status_t check_range(const void *p, size_t bytes, int ordinal = -1, bool *l
     if (local != nullptr) *local = false;
     if (bytes == 0) return GEMM_OK;
     if (p == nullptr) return GEMM_ERR_INVALID_ARG;
+    if (local == nullptr) {
+        // One driver call where it tells the extent: it knows device and pinned memory, and refuses pageable.
+        CUdeviceptr start = 0;
+        size_t extent = 0;
+        const DriverFns &f = driver_fns();
+        if (f.ok && f.addr_range(&start, &extent, reinterpret_cast<CUdeviceptr>(p)) == CUDA_SUCCESS && extent > 0) {
+            const uint64_t first = reinterpret_cast<uint64_t>(p);
+            return first >= start && first + bytes <= start + extent ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+        }
+    }
     cudaPointerAttributes attr;
     if (cudaPointerGetAttributes(&attr, p) != cudaSuccess) {
         cudaGetLastError();
@@ -1873,11 +1883,13 @@ gemm_status_t gemm_mx_grouped(int64_t G, int64_t M, int64_t N, int64_t K, gemm_m
         if ((st = check_range(W, extent_bytes(G, w_stride, N, w_pitch, k_bytes, 1, 1))) != GEMM_OK) return st;
         if ((st = check_range(w_scale, extent_bytes(G, ws_stride_g, N, ldws, blocks, 1, 1))) != GEMM_OK) return st;
         if (row_scale != nullptr && (st = check_range(row_scale, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
+        // only the maps that the kernel can come to: boxes up to the widest tile
+        const uint32_t widths = static_cast<uint32_t>(std::min<int64_t>(kMxgMost, (M + 15) / 16 * 16) / 16);
         if ((st = encode_3d(&m.w, kDtI8, W, k_bytes, N, w_pitch, G, w_stride, 128)) != GEMM_OK) return st;
-        for (uint32_t i = 0; i < kMxgMost / 32; ++i)
-            if ((st = encode_3d(&m.x[i], kDtI8, X, k_bytes, M, x_pitch, 1, 0, 16 * (i + 1))) != GEMM_OK) return st;
+        for (uint32_t i = 0; i < widths; ++i)
+            if ((st = encode_3d(&m.x[i], kDtI8, X, k_bytes, M, x_pitch, 1, 0, 8 * (i + 1))) != GEMM_OK) return st;
         if ((st = encode_scales(&m.ws, w_scale, blocks, N, ldws, G, ws_stride_g, 128, 3)) != GEMM_OK) return st;
-        for (uint32_t i = 0; i < 4; ++i)
+        for (uint32_t i = 0; i < 4 && (i == 0 || 16u << i < 16 * widths); ++i)
             if ((st = encode_scales(&m.xs[i], x_scale, blocks, M, ldxs, 1, 0, 32u << i, 2)) != GEMM_OK) return st;
         t.row_scale = row_scale;
     }

@@ -6,23 +6,24 @@
 // over the rows r of group g, x and w E4M3 or E2M1 elements with an E8M0 scale per
 // 32 k, applied by the tensor cores from tensor memory.  Computed transposed as in
 // gemm_grouped_tc.cu: the MMA's 256 rows are the weights' output channels, its
-// columns up to kMost rows of a group in steps of 32.
+// columns up to kMxgMost rows of a group in steps of 16.
 //
 // Scales stay row-major in memory, as the quantiser writes them; a group may begin
 // at any row, so that no layout made beforehand would fit its tiles.  A box of 16
-// scales (512 k) of each row arrives by TMA in a ring of its own, and a warp
-// turns it in place into the chunks that tcgen05.cp spreads over tensor memory:
-// row 32 g + l, block 4 c + j of a 128-row block at byte 512 c + 16 l + 4 g + j
-// (the four words that a lane reads of its rows, exchanged for the four it
-// writes: no lane needs another's).
+// scales (512 k) of each row arrives by TMA, and a warp turns it in place into the
+// chunks that tcgen05.cp spreads over tensor memory: row 32 g + l, block 4 c + j of
+// a 128-row block at byte 512 c + 16 l + 4 g + j (the four words that a lane reads
+// of its rows, exchanged for the four it writes: no lane needs another's).
 //
 // Roles, per CTA:
-//   warp 0       TMA producer: its 128 rows of W, its half of the tile's rows of X
-//                (128 bytes of k a stage) counted on the leader's barrier; the
-//                scales of its W rows and of all the tile's rows of X on its own;
+//   warp 0       loads (TMA) of its 128 rows of W, 128 bytes of k a stage, counted on
+//                the leader's barrier;
 //   warp 1       MMA issuer (leader CTA only), two accumulators;
-//   warp 2       scales: lays a box out and tells the leader;
-//   warps 3-10   epilogue: two per 32-lane quadrant of tensor memory, each half of
+//   warp 2       scales: lays out those of a pair of stages and arrives on the
+//                leader's barrier;
+//   warp 3       loads of its half of the tile's rows of X, and of the scales of its
+//                rows of W and of all the tile's rows of X, on a barrier of its own;
+//   warps 4-11   epilogue: two per 32-lane quadrant of tensor memory, each half of
 //                the tile's columns (store_chunk_t).
 #include "gemm_tcgen05.cuh"
 #include "grouped.cuh"
@@ -34,25 +35,56 @@ namespace {
 
 template <int ELEM>
 struct MxgConfig {
-    static constexpr int STAGES = 6, ENTRIES = 4;               // operand ring, scale ring
-    static constexpr int CHUNKS = MxTraits<ELEM>::kChunks;      // 128-k scale chunks of a stage
-    static constexpr int KPE = 4 / CHUNKS;                      // stages of a scale box (512 k)
-    static constexpr int A_BYTES = 128 * 128, B_BYTES = kMxgMost / 2 * 128, STAGE_BYTES = A_BYTES + B_BYTES;
-    static constexpr int SFA_BYTES = 128 * 16, ENTRY_BYTES = SFA_BYTES + 256 * 16;
+    static constexpr int PAIRS = 3, STAGES = 2 * PAIRS;         // a stage holds a block; two share their scales
+    static constexpr int BLOCK = 128;                           // bytes of k of a swizzled block
+    static constexpr int CHUNKS = MxTraits<ELEM>::kChunks;      // 128-k scale chunks of a block
+    static constexpr int A_BYTES = 128 * BLOCK, B_BYTES = kMxgMost / 2 * BLOCK, STAGE_BYTES = A_BYTES + B_BYTES;
+    static constexpr int SFA_BYTES = 128 * 16, SF_BYTES = SFA_BYTES + 256 * 16;  // boxes of 16 scales
     static constexpr int ACC_STRIDE = kMxgMost, TMEM_COLS = 512;
-    static constexpr int SF_COLS = 12 * CHUNKS, SF_SLOTS = 2;   // W: 4 per chunk, X: 8 per chunk
-    static constexpr int EPI_WARP0 = 3, EPI_WARPS = 8;
+    static constexpr int SF_COLS = 2 * 12 * CHUNKS, SF_SLOTS = 2;  // a pair's; W: 4 per chunk, X: 8 per chunk
+    static constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
     static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
     static constexpr int BAR_BYTES = 256, SMEM_MAX = 232448;
-    static_assert(2 * ACC_STRIDE + SF_SLOTS * SF_COLS <= TMEM_COLS, "accumulators and scale slots fit");
-    static_assert((2 * STAGES + 3 * ENTRIES + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
+    static_assert(2 * ACC_STRIDE + SF_SLOTS * SF_COLS <= TMEM_COLS, "accumulators and scales fit");
+    static_assert((2 * STAGES + PAIRS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
     static_assert(B_BYTES % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle atoms stay aligned");
-    // after up to 1023 bytes of alignment: [stages][scale boxes][barriers][group table]
+    // after up to 1023 bytes of alignment: [stages][scales][barriers][group table]
     static int smem_bytes(int G) {
-        return 1024 + STAGES * STAGE_BYTES + ENTRIES * ENTRY_BYTES + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16;
+        return 1024 + STAGES * STAGE_BYTES + PAIRS * SF_BYTES + BAR_BYTES + (group_table_bytes(G) + 15) / 16 * 16;
     }
-    static_assert(1024 + STAGES * STAGE_BYTES + ENTRIES * ENTRY_BYTES + BAR_BYTES + group_table_bytes(kMaxGroups) + 16 <=
+    static_assert(1024 + STAGES * STAGE_BYTES + PAIRS * SF_BYTES + BAR_BYTES + group_table_bytes(kMaxGroups) + 16 <=
                       SMEM_MAX, "fits the 227 KB opt-in shared memory");
+};
+
+// This cluster's tiles, in row_tile's order but in widths of steps of 16, without a division or a search per tile: a step moves `rt` and `ft` by
+// fixed amounts and the group forwards.
+struct MxgWalk {
+    const GroupTable &table;
+    int tiles_f, step_r, step_f, rt, ft, g, tiles, width;
+    __device__ __forceinline__ MxgWalk(const GroupTable &t, int tiles_f_, int cluster, int nclusters)
+        : table(t), tiles_f(tiles_f_), step_r(nclusters / tiles_f_), step_f(nclusters % tiles_f_),
+          rt(cluster / tiles_f_), ft(cluster % tiles_f_), g(-1), tiles(t.first[t.G]), width(0) {}
+    __device__ __forceinline__ bool next(GroupedTile &o) {
+        if (rt >= tiles) return false;
+        if (g < 0 || table.first[g + 1] <= rt) {
+            do ++g;
+            while (table.first[g + 1] <= rt);
+            const int nt = table.first[g + 1] - table.first[g];
+            width = ((table.hi[g] - table.lo[g] + nt - 1) / nt + 15) & ~15;
+        }
+        o.g = g;
+        o.f0 = ft * 256;
+        o.r0 = table.lo[g] + (rt - table.first[g]) * width;
+        o.nr = min(width, table.hi[g] - o.r0);
+        o.bn = (o.nr + 15) & ~15;
+        rt += step_r;
+        ft += step_f;
+        if (ft >= tiles_f) {
+            ft -= tiles_f;
+            ++rt;
+        }
+        return true;
+    }
 };
 
 // A 128-row block of scales, row-major in rows of 16 bytes, to four chunks in its place.  Warp-collective.
@@ -74,13 +106,12 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char *entries = smem + Cfg::STAGES * Cfg::STAGE_BYTES;
-    uint64_t *full = reinterpret_cast<uint64_t *>(entries + Cfg::ENTRIES * Cfg::ENTRY_BYTES);
+    unsigned char *scales = smem + Cfg::STAGES * Cfg::STAGE_BYTES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(scales + Cfg::PAIRS * Cfg::SF_BYTES);  // (leader's) operands landed;
+                                                  // a pair's first stage: and both CTAs' scales laid out
     uint64_t *empty = full + Cfg::STAGES;
-    uint64_t *landed = empty + Cfg::STAGES;       // this CTA's scale box has landed
-    uint64_t *ready = landed + Cfg::ENTRIES;      // (leader's) both CTAs' boxes are laid out
-    uint64_t *sempty = ready + Cfg::ENTRIES;      // the MMAs of the box are done
-    uint64_t *tfull = sempty + Cfg::ENTRIES;
+    uint64_t *landed = empty + Cfg::STAGES;       // this CTA's scales of a pair have landed
+    uint64_t *tfull = landed + Cfg::PAIRS;
     uint64_t *tempty = tfull + 2;
     uint64_t *mma_done = tempty + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mma_done + 1);
@@ -92,14 +123,10 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Cfg::STAGES; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], s % 2 == 0 ? 1 + CL : 1);
             mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < Cfg::ENTRIES; ++s) {
-            mbar_init(&landed[s], 1);
-            mbar_init(&ready[s], CL);
-            mbar_init(&sempty[s], 1);
-        }
+        for (int s = 0; s < Cfg::PAIRS; ++s) mbar_init(&landed[s], 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], CL * Cfg::EPI_WARPS);
@@ -125,42 +152,26 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
         threadIdx.x, Cfg::THREADS, RowTilesOf{args.most});
     const uint32_t tmem_base = *tmem_slot;
     const uint32_t full0_leader = mapa_shared(smem_u32(&full[0]), 0);
-    const uint32_t ready0_leader = mapa_shared(smem_u32(&ready[0]), 0);
     const uint32_t tempty0_leader = mapa_shared(smem_u32(&tempty[0]), 0);
     const uint32_t abort_local = smem_u32(const_cast<int *>(abort_flag));
-    const int num_kb = (args.K / (ELEM == kMxE2M1 ? 2 : 1) + 127) / 128;
-    const long long tiles = static_cast<long long>(table.first[args.G]) * args.tiles_f;
+    const int k_bytes = args.K / (ELEM == kMxE2M1 ? 2 : 1), blocks = (k_bytes + Cfg::BLOCK - 1) / Cfg::BLOCK;
+    const int steps = (blocks + 1) / 2;  // pairs of blocks; a last one may lack its second
+    MxgWalk walk(table, args.tiles_f, cluster, nclusters);
+    GroupedTile t;
 
-    if (warp == 0) {
+    if (warp == 0 || warp == 3) {
         if (lane == 0) {
-            // ------------------------------------------------ TMA producer --
-            uint32_t stage = 0, phase = 0, entry = 0, ephase = 0;
+            // ------------------------- TMA producers: W (warp 0), X and scales (warp 3) --
+            uint32_t stage = 0, phase = 0;
             bool ok = true, issued = false;
             const uint64_t keep = l2_policy_evict_last();
-            for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
-                const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
+            while (ok && steps > 0 && walk.next(t)) {
                 const int f = t.f0 + static_cast<int>(rank) * 128;
                 const int bnh = t.bn >> 1;
                 const int c0 = t.r0 + static_cast<int>(rank) * bnh;  // first of this CTA's MMA columns
-                const uint32_t bytes = Cfg::A_BYTES + bnh * 128u;
+                const uint32_t bytes = Cfg::A_BYTES + bnh * Cfg::BLOCK;
                 const int sm = t.bn <= 32 ? 0 : t.bn <= 64 ? 1 : t.bn <= 128 ? 2 : 3;  // box of 32 << sm rows' scales
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    if (kb % Cfg::KPE == 0) {
-                        if (!pair_wait<CL>(&sempty[entry], ephase ^ 1u, abort_flag, args.status, abort_local, rank)) {
-                            ok = false;
-                            break;
-                        }
-                        issued = true;
-                        unsigned char *sf = entries + entry * Cfg::ENTRY_BYTES;
-                        mbar_arrive_expect_tx(&landed[entry], Cfg::SFA_BYTES + (512u << sm));
-                        const int b = kb / Cfg::KPE * 16;
-                        tma_load_3d_hint(sf, &maps.ws, &landed[entry], b, f, t.g, keep);
-                        tma_load_2d_hint(sf + Cfg::SFA_BYTES, &maps.xs[sm], &landed[entry], b, t.r0, keep);
-                        if (++entry == Cfg::ENTRIES) {
-                            entry = 0;
-                            ephase ^= 1u;
-                        }
-                    }
+                for (int b = 0; b < 2 * steps; ++b) {
                     if (!pair_wait<CL>(&empty[stage], phase ^ 1u, abort_flag, args.status, abort_local, rank)) {
                         ok = false;
                         break;
@@ -168,9 +179,25 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
                     issued = true;
                     unsigned char *sA = smem + stage * Cfg::STAGE_BYTES;
                     const uint32_t fbar = full0_leader + 8u * stage;
-                    if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
-                    tma_load_3d_pair(sA, &maps.w, fbar, kb * 128, f, t.g, keep);
-                    tma_load_3d_pair(sA + Cfg::A_BYTES, &maps.x[(bnh >> 4) - 1], fbar, kb * 128, c0, 0, keep);
+                    if (warp == 0) {
+                        if (b < blocks) {
+                            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
+                            tma_load_3d_pair(sA, &maps.w, fbar, b * Cfg::BLOCK, f, t.g, keep);
+                        } else if (rank == 0) {
+                            mbar_arrive(&full[stage]);  // nothing to load
+                        }
+                    } else {
+                        if (b % 2 == 0) {
+                            uint64_t *bar = &landed[stage / 2];
+                            unsigned char *sf = scales + stage / 2 * Cfg::SF_BYTES;
+                            const int box = ELEM == kMxE2M1 ? b * 8 : b / 4 * 16;  // E4M3: a pair takes half of it
+                            mbar_arrive_expect_tx(bar, Cfg::SFA_BYTES + (512u << sm));
+                            tma_load_3d_hint(sf, &maps.ws, bar, box, f, t.g, keep);
+                            tma_load_2d_hint(sf + Cfg::SFA_BYTES, &maps.xs[sm], bar, box, t.r0, keep);
+                        }
+                        if (b < blocks)
+                            tma_load_3d_pair(sA + Cfg::A_BYTES, &maps.x[(bnh >> 3) - 1], fbar, b * Cfg::BLOCK, c0, 0, keep);
+                    }
                     if (++stage == Cfg::STAGES) {
                         stage = 0;
                         phase ^= 1u;
@@ -188,72 +215,73 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
         if (rank == 0) {
             // ---------------------------------------------------- MMA issuer --
             // The whole warp walks the loop and one elected lane issues, so that
-            // addresses and descriptors stay in uniform registers.
+            // addresses and descriptors stay in uniform registers; the next stage is
+            // asked for before this one's instructions issue.
             const uint64_t a_desc0 = sw128_desc(smem_u32(smem), 16u, 1024u);
             const uint64_t b_desc0 = sw128_desc(smem_u32(smem) + Cfg::A_BYTES, 16u, 1024u);
-            const uint64_t sf_desc0 = plain16_desc(smem_u32(entries));
-            uint32_t stage = 0, phase = 0, entry = 0, ephase = 0, slot = 0;
-            bool ok = true, issued = false;
+            const uint64_t sf_desc0 = plain16_desc(smem_u32(scales));
+            uint32_t stage = 0, phase = 0, slot = 0;
+            bool ok = true, issued = false, is_full = false;
             int local = 0;
-            for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
-                if (num_kb == 0) break;  // the epilogue alone
-                const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
+            while (ok && steps > 0 && walk.next(t)) {
                 const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
                 ++local;
                 ok = pair_wait<CL>(&tempty[acc], acc_phase ^ 1u, abort_flag, args.status, abort_local, rank);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                tc_fence_after();
                 const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    const int part = kb % Cfg::KPE;  // of the scale box
-                    if (part == 0) {
-                        ok = pair_wait<CL>(&ready[entry], ephase, abort_flag, args.status, abort_local, rank);
+                const uint32_t idesc0 = mma_idesc_bs(MxTraits<ELEM>::kFmt, 256, t.bn, 0, 0);
+                for (int b = 0; b < 2 * steps; ++b) {
+                    if (!is_full) {
+                        ok = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
-                        smem_acquire_cluster();
                     }
-                    ok = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
+                    if (b % 2 == 0) smem_acquire_cluster();  // the scales, written by ordinary stores
                     tc_fence_after();
+                    const uint32_t next = stage + 1 == Cfg::STAGES ? 0u : stage + 1;
+                    const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
+                    const bool next_full = mbar_test_wait(smem_u32(&full[next]), next_phase);
                     const uint32_t at = stage * (Cfg::STAGE_BYTES >> 4);  // addresses are in 16-byte units, below 2^14
                     const uint64_t ad = a_desc0 + at, bd = b_desc0 + at;
-                    const uint64_t sd = sf_desc0 + entry * (Cfg::ENTRY_BYTES >> 4);
-                    const uint32_t sfa = tmem_base + 2 * Cfg::ACC_STRIDE + slot * Cfg::SF_COLS, sfb = sfa + 4 * Cfg::CHUNKS;
-                    const bool last = kb + 1 == num_kb, box_done = last || part + 1 == Cfg::KPE;
+                    // E4M3: the second half of the box in odd pairs
+                    const uint64_t sd = sf_desc0 + (stage >> 1) * (Cfg::SF_BYTES >> 4) +
+                                        (ELEM == kMxE4M3 ? static_cast<uint32_t>(b >> 1 & 1) * 2 * 32u : 0u);
+                    // (the slot's last MMAs, two pairs back, are done: the scale warp waited for them)
+                    const uint32_t sfa = tmem_base + 2 * Cfg::ACC_STRIDE + slot * Cfg::SF_COLS;
+                    const uint32_t sfb = sfa + 2 * 4 * Cfg::CHUNKS;
+                    const bool both = b + 1 < blocks;
                     if (elect_one()) {
+                        if (b % 2 == 0) {
 #pragma unroll
-                        for (int c = 0; c < Cfg::CHUNKS; ++c) {
-                            const uint64_t ch = sd + static_cast<uint32_t>(part * Cfg::CHUNKS + c) * 32u;
-                            tc_cp_32x128b_x4_pair(sfa + 4 * c, ch);
-                            tc_cp_32x128b_x4_pair(sfb + 8 * c, ch + (Cfg::SFA_BYTES >> 4));
-                            if (t.bn > 128) tc_cp_32x128b_x4_pair(sfb + 8 * c + 4, ch + ((Cfg::SFA_BYTES + 2048) >> 4));
+                            for (int c = 0; c < 2 * Cfg::CHUNKS; ++c) {
+                                if (c >= Cfg::CHUNKS && !both) break;
+                                tc_cp_32x128b_x4_pair(sfa + 4 * c, sd + c * 32u);
+                                tc_cp_32x128b_x4_pair(sfb + 8 * c, sd + (Cfg::SFA_BYTES >> 4) + c * 32u);
+                                if (t.bn > 128)
+                                    tc_cp_32x128b_x4_pair(sfb + 8 * c + 4, sd + ((Cfg::SFA_BYTES + 2048) >> 4) + c * 32u);
+                            }
                         }
+                        if (b < blocks) {
+                            const uint32_t c0 = static_cast<uint32_t>(b & 1) * Cfg::CHUNKS;
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            const uint32_t chunk = Cfg::CHUNKS == 1 ? 0u : static_cast<uint32_t>(ks >> 1);
-                            const uint32_t sf_id = Cfg::CHUNKS == 1 ? static_cast<uint32_t>(ks)
-                                                                    : static_cast<uint32_t>((ks & 1) * 2);
-                            const uint32_t idesc = mma_idesc_bs(MxTraits<ELEM>::kFmt, 256, t.bn, sf_id, sf_id);
-                            tc_mma_bs_pair<MxTraits<ELEM>::kKind>(d_tmem, ad + ks * 2, bd + ks * 2, idesc, sfa + 4 * chunk,
-                                                                   sfb + 8 * chunk, (kb | ks) != 0 ? 1u : 0u);
+                            for (int ks = 0; ks < 4; ++ks) {
+                                const uint32_t chunk = c0 + (Cfg::CHUNKS == 1 ? 0 : ks >> 1);
+                                const uint32_t sf_id = Cfg::CHUNKS == 1 ? ks : (ks & 1) * 2;
+                                tc_mma_bs_pair<MxTraits<ELEM>::kKind>(d_tmem, ad + ks * 2, bd + ks * 2,
+                                                                       idesc0 | (sf_id << 4) | (sf_id << 29),
+                                                                       sfa + 4 * chunk, sfb + 8 * chunk,
+                                                                       (b | ks) != 0 ? 1u : 0u);
+                            }
                         }
                         tc_commit_pair(&empty[stage], 0x3);
-                        if (box_done) tc_commit_pair(&sempty[entry], 0x3);
-                        if (last) tc_commit_pair(&tfull[acc], 0x3);
+                        if (b + 1 == 2 * steps) tc_commit_pair(&tfull[acc], 0x3);
                     }
-                    __syncwarp();
                     issued = true;
-                    slot ^= 1u;
-                    if (box_done && ++entry == Cfg::ENTRIES) {
-                        entry = 0;
-                        ephase ^= 1u;
-                    }
-                    if (++stage == Cfg::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                    is_full = __all_sync(0xffffffffu, next_full);
+                    slot ^= static_cast<uint32_t>(b) & 1u;
+                    stage = next;
+                    phase = next_phase;
                 }
             }
             if (*abort_flag && issued) {
@@ -263,28 +291,42 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
         }
     } else if (warp == 2) {
         // -------------------------------------------------------- scales --
-        uint32_t entry = 0, ephase = 0;
+        // The issuer copies a pair's scales over those of two pairs before, and no order is promised between a copy and
+        // MMAs issued earlier.  So scales are only reported once those MMAs are done (the pair's last `empty`): the
+        // issuer's wait for them then covers that too.
+        uint32_t pair = 0, phase = 0, old = 0, old_phase = 0;
+        int ahead = 0;
         bool ok = true;
-        for (long long tile = cluster; ok && tile < tiles; tile += nclusters) {
-            const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
-            for (int kb = 0; kb < num_kb; kb += Cfg::KPE) {
-                const bool got = pair_wait<CL>(&landed[entry], ephase, abort_flag, args.status, abort_local, rank);
+        while (ok && steps > 0 && walk.next(t)) {
+            for (int st = 0; st < steps; ++st) {
+                bool got = pair_wait<CL>(&landed[pair], phase, abort_flag, args.status, abort_local, rank);
                 ok = __all_sync(0xffffffffu, got);
                 if (!ok) break;
-                const uint32_t sf = smem_u32(entries + entry * Cfg::ENTRY_BYTES);
+                const uint32_t sf = smem_u32(scales + pair * Cfg::SF_BYTES);
                 lay_out_scales(sf);
                 // (rows past the box are an earlier tile's scales or none: their columns are not stored)
                 lay_out_scales(sf + Cfg::SFA_BYTES);
                 if (t.bn > 128) lay_out_scales(sf + Cfg::SFA_BYTES + 2048);
+                if (ahead < Cfg::SF_SLOTS) {
+                    ++ahead;
+                } else {
+                    got = pair_wait<CL>(&empty[2 * old + 1], old_phase, abort_flag, args.status, abort_local, rank);
+                    ok = __all_sync(0xffffffffu, got);
+                    if (!ok) break;
+                    if (++old == Cfg::PAIRS) {
+                        old = 0;
+                        old_phase ^= 1u;
+                    }
+                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
                     smem_release_cluster();
-                    mbar_arrive_remote_relaxed(ready0_leader + 8u * entry);
+                    mbar_arrive_remote_relaxed(full0_leader + 16u * pair);
                 }
-                if (++entry == Cfg::ENTRIES) {
-                    entry = 0;
-                    ephase ^= 1u;
+                if (++pair == Cfg::PAIRS) {
+                    pair = 0;
+                    phase ^= 1u;
                 }
             }
         }
@@ -295,18 +337,17 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
         const int half = (warp - Cfg::EPI_WARP0) >> 2;  // which half of the tile's columns
         const StoreArgs e{args.ldc, args.alpha, args.beta, args.epi};
         int local = 0;
-        for (long long tile = cluster; tile < tiles; tile += nclusters) {
-            const GroupedTile t = row_tile(table, tile, args.tiles_f, args.K);
+        while (walk.next(t)) {
             const int f = t.f0 + static_cast<int>(rank) * 128 + quad * 32 + lane;
             const float bias = (e.epi != kEpiNone && f < args.F)
                                    ? args.bias[static_cast<long long>(t.g) * args.F + f] : 0.0f;
             OutT *c = static_cast<OutT *>(args.C) + t.r0 * args.ldc + f;
             const float *rs = args.row_scale != nullptr ? args.row_scale + t.r0 : nullptr;
-            const int chunks = t.bn >> 5;
+            const int chunks = (t.bn + 31) >> 5;  // (a last half chunk reads columns that are not stored)
             const int c_begin = half ? (chunks + 1) >> 1 : 0, nch = (half ? chunks : (chunks + 1) >> 1) - c_begin;
             const uint32_t t_quad = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c_begin * 32;
             const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
-            if (num_kb > 0) {
+            if (steps > 0) {
                 ++local;
                 const bool got = pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank);
                 if (!__all_sync(0xffffffffu, got)) break;
@@ -315,7 +356,7 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
 #pragma unroll 1
             for (int ch = 0; ch < nch; ++ch) {
                 float v[32];
-                if (num_kb > 0) {
+                if (steps > 0) {
                     uint32_t raw[32];
                     __syncwarp();
                     tmem_ld_issue(t_quad + acc * Cfg::ACC_STRIDE + ch * 32, raw);
@@ -326,7 +367,7 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = 0.0f;
                 }
-                if (num_kb > 0 && ch + 1 == nch) {
+                if (steps > 0 && ch + 1 == nch) {
                     // the accumulator is in registers: free it before the stores
                     tc_fence_before();
                     __syncwarp();
@@ -337,7 +378,7 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
                 chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row, rs != nullptr ? rs + row : nullptr, 1.0f, bias, e);
                 store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
             }
-            if (num_kb > 0 && nch == 0) {  // a 32-column tile has no second half
+            if (steps > 0 && nch == 0) {  // a tile of up to 32 columns has no second half
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);

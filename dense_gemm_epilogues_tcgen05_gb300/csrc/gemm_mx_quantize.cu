@@ -20,18 +20,68 @@ namespace {
 constexpr int kMxThreads = 256, kPieces = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
-// Eight values as fp32, and the bits of the largest |x| among them.
-template <int XT, bool VEC>
-__device__ __forceinline__ void load8(const typename Elem<XT>::T *p, float (&f)[8]) {
-    constexpr int PV = Vec16<XT>::kPerVec;
-    if constexpr (VEC) {
-#pragma unroll
-        for (int v = 0; v < 8 / PV; ++v) Vec16<XT>::unpack(__ldg(reinterpret_cast<const uint4 *>(p) + v), &f[v * PV]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = Elem<XT>::load(p + j);
-    }
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
 }
+
+// Eight values as they are stored.
+template <int XT, bool VEC> struct Eight {
+    static constexpr int PV = Vec16<XT>::kPerVec;
+    uint4 u[8 / PV];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int v = 0; v < 8 / PV; ++v) u[v] = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void load(const typename Elem<XT>::T *p) {
+#pragma unroll
+        for (int v = 0; v < 8 / PV; ++v) u[v] = ld_stream(reinterpret_cast<const uint4 *>(p) + v);
+    }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+#pragma unroll
+        for (int v = 0; v < 8 / PV; ++v) Vec16<XT>::unpack(u[v], &f[v * PV]);
+    }
+    // The bits of the largest |x|, as fp32: with the sign cleared values are ordered as integers, infinities and NaN
+    // last; 16-bit ones two at a time.
+    __device__ __forceinline__ unsigned max_bits() const {
+        unsigned m = 0;
+#pragma unroll
+        for (int v = 0; v < 8 / PV; ++v) {
+            const uint32_t w[4] = {u[v].x, u[v].y, u[v].z, u[v].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = XT == kDtF32 ? max(m, w[i] & 0x7FFFFFFFu) : __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        }
+        if constexpr (XT == kDtF32) return m;
+        m = max(m & 0xFFFFu, m >> 16);
+        if constexpr (XT == kDtBF16) return m << 16;
+        return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
+    }
+};
+template <int XT> struct Eight<XT, false> {
+    float f8[8];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f8[j] = 0.0f;
+    }
+    __device__ __forceinline__ void load(const typename Elem<XT>::T *p) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f8[j] = Elem<XT>::load(p + j);
+    }
+    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] = f8[j];
+    }
+    __device__ __forceinline__ unsigned max_bits() const {
+        unsigned m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f8[j]) & 0x7FFFFFFFu);
+        return m;
+    }
+};
 
 // Pairs of fp32 values to E2M1 (nearest even, saturating), the first of each pair in the low nibble.
 __device__ __forceinline__ uint32_t e2m1_of(const float (&f)[8]) {
@@ -71,66 +121,74 @@ __device__ __forceinline__ uint2 e4m3_of(const float (&f)[8]) {
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-// Row and piece (of 8 values) of the block's i-th piece, counted through all rows.
+// Row and piece (of 8 values) of this thread's pieces, kMxThreads apart, counted through all rows.
 struct Place {
-    long long row;
-    int piece;
+    int row, piece;  // (row M: past the end)
 };
-struct Places {
-    long long row0;
-    unsigned rem, per;
-    __device__ __forceinline__ Places(long long first, int per_row) : per(static_cast<unsigned>(per_row)) {
-        row0 = first / per_row;
-        rem = static_cast<unsigned>(first - row0 * per_row);
+__device__ __forceinline__ void places_of(const MxQuantArgs &a, Place (&at)[kPieces]) {
+    const unsigned per = static_cast<unsigned>(a.K) / 8u;
+    const long long first = static_cast<long long>(blockIdx.x) * (kMxThreads * kPieces), row0 = first / per;
+    const unsigned q = static_cast<unsigned>(first - row0 * per) + threadIdx.x, r = q / per;
+    long long row = row0 + r;
+    unsigned piece = q - r * per;
+    const unsigned step_r = kMxThreads / per, step_p = kMxThreads - step_r * per;
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) {
+        at[i] = {static_cast<int>(row < a.M ? row : a.M), static_cast<int>(piece)};
+        piece += step_p;
+        row += step_r;
+        if (piece >= per) {
+            piece -= per;
+            ++row;
+        }
     }
-    __device__ __forceinline__ Place at(unsigned i) const {
-        const unsigned q = rem + i, r = q / per;
-        return {row0 + r, static_cast<int>(q - r * per)};
-    }
-};
+}
 
 // XV: X may be read in 16-byte pieces.  QV: Q written in whole pieces' codes.
 template <int ELEM, int XT, bool XV, bool QV>
 __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const __grid_constant__ MxQuantArgs a) {
     using T = typename Elem<XT>::T;
-    const Places places(static_cast<long long>(blockIdx.x) * (kMxThreads * kPieces), a.K / 8);
-    float f[kPieces][8];
+    Eight<XT, XV> raw[kPieces];
     Place at[kPieces];
     bool live[kPieces];
+    int src[kPieces];
+    places_of(a, at);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        at[i] = places.at(threadIdx.x + i * kMxThreads);
         live[i] = at[i].row < a.M;
-        long long src = at[i].row;
-        if (live[i] && a.source != nullptr) {
-            const int p = __ldg(a.source + at[i].row);
-            src = p >= 0 ? p / a.top : -1;
-            live[i] = src >= 0 && src < a.rows_x;
-        }
-        if (live[i]) {
-            load8<XT, XV>(static_cast<const T *>(a.X) + src * a.ldx + at[i].piece * 8, f[i]);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f[i][j] = 0.0f;
-        }
+        src[i] = at[i].row;
+        if (live[i] && a.source != nullptr) src[i] = __ldg(a.source + at[i].row);
     }
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        unsigned m = 0;
+        if (a.source != nullptr) {
+            src[i] = src[i] >= 0 ? src[i] / a.top : -1;
+            live[i] = live[i] && src[i] >= 0 && src[i] < a.rows_x;
+        }
+        raw[i].zero();
+        if (live[i]) raw[i].load(static_cast<const T *>(a.X) + src[i] * a.ldx + at[i].piece * 8);
+    }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[i][j]) & 0x7FFFFFFFu);
+    for (int i = 0; i < kPieces; ++i) {
+        unsigned m = raw[i].max_bits();
         m = max(m, __shfl_xor_sync(kAll, m, 1));
         m = max(m, __shfl_xor_sync(kAll, m, 2));
         constexpr int kEmax = ELEM == kMxE2M1 ? 2 : 8;
         const bool finite = m < 0x7F800000u;
         const int code = max(static_cast<int>(m >> 23) - kEmax, 0);  // (a subnormal maximum has exponent bits 0)
         const float inv = __uint_as_float(static_cast<unsigned>(254 - code) << 23);
+        float f[8];
+        raw[i].unpack(f);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = finite ? f[i][j] * inv : 0.0f;
+        for (int j = 0; j < 8; j += 2) f2_unpack(f2_mul(f2_pack(f[j], f[j + 1]), f2_splat(inv)), f[j], f[j + 1]);
+        if (!finite) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+        }
         if (!live[i]) continue;
         unsigned char *q = a.Q + at[i].row * a.q_pitch;
         if constexpr (ELEM == kMxE2M1) {
-            const uint32_t w = e2m1_of(f[i]);
+            const uint32_t w = e2m1_of(f);
             q += at[i].piece * 4;
             if constexpr (QV) {
                 *reinterpret_cast<uint32_t *>(q) = w;
@@ -139,7 +197,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const __grid_co
                 for (int j = 0; j < 4; ++j) q[j] = static_cast<unsigned char>(w >> (8 * j));
             }
         } else {
-            const uint2 w = e4m3_of(f[i]);
+            const uint2 w = e4m3_of(f);
             q += static_cast<long long>(at[i].piece) * 8;
             if constexpr (QV) {
                 *reinterpret_cast<uint2 *>(q) = w;
@@ -158,13 +216,12 @@ template <int ELEM, int YT, bool QV, bool YV>
 __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const __grid_constant__ MxQuantArgs a) {
     using T = typename Elem<YT>::T;
     constexpr int PV = Vec16<YT>::kPerVec;
-    const Places places(static_cast<long long>(blockIdx.x) * (kMxThreads * kPieces), a.K / 8);
     uint2 w[kPieces];
     unsigned code[kPieces];
     Place at[kPieces];
+    places_of(a, at);
 #pragma unroll
     for (int i = 0; i < kPieces; ++i) {
-        at[i] = places.at(threadIdx.x + i * kMxThreads);
         w[i] = make_uint2(0, 0);
         code[i] = 0;
         if (at[i].row >= a.M) continue;

@@ -8,9 +8,11 @@
 //
 // A warp takes a token; lane l holds the experts l NPL .. l NPL + NPL - 1 in
 // registers, so that the lowest lane of a ballot is the lowest expert, and the
-// experts of a group lie in neighbouring lanes.  Each of the `top` rounds takes
-// the maximum of the lanes' maxima (one redux on the value's bits, ordered as
-// integers) and strikes it out.
+// experts of a group lie in neighbouring lanes.  Values are compared as integers of
+// the same order, a warp's maximum by one redux.  The top-th largest of the lanes'
+// maxima bounds the chosen ones from below: what reaches it, rarely more than a few
+// values over `top`, is gathered one to a lane (in the experts' order), and each
+// further round costs a redux and a ballot, no search through a lane's registers.
 //
 // Which experts are chosen is decided as by 64-bit scores.  Without a bias (and
 // without sums over a group) the scores have the logits' order, and the logits
@@ -30,32 +32,14 @@ constexpr int kRouteWarps = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
 // Values as unsigned integers of the same order; 0 is below every value.
-struct Order32 {
-    using F = float;
-    using K = unsigned;
-    static __device__ __forceinline__ K key(F f) {
-        const unsigned u = __float_as_uint(f);
-        return u ^ (static_cast<unsigned>(static_cast<int>(u) >> 31) | 0x80000000u);
-    }
-    static __device__ __forceinline__ F value(K k) {
-        return __uint_as_float(k ^ (static_cast<int>(k) < 0 ? 0x80000000u : kAll));
-    }
-    static __device__ __forceinline__ K warp_max(K k) { return __reduce_max_sync(kAll, k); }
-};
-struct Order64 {
-    using F = double;
-    using K = unsigned long long;
-    static __device__ __forceinline__ K key(F f) {
-        const long long u = __double_as_longlong(f);
-        return static_cast<K>(u) ^ (static_cast<K>(u >> 63) | 0x8000000000000000ull);
-    }
-    static __device__ __forceinline__ K warp_max(K k) {
-        const unsigned hi = __reduce_max_sync(kAll, static_cast<unsigned>(k >> 32));
-        const unsigned lo = __reduce_max_sync(kAll, static_cast<unsigned>(k >> 32) == hi ? static_cast<unsigned>(k) : 0u);
-        return static_cast<K>(hi) << 32 | lo;
-    }
-};
-
+__device__ __forceinline__ unsigned order_key(float f) {
+    const unsigned u = __float_as_uint(f);
+    return u ^ (static_cast<unsigned>(static_cast<int>(u) >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(unsigned k) {
+    return __uint_as_float(k ^ (static_cast<int>(k) < 0 ? 0x80000000u : kAll));
+}
+__device__ __forceinline__ float warp_max(float v) { return order_value(__reduce_max_sync(kAll, order_key(v))); }
 // -infinity and NaN: not available; +infinity counts as the largest finite
 // value; -0 as 0, whose bits it must not be told from.
 __device__ __forceinline__ float logit_value(float x) { return x > -INFINITY ? fminf(x, FLT_MAX) + 0.0f : -INFINITY; }
@@ -88,7 +72,7 @@ __device__ __forceinline__ float warp_max_of(const float (&x)[NPL]) {
     float m = x[0];
 #pragma unroll
     for (int j = 1; j < NPL; ++j) m = fmaxf(m, x[j]);
-    return Order32::value(Order32::warp_max(Order32::key(m)));
+    return warp_max(m);
 }
 
 template <typename F>
@@ -98,120 +82,205 @@ __device__ __forceinline__ F warp_sum(F v) {
     return v;
 }
 
-// The larger two of two pairs.
+// Takes v into the larger two values seen.
 template <typename F>
-__device__ __forceinline__ void merge_top2(F &a1, F &a2, F b1, F b2) {
-    const F low = a1 < b1 ? a1 : b1, second = a2 < b2 ? b2 : a2;
-    a1 = a1 < b1 ? b1 : a1;
-    a2 = low < second ? second : low;
+__device__ __forceinline__ void take_top2(F &t1, F &t2, F v) {
+    const F low = t1 < v ? t1 : v;
+    t1 = t1 < v ? v : t1;
+    t2 = t2 < low ? low : t2;
 }
 
-// The chosen experts of a token: lane s gets the s-th (or -1).  sel: the lane's
-// selection scores, -infinity where there is none.  Returns whether two values
-// that the choice depends on are within margin (1 + their size) of each other.
-template <class O, int NPL>
-__device__ __forceinline__ bool choose(const typename O::F (&sel)[NPL], const RouteArgs &a, typename O::F *stage,
-                                       float margin, int &expert) {
-    using F = typename O::F;
-    using K = typename O::K;
+// Which groups stay, one bit each; lane g * per holds the worth of group g (-infinity: none), and the lanes beside it.
+// `close`: whether the last that stays and the first that does not are within margin (1 + their size).
+template <typename F>
+__device__ __forceinline__ bool group_stays(F worth, int per, const RouteArgs &a, bool &kept) {
+    const int lane = threadIdx.x & 31, g = lane / per;
+    int rank = 0;
+    for (int h = 0; h < a.groups; ++h) {
+        const F other = __shfl_sync(kAll, worth, h * per);
+        rank += other > worth || (other == worth && h < g);
+    }
+    const bool is_group = g < a.groups && worth > -INFINITY;
+    kept = is_group && rank < a.top_groups;
+    return is_group;
+}
+
+// How far fp32 selection scores can be off: a difference of two by less than `score` + 2^-23 of the larger (0: exact).
+// Whether x may in truth not be above y, the next one.
+__device__ __forceinline__ bool too_close(float x, float y, float score) {
+    return !(x - y > score + 0x1p-23f * fmaxf(fabsf(x), fabsf(y)));
+}
+
+struct Candidate {
+    unsigned key;
+    int expert;
+};
+
+// The chosen experts of a token by fp32 values: lane s gets the s-th (or -1).  sel: the lane's selection scores,
+// -infinity where there is none; cand: 32 slots of the warp; margin: too_close's.  `exactly`(expert) is a selection
+// score in 64 bits (warp-collective; -1: -infinity): it decides among the candidates where fp32 ones cannot.  Returns whether even that is not enough
+// (groups too close, or more candidates than lanes).
+template <int NPL, typename Exactly>
+__device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs &a, float *stage, Candidate *cand,
+                                       float margin, int &expert, Exactly exactly) {
     const int lane = threadIdx.x & 31;
-    K key[NPL];
+    unsigned key[NPL];
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) key[j] = sel[j] > -INFINITY ? O::key(sel[j]) : 0;
+    for (int j = 0; j < NPL; ++j) key[j] = sel[j] > -INFINITY ? order_key(sel[j]) : 0u;
     bool close = false;
     if (a.groups > 1) {
         // the worth of group g in lane g * per (and those beside it)
         const int per = a.group_lanes > 0 ? a.group_lanes : 1;
-        F t1 = -INFINITY, t2 = -INFINITY;
+        float t1 = -INFINITY, t2 = -INFINITY;
         if (a.group_lanes > 0) {
 #pragma unroll
-            for (int j = 0; j < NPL; ++j) merge_top2<F>(t1, t2, sel[j] > -INFINITY ? sel[j] : -INFINITY, -INFINITY);
-            for (int d = 1; d < per; d <<= 1)
-                merge_top2<F>(t1, t2, __shfl_xor_sync(kAll, t1, d), __shfl_xor_sync(kAll, t2, d));
+            for (int j = 0; j < NPL; ++j) take_top2(t1, t2, fmaxf(sel[j], -INFINITY));  // (NaN: none)
+            for (int d = 1; d < per; d <<= 1) {
+                const float o1 = __shfl_xor_sync(kAll, t1, d), o2 = __shfl_xor_sync(kAll, t2, d);
+                take_top2(t1, t2, o1);
+                t2 = fmaxf(t2, o2);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
-                if (lane * NPL + j < a.E) stage[lane * NPL + j] = sel[j] > -INFINITY ? sel[j] : -INFINITY;
+                if (lane * NPL + j < a.E) stage[lane * NPL + j] = fmaxf(sel[j], -INFINITY);
             __syncwarp();
             if (lane < a.groups)
                 for (int i = 0; i < a.group_size; ++i) {
                     const int at = i + lane < a.group_size ? i + lane : (i + lane) % a.group_size;  // (other banks)
-                    merge_top2<F>(t1, t2, stage[lane * a.group_size + at], -INFINITY);
+                    take_top2(t1, t2, stage[lane * a.group_size + at]);
                 }
             __syncwarp();
         }
-        const F worth = t1 + (a.group_sum == 2 && t2 > -INFINITY ? t2 : F(0));
-        const int g = lane / per;
-        int rank = 0;
-        for (int h = 0; h < a.groups; ++h) {
-            const F other = __shfl_sync(kAll, worth, h * per);
-            rank += other > worth || (other == worth && h < g);
-        }
-        const bool is_group = g < a.groups && worth > -INFINITY, kept = is_group && rank < a.top_groups;
+        const float worth = t1 + (a.group_sum == 2 && t2 > -INFINITY ? t2 : 0.0f);
+        bool kept;
+        const bool is_group = group_stays(worth, per, a, kept);
         if (margin > 0.0f) {
-            const K none = ~K(0);
-            const K low = ~O::warp_max(~(kept ? O::key(worth) : none)), high = O::warp_max(is_group && !kept ? O::key(worth) : 0);
-            if (high != 0) {
-                const float lo = Order32::value(static_cast<unsigned>(low)), hi = Order32::value(static_cast<unsigned>(high));
-                close = !(lo - hi > 2.0f * margin * (1.0f + fmaxf(fabsf(lo), fabsf(hi))));
-            }
+            const unsigned low = ~__reduce_max_sync(kAll, kept ? ~order_key(worth) : 0u);
+            const unsigned high = __reduce_max_sync(kAll, is_group && !kept ? order_key(worth) : 0u);
+            // (the biases' roundings go by the sums' terms, which may be far above the sums)
+            const float size = warp_max(is_group ? fabsf(t1) + (t2 > -INFINITY ? fabsf(t2) : 0.0f) : 0.0f);
+            if (high != 0u) close = too_close(order_value(low), order_value(high), 2.0f * margin + 0x1p-22f * size);
         }
-        const unsigned stays = __ballot_sync(kAll, kept);
         if (a.group_lanes > 0) {
 #pragma unroll
-            for (int j = 0; j < NPL; ++j) key[j] = kept ? key[j] : 0;
+            for (int j = 0; j < NPL; ++j) key[j] = kept ? key[j] : 0u;
         } else {
+            const unsigned stays = __ballot_sync(kAll, kept);
 #pragma unroll
             for (int j = 0; j < NPL; ++j) {
                 const int eg = (lane * NPL + j) / a.group_size;
-                if (eg >= 32 || (stays >> eg & 1u) == 0) key[j] = 0;
+                if (eg >= 32 || (stays >> eg & 1u) == 0) key[j] = 0u;
             }
         }
     }
-    K best = key[0];
+    const int rounds = margin > 0.0f ? a.top + 1 : a.top;  // one more than is chosen, to compare with
+    unsigned best = key[0], least = 0u;
+    if (NPL > 1) {
 #pragma unroll
-    for (int j = 1; j < NPL; ++j) best = best < key[j] ? key[j] : best;
-    expert = -1;
-    float last = 0.0f;
-    const int rounds = margin > 0.0f ? a.top + 1 : a.top;
-    for (int s = 0; s < rounds; ++s) {
-        const K top = O::warp_max(best);
-        if (top == 0) break;
-        if (margin > 0.0f) {
-            const float v = Order32::value(static_cast<unsigned>(top));
-            if (s > 0) close = close || !(last - v > margin * (1.0f + fmaxf(fabsf(last), fabsf(v))));
-            last = v;
-            if (s == a.top) break;
+        for (int j = 1; j < NPL; ++j) best = max(best, key[j]);
+        unsigned rest = best;
+        for (int s = 0; s < rounds; ++s) {
+            least = __reduce_max_sync(kAll, rest);
+            rest = rest == least ? 0u : rest;
         }
-        const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
-        int j_top = 0;
-        if (lane == owner) {
+    }
+    if (margin > 0.0f && least != 0u) {
+        // and what may in truth reach it
+        const float v = order_value(least);
+        if (v < INFINITY) least = order_key(v - (margin + 0x1p-22f * fabsf(v)));
+    }
+    least = max(least, 1u);
+    int n = 0;
 #pragma unroll
-            for (int j = NPL - 1; j >= 0; --j) j_top = key[j] == top ? j : j_top;
-            best = 0;
+    for (int j = 0; j < NPL; ++j) n += key[j] >= least;
+    unsigned mine = 0u;
+    int my_expert = -1, owner_of = -1;
+    const int total = __reduce_add_sync(kAll, n);
+    expert = -1;
+    float value = 0.0f;  // of the lane's choice
+    int found = 0;
+    if (total <= 32) {
+        if (NPL > 1) {
+            int at = n;
 #pragma unroll
-            for (int j = 0; j < NPL; ++j) {
-                if (j == j_top) key[j] = 0;
-                best = best < key[j] ? key[j] : best;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(kAll, at, d);
+                at += lane >= d ? o : 0;
+            }
+            at -= n;
+#pragma unroll
+            for (int j = 0; j < NPL; ++j)
+                if (key[j] >= least) cand[at++] = {key[j], lane * NPL + j};
+            __syncwarp();
+            if (lane < total) {
+                mine = cand[lane].key;
+                my_expert = cand[lane].expert;
+            }
+            __syncwarp();
+        } else {
+            mine = key[0];
+            my_expert = lane;
+        }
+        const bool candidate = mine != 0u;
+        for (; found < rounds; ++found) {
+            const unsigned top = __reduce_max_sync(kAll, mine);
+            if (top == 0u) break;
+            const int owner = __ffs(__ballot_sync(kAll, mine == top)) - 1;
+            if (lane == found) {
+                owner_of = owner;
+                value = order_value(top);
+            }
+            if (lane == owner) mine = 0u;
+        }
+        expert = __shfl_sync(kAll, my_expert, owner_of & 31);
+        expert = owner_of >= 0 && lane < a.top ? expert : -1;
+        if (margin > 0.0f) {
+            const float next = __shfl_down_sync(kAll, value, 1);
+            if (!close && __any_sync(kAll, lane + 1 < found && too_close(value, next, margin))) {
+                // each candidate's rank by its 64-bit score; the candidates are in the experts' order
+                const double v = exactly(candidate ? my_expert : -1);
+                int rank = 0;
+                for (int i = 0; i < 32; ++i) {
+                    const double o = __shfl_sync(kAll, v, i);
+                    rank += o > v || (o == v && i < lane);
+                }
+                if (candidate) cand[rank].expert = my_expert;
+                __syncwarp();
+                expert = lane < min(found, a.top) ? cand[lane].expert : -1;
+                __syncwarp();
             }
         }
-        const int e = owner * NPL + __shfl_sync(kAll, j_top, owner);
-        if (lane == s) expert = e;
+    } else {
+        // many equal maxima, or more experts to choose than lanes can bound: through the registers
+        float last = 0.0f;
+        for (; found < rounds; ++found) {
+            const unsigned top = __reduce_max_sync(kAll, best);
+            if (top == 0u) break;
+            const float v = order_value(top);
+            if (margin > 0.0f && found > 0) close = close || too_close(last, v, margin);
+            last = v;
+            if (found == a.top) break;
+            const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
+            int j_top = 0;
+            if (lane == owner) {
+#pragma unroll
+                for (int j = NPL - 1; j >= 0; --j) j_top = key[j] == top ? j : j_top;
+                best = 0u;
+#pragma unroll
+                for (int j = 0; j < NPL; ++j) {
+                    if (j == j_top) key[j] = 0u;
+                    best = max(best, key[j]);
+                }
+            }
+            const int e = owner * NPL + __shfl_sync(kAll, j_top, owner);
+            if (lane == found) expert = e;
+        }
     }
     return close;
 }
 
 // exp(x - m) of the lane's logits (0 for -infinity) and their sum over the warp.
-template <typename F, int NPL>
-__device__ __forceinline__ F softmax_parts(const float (&x)[NPL], float m, F (&p)[NPL]) {
-    F sum = 0;
-#pragma unroll
-    for (int j = 0; j < NPL; ++j) {
-        p[j] = x[j] > -INFINITY ? exp(static_cast<F>(x[j]) - static_cast<F>(m)) : F(0);
-        sum += p[j];
-    }
-    return warp_sum(sum);
-}
 template <int NPL>
 __device__ __forceinline__ float softmax_parts(const float (&x)[NPL], float m, float (&p)[NPL]) {
     float sum = 0.0f;
@@ -223,28 +292,69 @@ __device__ __forceinline__ float softmax_parts(const float (&x)[NPL], float m, f
     return warp_sum(sum);
 }
 
-template <int NPL>
-__device__ __forceinline__ float bias_of(const RouteArgs &a, int j) {
-    const int e = (threadIdx.x & 31) * NPL + j;
-    return a.bias != nullptr && e < a.E ? __ldg(a.bias + e) : 0.0f;
+// A selection score in 64 bits; m, sum: of the softmax.
+__device__ __forceinline__ double exact_score(float x, float bias, int score, float m, double sum) {
+    const double z = score == kScoreSoftmax ? exp(static_cast<double>(x) - static_cast<double>(m)) / sum
+                                            : 1.0 / (1.0 + exp(-static_cast<double>(x)));
+    return z + static_cast<double>(bias);
+}
+template <int LT>
+__device__ __forceinline__ double exact_sum(const typename Elem<LT>::T *row, int E, float m) {
+    double sum = 0.0;
+#pragma unroll 4
+    for (int e = threadIdx.x & 31; e < E; e += 32) {
+        const float x = logit_value(Elem<LT>::load(row + e));
+        sum += x > -INFINITY ? exp(static_cast<double>(x) - static_cast<double>(m)) : 0.0;
+    }
+    return warp_sum(sum);
 }
 
-// The choice by 64-bit scores.
-template <int NPL>
-__device__ __noinline__ int choose_exactly(const float (&x)[NPL], float m, const RouteArgs &a, double *stage) {
-    double sel[NPL];
-    if (a.score == kScoreSoftmax) {
-        const double sum = softmax_parts<double, NPL>(x, m, sel);
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) sel[j] /= sum;
-    } else {
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) sel[j] = 1.0 / (1.0 + exp(-static_cast<double>(x[j])));
+// The choice by 64-bit scores, in `stage` (E values of the warp); few tokens come here.
+template <int LT>
+__device__ __noinline__ int choose_exactly(const typename Elem<LT>::T *row, float m, const RouteArgs &a, double *stage) {
+    const int lane = threadIdx.x & 31;
+    const double sum = a.score == kScoreSoftmax ? exact_sum<LT>(row, a.E, m) : 1.0;
+#pragma unroll 4
+    for (int e = lane; e < a.E; e += 32) {
+        const float x = logit_value(Elem<LT>::load(row + e));
+        const double v = exact_score(x, a.bias != nullptr ? __ldg(a.bias + e) : 0.0f, a.score, m, sum);
+        stage[e] = x > -INFINITY && v > -INFINITY ? v : -INFINITY;
     }
+    __syncwarp();
+    if (a.groups > 1) {
+        double t1 = -INFINITY, t2 = -INFINITY;
+        if (lane < a.groups)
+            for (int i = 0; i < a.group_size; ++i) take_top2(t1, t2, stage[lane * a.group_size + i]);
+        bool kept;
+        group_stays(t1 + (a.group_sum == 2 && t2 > -INFINITY ? t2 : 0.0), 1, a, kept);
+        const unsigned stays = __ballot_sync(kAll, kept);
+        for (int e = lane; e < a.E; e += 32)
+            if ((stays >> (e / a.group_size) & 1u) == 0) stage[e] = -INFINITY;
+        __syncwarp();
+    }
+    int expert = -1;
+    for (int s = 0; s < a.top; ++s) {
+        double best = -INFINITY;
+        int at = a.E;
+        for (int e = lane; e < a.E; e += 32) {
+            const double v = stage[e];
+            at = v > best ? e : at;
+            best = v > best ? v : best;
+        }
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) sel[j] = x[j] > -INFINITY ? sel[j] + static_cast<double>(bias_of<NPL>(a, j)) : -INFINITY;
-    int expert;
-    choose<Order64, NPL>(sel, a, stage, 0.0f, expert);
+        for (int d = 16; d > 0; d >>= 1) {
+            const double o = __shfl_xor_sync(kAll, best, d);
+            const int oe = __shfl_xor_sync(kAll, at, d);
+            const bool takes = o > best || (o == best && oe < at);
+            best = takes ? o : best;
+            at = takes ? oe : at;
+        }
+        if (at >= a.E) break;
+        if (lane == s) expert = at;
+        if (lane == 0) stage[at] = -INFINITY;
+        __syncwarp();
+    }
+    __syncwarp();
     return expert;
 }
 
@@ -254,7 +364,7 @@ __device__ __forceinline__ float chosen_score(float x, bool live, int score, boo
                                               float &total) {
     float v;
     if (score == kScoreSoftmax) {
-        if (renorm) m = Order32::value(Order32::warp_max(Order32::key(live ? x : -INFINITY)));
+        if (renorm) m = warp_max(live ? x : -INFINITY);
         v = live && x > -INFINITY ? expf(x - m) : 0.0f;
         total = renorm ? warp_sum(v) : sum;
     } else {
@@ -263,7 +373,7 @@ __device__ __forceinline__ float chosen_score(float x, bool live, int score, boo
         const float low = fminf(x, 0.0f);
         float c = 0.0f;
         if (renorm) {
-            c = Order32::value(Order32::warp_max(Order32::key(live ? low : -INFINITY)));
+            c = warp_max(live ? low : -INFINITY);
             c = c > -INFINITY ? c : 0.0f;
         }
         v = live && x > -INFINITY ? __fdiv_rn(expf(low - c), 1.0f + expf(-fabsf(x))) : 0.0f;
@@ -272,12 +382,22 @@ __device__ __forceinline__ float chosen_score(float x, bool live, int score, boo
     return v;
 }
 
-template <int LT, int NPL>
+// BY_LOGIT: the selection scores have the logits' order.
+template <int LT, int NPL, bool BY_LOGIT>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ RouteArgs a) {
     using T = typename Elem<LT>::T;
     extern __shared__ double stage_all[];
+    __shared__ Candidate cand_all[kRouteWarps][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     double *stage = stage_all + warp * a.stage;
+    float b[BY_LOGIT ? 1 : NPL];
+    if (!BY_LOGIT) {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) {
+            const int e = lane * NPL + j;
+            b[BY_LOGIT ? 0 : j] = a.bias != nullptr && e < a.E ? __ldg(a.bias + e) : 0.0f;
+        }
+    }
     for (long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp; t < a.T;
          t += static_cast<long long>(gridDim.x) * kRouteWarps) {
         const T *row = static_cast<const T *>(a.logits) + t * a.ldl;
@@ -285,13 +405,13 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
         load_logits<LT, NPL>(row, a.E, a.vec, x);
         float m = 0.0f, sum = 1.0f;
         int expert;
-        if (a.by_logit) {
+        if constexpr (BY_LOGIT) {
             if (a.score == kScoreSoftmax && !a.renorm) {
                 float p[NPL];
                 m = warp_max_of(x);
                 sum = softmax_parts<NPL>(x, m, p);
             }
-            choose<Order32, NPL>(x, a, reinterpret_cast<float *>(stage), 0.0f, expert);
+            choose<NPL>(x, a, reinterpret_cast<float *>(stage), cand_all[warp], 0.0f, expert, [](int) { return 0.0; });
         } else {
             float sel[NPL];
             if (a.score == kScoreSoftmax) {
@@ -304,16 +424,20 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
                 for (int j = 0; j < NPL; ++j) sel[j] = __fdividef(1.0f, 1.0f + __expf(-x[j]));
             }
 #pragma unroll
-            for (int j = 0; j < NPL; ++j) sel[j] = x[j] > -INFINITY ? sel[j] + bias_of<NPL>(a, j) + 0.0f : -INFINITY;
-            // What a difference of two scores may be off by, relative to 1 + the larger: sigmoid, two errors of
-            // less than 2^-21 (exponential, quotient, the bias's addition); softmax, its sum's 37 roundings too.
-            const float margin = a.score == kScoreSoftmax ? 0x1p-17f : 0x1p-19f;
-            if (choose<Order32, NPL>(sel, a, reinterpret_cast<float *>(stage), margin, expert)) {
-                float copy[NPL];  // (the call takes an address: x itself stays in registers)
-#pragma unroll
-                for (int j = 0; j < NPL; ++j) copy[j] = x[j];
-                expert = choose_exactly<NPL>(copy, m, a, stage);
-            }
+            for (int j = 0; j < NPL; ++j) sel[j] = x[j] > -INFINITY ? sel[j] + b[j] + 0.0f : -INFINITY;
+            // What a difference of two scores may be off by, apart from the biases' roundings.  Sigmoid: each by less
+            // than 1.6 x 2^-22, namely 1 for the quotient, 1/4 for the sum's rounding, 1/4 (the score's slope) for the
+            // exponential and 0.09 for its argument's rounding (slope times |x| is at most 0.224).  Softmax, relative
+            // to the largest score, 1 / sum: the sum's 37 roundings of 2^-24, common to both, and 9 each of
+            // exponential and quotient.
+            const float margin = a.score == kScoreSoftmax ? __fdividef(0x1p-18f, sum) : 0x1p-20f;
+            const bool unsure = choose<NPL>(sel, a, reinterpret_cast<float *>(stage), cand_all[warp], margin, expert,
+                                            [&](int e) {
+                const double total = a.score == kScoreSoftmax ? exact_sum<LT>(row, a.E, m) : 1.0;  // (by the warp)
+                return e < 0 ? -INFINITY : exact_score(logit_value(Elem<LT>::load(row + e)),
+                                                       a.bias != nullptr ? __ldg(a.bias + e) : 0.0f, a.score, m, total);
+            });
+            if (unsure) expert = choose_exactly<LT>(row, m, a, stage);
         }
         const bool live = expert >= 0;
         const float xs = live ? logit_value(Elem<LT>::load(row + expert)) : 0.0f;
@@ -402,8 +526,12 @@ cudaError_t launch_route_npl(const RouteArgs &in, int sms, cudaStream_t s) {
     a.group_size = a.E / a.groups;
     a.group_lanes = 0;
     if (a.groups > 1 && a.E == 32 * NPL && 32 % a.groups == 0) a.group_lanes = 32 / a.groups;
-    a.stage = a.groups > 1 && a.group_lanes == 0 ? a.E : 0;
-    route_kernel<LT, NPL><<<route_blocks(a.T, sms), 32 * kRouteWarps, kRouteWarps * a.stage * 8, s>>>(a);
+    a.stage = !a.by_logit || (a.groups > 1 && a.group_lanes == 0) ? a.E : 0;
+    const int bytes = kRouteWarps * a.stage * 8;
+    if (a.by_logit)
+        route_kernel<LT, NPL, true><<<route_blocks(a.T, sms), 32 * kRouteWarps, bytes, s>>>(a);
+    else
+        route_kernel<LT, NPL, false><<<route_blocks(a.T, sms), 32 * kRouteWarps, bytes, s>>>(a);
     return cudaGetLastError();
 }
 

@@ -7,6 +7,7 @@
 // expert, a place behind the last pair).
 #include "epilogue.cuh"
 #include "kernel_args.h"
+#include "sm103_ptx.cuh"
 
 namespace gb300 {
 
@@ -25,6 +26,7 @@ constexpr int kCountThreads = 256;
 
 __global__ void __launch_bounds__(kCountThreads) route_count_kernel(const __grid_constant__ RouteRowsArgs a) {
     extern __shared__ int counts[];
+    grid_dep_launch();  // the second kernel may begin to count its chunks
     for (int e = threadIdx.x; e < a.E; e += kCountThreads) counts[e] = 0;
     __syncthreads();
     const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.P);
@@ -34,7 +36,7 @@ __global__ void __launch_bounds__(kCountThreads) route_count_kernel(const __grid
     }
     __syncthreads();
     for (int e = threadIdx.x; e < a.E; e += kCountThreads)
-        a.counts[static_cast<long long>(blockIdx.x) * a.E + e] = counts[e];
+        a.counts[static_cast<long long>(e) * gridDim.x + blockIdx.x] = counts[e];
 }
 
 // Pairs begin .. end - 1 of one warp, 32 at a time: f(pair, expert, lanes of the same expert), expert -1 where there
@@ -50,11 +52,12 @@ __device__ __forceinline__ void warp_pairs(const RouteRowsArgs &a, int begin, in
     }
 }
 
-__global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant__ RouteRowsArgs a) {
+__global__ void __launch_bounds__(512) route_rows_kernel(const __grid_constant__ RouteRowsArgs a) {
     extern __shared__ int smem[];
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *first = smem;              // E + 1: pairs of the experts before
-    int *own = smem + a.E + 1;      // warps x E: counts, then places
+    int *start = first + a.E + 1;   // E: an expert's pairs in the chunks before
+    int *own = start + a.E;         // warps x E: counts, then places
     for (int i = threadIdx.x; i < warps * a.E; i += blockDim.x) own[i] = 0;
     __syncthreads();
     const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.P);
@@ -66,25 +69,48 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant_
         __syncwarp();
     });
     __syncthreads();
-    // every expert's total, and what lies before this chunk
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        int before = 0, total = 0;
-        if (gridDim.x > 1) {
-            for (int c = 0; c < static_cast<int>(gridDim.x); ++c) {
-                const int n = __ldg(a.counts + static_cast<long long>(c) * a.E + e);
-                before += c < static_cast<int>(blockIdx.x) ? n : 0;
-                total += n;
+    // every expert's total, and what lies before this chunk (a warp takes an expert, its lanes the chunks)
+    if (gridDim.x > 1) {
+        grid_dep_wait();  // for the first kernel's counts
+        const int chunks = gridDim.x;
+        constexpr int kPer = (kRowsChunks + 31) / 32, kAtOnce = 4;  // loads of a lane per expert, experts at once
+        for (int e0 = warp; e0 < a.E; e0 += kAtOnce * warps) {
+            int n[kAtOnce][kPer];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    const int e = e0 + i * warps, c = lane + 32 * k;
+                    n[i][k] = e < a.E && c < chunks ? __ldcg(a.counts + static_cast<long long>(e) * chunks + c) : 0;
+                }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                int before = 0, total = 0;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    before += lane + 32 * k < static_cast<int>(blockIdx.x) ? n[i][k] : 0;
+                    total += n[i][k];
+                }
+                before = __reduce_add_sync(kAll, before);
+                total = __reduce_add_sync(kAll, total);
+                const int e = e0 + i * warps;
+                if (lane == 0 && e < a.E) {
+                    first[e + 1] = total;
+                    start[e] = before;
+                }
             }
-        } else {
-            for (int w = 0; w < warps; ++w) total += own[w * a.E + e];
         }
+        __syncthreads();
+    }
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        const int before = gridDim.x > 1 ? start[e] : 0;
         int at = before;
         for (int w = 0; w < warps; ++w) {
             const int n = own[w * a.E + e];
             own[w * a.E + e] = at;
             at += n;
         }
-        first[e + 1] = total;
+        if (gridDim.x == 1) first[e + 1] = at;
     }
     if (threadIdx.x == 0) first[0] = 0;
     __syncthreads();
@@ -129,12 +155,21 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant_
 
 constexpr int kMoveThreads = 256;
 
-// A piece of a row: 16 bytes (V) or one element.
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 ld_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// A piece of a row: 16 bytes (V) or one element, as stored until it is used, so that many are on their way at once.
 template <int DT, bool V> struct Piece {
     static constexpr int N = Vec16<DT>::kPerVec;
-    static __device__ __forceinline__ void load(const void *row, long long i, float (&f)[N]) {
-        Vec16<DT>::unpack(__ldg(static_cast<const uint4 *>(row) + i), f);
-    }
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw load(const void *row, long long i) { return ld_stream(static_cast<const uint4 *>(row) + i); }
+    static __device__ __forceinline__ void unpack(const Raw &u, float (&f)[N]) { Vec16<DT>::unpack(u, f); }
     static __device__ __forceinline__ void store(void *row, long long i, const float (&f)[N]) {
         static_cast<uint4 *>(row)[i] = Vec16<DT>::pack(f);
     }
@@ -142,9 +177,9 @@ template <int DT, bool V> struct Piece {
 template <int DT> struct Piece<DT, false> {
     static constexpr int N = 1;
     using T = typename Elem<DT>::T;
-    static __device__ __forceinline__ void load(const void *row, long long i, float (&f)[1]) {
-        f[0] = Elem<DT>::load(static_cast<const T *>(row) + i);
-    }
+    using Raw = T;
+    static __device__ __forceinline__ Raw load(const void *row, long long i) { return static_cast<const T *>(row)[i]; }
+    static __device__ __forceinline__ void unpack(const Raw &u, float (&f)[1]) { f[0] = Elem<DT>::load(&u); }
     static __device__ __forceinline__ void store(void *row, long long i, const float (&f)[1]) {
         static_cast<T *>(row)[i] = Elem<DT>::cvt(f[0]);
     }
@@ -163,6 +198,7 @@ __device__ __forceinline__ char *row_at(void *base, long long row, long long ld)
 template <int DT, bool V>
 __global__ void __launch_bounds__(kMoveThreads) rows_gather_kernel(const __grid_constant__ RowsArgs a) {
     using P = Piece<DT, V>;
+    constexpr int kAhead = 4;
     const int pieces = a.D / P::N, tid = threadIdx.x;
     for (long long r = blockIdx.x; r < a.R; r += gridDim.x) {
         const int p = __ldg(a.source + r);
@@ -170,30 +206,49 @@ __global__ void __launch_bounds__(kMoveThreads) rows_gather_kernel(const __grid_
         const float w = a.weight != nullptr ? __ldg(a.weight + p) : 1.0f;
         const void *x = row_at<DT>(a.X, p / a.top, a.ldx);
         void *y = row_at<DT>(a.Y, r, a.ldy);
-#pragma unroll 4
-        for (int i = tid; i < pieces; i += kMoveThreads) {
-            float f[P::N];
-            P::load(x, i, f);
-            if (a.weight != nullptr) {
+        for (int i0 = tid; i0 < pieces; i0 += kAhead * kMoveThreads) {
+            typename P::Raw raw[kAhead];
 #pragma unroll
-                for (int j = 0; j < P::N; ++j) f[j] *= w;
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k * kMoveThreads < pieces) raw[k] = P::load(x, i0 + k * kMoveThreads);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (i0 + k * kMoveThreads >= pieces) break;
+                float f[P::N];
+                P::unpack(raw[k], f);
+                if (a.weight != nullptr) {
+#pragma unroll
+                    for (int j = 0; j < P::N; ++j) f[j] *= w;
+                }
+                P::store(y, i0 + k * kMoveThreads, f);
             }
-            P::store(y, i, f);
         }
     }
 }
 
 constexpr int kSlots = 8;  // rows in flight per piece
 
+// The rows and weights of kSlots slots of a token from slot s0 on; -1: none.
+__device__ __forceinline__ void slots_of(const RowsArgs &a, long long t, int s0, int (&r)[kSlots], float (&w)[kSlots]) {
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s) {
+        r[s] = s0 + s < a.top ? __ldg(a.row + t * a.top + s0 + s) : -1;
+        w[s] = a.weight != nullptr && s0 + s < a.top ? __ldg(a.weight + t * a.top + s0 + s) : 1.0f;
+    }
+#pragma unroll
+    for (int s = 0; s < kSlots; ++s)
+        if (static_cast<unsigned>(r[s]) >= static_cast<unsigned>(a.R)) r[s] = -1;
+}
+
 // Out[t] = sum_s w[t][s] Y[row[t][s]] + beta Out[t]; slots without a row add nothing.
 template <int YT, int OT, bool V>
-__global__ void __launch_bounds__(kMoveThreads) rows_combine_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kMoveThreads, 4) rows_combine_kernel(const __grid_constant__ RowsArgs a) {
     using P = Piece<YT, V>;
     using O = Piece<OT, V>;
     constexpr int OV = P::N / O::N;  // pieces of the output per piece of Y: 1, 2, or 0 for half a piece
     const int pieces = a.D / P::N;
     const long long t = blockIdx.x;
-    const int i = blockIdx.y * kMoveThreads + threadIdx.x;
+    const int i = blockIdx.y * blockDim.x + threadIdx.x;
     if (i >= pieces) return;
     float acc[P::N];
     char *out = row_at<OT>(a.X, t, a.ldx) + static_cast<long long>(i) * P::N * sizeof(typename Elem<OT>::T);
@@ -201,21 +256,19 @@ __global__ void __launch_bounds__(kMoveThreads) rows_combine_kernel(const __grid
     for (int j = 0; j < P::N; ++j) acc[j] = 0.0f;
     for (int s0 = 0; s0 < a.top; s0 += kSlots) {
         int r[kSlots];
-        float w[kSlots], f[kSlots][P::N];
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
-            r[s] = s0 + s < a.top ? __ldg(a.row + t * a.top + s0 + s) : -1;
-            if (static_cast<unsigned>(r[s]) >= static_cast<unsigned>(a.R)) r[s] = -1;
-            w[s] = a.weight != nullptr && r[s] >= 0 ? __ldg(a.weight + t * a.top + s0 + s) : 1.0f;
-        }
+        float w[kSlots];
+        typename P::Raw raw[kSlots];
+        slots_of(a, t, s0, r, w);
 #pragma unroll
         for (int s = 0; s < kSlots; ++s)
-            if (r[s] >= 0) P::load(row_at<YT>(a.Y, r[s], a.ldy), i, f[s]);
+            if (r[s] >= 0) raw[s] = P::load(row_at<YT>(a.Y, r[s], a.ldy), i);
 #pragma unroll
         for (int s = 0; s < kSlots; ++s)
             if (r[s] >= 0) {
+                float f[P::N];
+                P::unpack(raw[s], f);
 #pragma unroll
-                for (int j = 0; j < P::N; ++j) acc[j] = fmaf(w[s], f[s][j], acc[j]);
+                for (int j = 0; j < P::N; ++j) acc[j] = fmaf(w[s], f[j], acc[j]);
             }
     }
     if constexpr (!V) {
@@ -248,63 +301,70 @@ __global__ void __launch_bounds__(kMoveThreads) rows_combine_kernel(const __grid
     }
 }
 
-// dY[row] = w dOut[t], dweight[t][s] = dOut[t] . Y[row]; slots without a row: dweight 0.
+constexpr int kGradThreads = 320;
+
+// dY[row] = w dOut[t], dweight[t][s] = dOut[t] . Y[row]; slots without a row: dweight 0.  A block takes a token.
 template <int DT, int YT, bool V>
-__global__ void __launch_bounds__(kMoveThreads) rows_combine_grad_kernel(const __grid_constant__ RowsArgs a) {
+__global__ void __launch_bounds__(kGradThreads, 3) rows_combine_grad_kernel(const __grid_constant__ RowsArgs a) {
     using P = Piece<DT, V>;
     using Q = Piece<YT, V>;
-    // the widest piece of the two is the step: HV of P, YV of Q
+    // the wider piece of the two is the step: HV of P, YV of Q
     constexpr int N = P::N > Q::N ? P::N : Q::N, HV = N / P::N, YV = N / Q::N;
-    __shared__ float part[kMoveThreads / 32][kSlots];
+    __shared__ float part[kGradThreads / 32][kSlots];
+    __shared__ int r[kSlots];  // (in shared memory: a thread's registers hold rows on their way)
+    __shared__ float w[kSlots];
     const int steps = a.D / N, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
     const long long t = blockIdx.x;
     const void *d = row_at<DT>(a.X, t, a.ldx);
     for (int s0 = 0; s0 < a.top; s0 += kSlots) {
-        int r[kSlots];
-        float w[kSlots], dot[kSlots];
-#pragma unroll
-        for (int s = 0; s < kSlots; ++s) {
-            r[s] = s0 + s < a.top ? __ldg(a.row + t * a.top + s0 + s) : -1;
-            if (static_cast<unsigned>(r[s]) >= static_cast<unsigned>(a.R)) r[s] = -1;
-            w[s] = a.weight != nullptr && r[s] >= 0 ? __ldg(a.weight + t * a.top + s0 + s) : 1.0f;
-            dot[s] = 0.0f;
+        float dot[kSlots];
+        if (tid < kSlots) {
+            const bool slot = s0 + tid < a.top;
+            const int row = slot ? __ldg(a.row + t * a.top + s0 + tid) : -1;
+            r[tid] = static_cast<unsigned>(row) < static_cast<unsigned>(a.R) ? row : -1;
+            w[tid] = a.weight != nullptr && slot ? __ldg(a.weight + t * a.top + s0 + tid) : 1.0f;
         }
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < kSlots; ++s) dot[s] = 0.0f;
         for (int i = tid; i < steps; i += n) {
             float g[N];
 #pragma unroll
             for (int v = 0; v < HV; ++v) {
                 float h[P::N];
-                P::load(d, static_cast<long long>(i) * HV + v, h);
+                P::unpack(P::load(d, static_cast<long long>(i) * HV + v), h);
 #pragma unroll
                 for (int j = 0; j < P::N; ++j) g[v * P::N + j] = h[j];
             }
-            if (a.dweight != nullptr) {
-                float y[kSlots][Q::N];
 #pragma unroll
-                for (int v = 0; v < YV; ++v) {
+            for (int v = 0; v < YV; ++v) {
+                const long long at = static_cast<long long>(i) * YV + v;
+                typename Q::Raw raw[kSlots];
+                if (a.dweight != nullptr) {
 #pragma unroll
                     for (int s = 0; s < kSlots; ++s)
-                        if (r[s] >= 0) Q::load(row_at<YT>(a.Y, r[s], a.ldy), static_cast<long long>(i) * YV + v, y[s]);
+                        if (r[s] >= 0) raw[s] = Q::load(row_at<YT>(a.Y, r[s], a.ldy), at);
+                }
+                if (a.dY != nullptr) {
 #pragma unroll
                     for (int s = 0; s < kSlots; ++s)
                         if (r[s] >= 0) {
-#pragma unroll
-                            for (int j = 0; j < Q::N; ++j) dot[s] = fmaf(g[v * Q::N + j], y[s][j], dot[s]);
-                        }
-                }
-            }
-            if (a.dY != nullptr) {
-#pragma unroll
-                for (int s = 0; s < kSlots; ++s)
-                    if (r[s] >= 0) {
-#pragma unroll
-                        for (int v = 0; v < YV; ++v) {
                             float o[Q::N];
 #pragma unroll
                             for (int j = 0; j < Q::N; ++j) o[j] = w[s] * g[v * Q::N + j];
-                            Q::store(row_at<YT>(a.dY, r[s], a.lddy), static_cast<long long>(i) * YV + v, o);
+                            Q::store(row_at<YT>(a.dY, r[s], a.lddy), at, o);
                         }
-                    }
+                }
+                if (a.dweight != nullptr) {
+#pragma unroll
+                    for (int s = 0; s < kSlots; ++s)
+                        if (r[s] >= 0) {
+                            float y[Q::N];
+                            Q::unpack(raw[s], y);
+#pragma unroll
+                            for (int j = 0; j < Q::N; ++j) dot[s] = fmaf(g[v * Q::N + j], y[j], dot[s]);
+                        }
+                }
             }
         }
         if (a.dweight != nullptr) {
@@ -321,26 +381,32 @@ __global__ void __launch_bounds__(kMoveThreads) rows_combine_grad_kernel(const _
                 for (int k = 0; k < n >> 5; ++k) v += part[k][tid];
                 a.dweight[t * a.top + s0 + tid] = v;
             }
-            __syncthreads();
         }
+        if (s0 + kSlots < a.top) __syncthreads();
     }
+}
+
+// Threads of a block, at most `most`, that share `pieces` of a row evenly: whole warps, no round nearly empty.
+int block_for(int pieces, int most) {
+    const int rounds = (pieces + most - 1) / most;
+    return pieces <= 0 ? 32 : ((pieces + rounds - 1) / rounds + 31) / 32 * 32;
 }
 
 template <int YT, int OT>
 cudaError_t launch_combine(const RowsArgs &a, bool vec, cudaStream_t s) {
-    const int pieces = vec ? a.D / Vec16<YT>::kPerVec : a.D;
-    const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>((pieces + kMoveThreads - 1) / kMoveThreads));
+    const int pieces = vec ? a.D / Vec16<YT>::kPerVec : a.D, n = block_for(pieces, kMoveThreads);
+    const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>((pieces + n - 1) / n));
     if (vec)
-        rows_combine_kernel<YT, OT, true><<<grid, kMoveThreads, 0, s>>>(a);
+        rows_combine_kernel<YT, OT, true><<<grid, n, 0, s>>>(a);
     else
-        rows_combine_kernel<YT, OT, false><<<grid, kMoveThreads, 0, s>>>(a);
+        rows_combine_kernel<YT, OT, false><<<grid, n, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <int DT, int YT>
 cudaError_t launch_grad(const RowsArgs &a, bool vec, cudaStream_t s) {
     const int per = vec ? (Vec16<DT>::kPerVec > Vec16<YT>::kPerVec ? Vec16<DT>::kPerVec : Vec16<YT>::kPerVec) : 1;
-    const int want = (a.D / per + 31) / 32 * 32, n = want < 32 ? 32 : want < kMoveThreads ? want : kMoveThreads;
+    const int n = block_for(a.D / per, kGradThreads);
     if (vec)
         rows_combine_grad_kernel<DT, YT, true><<<static_cast<unsigned>(a.T), n, 0, s>>>(a);
     else
@@ -354,12 +420,28 @@ cudaError_t launch_route_rows(const RouteRowsArgs &in, cudaStream_t s) {
     RouteRowsArgs a = in;
     const int chunks = route_rows_chunks(a.P);
     a.chunk = static_cast<int>(((static_cast<long long>(a.P) + chunks - 1) / chunks + 31) / 32 * 32);
-    // as many warps as 32 KB of counts allow, and as there are pairs for
-    const int most = 8192 / a.E < 32 ? 8192 / a.E : 32, want = (a.chunk + 31) / 32;
-    const int warps = want < 1 ? 1 : want < most ? want : most;
-    if (chunks > 1) route_count_kernel<<<chunks, kCountThreads, a.E * 4, s>>>(a);
-    route_rows_kernel<<<chunks, 32 * warps, (a.E + 1 + warps * a.E) * 4, s>>>(a);
-    return cudaGetLastError();
+    // as many warps as 32 KB of counts allow, and as there are pairs for; at most 16, each expert's counts are summed
+    // over them one by one
+    const int most = 8192 / a.E < 16 ? 8192 / a.E : 16, want = (a.chunk + 31) / 32;
+    const int warps = want < 1 ? 1 : want < most ? want : most, bytes = (2 * a.E + 1 + warps * a.E) * 4;
+    if (chunks == 1) {
+        route_rows_kernel<<<1, 32 * warps, bytes, s>>>(a);
+        return cudaGetLastError();
+    }
+    route_count_kernel<<<chunks, kCountThreads, a.E * 4, s>>>(a);
+    cudaError_t err = cudaGetLastError();
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(chunks, 1, 1);
+    cfg.blockDim = dim3(32 * warps, 1, 1);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, route_rows_kernel, a);
 }
 
 cudaError_t launch_rows_gather(int dtype, const RowsArgs &a, bool vec, int sms, cudaStream_t s) {

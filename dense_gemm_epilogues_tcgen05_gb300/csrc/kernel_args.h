@@ -211,7 +211,7 @@ struct RouteGradArgs {
     long long ldd;
 };
 
-// Pairs sorted by expert (gemm_rows.cu).  P = T top; counts: chunks x E, unused by one chunk.
+// Pairs sorted by expert (gemm_rows.cu).  P = T top; counts: E x chunks, unused by one chunk.
 struct RouteRowsArgs {
     int P, E;
     const int *expert;
@@ -219,8 +219,9 @@ struct RouteRowsArgs {
     int chunk;                      // set by the launcher: pairs of a block
 };
 // Blocks of a sort: one up to 4096 pairs, where its own launch is all that a second one would save.
+constexpr int kRowsChunks = 144;
 constexpr int route_rows_chunks(long long P) {
-    return P <= 4096 ? 1 : P >= 144ll * 1024 ? 144 : static_cast<int>((P + 1023) / 1024);
+    return P <= 4096 ? 1 : P >= kRowsChunks * 1024ll ? kRowsChunks : static_cast<int>((P + 1023) / 1024);
 }
 
 // Movement of rows (gemm_rows.cu): X token order (R: rows of Y), Y expert order.  The output of a combination is X
@@ -341,11 +342,12 @@ cudaError_t launch_mx_pair(int elem, int out, const CUtensorMap &ta, const CUten
 cudaError_t launch_mx_sf_pack(const unsigned char *src, long long rows, long long blocks, unsigned char *dst,
                               long long row_blocks, long long kc_count, cudaStream_t stream);
 // Block-scaled product grouped by expert, `clusters` SM pairs, tiles of args.most rows at most.  Operands as bytes:
-// w = (K, F, G) in boxes of 128 x 128, x[i] = (K, T) in boxes of 128 x 16 (i + 1), 128-byte swizzle; their scales
-// ws = (K / 32, F, G) in boxes of 16 x 128 and xs[i] = (K / 32, T) in boxes of 16 x (32 << i), not swizzled.
-constexpr int kMxgMost = 224;       // its widest row tile: two accumulators and the scales in tensor memory
+// w = (K, F, G) in boxes of 128 x 128, x[i] = (K, T) in boxes of 128 x 8 (i + 1), 128-byte swizzle; their scales
+// ws = (K / 32, F, G) in boxes of 16 x 128 and xs[i] = (K / 32, T) in boxes of 16 x (32 << i), not swizzled.  Maps of
+// boxes wider than half of T rounded up to 16 (scales: T) are not read.
+constexpr int kMxgMost = 208;       // its widest row tile: two accumulators and two boxes of scales in tensor memory
 struct MxgMaps {
-    CUtensorMap w, x[kMxgMost / 32], ws, xs[4];
+    CUtensorMap w, x[kMxgMost / 16], ws, xs[4];
 };
 cudaError_t launch_mx_grouped(int elem, int out, const MxgMaps &maps, const GtcArgs &args, int clusters,
                               cudaStream_t stream);
