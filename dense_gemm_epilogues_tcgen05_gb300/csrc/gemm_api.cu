@@ -1794,8 +1794,9 @@ gemm_status_t gemm_mx_quantize(int64_t M, int64_t K, gemm_mx_elem_t elem, gemm_d
     a.top = source != nullptr ? static_cast<int>(top) : 1;
     a.Q = static_cast<unsigned char *>(Q); a.q_pitch = ldq / per_byte;
     a.scale = scale; a.s_pitch = lds;
-    return launch_mx_quantize(elem, x_dtype, a, rows_at(X, rows_x, ldx * es, 16),
-                              rows_at(Q, M, a.q_pitch, 8 / per_byte), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    const int x_bytes = rows_at(X, rows_x, ldx * es, 32) ? 32 : rows_at(X, rows_x, ldx * es, 16) ? 16 : 0;
+    return launch_mx_quantize(elem, x_dtype, a, x_bytes, rows_at(Q, M, a.q_pitch, 16 / per_byte),
+                              reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GEMM_OK : GEMM_ERR_CUDA;
 }
 

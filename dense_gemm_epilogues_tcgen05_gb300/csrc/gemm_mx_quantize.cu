@@ -8,52 +8,63 @@
 // block of zeros has code 0; one with a NaN or an infinity the NaN code 0xFF, so
 // that a product shows it, and elements 0.
 //
-// A thread takes 8 consecutive values, four neighbouring lanes a block of 32.
-// Bound by HBM; kPieces loads per thread are in flight before the first is used.
+// Quantising, a thread takes 16 consecutive values, two neighbouring lanes a block
+// of 32; back, 8 values.  Bound by HBM, the quantiser also by its instructions: with
+// 8 values a thread, 120 of them per 8 values and 66 us for 32768 x 4096 bf16.
+// Several pieces of a thread are on their way before the first is used.
 #include "epilogue.cuh"
 #include "kernel_args.h"
+#include "launch.cuh"
 
 namespace gb300 {
 
 namespace {
 
-constexpr int kMxThreads = 256, kPieces = 4;
+constexpr int kMxThreads = 256;
+constexpr int kTo = 2, kFrom = 4;  // pieces of a thread: 16 values to codes, 8 codes to values
 constexpr unsigned kAll = 0xffffffffu;
 
-// 16 bytes that are read once.
-__device__ __forceinline__ uint4 ld_stream(const uint4 *p) {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
-}
+// How rows of X may be read: one value, 16 or 32 bytes at a time.
+enum { kOne = 0, kSixteen = 1, kThirtyTwo = 2 };
 
-// Eight values as they are stored.
-template <int XT, bool VEC> struct Eight {
-    static constexpr int PV = Vec16<XT>::kPerVec;
-    uint4 u[8 / PV];
+// Sixteen values as they are stored.
+template <int XT, int HOW> struct Sixteen {
+    static constexpr int PV = Vec16<XT>::kPerVec, N = 16 / PV;
+    uint4 u[N];
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int v = 0; v < 8 / PV; ++v) u[v] = make_uint4(0, 0, 0, 0);
+        for (int v = 0; v < N; ++v) u[v] = make_uint4(0, 0, 0, 0);
     }
     __device__ __forceinline__ void load(const typename Elem<XT>::T *p) {
+        if constexpr (HOW == kThirtyTwo) {
 #pragma unroll
-        for (int v = 0; v < 8 / PV; ++v) u[v] = ld_stream(reinterpret_cast<const uint4 *>(p) + v);
+            for (int v = 0; v < N; v += 2)
+                asm volatile("ld.global.nc.L1::no_allocate.v8.u32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                             : "=r"(u[v].x), "=r"(u[v].y), "=r"(u[v].z), "=r"(u[v].w), "=r"(u[v + 1].x),
+                               "=r"(u[v + 1].y), "=r"(u[v + 1].z), "=r"(u[v + 1].w)
+                             : "l"(reinterpret_cast<const uint4 *>(p) + v));
+        } else {
+#pragma unroll
+            for (int v = 0; v < N; ++v) u[v] = __ldg(reinterpret_cast<const uint4 *>(p) + v);
+        }
     }
-    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    __device__ __forceinline__ void unpack(float (&f)[16]) const {
 #pragma unroll
-        for (int v = 0; v < 8 / PV; ++v) Vec16<XT>::unpack(u[v], &f[v * PV]);
+        for (int v = 0; v < N; ++v) Vec16<XT>::unpack(u[v], &f[v * PV]);
     }
     // The bits of the largest |x|, as fp32: with the sign cleared values are ordered as integers, infinities and NaN
     // last; 16-bit ones two at a time.
     __device__ __forceinline__ unsigned max_bits() const {
         unsigned m = 0;
 #pragma unroll
-        for (int v = 0; v < 8 / PV; ++v) {
-            const uint32_t w[4] = {u[v].x, u[v].y, u[v].z, u[v].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) m = XT == kDtF32 ? max(m, w[i] & 0x7FFFFFFFu) : __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        for (int v = 0; v < N; ++v) {
+            if constexpr (XT == kDtF32) {
+                m = max(max(m, u[v].x & 0x7FFFFFFFu), u[v].y & 0x7FFFFFFFu);
+                m = max(max(m, u[v].z & 0x7FFFFFFFu), u[v].w & 0x7FFFFFFFu);
+            } else {
+                m = __vimax3_u16x2(m, u[v].x & 0x7FFF7FFFu, u[v].y & 0x7FFF7FFFu);
+                m = __vimax3_u16x2(m, u[v].z & 0x7FFF7FFFu, u[v].w & 0x7FFF7FFFu);
+            }
         }
         if constexpr (XT == kDtF32) return m;
         m = max(m & 0xFFFFu, m >> 16);
@@ -61,30 +72,30 @@ template <int XT, bool VEC> struct Eight {
         return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(m))));
     }
 };
-template <int XT> struct Eight<XT, false> {
-    float f8[8];
+template <int XT> struct Sixteen<XT, kOne> {
+    float v[16];
     __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f8[j] = 0.0f;
+        for (int j = 0; j < 16; ++j) v[j] = 0.0f;
     }
     __device__ __forceinline__ void load(const typename Elem<XT>::T *p) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f8[j] = Elem<XT>::load(p + j);
+        for (int j = 0; j < 16; ++j) v[j] = Elem<XT>::load(p + j);
     }
-    __device__ __forceinline__ void unpack(float (&f)[8]) const {
+    __device__ __forceinline__ void unpack(float (&f)[16]) const {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] = f8[j];
+        for (int j = 0; j < 16; ++j) f[j] = v[j];
     }
     __device__ __forceinline__ unsigned max_bits() const {
         unsigned m = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f8[j]) & 0x7FFFFFFFu);
+        for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
         return m;
     }
 };
 
 // Pairs of fp32 values to E2M1 (nearest even, saturating), the first of each pair in the low nibble.
-__device__ __forceinline__ uint32_t e2m1_of(const float (&f)[8]) {
+__device__ __forceinline__ uint32_t e2m1_of(const float *f) {
     uint32_t r;
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
@@ -113,7 +124,7 @@ __device__ __forceinline__ void e2m1_values(uint32_t c, float (&f)[8]) {
         f[2 * i + 1] = t.y;
     }
 }
-__device__ __forceinline__ uint2 e4m3_of(const float (&f)[8]) {
+__device__ __forceinline__ uint2 e4m3_of(const float *f) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -121,19 +132,21 @@ __device__ __forceinline__ uint2 e4m3_of(const float (&f)[8]) {
     return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
 }
 
-// Row and piece (of 8 values) of this thread's pieces, kMxThreads apart, counted through all rows.
+// Row and piece (of V values) of each of this thread's N pieces, kMxThreads apart, counted through all rows.
 struct Place {
     int row, piece;  // (row M: past the end)
 };
-__device__ __forceinline__ void places_of(const MxQuantArgs &a, Place (&at)[kPieces]) {
-    const unsigned per = static_cast<unsigned>(a.K) / 8u;
-    const long long first = static_cast<long long>(blockIdx.x) * (kMxThreads * kPieces), row0 = first / per;
+template <int V, int N>
+__device__ __forceinline__ void places_of(const MxQuantArgs &a, Place (&at)[N]) {
+    const unsigned per = static_cast<unsigned>(a.K) / V;
+    const unsigned long long first = static_cast<unsigned long long>(blockIdx.x) * (kMxThreads * N);
+    const long long row0 = first >> 32 == 0 ? static_cast<unsigned>(first) / per : first / per;
     const unsigned q = static_cast<unsigned>(first - row0 * per) + threadIdx.x, r = q / per;
     long long row = row0 + r;
     unsigned piece = q - r * per;
     const unsigned step_r = kMxThreads / per, step_p = kMxThreads - step_r * per;
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < N; ++i) {
         at[i] = {static_cast<int>(row < a.M ? row : a.M), static_cast<int>(piece)};
         piece += step_p;
         row += step_r;
@@ -144,84 +157,80 @@ __device__ __forceinline__ void places_of(const MxQuantArgs &a, Place (&at)[kPie
     }
 }
 
-// XV: X may be read in 16-byte pieces.  QV: Q written in whole pieces' codes.
-template <int ELEM, int XT, bool XV, bool QV>
+// QV: Q written in whole pieces' codes.
+template <int ELEM, int XT, int HOW, bool QV>
 __global__ void __launch_bounds__(kMxThreads) mx_quantize_kernel(const __grid_constant__ MxQuantArgs a) {
+    begin_after();
     using T = typename Elem<XT>::T;
-    Eight<XT, XV> raw[kPieces];
-    Place at[kPieces];
-    bool live[kPieces];
-    int src[kPieces];
-    places_of(a, at);
+    Sixteen<XT, HOW> raw[kTo];
+    Place at[kTo];
+    bool live[kTo];
+    int src[kTo];
+    places_of<16>(a, at);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < kTo; ++i) {
         live[i] = at[i].row < a.M;
         src[i] = at[i].row;
         if (live[i] && a.source != nullptr) src[i] = __ldg(a.source + at[i].row);
     }
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < kTo; ++i) {
         if (a.source != nullptr) {
             src[i] = src[i] >= 0 ? src[i] / a.top : -1;
             live[i] = live[i] && src[i] >= 0 && src[i] < a.rows_x;
         }
         raw[i].zero();
-        if (live[i]) raw[i].load(static_cast<const T *>(a.X) + src[i] * a.ldx + at[i].piece * 8);
+        if (live[i]) raw[i].load(static_cast<const T *>(a.X) + src[i] * a.ldx + at[i].piece * 16);
     }
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < kTo; ++i) {
         unsigned m = raw[i].max_bits();
         m = max(m, __shfl_xor_sync(kAll, m, 1));
-        m = max(m, __shfl_xor_sync(kAll, m, 2));
         constexpr int kEmax = ELEM == kMxE2M1 ? 2 : 8;
         const bool finite = m < 0x7F800000u;
         const int code = max(static_cast<int>(m >> 23) - kEmax, 0);  // (a subnormal maximum has exponent bits 0)
         const float inv = __uint_as_float(static_cast<unsigned>(254 - code) << 23);
-        float f[8];
+        float f[16];
         raw[i].unpack(f);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) f2_unpack(f2_mul(f2_pack(f[j], f[j + 1]), f2_splat(inv)), f[j], f[j + 1]);
+        for (int j = 0; j < 16; j += 2) f2_unpack(f2_mul(f2_pack(f[j], f[j + 1]), f2_splat(inv)), f[j], f[j + 1]);
         if (!finite) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+            for (int j = 0; j < 16; ++j) f[j] = 0.0f;
         }
         if (!live[i]) continue;
-        unsigned char *q = a.Q + at[i].row * a.q_pitch;
+        unsigned char *q = a.Q + at[i].row * a.q_pitch + static_cast<long long>(at[i].piece) * (ELEM == kMxE2M1 ? 8 : 16);
+        uint32_t w[ELEM == kMxE2M1 ? 2 : 4];
         if constexpr (ELEM == kMxE2M1) {
-            const uint32_t w = e2m1_of(f);
-            q += at[i].piece * 4;
-            if constexpr (QV) {
-                *reinterpret_cast<uint32_t *>(q) = w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 4; ++j) q[j] = static_cast<unsigned char>(w >> (8 * j));
-            }
+            w[0] = e2m1_of(f);
+            w[1] = e2m1_of(f + 8);
+            if constexpr (QV) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
         } else {
-            const uint2 w = e4m3_of(f);
-            q += static_cast<long long>(at[i].piece) * 8;
-            if constexpr (QV) {
-                *reinterpret_cast<uint2 *>(q) = w;
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) q[j] = static_cast<unsigned char>((j < 4 ? w.x : w.y) >> (8 * (j & 3)));
-            }
+            const uint2 lo = e4m3_of(f), hi = e4m3_of(f + 8);
+            w[0] = lo.x; w[1] = lo.y; w[2] = hi.x; w[3] = hi.y;
+            if constexpr (QV) *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if ((threadIdx.x & 3) == 0)
-            a.scale[at[i].row * a.s_pitch + (at[i].piece >> 2)] = static_cast<unsigned char>(finite ? code : 255);
+        if constexpr (!QV) {
+#pragma unroll
+            for (int j = 0; j < (ELEM == kMxE2M1 ? 8 : 16); ++j) q[j] = static_cast<unsigned char>(w[j / 4] >> (8 * (j & 3)));
+        }
+        if ((threadIdx.x & 1) == 0)
+            a.scale[at[i].row * a.s_pitch + (at[i].piece >> 1)] = static_cast<unsigned char>(finite ? code : 255);
     }
 }
 
 // y[i][k] = q[i][k] 2^(code - 127), exact up to the output's rounding.
 template <int ELEM, int YT, bool QV, bool YV>
 __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const __grid_constant__ MxQuantArgs a) {
+    begin_after();
     using T = typename Elem<YT>::T;
     constexpr int PV = Vec16<YT>::kPerVec;
-    uint2 w[kPieces];
-    unsigned code[kPieces];
-    Place at[kPieces];
-    places_of(a, at);
+    uint2 w[kFrom];
+    unsigned code[kFrom];
+    Place at[kFrom];
+    places_of<8>(a, at);
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < kFrom; ++i) {
         w[i] = make_uint2(0, 0);
         code[i] = 0;
         if (at[i].row >= a.M) continue;
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const __grid_
         code[i] = __ldg(a.scale + at[i].row * a.s_pitch + (at[i].piece >> 2));
     }
 #pragma unroll
-    for (int i = 0; i < kPieces; ++i) {
+    for (int i = 0; i < kFrom; ++i) {
         if (at[i].row >= a.M) continue;
         float f[8];
         if constexpr (ELEM == kMxE2M1) {
@@ -268,42 +277,39 @@ __global__ void __launch_bounds__(kMxThreads) mx_dequantize_kernel(const __grid_
     }
 }
 
-unsigned mx_blocks(const MxQuantArgs &a) {
-    return static_cast<unsigned>((static_cast<long long>(a.M) * (a.K / 8) + kMxThreads * kPieces - 1) /
-                                 (kMxThreads * kPieces));
+// Blocks for M rows in pieces of `values`, `pieces` to a thread.
+dim3 mx_blocks(const MxQuantArgs &a, int values, int pieces) {
+    const long long n = kMxThreads * pieces;
+    return dim3(static_cast<unsigned>((static_cast<long long>(a.M) * (a.K / values) + n - 1) / n));
 }
 
 template <int ELEM, int XT>
-cudaError_t quantize_of(const MxQuantArgs &a, bool xv, bool qv, cudaStream_t s) {
-    const unsigned n = mx_blocks(a);
-    if (xv && qv) mx_quantize_kernel<ELEM, XT, true, true><<<n, kMxThreads, 0, s>>>(a);
-    else if (xv) mx_quantize_kernel<ELEM, XT, true, false><<<n, kMxThreads, 0, s>>>(a);
-    else if (qv) mx_quantize_kernel<ELEM, XT, false, true><<<n, kMxThreads, 0, s>>>(a);
-    else mx_quantize_kernel<ELEM, XT, false, false><<<n, kMxThreads, 0, s>>>(a);
-    return cudaGetLastError();
+cudaError_t quantize_of(const MxQuantArgs &a, int x_bytes, bool qv, cudaStream_t s) {
+    const auto kern =
+        x_bytes == 32 ? (qv ? mx_quantize_kernel<ELEM, XT, kThirtyTwo, true> : mx_quantize_kernel<ELEM, XT, kThirtyTwo, false>)
+        : x_bytes == 16 ? (qv ? mx_quantize_kernel<ELEM, XT, kSixteen, true> : mx_quantize_kernel<ELEM, XT, kSixteen, false>)
+                        : (qv ? mx_quantize_kernel<ELEM, XT, kOne, true> : mx_quantize_kernel<ELEM, XT, kOne, false>);
+    return launch_after(kern, mx_blocks(a, 16, kTo), kMxThreads, 0, s, a);
 }
 
 template <int ELEM, int YT>
 cudaError_t dequantize_of(const MxQuantArgs &a, bool qv, bool yv, cudaStream_t s) {
-    const unsigned n = mx_blocks(a);
-    if (qv && yv) mx_dequantize_kernel<ELEM, YT, true, true><<<n, kMxThreads, 0, s>>>(a);
-    else if (qv) mx_dequantize_kernel<ELEM, YT, true, false><<<n, kMxThreads, 0, s>>>(a);
-    else if (yv) mx_dequantize_kernel<ELEM, YT, false, true><<<n, kMxThreads, 0, s>>>(a);
-    else mx_dequantize_kernel<ELEM, YT, false, false><<<n, kMxThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    const auto kern = qv ? (yv ? mx_dequantize_kernel<ELEM, YT, true, true> : mx_dequantize_kernel<ELEM, YT, true, false>)
+                         : (yv ? mx_dequantize_kernel<ELEM, YT, false, true> : mx_dequantize_kernel<ELEM, YT, false, false>);
+    return launch_after(kern, mx_blocks(a, 8, kFrom), kMxThreads, 0, s, a);
 }
 
 }  // namespace
 
-cudaError_t launch_mx_quantize(int elem, int x_dtype, const MxQuantArgs &a, bool x_vec, bool q_vec, cudaStream_t s) {
+cudaError_t launch_mx_quantize(int elem, int x_dtype, const MxQuantArgs &a, int x_bytes, bool q_vec, cudaStream_t s) {
     if (elem == kMxE2M1) {
-        if (x_dtype == kDtF32) return quantize_of<kMxE2M1, kDtF32>(a, x_vec, q_vec, s);
-        if (x_dtype == kDtF16) return quantize_of<kMxE2M1, kDtF16>(a, x_vec, q_vec, s);
-        if (x_dtype == kDtBF16) return quantize_of<kMxE2M1, kDtBF16>(a, x_vec, q_vec, s);
+        if (x_dtype == kDtF32) return quantize_of<kMxE2M1, kDtF32>(a, x_bytes, q_vec, s);
+        if (x_dtype == kDtF16) return quantize_of<kMxE2M1, kDtF16>(a, x_bytes, q_vec, s);
+        if (x_dtype == kDtBF16) return quantize_of<kMxE2M1, kDtBF16>(a, x_bytes, q_vec, s);
     } else if (elem == kMxE4M3) {
-        if (x_dtype == kDtF32) return quantize_of<kMxE4M3, kDtF32>(a, x_vec, q_vec, s);
-        if (x_dtype == kDtF16) return quantize_of<kMxE4M3, kDtF16>(a, x_vec, q_vec, s);
-        if (x_dtype == kDtBF16) return quantize_of<kMxE4M3, kDtBF16>(a, x_vec, q_vec, s);
+        if (x_dtype == kDtF32) return quantize_of<kMxE4M3, kDtF32>(a, x_bytes, q_vec, s);
+        if (x_dtype == kDtF16) return quantize_of<kMxE4M3, kDtF16>(a, x_bytes, q_vec, s);
+        if (x_dtype == kDtBF16) return quantize_of<kMxE4M3, kDtBF16>(a, x_bytes, q_vec, s);
     }
     return cudaErrorInvalidValue;
 }

@@ -23,6 +23,7 @@
 
 #include "epilogue.cuh"
 #include "kernel_args.h"
+#include "launch.cuh"
 
 namespace gb300 {
 
@@ -111,6 +112,17 @@ __device__ __forceinline__ bool too_close(float x, float y, float score) {
     return !(x - y > score + 0x1p-23f * fmaxf(fabsf(x), fabsf(y)));
 }
 
+// Sum of n over the lanes before this one.
+__device__ __forceinline__ int lanes_before(int n) {
+    int sum = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(kAll, sum, d);
+        sum += (threadIdx.x & 31) >= static_cast<unsigned>(d) ? o : 0;
+    }
+    return sum - n;
+}
+
 struct Candidate {
     unsigned key;
     int expert;
@@ -154,6 +166,7 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
         }
         const float worth = t1 + (a.group_sum == 2 && t2 > -INFINITY ? t2 : 0.0f);
         bool kept;
+        const int g = lane / per;
         const bool is_group = group_stays(worth, per, a, kept);
         if (margin > 0.0f) {
             const unsigned low = ~__reduce_max_sync(kAll, kept ? ~order_key(worth) : 0u);
@@ -162,11 +175,43 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
             const float size = warp_max(is_group ? fabsf(t1) + (t2 > -INFINITY ? fabsf(t2) : 0.0f) : 0.0f);
             if (high != 0u) close = too_close(order_value(low), order_value(high), 2.0f * margin + 0x1p-22f * size);
         }
+        unsigned stays = __ballot_sync(kAll, kept && lane == g * per);  // bit g * per
+        if (close) {
+            // The groups' worths in 64 bits, from the experts that may be among a group's highest: one to a lane.
+            const float least = a.group_sum == 2 ? t2 : t1;
+            if (lane == g * per && g < a.groups)
+                cand[g].key = __float_as_uint(least > -INFINITY && least < INFINITY ? least - (margin + 0x1p-22f * fabsf(least)) : least);
+            __syncwarp();
+            unsigned flags = 0u;
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) {
+                const int eg = a.group_lanes > 0 ? g : (lane * NPL + j) / a.group_size;
+                if (key[j] != 0u && sel[j] >= __uint_as_float(cand[eg].key)) flags |= 1u << j;
+            }
+            __syncwarp();
+            if (__reduce_add_sync(kAll, __popc(flags)) > 32) return true;
+            int at = lanes_before(__popc(flags));
+            for (; flags != 0u; flags &= flags - 1u) cand[at++].expert = lane * NPL + __ffs(flags) - 1;
+            const int total = __shfl_sync(kAll, at, 31);
+            __syncwarp();
+            const int e = lane < total ? cand[lane].expert : -1;
+            __syncwarp();
+            const double v = exactly(e);
+            const int eg = e / a.group_size;
+            double x1 = -INFINITY, x2 = -INFINITY;
+            for (int i = 0; i < total; ++i) {
+                const double o = __shfl_sync(kAll, v, i);
+                if (__shfl_sync(kAll, eg, i) == lane) take_top2(x1, x2, o);
+            }
+            group_stays(x1 + (a.group_sum == 2 && x2 > -INFINITY ? x2 : 0.0), 1, a, kept);
+            const unsigned by_group = __ballot_sync(kAll, kept);
+            stays = __ballot_sync(kAll, lane == g * per && (by_group >> g & 1u) != 0u);
+        }
         if (a.group_lanes > 0) {
+            kept = (stays >> (g * per) & 1u) != 0u;
 #pragma unroll
             for (int j = 0; j < NPL; ++j) key[j] = kept ? key[j] : 0u;
         } else {
-            const unsigned stays = __ballot_sync(kAll, kept);
 #pragma unroll
             for (int j = 0; j < NPL; ++j) {
                 const int eg = (lane * NPL + j) / a.group_size;
@@ -202,13 +247,7 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
     int found = 0;
     if (total <= 32) {
         if (NPL > 1) {
-            int at = n;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(kAll, at, d);
-                at += lane >= d ? o : 0;
-            }
-            at -= n;
+            int at = lanes_before(n);
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
                 if (key[j] >= least) cand[at++] = {key[j], lane * NPL + j};
@@ -237,7 +276,7 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
         expert = owner_of >= 0 && lane < a.top ? expert : -1;
         if (margin > 0.0f) {
             const float next = __shfl_down_sync(kAll, value, 1);
-            if (!close && __any_sync(kAll, lane + 1 < found && too_close(value, next, margin))) {
+            if (__any_sync(kAll, lane + 1 < found && too_close(value, next, margin))) {
                 // each candidate's rank by its 64-bit score; the candidates are in the experts' order
                 const double v = exactly(candidate ? my_expert : -1);
                 int rank = 0;
@@ -258,7 +297,7 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
             const unsigned top = __reduce_max_sync(kAll, best);
             if (top == 0u) break;
             const float v = order_value(top);
-            if (margin > 0.0f && found > 0) close = close || too_close(last, v, margin);
+            if (margin > 0.0f && found > 0 && too_close(last, v, margin)) return true;
             last = v;
             if (found == a.top) break;
             const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
@@ -277,7 +316,7 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
             if (lane == found) expert = e;
         }
     }
-    return close;
+    return false;
 }
 
 // exp(x - m) of the lane's logits (0 for -infinity) and their sum over the warp.
@@ -384,7 +423,8 @@ __device__ __forceinline__ float chosen_score(float x, bool live, int score, boo
 
 // BY_LOGIT: the selection scores have the logits' order.
 template <int LT, int NPL, bool BY_LOGIT>
-__global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_constant__ RouteArgs a) {
+__global__ void __launch_bounds__(32 * kRouteWarps, NPL <= 8 ? 8 : 1) route_kernel(const __grid_constant__ RouteArgs a) {
+    begin_after();
     using T = typename Elem<LT>::T;
     extern __shared__ double stage_all[];
     __shared__ Candidate cand_all[kRouteWarps][32];
@@ -458,6 +498,7 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_kernel(const __grid_co
 //     softmax        dx_j += g_j p_j, and every expert's dx_e -= p_e sum_i g_i p_i
 template <int LT, int NPL>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __grid_constant__ RouteGradArgs a) {
+    begin_after();
     using T = typename Elem<LT>::T;
     constexpr int PV = Vec16<LT>::kPerVec;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -528,17 +569,13 @@ cudaError_t launch_route_npl(const RouteArgs &in, int sms, cudaStream_t s) {
     if (a.groups > 1 && a.E == 32 * NPL && 32 % a.groups == 0) a.group_lanes = 32 / a.groups;
     a.stage = !a.by_logit || (a.groups > 1 && a.group_lanes == 0) ? a.E : 0;
     const int bytes = kRouteWarps * a.stage * 8;
-    if (a.by_logit)
-        route_kernel<LT, NPL, true><<<route_blocks(a.T, sms), 32 * kRouteWarps, bytes, s>>>(a);
-    else
-        route_kernel<LT, NPL, false><<<route_blocks(a.T, sms), 32 * kRouteWarps, bytes, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(a.by_logit ? route_kernel<LT, NPL, true> : route_kernel<LT, NPL, false>,
+                        dim3(route_blocks(a.T, sms)), 32 * kRouteWarps, bytes, s, a);
 }
 
 template <int LT, int NPL>
 cudaError_t launch_route_grad_npl(const RouteGradArgs &a, int sms, cudaStream_t s) {
-    route_grad_kernel<LT, NPL><<<route_blocks(a.T, sms), 32 * kRouteWarps, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(route_grad_kernel<LT, NPL>, dim3(route_blocks(a.T, sms)), 32 * kRouteWarps, 0, s, a);
 }
 
 template <int LT>

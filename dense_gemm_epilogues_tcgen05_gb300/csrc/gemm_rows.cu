@@ -7,7 +7,7 @@
 // expert, a place behind the last pair).
 #include "epilogue.cuh"
 #include "kernel_args.h"
-#include "sm103_ptx.cuh"
+#include "launch.cuh"
 
 namespace gb300 {
 
@@ -26,7 +26,7 @@ constexpr int kCountThreads = 256;
 
 __global__ void __launch_bounds__(kCountThreads) route_count_kernel(const __grid_constant__ RouteRowsArgs a) {
     extern __shared__ int counts[];
-    grid_dep_launch();  // the second kernel may begin to count its chunks
+    begin_after();  // (the second kernel then begins to count its own chunks)
     for (int e = threadIdx.x; e < a.E; e += kCountThreads) counts[e] = 0;
     __syncthreads();
     const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.P);
@@ -52,9 +52,12 @@ __device__ __forceinline__ void warp_pairs(const RouteRowsArgs &a, int begin, in
     }
 }
 
-__global__ void __launch_bounds__(512) route_rows_kernel(const __grid_constant__ RouteRowsArgs a) {
+__global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant__ RouteRowsArgs a) {
     extern __shared__ int smem[];
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // Many blocks: the first kernel, which ran after all before it, has begun, so the pairs are there; what it writes
+    // is waited for below.
+    if (gridDim.x == 1) begin_after();
     int *first = smem;              // E + 1: pairs of the experts before
     int *start = first + a.E + 1;   // E: an expert's pairs in the chunks before
     int *own = start + a.E;         // warps x E: counts, then places
@@ -71,9 +74,9 @@ __global__ void __launch_bounds__(512) route_rows_kernel(const __grid_constant__
     __syncthreads();
     // every expert's total, and what lies before this chunk (a warp takes an expert, its lanes the chunks)
     if (gridDim.x > 1) {
-        grid_dep_wait();  // for the first kernel's counts
+        begin_after();  // for the first kernel's counts
         const int chunks = gridDim.x;
-        constexpr int kPer = (kRowsChunks + 31) / 32, kAtOnce = 4;  // loads of a lane per expert, experts at once
+        constexpr int kPer = (kRowsChunks + 31) / 32, kAtOnce = 8;  // loads of a lane per expert, experts at once
         for (int e0 = warp; e0 < a.E; e0 += kAtOnce * warps) {
             int n[kAtOnce][kPer];
 #pragma unroll
@@ -105,6 +108,7 @@ __global__ void __launch_bounds__(512) route_rows_kernel(const __grid_constant__
     for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
         const int before = gridDim.x > 1 ? start[e] : 0;
         int at = before;
+#pragma unroll 8
         for (int w = 0; w < warps; ++w) {
             const int n = own[w * a.E + e];
             own[w * a.E + e] = at;
@@ -197,6 +201,7 @@ __device__ __forceinline__ char *row_at(void *base, long long row, long long ld)
 // Y[r] = w[source[r]] X[source[r] / top]; places without a pair stay as they are.
 template <int DT, bool V>
 __global__ void __launch_bounds__(kMoveThreads) rows_gather_kernel(const __grid_constant__ RowsArgs a) {
+    begin_after();
     using P = Piece<DT, V>;
     constexpr int kAhead = 4;
     const int pieces = a.D / P::N, tid = threadIdx.x;
@@ -243,6 +248,7 @@ __device__ __forceinline__ void slots_of(const RowsArgs &a, long long t, int s0,
 // Out[t] = sum_s w[t][s] Y[row[t][s]] + beta Out[t]; slots without a row add nothing.
 template <int YT, int OT, bool V>
 __global__ void __launch_bounds__(kMoveThreads, 4) rows_combine_kernel(const __grid_constant__ RowsArgs a) {
+    begin_after();
     using P = Piece<YT, V>;
     using O = Piece<OT, V>;
     constexpr int OV = P::N / O::N;  // pieces of the output per piece of Y: 1, 2, or 0 for half a piece
@@ -306,6 +312,7 @@ constexpr int kGradThreads = 320;
 // dY[row] = w dOut[t], dweight[t][s] = dOut[t] . Y[row]; slots without a row: dweight 0.  A block takes a token.
 template <int DT, int YT, bool V>
 __global__ void __launch_bounds__(kGradThreads, 3) rows_combine_grad_kernel(const __grid_constant__ RowsArgs a) {
+    begin_after();
     using P = Piece<DT, V>;
     using Q = Piece<YT, V>;
     // the wider piece of the two is the step: HV of P, YV of Q
@@ -396,22 +403,15 @@ template <int YT, int OT>
 cudaError_t launch_combine(const RowsArgs &a, bool vec, cudaStream_t s) {
     const int pieces = vec ? a.D / Vec16<YT>::kPerVec : a.D, n = block_for(pieces, kMoveThreads);
     const dim3 grid(static_cast<unsigned>(a.T), static_cast<unsigned>((pieces + n - 1) / n));
-    if (vec)
-        rows_combine_kernel<YT, OT, true><<<grid, n, 0, s>>>(a);
-    else
-        rows_combine_kernel<YT, OT, false><<<grid, n, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(vec ? rows_combine_kernel<YT, OT, true> : rows_combine_kernel<YT, OT, false>, grid, n, 0, s, a);
 }
 
 template <int DT, int YT>
 cudaError_t launch_grad(const RowsArgs &a, bool vec, cudaStream_t s) {
     const int per = vec ? (Vec16<DT>::kPerVec > Vec16<YT>::kPerVec ? Vec16<DT>::kPerVec : Vec16<YT>::kPerVec) : 1;
     const int n = block_for(a.D / per, kGradThreads);
-    if (vec)
-        rows_combine_grad_kernel<DT, YT, true><<<static_cast<unsigned>(a.T), n, 0, s>>>(a);
-    else
-        rows_combine_grad_kernel<DT, YT, false><<<static_cast<unsigned>(a.T), n, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_after(vec ? rows_combine_grad_kernel<DT, YT, true> : rows_combine_grad_kernel<DT, YT, false>,
+                        dim3(static_cast<unsigned>(a.T)), n, 0, s, a);
 }
 
 }  // namespace
@@ -420,45 +420,25 @@ cudaError_t launch_route_rows(const RouteRowsArgs &in, cudaStream_t s) {
     RouteRowsArgs a = in;
     const int chunks = route_rows_chunks(a.P);
     a.chunk = static_cast<int>(((static_cast<long long>(a.P) + chunks - 1) / chunks + 31) / 32 * 32);
-    // as many warps as 32 KB of counts allow, and as there are pairs for; at most 16, each expert's counts are summed
-    // over them one by one
-    const int most = 8192 / a.E < 16 ? 8192 / a.E : 16, want = (a.chunk + 31) / 32;
+    // as many warps as 32 KB of counts allow, and as there are pairs for
+    const int most = 8192 / a.E < 32 ? 8192 / a.E : 32, want = (a.chunk + 31) / 32;
     const int warps = want < 1 ? 1 : want < most ? want : most, bytes = (2 * a.E + 1 + warps * a.E) * 4;
-    if (chunks == 1) {
-        route_rows_kernel<<<1, 32 * warps, bytes, s>>>(a);
-        return cudaGetLastError();
+    if (chunks > 1) {
+        cudaError_t err = launch_after(route_count_kernel, dim3(chunks), kCountThreads, a.E * 4, s, a);
+        if (err != cudaSuccess) return err;
     }
-    route_count_kernel<<<chunks, kCountThreads, a.E * 4, s>>>(a);
-    cudaError_t err = cudaGetLastError();
-    if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(chunks, 1, 1);
-    cfg.blockDim = dim3(32 * warps, 1, 1);
-    cfg.dynamicSmemBytes = bytes;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, route_rows_kernel, a);
+    return launch_after(route_rows_kernel, dim3(chunks), 32 * warps, bytes, s, a);
 }
 
 cudaError_t launch_rows_gather(int dtype, const RowsArgs &a, bool vec, int sms, cudaStream_t s) {
     const long long most = 32ll * sms;
     const unsigned grid = static_cast<unsigned>(a.R < most ? a.R : most);
-#define GB300_GATHER(DT)                                                                \
-    if (dtype == DT) {                                                                  \
-        if (vec)                                                                        \
-            rows_gather_kernel<DT, true><<<grid, kMoveThreads, 0, s>>>(a);              \
-        else                                                                            \
-            rows_gather_kernel<DT, false><<<grid, kMoveThreads, 0, s>>>(a);             \
-        return cudaGetLastError();                                                      \
-    }
-    GB300_GATHER(kDtF32)
-    GB300_GATHER(kDtF16)
-    GB300_GATHER(kDtBF16)
-#undef GB300_GATHER
+    const auto launch = [&](auto whole, auto single) {
+        return launch_after(vec ? whole : single, dim3(grid), kMoveThreads, 0, s, a);
+    };
+    if (dtype == kDtF32) return launch(rows_gather_kernel<kDtF32, true>, rows_gather_kernel<kDtF32, false>);
+    if (dtype == kDtF16) return launch(rows_gather_kernel<kDtF16, true>, rows_gather_kernel<kDtF16, false>);
+    if (dtype == kDtBF16) return launch(rows_gather_kernel<kDtBF16, true>, rows_gather_kernel<kDtBF16, false>);
     return cudaErrorInvalidValue;
 }
 

@@ -351,8 +351,9 @@ struct MxgMaps {
 };
 cudaError_t launch_mx_grouped(int elem, int out, const MxgMaps &maps, const GtcArgs &args, int clusters,
                               cudaStream_t stream);
-//   rows to block-scaled numbers (x_vec: 16-byte reads of X; q_vec: 8 values' codes written at once) and back:
-cudaError_t launch_mx_quantize(int elem, int x_dtype, const MxQuantArgs &args, bool x_vec, bool q_vec,
+//   rows to block-scaled numbers (x_bytes: X may be read in pieces of 32 or 16 bytes, 0: in neither; q_vec: 16 values'
+//   codes written at once) and back (q_vec, y_vec: 8 values' codes read, 16 bytes of Y written at once):
+cudaError_t launch_mx_quantize(int elem, int x_dtype, const MxQuantArgs &args, int x_bytes, bool q_vec,
                                cudaStream_t stream);
 cudaError_t launch_mx_dequantize(int elem, int y_dtype, const MxQuantArgs &args, bool q_vec, bool y_vec,
                                  cudaStream_t stream);
