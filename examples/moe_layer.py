@@ -1,10 +1,10 @@
-"""A mixture-of-experts layer on the grouped and 8-bit products: serving in 16 bits, serving with 8-bit
-weights and activations, and one training step with its gradients.
+"""A mixture-of-experts layer on the routing and the grouped products: serving in 16 bits, with 8-bit weights and
+activations, with 4-bit block-scaled ones, and one training step with its gradients.
 
     python examples/moe_layer.py [--tokens 2048 --experts 32 --top 4 --d 2048 --f 1024]
 
-Each token goes to its `top` experts.  Sorted by expert, the token copies are rows of one array, and the
-experts' row ranges (`offsets`) stay on the device: no copy back, no loop over experts.
+Each token goes to its `top` experts (gemm_route).  Sorted by expert (gemm_route_rows), the token copies are rows of
+one array, and the experts' row ranges (`offsets`) stay on the device: no copy back, no loop over experts.
 
     y[token] = sum over its experts e of  w[token, e] * ( act(x W1[e]^T + b1[e]) W2[e]^T )
 """
@@ -33,16 +33,44 @@ class MoeLayer:
         self.b1 = normal(experts, f, std=0.1, dtype=torch.float32)
         self.w2 = normal(experts, d, f, std=f ** -0.5)
 
+    def choose(self, x):
+        """The router's logits, each token's experts and their weights (tokens x top)."""
+        T, dev = x.shape[0], x.device
+        logits = x.float() @ self.router.t()
+        expert = torch.empty(T, self.top, dtype=torch.int32, device=dev)
+        weight = torch.empty(T, self.top, device=dev)
+        g.gemm_route(T, self.experts, self.top, g.F32, logits, self.experts, expert, weight)
+        return logits, expert, weight
+
+    def sort(self, expert):
+        """Offsets of the experts' rows, the row of each pair and the pair of each row."""
+        T, E, dev = expert.shape[0], self.experts, expert.device
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=dev)
+        row, source = torch.empty_like(expert), torch.empty(expert.numel(), dtype=torch.int32, device=dev)
+        need = g.gemm_route_rows_workspace_size(T, self.top, E)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+        g.gemm_route_rows(T, self.top, E, expert, offsets, row, source, workspace, need)
+        return offsets, row, source
+
     def route(self, x):
         """Offsets of the experts' rows, the token of each row and its weight, rows sorted by expert."""
-        weight, expert = torch.topk(torch.softmax(x.float() @ self.router.t(), -1), self.top, sorted=False)
-        weight = weight / weight.sum(-1, keepdim=True)
-        flat = expert.flatten()
-        order = torch.argsort(flat, stable=True)
-        counts = torch.bincount(flat, minlength=self.experts)
-        offsets = torch.zeros(self.experts + 1, dtype=torch.int32, device=x.device)
-        offsets[1:] = counts.cumsum(0)
-        return offsets, order // self.top, weight.flatten()[order]
+        _, expert, weight = self.choose(x)
+        offsets, _, source = self.sort(expert)
+        return offsets, source.long() // self.top, weight.flatten()[source.long()]
+
+    def gather(self, x, source):
+        """The tokens' rows in the experts' order."""
+        rows = torch.empty(source.numel(), x.shape[1], dtype=x.dtype, device=x.device)
+        g.gemm_rows_gather(rows.shape[0], x.shape[1], x.shape[0], self.top, g.BF16, x, x.stride(0), source, None, rows,
+                           rows.shape[1])
+        return rows
+
+    def combine(self, y, row, weight=None):
+        """The (weighted) sum of each token's rows, fp32."""
+        out = torch.empty(row.shape[0], y.shape[1], device=y.device)
+        g.gemm_rows_combine(row.shape[0], self.top, y.shape[1], y.shape[0], g.BF16, y, y.shape[1], row, weight, 0.0, g.F32,
+                            out, out.shape[1])
+        return out
 
     def _up(self, rows, offsets, epilogue):
         out = torch.empty(rows.shape[0], self.f, dtype=torch.bfloat16, device=rows.device)
@@ -50,17 +78,18 @@ class MoeLayer:
                        self.f * self.d, 1, self.d, out, self.f, g.BF16, 1.0, 0.0, self.b1, epilogue)
         return out
 
-    def _down(self, h, offsets, weight):
+    def _down(self, h, offsets, weight=None):
         out = torch.empty(h.shape[0], self.d, dtype=torch.bfloat16, device=h.device)
         g.gemm_grouped(self.experts, h.shape[0], self.d, self.f, g.BF16, offsets, h, self.f, 1, self.w2,
                        self.d * self.f, 1, self.f, out, self.d, g.BF16, 1.0, 0.0, None, g.EPI_NONE, row_scale=weight)
         return out
 
     def forward(self, x):
-        """Serving: two grouped products, bias and SiLU in the first, the router's weights in the second."""
-        offsets, token, weight = self.route(x)
-        y = self._down(self._up(x[token], offsets, g.EPI_BIAS_SILU), offsets, weight)
-        return torch.zeros_like(x, dtype=torch.float32).index_add_(0, token, y.float())
+        """Serving: rows gathered, two grouped products with bias and SiLU in the first, the weighted sum."""
+        _, expert, weight = self.choose(x)
+        offsets, row, source = self.sort(expert)
+        y = self._down(self._up(self.gather(x, source), offsets, g.EPI_BIAS_SILU), offsets)
+        return self.combine(y, row, weight)
 
     def quantize(self):
         """8-bit weights, a scale for each output channel."""
@@ -81,18 +110,46 @@ class MoeLayer:
                           self.d * self.f, self.f, self.s2, y, self.d, g.BF16, 1.0, 0.0, None, g.EPI_NONE)
         return torch.zeros_like(x, dtype=torch.float32).index_add_(0, token, y.float())
 
-    def train_step(self, x, dy):
-        """Output and the gradients of x, W1, b1 and W2 for the output's gradient dy (the routing held fixed)."""
-        offsets, token, weight = self.route(x)
-        rows, E = token.shape[0], self.experts
-        xr = x[token]
+    def quantize_mx(self):
+        """4-bit weights, a power of two for each 32 inputs."""
+        self.m1, self.ms1 = quantize_mx_rows(self.w1.view(-1, self.d))
+        self.m2, self.ms2 = quantize_mx_rows(self.w2.view(-1, self.f))
+
+    def forward_mx(self, x):
+        """Serving with 4-bit block-scaled weights and activations (D and F multiples of 32): tokens are quantised as
+        they are gathered."""
+        _, expert, weight = self.choose(x)
+        offsets, row, source = self.sort(expert)
+        rows = source.numel()
+        h = torch.empty(rows, self.f, dtype=torch.bfloat16, device=x.device)
+        self._mx_product(quantize_mx_rows(x, source, self.top), (self.m1, self.ms1), offsets, self.d, self.b1,
+                         g.EPI_BIAS_SILU, h)
+        y = torch.empty(rows, self.d, dtype=torch.bfloat16, device=x.device)
+        self._mx_product(quantize_mx_rows(h), (self.m2, self.ms2), offsets, self.f, None, g.EPI_NONE, y)
+        return self.combine(y, row, weight)
+
+    def _mx_product(self, x, w, offsets, k, bias, epilogue, out):
+        (qx, sx), (qw, sw), n = x, w, out.shape[1]
+        g.gemm_mx_grouped(self.experts, out.shape[0], n, k, g.MX_E2M1, offsets, qx, 2 * qx.shape[1], sx, sx.shape[1], qw,
+                          2 * n * qw.shape[1], 2 * qw.shape[1], sw, n * sw.shape[1], sw.shape[1], out, n, g.BF16, 1.0, 0.0,
+                          bias, epilogue)
+
+    def train_step(self, x, dy, router=False):
+        """Output and the gradients of x, W1, b1 and W2 for the output's gradient dy; with `router` also that of the
+        router, through the weights (the choice of experts held fixed)."""
+        logits, expert, weight = self.choose(x)
+        offsets, row, source = self.sort(expert)
+        rows, E, T = source.numel(), self.experts, x.shape[0]
+        xr = self.gather(x, source)
         z = self._up(xr, offsets, g.EPI_BIAS)  # kept for the backward pass
         sig = torch.sigmoid(z.float())
         h = (z.float() * sig).to(torch.bfloat16)
-        y = self._down(h, offsets, weight)
-        out = torch.zeros_like(x, dtype=torch.float32).index_add_(0, token, y.float())
+        y = self._down(h, offsets)
+        out = self.combine(y, row, weight)
 
-        dr = (dy[token].float() * weight[:, None]).to(torch.bfloat16)
+        dr, dw = torch.empty_like(y), torch.empty_like(weight) if router else None
+        g.gemm_rows_combine_grad(T, self.top, self.d, rows, g.BF16, dy, dy.stride(0), g.BF16, y, self.d, row, weight, dr,
+                                 self.d, dw)
         dw2 = torch.empty(E, self.d, self.f, device=x.device)
         g.gemm_grouped_wgrad(E, rows, self.d, self.f, g.BF16, offsets, dr, self.d, 1, h, self.f, 1, dw2,
                              self.d * self.f, self.f, g.F32, 1.0, 0.0)
@@ -107,14 +164,26 @@ class MoeLayer:
         dxr = torch.empty(rows, self.d, dtype=torch.bfloat16, device=x.device)
         g.gemm_grouped(E, rows, self.d, self.f, g.BF16, offsets, dz, self.f, 1, self.w1, self.f * self.d, self.d, 1,
                        dxr, self.d, g.BF16, 1.0, 0.0, None, g.EPI_NONE)
-        dx = torch.zeros_like(x, dtype=torch.float32).index_add_(0, token, dxr.float())
-        return out, {"x": dx, "w1": dw1, "b1": db1, "w2": dw2}
+        grads = {"x": self.combine(dxr, row), "w1": dw1, "b1": db1, "w2": dw2}  # a gather's gradient is the sum
+        if router:
+            dlogits = torch.empty_like(logits)
+            g.gemm_route_grad(T, E, self.top, g.F32, logits, E, expert, dw, dlogits, E)
+            grads["x"] += dlogits @ self.router
+            grads["router"] = dlogits.t() @ x.float()
+        return out, grads
 
-    def reference(self, x, requires_grad=False):
-        """The same layer expert by expert in plain fp32 operations; with gradients, its leaves as well."""
+    def reference(self, x, requires_grad=False, router=False):
+        """The same layer expert by expert in plain fp32 operations; with gradients, its leaves as well (with `router`,
+        the router's weights among them)."""
         offsets, token, weight = self.route(x)
         leaf = [t.float().requires_grad_(requires_grad) for t in (x, self.w1, self.b1, self.w2)]
-        x, w1, b1, w2 = leaf
+        if router:
+            leaf.append(self.router.clone().requires_grad_(requires_grad))
+            _, expert, _ = self.choose(x)
+            _, _, source = self.sort(expert)
+            chosen = torch.softmax((leaf[0] @ leaf[4].t()).gather(1, expert.long()), 1)
+            weight = chosen.flatten()[source.long()]
+        x, w1, b1, w2 = leaf[:4]
         ends, parts = offsets.tolist(), []
         for e in range(self.experts):
             r = slice(ends[e], ends[e + 1])
@@ -131,6 +200,16 @@ def quantize_rows(x):
     return q, scale
 
 
+def quantize_mx_rows(x, source=None, top=1):
+    """4-bit codes and scales of x's rows (or of those that `source` names), pitches of whole 16 bytes."""
+    rows, k = x.shape[0] if source is None else source.numel(), x.shape[1]
+    codes = torch.empty(rows, (k // 2 + 15) // 16 * 16, dtype=torch.uint8, device=x.device)
+    scale = torch.empty(rows, (k // 32 + 15) // 16 * 16, dtype=torch.uint8, device=x.device)
+    g.gemm_mx_quantize(rows, k, g.MX_E2M1, g.BF16, x, x.stride(0), codes, 2 * codes.shape[1], scale, scale.shape[1], source,
+                       top, x.shape[0])
+    return codes, scale
+
+
 def relative(a, b):
     a, b = a.detach().double(), b.detach().double()
     return float((a - b).norm() / b.norm())
@@ -143,18 +222,21 @@ def main():
     a = ap.parse_args()
     layer = MoeLayer(a.d, a.f, a.experts, a.top)
     layer.quantize()
+    layer.quantize_mx()
     x = torch.randn(a.tokens, a.d, device="cuda").bfloat16()
     dy = torch.randn(a.tokens, a.d, device="cuda").bfloat16()
-    want, leaf = layer.reference(x, requires_grad=True)
+    want, leaf = layer.reference(x, requires_grad=True, router=True)
     want.backward(dy.float())
     print(f"serving, bf16        off by {relative(layer.forward(x), want):.1e}")
     print(f"serving, 8-bit       off by {relative(layer.forward_i8(x), want):.1e}")
-    out, grads = layer.train_step(x, dy)
+    print(f"serving, 4-bit       off by {relative(layer.forward_mx(x), want):.1e}")
+    out, grads = layer.train_step(x, dy, router=True)
     print(f"training, output     off by {relative(out, want):.1e}")
     for (name, grad), t in zip(grads.items(), leaf):
         print(f"training, d{name:<9} off by {relative(grad, t.grad):.1e}")
     for name, step in (("serving, bf16", lambda: layer.forward(x)), ("serving, 8-bit", lambda: layer.forward_i8(x)),
-                       ("training step", lambda: layer.train_step(x, dy))):
+                       ("serving, 4-bit", lambda: layer.forward_mx(x)),
+                       ("training step", lambda: layer.train_step(x, dy, router=True))):
         for _ in range(3):
             step()
         t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)

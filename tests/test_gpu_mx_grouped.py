@@ -173,3 +173,19 @@ def test_offsets_that_fall_or_leave_the_arrays(cuda_lib):
         assert g.gemm_device_status() == 0
         assert (C[0] == CANARY).all() and (C[M + 1] == CANARY).all()
         assert ((C == CANARY) | (C == K)).all()
+
+
+@pytest.mark.parametrize("elem", [E2M1, E4M3], ids=["e2m1", "e4m3"])
+def test_long_one_sided_sums(cuda_lib, elem):
+    """8192 positive products: nothing cancels, and what the tensor cores cut off adds up to no more than the bound."""
+    rng = np.random.default_rng(0)
+    M, N, K, g = 48, 272, 8192, cuda_lib
+    codes = [rng.integers(1, 8 if elem == E2M1 else 127, (r, K)) for r in (M, N)]
+    scales = [rng.integers(120, 130, (r, K // 32)) for r in (M, N)]
+    xv, wv = (om.values_of(c, s, elem) for c, s in zip(codes, scales))
+    X, W = (torch.from_numpy(om.packed(c, elem)).cuda() for c in codes)
+    XS, WS = (torch.from_numpy(s.astype(np.uint8)).cuda() for s in scales)
+    C = torch.empty(M, N, device="cuda")
+    g.gemm_mx_grouped(1, M, N, K, elem, None, X, K, XS, K // 32, W, 0, K, WS, 0, K // 32, C, N, F32, 1.0, 0.0, None, 0)
+    want = xv @ wv.T
+    check(C.cpu().double().numpy(), want, want, F32, K, elem)
