@@ -214,6 +214,8 @@ class GemmError(RuntimeError):
 
 
 def _ptr(x):
+    if type(x) is torch.Tensor:
+        return x.data_ptr()
     if x is None:
         return None
     if isinstance(x, int):

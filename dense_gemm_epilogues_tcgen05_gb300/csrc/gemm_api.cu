@@ -237,6 +237,31 @@ gemm_status_t check_range(const void *p, size_t bytes, int ordinal = -1, bool *l
     return GEMM_OK;
 }
 
+// The ranges of one call: arrays that lie in an allocation already asked about (a caching allocator's blocks mostly
+// do) cost no further driver call.
+class Ranges {
+public:
+    gemm_status_t check(const void *p, size_t bytes) {
+        const uint64_t first = reinterpret_cast<uint64_t>(p);
+        if (bytes == 0 || (first >= start_ && first - start_ <= extent_ && bytes <= extent_ - (first - start_)))
+            return GEMM_OK;
+        const DriverFns &f = driver_fns();
+        CUdeviceptr start = 0;
+        size_t extent = 0;
+        if (p != nullptr && f.ok && f.addr_range(&start, &extent, static_cast<CUdeviceptr>(first)) == CUDA_SUCCESS &&
+            extent > 0) {
+            start_ = start;
+            extent_ = extent;
+            return first >= start && first - start <= extent && bytes <= extent - (first - start) ? GEMM_OK
+                                                                                                  : GEMM_ERR_INVALID_ARG;
+        }
+        return check_range(p, bytes);
+    }
+
+private:
+    uint64_t start_ = 0, extent_ = 0;
+};
+
 size_t span_bytes(int64_t rows, int64_t cols, int64_t s_rows, int64_t s_cols, int es) {
     if (rows == 0 || cols == 0) return 0;
     return static_cast<size_t>(((rows - 1) * s_rows + (cols - 1) * s_cols + 1) * es);
@@ -1780,12 +1805,13 @@ gemm_status_t gemm_mx_quantize(int64_t M, int64_t K, gemm_mx_elem_t elem, gemm_d
     const int es = elem_bytes(x_dtype), per_byte = elem == GEMM_MX_E2M1 ? 2 : 1;
     if (!elements_aligned({{X, es}, {source, 4}})) return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    Ranges ranges;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    if ((st = check_range(X, extent_bytes(1, 0, rows_x, ldx, K, 1, es))) != GEMM_OK) return st;
-    if (source != nullptr && (st = check_range(source, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
-    if ((st = check_range(Q, extent_bytes(1, 0, M, ldq / per_byte, K / per_byte, 1, 1))) != GEMM_OK) return st;
-    if ((st = check_range(scale, extent_bytes(1, 0, M, lds, K / 32, 1, 1))) != GEMM_OK) return st;
+    if ((st = ranges.check(X, extent_bytes(1, 0, rows_x, ldx, K, 1, es))) != GEMM_OK) return st;
+    if (source != nullptr && (st = ranges.check(source, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(Q, extent_bytes(1, 0, M, ldq / per_byte, K / per_byte, 1, 1))) != GEMM_OK) return st;
+    if ((st = ranges.check(scale, extent_bytes(1, 0, M, lds, K / 32, 1, 1))) != GEMM_OK) return st;
     MxQuantArgs a = {};
     a.M = static_cast<int>(M);
     a.K = static_cast<int>(K);
@@ -1809,11 +1835,12 @@ gemm_status_t gemm_mx_dequantize(int64_t M, int64_t K, gemm_mx_elem_t elem, cons
     const int es = elem_bytes(y_dtype), per_byte = elem == GEMM_MX_E2M1 ? 2 : 1;
     if (!elements_aligned({{Y, es}})) return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    Ranges ranges;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    if ((st = check_range(Y, extent_bytes(1, 0, M, ldy, K, 1, es))) != GEMM_OK) return st;
-    if ((st = check_range(Q, extent_bytes(1, 0, M, ldq / per_byte, K / per_byte, 1, 1))) != GEMM_OK) return st;
-    if ((st = check_range(scale, extent_bytes(1, 0, M, lds, K / 32, 1, 1))) != GEMM_OK) return st;
+    if ((st = ranges.check(Y, extent_bytes(1, 0, M, ldy, K, 1, es))) != GEMM_OK) return st;
+    if ((st = ranges.check(Q, extent_bytes(1, 0, M, ldq / per_byte, K / per_byte, 1, 1))) != GEMM_OK) return st;
+    if ((st = ranges.check(scale, extent_bytes(1, 0, M, lds, K / 32, 1, 1))) != GEMM_OK) return st;
     MxQuantArgs a = {};
     a.M = static_cast<int>(M);
     a.K = static_cast<int>(K);
@@ -1871,19 +1898,20 @@ gemm_status_t gemm_mx_grouped(int64_t G, int64_t M, int64_t N, int64_t K, gemm_m
                     !group_stride_ok(G, ws_stride_g, 1)))
         return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    Ranges ranges;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    if (offsets != nullptr && (st = check_range(offsets, static_cast<size_t>(G + 1) * 4)) != GEMM_OK) return st;
-    if ((st = check_range(C, extent_bytes(1, 0, M, ldc, N, 1, elem_bytes(c_dtype)))) != GEMM_OK) return st;
-    if (epilogue != GEMM_EPI_NONE && (st = check_range(bias, static_cast<size_t>(G) * N * 4)) != GEMM_OK) return st;
+    if (offsets != nullptr && (st = ranges.check(offsets, static_cast<size_t>(G + 1) * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(C, extent_bytes(1, 0, M, ldc, N, 1, elem_bytes(c_dtype)))) != GEMM_OK) return st;
+    if (epilogue != GEMM_EPI_NONE && (st = ranges.check(bias, static_cast<size_t>(G) * N * 4)) != GEMM_OK) return st;
     GtcArgs t = {};
     MxgMaps m = {};
     if (product) {
-        if ((st = check_range(X, extent_bytes(1, 0, M, x_pitch, k_bytes, 1, 1))) != GEMM_OK) return st;
-        if ((st = check_range(x_scale, extent_bytes(1, 0, M, ldxs, blocks, 1, 1))) != GEMM_OK) return st;
-        if ((st = check_range(W, extent_bytes(G, w_stride, N, w_pitch, k_bytes, 1, 1))) != GEMM_OK) return st;
-        if ((st = check_range(w_scale, extent_bytes(G, ws_stride_g, N, ldws, blocks, 1, 1))) != GEMM_OK) return st;
-        if (row_scale != nullptr && (st = check_range(row_scale, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
+        if ((st = ranges.check(X, extent_bytes(1, 0, M, x_pitch, k_bytes, 1, 1))) != GEMM_OK) return st;
+        if ((st = ranges.check(x_scale, extent_bytes(1, 0, M, ldxs, blocks, 1, 1))) != GEMM_OK) return st;
+        if ((st = ranges.check(W, extent_bytes(G, w_stride, N, w_pitch, k_bytes, 1, 1))) != GEMM_OK) return st;
+        if ((st = ranges.check(w_scale, extent_bytes(G, ws_stride_g, N, ldws, blocks, 1, 1))) != GEMM_OK) return st;
+        if (row_scale != nullptr && (st = ranges.check(row_scale, static_cast<size_t>(M) * 4)) != GEMM_OK) return st;
         // only the maps that the kernel can come to: boxes up to the widest tile
         const uint32_t widths = static_cast<uint32_t>(std::min<int64_t>(kMxgMost, (M + 15) / 16 * 16) / 16);
         if ((st = encode_3d(&m.w, kDtI8, W, k_bytes, N, w_pitch, G, w_stride, 128)) != GEMM_OK) return st;
@@ -1929,13 +1957,14 @@ gemm_status_t gemm_route(int64_t T, int64_t E, int64_t top, gemm_dtype_t l_dtype
     const int es = elem_bytes(l_dtype);
     if (!elements_aligned({{logits, es}, {bias, 4}, {expert, 4}, {weight, 4}})) return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    Ranges ranges;
     DeviceState *dev = nullptr;
     gemm_status_t st;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    if ((st = check_range(logits, extent_bytes(1, 0, T, ldl, E, 1, es))) != GEMM_OK) return st;
-    if (bias != nullptr && (st = check_range(bias, static_cast<size_t>(E) * 4)) != GEMM_OK) return st;
-    if ((st = check_range(expert, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
-    if ((st = check_range(weight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(logits, extent_bytes(1, 0, T, ldl, E, 1, es))) != GEMM_OK) return st;
+    if (bias != nullptr && (st = ranges.check(bias, static_cast<size_t>(E) * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(expert, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(weight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
     RouteArgs a = {};
     a.T = T;
     a.E = static_cast<int>(E); a.top = static_cast<int>(top);
@@ -1967,13 +1996,14 @@ gemm_status_t gemm_route_grad(int64_t T, int64_t E, int64_t top, gemm_dtype_t l_
     const int es = elem_bytes(l_dtype);
     if (!elements_aligned({{logits, es}, {dlogits, es}, {expert, 4}, {dweight, 4}})) return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    Ranges ranges;
     DeviceState *dev = nullptr;
     gemm_status_t st;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    if ((st = check_range(logits, extent_bytes(1, 0, T, ldl, E, 1, es))) != GEMM_OK) return st;
-    if ((st = check_range(dlogits, extent_bytes(1, 0, T, ldd, E, 1, es))) != GEMM_OK) return st;
-    if ((st = check_range(expert, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
-    if ((st = check_range(dweight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(logits, extent_bytes(1, 0, T, ldl, E, 1, es))) != GEMM_OK) return st;
+    if ((st = ranges.check(dlogits, extent_bytes(1, 0, T, ldd, E, 1, es))) != GEMM_OK) return st;
+    if ((st = ranges.check(expert, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(dweight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
     RouteGradArgs a = {};
     a.T = T;
     a.E = static_cast<int>(E); a.top = static_cast<int>(top);
@@ -2006,14 +2036,15 @@ gemm_status_t gemm_route_rows(int64_t T, int64_t top, int64_t E, const int32_t *
                      workspace_bytes < need))
         return GEMM_ERR_WORKSPACE;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    Ranges ranges;
     DeviceState *dev = nullptr;
     gemm_status_t st;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    if ((st = check_range(offsets, static_cast<size_t>(E + 1) * 4)) != GEMM_OK) return st;
-    if ((st = check_range(expert, pairs)) != GEMM_OK) return st;
-    if ((st = check_range(source, pairs)) != GEMM_OK) return st;
-    if (row != nullptr && (st = check_range(row, pairs)) != GEMM_OK) return st;
-    if ((st = check_range(workspace, need)) != GEMM_OK) return st;
+    if ((st = ranges.check(offsets, static_cast<size_t>(E + 1) * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(expert, pairs)) != GEMM_OK) return st;
+    if ((st = ranges.check(source, pairs)) != GEMM_OK) return st;
+    if (row != nullptr && (st = ranges.check(row, pairs)) != GEMM_OK) return st;
+    if ((st = ranges.check(workspace, need)) != GEMM_OK) return st;
     RouteRowsArgs a = {};
     a.P = static_cast<int>(T * top); a.E = static_cast<int>(E);
     a.expert = expert; a.offsets = offsets; a.row = row; a.source = source;
@@ -2044,12 +2075,13 @@ gemm_status_t gemm_rows_gather(int64_t R, int64_t D, int64_t T, int64_t top, gem
     const int es = elem_bytes(dtype);
     if (!elements_aligned({{X, es}, {Y, es}, {source, 4}, {weight, 4}})) return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    Ranges ranges;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    if ((st = check_range(X, extent_bytes(1, 0, T, ldx, D, 1, es))) != GEMM_OK) return st;
-    if ((st = check_range(Y, extent_bytes(1, 0, R, ldy, D, 1, es))) != GEMM_OK) return st;
-    if ((st = check_range(source, static_cast<size_t>(R) * 4)) != GEMM_OK) return st;
-    if (weight != nullptr && (st = check_range(weight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(X, extent_bytes(1, 0, T, ldx, D, 1, es))) != GEMM_OK) return st;
+    if ((st = ranges.check(Y, extent_bytes(1, 0, R, ldy, D, 1, es))) != GEMM_OK) return st;
+    if ((st = ranges.check(source, static_cast<size_t>(R) * 4)) != GEMM_OK) return st;
+    if (weight != nullptr && (st = ranges.check(weight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
     RowsArgs a = {};
     a.T = T; a.R = R; a.top = static_cast<int>(top); a.D = static_cast<int>(D);
     a.X = const_cast<void *>(X); a.ldx = ldx;
@@ -2072,12 +2104,13 @@ gemm_status_t gemm_rows_combine(int64_t T, int64_t top, int64_t D, int64_t R, ge
     const int es = elem_bytes(y_dtype), os = elem_bytes(out_dtype);
     if (!elements_aligned({{R > 0 ? Y : nullptr, es}, {Out, os}, {row, 4}, {weight, 4}})) return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    Ranges ranges;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    if ((st = check_range(Y, extent_bytes(1, 0, R, ldy, D, 1, es))) != GEMM_OK) return st;
-    if ((st = check_range(Out, extent_bytes(1, 0, T, ldo, D, 1, os))) != GEMM_OK) return st;
-    if ((st = check_range(row, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
-    if (weight != nullptr && (st = check_range(weight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if ((st = ranges.check(Y, extent_bytes(1, 0, R, ldy, D, 1, es))) != GEMM_OK) return st;
+    if ((st = ranges.check(Out, extent_bytes(1, 0, T, ldo, D, 1, os))) != GEMM_OK) return st;
+    if ((st = ranges.check(row, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
+    if (weight != nullptr && (st = ranges.check(weight, static_cast<size_t>(T) * top * 4)) != GEMM_OK) return st;
     RowsArgs a = {};
     a.T = T; a.R = R; a.top = static_cast<int>(top); a.D = static_cast<int>(D);
     a.X = Out; a.ldx = ldo;
@@ -2107,15 +2140,16 @@ gemm_status_t gemm_rows_combine_grad(int64_t T, int64_t top, int64_t D, int64_t 
                            {row, 4}, {weight, 4}, {dweight, 4}}))
         return GEMM_ERR_MISALIGNED;
     if (!driver_fns().ok) return GEMM_ERR_CUDA;
+    Ranges ranges;
     DeviceState *dev = nullptr;
     if ((st = device_state(&dev)) != GEMM_OK) return st;
-    if ((st = check_range(dOut, extent_bytes(1, 0, T, ldd, D, 1, ds))) != GEMM_OK) return st;
-    if (reads_y && (st = check_range(Y, extent_bytes(1, 0, R, ldy, D, 1, es))) != GEMM_OK) return st;
-    if (writes && (st = check_range(dY, extent_bytes(1, 0, R, lddy, D, 1, es))) != GEMM_OK) return st;
+    if ((st = ranges.check(dOut, extent_bytes(1, 0, T, ldd, D, 1, ds))) != GEMM_OK) return st;
+    if (reads_y && (st = ranges.check(Y, extent_bytes(1, 0, R, ldy, D, 1, es))) != GEMM_OK) return st;
+    if (writes && (st = ranges.check(dY, extent_bytes(1, 0, R, lddy, D, 1, es))) != GEMM_OK) return st;
     const size_t pairs = static_cast<size_t>(T) * top * 4;
-    if ((st = check_range(row, pairs)) != GEMM_OK) return st;
-    if (weight != nullptr && (st = check_range(weight, pairs)) != GEMM_OK) return st;
-    if (dweight != nullptr && (st = check_range(dweight, pairs)) != GEMM_OK) return st;
+    if ((st = ranges.check(row, pairs)) != GEMM_OK) return st;
+    if (weight != nullptr && (st = ranges.check(weight, pairs)) != GEMM_OK) return st;
+    if (dweight != nullptr && (st = ranges.check(dweight, pairs)) != GEMM_OK) return st;
     RowsArgs a = {};
     a.T = T; a.R = R; a.top = static_cast<int>(top); a.D = static_cast<int>(D);
     a.X = const_cast<void *>(dOut); a.ldx = ldd;
@@ -2126,7 +2160,8 @@ gemm_status_t gemm_rows_combine_grad(int64_t T, int64_t top, int64_t D, int64_t 
     const int widest = std::min(ds, es);  // 16 bytes of the narrower type hold the most values
     const bool vec = (D == 0 || rows_at(dOut, T, ldd * ds, 16)) && (!reads_y || rows_at(Y, R, ldy * es, 16)) &&
                      (!writes || rows_at(dY, R, lddy * es, 16)) && D * widest % 16 == 0;
-    return launch_rows_combine_grad(d_dtype, y_dtype, a, vec, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    return launch_rows_combine_grad(d_dtype, y_dtype, a, vec, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)) ==
+                   cudaSuccess
                ? GEMM_OK : GEMM_ERR_CUDA;
 }
 

@@ -309,7 +309,30 @@ __global__ void __launch_bounds__(kMoveThreads, 4) rows_combine_kernel(const __g
 
 constexpr int kGradThreads = 320;
 
-// dY[row] = w dOut[t], dweight[t][s] = dOut[t] . Y[row]; slots without a row: dweight 0.  A block takes a token.
+// The sums over the warp of eight values of each lane: lane l (and those beside it) gets that of value l / 4.  Halves
+// the values a lane carries with each exchange: 9 shuffles instead of 40.
+__device__ __forceinline__ float warp_sums_of_8(const float (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+    float a[4], b[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const bool hi = (lane & 16) != 0;
+        a[i] = (hi ? v[i + 4] : v[i]) + __shfl_xor_sync(kAll, hi ? v[i] : v[i + 4], 16);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const bool hi = (lane & 8) != 0;
+        b[i] = (hi ? a[i + 2] : a[i]) + __shfl_xor_sync(kAll, hi ? a[i] : a[i + 2], 8);
+    }
+    const bool hi = (lane & 4) != 0;
+    float c = (hi ? b[1] : b[0]) + __shfl_xor_sync(kAll, hi ? b[0] : b[1], 4);
+    c += __shfl_xor_sync(kAll, c, 2);
+    return c + __shfl_xor_sync(kAll, c, 1);
+}
+
+// dY[row] = w dOut[t], dweight[t][s] = dOut[t] . Y[row]; slots without a row: dweight 0.  Persistent blocks; an item is
+// a token and kSlots of its slots.  The next item's rows and weights are on their way while an item's rows are, and
+// one barrier an item hands over both these and the partial sums.
 template <int DT, int YT, bool V>
 __global__ void __launch_bounds__(kGradThreads, 3) rows_combine_grad_kernel(const __grid_constant__ RowsArgs a) {
     begin_after();
@@ -317,23 +340,41 @@ __global__ void __launch_bounds__(kGradThreads, 3) rows_combine_grad_kernel(cons
     using Q = Piece<YT, V>;
     // the wider piece of the two is the step: HV of P, YV of Q
     constexpr int N = P::N > Q::N ? P::N : Q::N, HV = N / P::N, YV = N / Q::N;
-    __shared__ float part[kGradThreads / 32][kSlots];
-    __shared__ int r[kSlots];  // (in shared memory: a thread's registers hold rows on their way)
-    __shared__ float w[kSlots];
+    __shared__ float part[2][kGradThreads / 32][kSlots];
+    __shared__ int rows[2][kSlots];  // (in shared memory: a thread's registers hold rows on their way)
+    __shared__ float weights[2][kSlots];
+    static_assert(kSlots == 8, "warp_sums_of_8");
     const int steps = a.D / N, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n = blockDim.x;
-    const long long t = blockIdx.x;
-    const void *d = row_at<DT>(a.X, t, a.ldx);
-    for (int s0 = 0; s0 < a.top; s0 += kSlots) {
-        float dot[kSlots];
-        if (tid < kSlots) {
-            const bool slot = s0 + tid < a.top;
-            const int row = slot ? __ldg(a.row + t * a.top + s0 + tid) : -1;
-            r[tid] = static_cast<unsigned>(row) < static_cast<unsigned>(a.R) ? row : -1;
-            w[tid] = a.weight != nullptr && slot ? __ldg(a.weight + t * a.top + s0 + tid) : 1.0f;
+    const int batches = (a.top + kSlots - 1) / kSlots;
+    const int items = static_cast<int>(a.T) * batches;  // (at most 2^30)
+    int next_row = -1;
+    float next_weight = 1.0f;
+    auto fetch = [&](int item) {  // by the first kSlots threads
+        const int t = item / batches, s = (item - t * batches) * kSlots + tid;
+        next_row = -1;
+        next_weight = 1.0f;
+        if (item < items && s < a.top) {
+            const int r = __ldg(a.row + static_cast<long long>(t) * a.top + s);
+            next_row = static_cast<unsigned>(r) < static_cast<unsigned>(a.R) ? r : -1;
+            if (a.weight != nullptr) next_weight = __ldg(a.weight + static_cast<long long>(t) * a.top + s);
         }
-        __syncthreads();
+    };
+    if (tid < kSlots) {
+        fetch(blockIdx.x);
+        rows[0][tid] = next_row;
+        weights[0][tid] = next_weight;
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int item = blockIdx.x; item < items; item += gridDim.x, buf ^= 1) {
+        const int t = item / batches, s0 = (item - t * batches) * kSlots;
+        const void *d = row_at<DT>(a.X, t, a.ldx);
+        const int *r = rows[buf];
+        const float *w = weights[buf];
+        float dot[kSlots];
 #pragma unroll
         for (int s = 0; s < kSlots; ++s) dot[s] = 0.0f;
+        if (tid < kSlots) fetch(item + static_cast<int>(gridDim.x));
         for (int i = tid; i < steps; i += n) {
             float g[N];
 #pragma unroll
@@ -374,22 +415,18 @@ __global__ void __launch_bounds__(kGradThreads, 3) rows_combine_grad_kernel(cons
                 }
             }
         }
-        if (a.dweight != nullptr) {
-#pragma unroll
-            for (int s = 0; s < kSlots; ++s) {
-                float v = dot[s];
-#pragma unroll
-                for (int k = 16; k > 0; k >>= 1) v += __shfl_xor_sync(kAll, v, k);
-                if (lane == 0) part[warp][s] = v;
-            }
-            __syncthreads();
-            if (tid < kSlots && s0 + tid < a.top) {
-                float v = 0.0f;
-                for (int k = 0; k < n >> 5; ++k) v += part[k][tid];
-                a.dweight[t * a.top + s0 + tid] = v;
-            }
+        const float sum = warp_sums_of_8(dot);
+        if ((lane & 3) == 0) part[buf][warp][lane >> 2] = sum;
+        if (tid < kSlots) {
+            rows[buf ^ 1][tid] = next_row;
+            weights[buf ^ 1][tid] = next_weight;
         }
-        if (s0 + kSlots < a.top) __syncthreads();
+        __syncthreads();
+        if (a.dweight != nullptr && tid < kSlots && s0 + tid < a.top) {
+            float v = 0.0f;
+            for (int k = 0; k < n >> 5; ++k) v += part[buf][k][tid];
+            a.dweight[static_cast<long long>(t) * a.top + s0 + tid] = v;
+        }
     }
 }
 
@@ -407,11 +444,12 @@ cudaError_t launch_combine(const RowsArgs &a, bool vec, cudaStream_t s) {
 }
 
 template <int DT, int YT>
-cudaError_t launch_grad(const RowsArgs &a, bool vec, cudaStream_t s) {
+cudaError_t launch_grad(const RowsArgs &a, bool vec, int sms, cudaStream_t s) {
     const int per = vec ? (Vec16<DT>::kPerVec > Vec16<YT>::kPerVec ? Vec16<DT>::kPerVec : Vec16<YT>::kPerVec) : 1;
     const int n = block_for(a.D / per, kGradThreads);
+    const long long items = a.T * ((a.top + kSlots - 1) / kSlots), most = static_cast<long long>(sms) * (1024 / n);
     return launch_after(vec ? rows_combine_grad_kernel<DT, YT, true> : rows_combine_grad_kernel<DT, YT, false>,
-                        dim3(static_cast<unsigned>(a.T)), n, 0, s, a);
+                        dim3(static_cast<unsigned>(items < most ? items : most)), n, 0, s, a);
 }
 
 }  // namespace
@@ -453,12 +491,12 @@ cudaError_t launch_rows_combine(int y_dtype, int out_dtype, const RowsArgs &a, b
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_rows_combine_grad(int d_dtype, int y_dtype, const RowsArgs &a, bool vec, cudaStream_t s) {
-    if (d_dtype == kDtF32 && y_dtype == kDtF32) return launch_grad<kDtF32, kDtF32>(a, vec, s);
-    if (d_dtype == kDtF32 && y_dtype == kDtF16) return launch_grad<kDtF32, kDtF16>(a, vec, s);
-    if (d_dtype == kDtF32 && y_dtype == kDtBF16) return launch_grad<kDtF32, kDtBF16>(a, vec, s);
-    if (d_dtype == kDtF16 && y_dtype == kDtF16) return launch_grad<kDtF16, kDtF16>(a, vec, s);
-    if (d_dtype == kDtBF16 && y_dtype == kDtBF16) return launch_grad<kDtBF16, kDtBF16>(a, vec, s);
+cudaError_t launch_rows_combine_grad(int d_dtype, int y_dtype, const RowsArgs &a, bool vec, int sms, cudaStream_t s) {
+    if (d_dtype == kDtF32 && y_dtype == kDtF32) return launch_grad<kDtF32, kDtF32>(a, vec, sms, s);
+    if (d_dtype == kDtF32 && y_dtype == kDtF16) return launch_grad<kDtF32, kDtF16>(a, vec, sms, s);
+    if (d_dtype == kDtF32 && y_dtype == kDtBF16) return launch_grad<kDtF32, kDtBF16>(a, vec, sms, s);
+    if (d_dtype == kDtF16 && y_dtype == kDtF16) return launch_grad<kDtF16, kDtF16>(a, vec, sms, s);
+    if (d_dtype == kDtBF16 && y_dtype == kDtBF16) return launch_grad<kDtBF16, kDtBF16>(a, vec, sms, s);
     return cudaErrorInvalidValue;
 }
 

@@ -363,7 +363,8 @@ cudaError_t launch_route_grad(int l_dtype, const RouteGradArgs &args, int sms, c
 cudaError_t launch_route_rows(const RouteRowsArgs &args, cudaStream_t stream);
 cudaError_t launch_rows_gather(int dtype, const RowsArgs &args, bool vec, int sms, cudaStream_t stream);
 cudaError_t launch_rows_combine(int y_dtype, int out_dtype, const RowsArgs &args, bool vec, cudaStream_t stream);
-cudaError_t launch_rows_combine_grad(int d_dtype, int y_dtype, const RowsArgs &args, bool vec, cudaStream_t stream);
+cudaError_t launch_rows_combine_grad(int d_dtype, int y_dtype, const RowsArgs &args, bool vec, int sms,
+                                     cudaStream_t stream);
 cudaError_t launch_wait_selftest(const unsigned int *never_set, unsigned long long limit_ns, unsigned int *status,
                                  cudaStream_t stream);
 
