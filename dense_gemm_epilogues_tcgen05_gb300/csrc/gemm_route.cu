@@ -8,8 +8,7 @@
 //
 // A warp takes a token; lane l holds the experts l NPL .. l NPL + NPL - 1 in
 // registers, so that the lowest lane of a ballot is the lowest expert, and the
-// experts of a group lie in neighbouring lanes.  Values are compared as integers of
-// the same order, a warp's maximum by one redux.  The top-th largest of the lanes'
+// experts of a group lie in neighbouring lanes.  A warp's maximum is one redux.  The top-th largest of the lanes'
 // maxima bounds the chosen ones from below: what reaches it, rarely more than a few
 // values over `top`, is gathered one to a lane (in the experts' order), and each
 // further round costs a redux and a ballot, no search through a lane's registers.
@@ -32,18 +31,23 @@ namespace {
 constexpr int kRouteWarps = 4;
 constexpr unsigned kAll = 0xffffffffu;
 
-// Values as unsigned integers of the same order; 0 is below every value.
-__device__ __forceinline__ unsigned order_key(float f) {
-    const unsigned u = __float_as_uint(f);
-    return u ^ (static_cast<unsigned>(static_cast<int>(u) >> 31) | 0x80000000u);
+__device__ __forceinline__ float warp_max(float v) {
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
 }
-__device__ __forceinline__ float order_value(unsigned k) {
-    return __uint_as_float(k ^ (static_cast<int>(k) < 0 ? 0x80000000u : kAll));
-}
-__device__ __forceinline__ float warp_max(float v) { return order_value(__reduce_max_sync(kAll, order_key(v))); }
+
 // -infinity and NaN: not available; +infinity counts as the largest finite
 // value; -0 as 0, whose bits it must not be told from.
-__device__ __forceinline__ float logit_value(float x) { return x > -INFINITY ? fminf(x, FLT_MAX) + 0.0f : -INFINITY; }
+__device__ __forceinline__ float logit_value(float x) { return fminf(fmaxf(x, -INFINITY), FLT_MAX) + 0.0f; }
+
+// 1 / (1 + e^-x) by the hardware's 2^x and reciprocal; below 2^-126 it is 0.
+__device__ __forceinline__ float sigmoid_approx(float x) {
+    float e, s;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * -1.44269504f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + e));
+    return s;
+}
 
 // This lane's logits of a row (-infinity past the last expert).
 template <int LT, int NPL>
@@ -124,21 +128,21 @@ __device__ __forceinline__ int lanes_before(int n) {
 }
 
 struct Candidate {
-    unsigned key;
+    float value;
     int expert;
 };
 
 // The chosen experts of a token by fp32 values: lane s gets the s-th (or -1).  sel: the lane's selection scores,
-// -infinity where there is none; cand: 32 slots of the warp; margin: too_close's.  `exactly`(expert) is a selection
+// -infinity where there is none, no NaN; cand: 32 slots of the warp; margin: too_close's.  `exactly`(expert) is a selection
 // score in 64 bits (warp-collective; -1: -infinity): it decides among the candidates where fp32 ones cannot.  Returns whether even that is not enough
 // (groups too close, or more candidates than lanes).
 template <int NPL, typename Exactly>
 __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs &a, float *stage, Candidate *cand,
                                        float margin, int &expert, Exactly exactly) {
     const int lane = threadIdx.x & 31;
-    unsigned key[NPL];
+    float val[NPL];  // -infinity: none, or struck out
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) key[j] = sel[j] > -INFINITY ? order_key(sel[j]) : 0u;
+    for (int j = 0; j < NPL; ++j) val[j] = sel[j];
     bool close = false;
     if (a.groups > 1) {
         // the worth of group g in lane g * per (and those beside it)
@@ -146,7 +150,7 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
         float t1 = -INFINITY, t2 = -INFINITY;
         if (a.group_lanes > 0) {
 #pragma unroll
-            for (int j = 0; j < NPL; ++j) take_top2(t1, t2, fmaxf(sel[j], -INFINITY));  // (NaN: none)
+            for (int j = 0; j < NPL; ++j) take_top2(t1, t2, sel[j]);
             for (int d = 1; d < per; d <<= 1) {
                 const float o1 = __shfl_xor_sync(kAll, t1, d), o2 = __shfl_xor_sync(kAll, t2, d);
                 take_top2(t1, t2, o1);
@@ -155,7 +159,7 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
         } else {
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
-                if (lane * NPL + j < a.E) stage[lane * NPL + j] = fmaxf(sel[j], -INFINITY);
+                if (lane * NPL + j < a.E) stage[lane * NPL + j] = sel[j];
             __syncwarp();
             if (lane < a.groups)
                 for (int i = 0; i < a.group_size; ++i) {
@@ -169,24 +173,23 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
         const int g = lane / per;
         const bool is_group = group_stays(worth, per, a, kept);
         if (margin > 0.0f) {
-            const unsigned low = ~__reduce_max_sync(kAll, kept ? ~order_key(worth) : 0u);
-            const unsigned high = __reduce_max_sync(kAll, is_group && !kept ? order_key(worth) : 0u);
+            const float low = -warp_max(kept ? -worth : -INFINITY), high = warp_max(is_group && !kept ? worth : -INFINITY);
             // (the biases' roundings go by the sums' terms, which may be far above the sums)
             const float size = warp_max(is_group ? fabsf(t1) + (t2 > -INFINITY ? fabsf(t2) : 0.0f) : 0.0f);
-            if (high != 0u) close = too_close(order_value(low), order_value(high), 2.0f * margin + 0x1p-22f * size);
+            if (high > -INFINITY) close = too_close(low, high, 2.0f * margin + 0x1p-22f * size);
         }
         unsigned stays = __ballot_sync(kAll, kept && lane == g * per);  // bit g * per
         if (close) {
             // The groups' worths in 64 bits, from the experts that may be among a group's highest: one to a lane.
             const float least = a.group_sum == 2 ? t2 : t1;
             if (lane == g * per && g < a.groups)
-                cand[g].key = __float_as_uint(least > -INFINITY && least < INFINITY ? least - (margin + 0x1p-22f * fabsf(least)) : least);
+                cand[g].value = least > -INFINITY && least < INFINITY ? least - (margin + 0x1p-22f * fabsf(least)) : least;
             __syncwarp();
             unsigned flags = 0u;
 #pragma unroll
             for (int j = 0; j < NPL; ++j) {
                 const int eg = a.group_lanes > 0 ? g : (lane * NPL + j) / a.group_size;
-                if (key[j] != 0u && sel[j] >= __uint_as_float(cand[eg].key)) flags |= 1u << j;
+                if (val[j] > -INFINITY && val[j] >= cand[eg].value) flags |= 1u << j;
             }
             __syncwarp();
             if (__reduce_add_sync(kAll, __popc(flags)) > 32) return true;
@@ -210,36 +213,33 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
         if (a.group_lanes > 0) {
             kept = (stays >> (g * per) & 1u) != 0u;
 #pragma unroll
-            for (int j = 0; j < NPL; ++j) key[j] = kept ? key[j] : 0u;
+            for (int j = 0; j < NPL; ++j) val[j] = kept ? val[j] : -INFINITY;
         } else {
 #pragma unroll
             for (int j = 0; j < NPL; ++j) {
                 const int eg = (lane * NPL + j) / a.group_size;
-                if (eg >= 32 || (stays >> eg & 1u) == 0) key[j] = 0u;
+                if (eg >= 32 || (stays >> eg & 1u) == 0) val[j] = -INFINITY;
             }
         }
     }
     const int rounds = margin > 0.0f ? a.top + 1 : a.top;  // one more than is chosen, to compare with
-    unsigned best = key[0], least = 0u;
+    float best = val[0], least = -INFINITY;
     if (NPL > 1) {
 #pragma unroll
-        for (int j = 1; j < NPL; ++j) best = max(best, key[j]);
-        unsigned rest = best;
+        for (int j = 1; j < NPL; ++j) best = fmaxf(best, val[j]);
+        float rest = best;
         for (int s = 0; s < rounds; ++s) {
-            least = __reduce_max_sync(kAll, rest);
-            rest = rest == least ? 0u : rest;
+            least = warp_max(rest);
+            rest = rest == least ? -INFINITY : rest;
         }
-    }
-    if (margin > 0.0f && least != 0u) {
         // and what may in truth reach it
-        const float v = order_value(least);
-        if (v < INFINITY) least = order_key(v - (margin + 0x1p-22f * fabsf(v)));
+        if (margin > 0.0f && fabsf(least) < INFINITY) least -= margin + 0x1p-22f * fabsf(least);
     }
-    least = max(least, 1u);
+    least = fmaxf(least, -FLT_MAX);
     int n = 0;
 #pragma unroll
-    for (int j = 0; j < NPL; ++j) n += key[j] >= least;
-    unsigned mine = 0u;
+    for (int j = 0; j < NPL; ++j) n += val[j] >= least;
+    float mine = -INFINITY;
     int my_expert = -1, owner_of = -1;
     const int total = __reduce_add_sync(kAll, n);
     expert = -1;
@@ -250,27 +250,27 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
             int at = lanes_before(n);
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
-                if (key[j] >= least) cand[at++] = {key[j], lane * NPL + j};
+                if (val[j] >= least) cand[at++] = {val[j], lane * NPL + j};
             __syncwarp();
             if (lane < total) {
-                mine = cand[lane].key;
+                mine = cand[lane].value;
                 my_expert = cand[lane].expert;
             }
             __syncwarp();
         } else {
-            mine = key[0];
+            mine = val[0];
             my_expert = lane;
         }
-        const bool candidate = mine != 0u;
+        const bool candidate = mine > -INFINITY;
         for (; found < rounds; ++found) {
-            const unsigned top = __reduce_max_sync(kAll, mine);
-            if (top == 0u) break;
+            const float top = warp_max(mine);
+            if (top == -INFINITY) break;
             const int owner = __ffs(__ballot_sync(kAll, mine == top)) - 1;
             if (lane == found) {
                 owner_of = owner;
-                value = order_value(top);
+                value = top;
             }
-            if (lane == owner) mine = 0u;
+            if (lane == owner) mine = -INFINITY;
         }
         expert = __shfl_sync(kAll, my_expert, owner_of & 31);
         expert = owner_of >= 0 && lane < a.top ? expert : -1;
@@ -280,7 +280,7 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
                 // each candidate's rank by its 64-bit score; the candidates are in the experts' order
                 const double v = exactly(candidate ? my_expert : -1);
                 int rank = 0;
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < (NPL > 1 ? total : 32); ++i) {
                     const double o = __shfl_sync(kAll, v, i);
                     rank += o > v || (o == v && i < lane);
                 }
@@ -294,22 +294,21 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
         // many equal maxima, or more experts to choose than lanes can bound: through the registers
         float last = 0.0f;
         for (; found < rounds; ++found) {
-            const unsigned top = __reduce_max_sync(kAll, best);
-            if (top == 0u) break;
-            const float v = order_value(top);
-            if (margin > 0.0f && found > 0 && too_close(last, v, margin)) return true;
-            last = v;
+            const float top = warp_max(best);
+            if (top == -INFINITY) break;
+            if (margin > 0.0f && found > 0 && too_close(last, top, margin)) return true;
+            last = top;
             if (found == a.top) break;
             const int owner = __ffs(__ballot_sync(kAll, best == top)) - 1;
             int j_top = 0;
             if (lane == owner) {
 #pragma unroll
-                for (int j = NPL - 1; j >= 0; --j) j_top = key[j] == top ? j : j_top;
-                best = 0u;
+                for (int j = NPL - 1; j >= 0; --j) j_top = val[j] == top ? j : j_top;
+                best = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < NPL; ++j) {
-                    if (j == j_top) key[j] = 0u;
-                    best = max(best, key[j]);
+                    if (j == j_top) val[j] = -INFINITY;
+                    best = fmaxf(best, val[j]);
                 }
             }
             const int e = owner * NPL + __shfl_sync(kAll, j_top, owner);
@@ -461,10 +460,10 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NPL <= 8 ? 8 : 1) route_kern
                 for (int j = 0; j < NPL; ++j) sel[j] = __fdividef(sel[j], sum);
             } else {
 #pragma unroll
-                for (int j = 0; j < NPL; ++j) sel[j] = __fdividef(1.0f, 1.0f + __expf(-x[j]));
+                for (int j = 0; j < NPL; ++j) sel[j] = sigmoid_approx(x[j]);
             }
 #pragma unroll
-            for (int j = 0; j < NPL; ++j) sel[j] = x[j] > -INFINITY ? sel[j] + b[j] + 0.0f : -INFINITY;
+            for (int j = 0; j < NPL; ++j) sel[j] = x[j] > -INFINITY ? fmaxf(sel[j] + b[j], -INFINITY) : -INFINITY;  // (NaN: none)
             // What a difference of two scores may be off by, apart from the biases' roundings.  Sigmoid: each by less
             // than 1.6 x 2^-22, namely 1 for the quotient, 1/4 for the sum's rounding, 1/4 (the score's slope) for the
             // exponential and 0.09 for its argument's rounding (slope times |x| is at most 0.224).  Softmax, relative
@@ -501,7 +500,9 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
     begin_after();
     using T = typename Elem<LT>::T;
     constexpr int PV = Vec16<LT>::kPerVec;
+    __shared__ __align__(16) float rows[kRouteWarps][32 * NPL];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float *buf = rows[warp];
     const bool whole = a.score == kScoreSoftmax && !a.renorm;  // every logit has a gradient
     for (long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp; t < a.T;
          t += static_cast<long long>(gridDim.x) * kRouteWarps) {
@@ -536,12 +537,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
 #pragma unroll
             for (int j = 0; j < NPL; ++j) d[j] = 0.0f;
         }
-        for (int s = 0; s < a.top; ++s) {  // in the slots' order, also where an expert is in two of them
-            const int e = __shfl_sync(kAll, expert, s) - lane * NPL;
-            const float cs = __shfl_sync(kAll, c, s);
+        // The chosen experts' parts, added in the row's place in shared memory: by their lanes at once, or one after
+        // the other where an expert is in two slots.
 #pragma unroll
-            for (int j = 0; j < NPL; ++j) d[j] += e == j ? cs : 0.0f;
+        for (int j = 0; j < NPL; ++j) buf[lane * NPL + j] = d[j];
+        __syncwarp();
+        const unsigned same = __match_any_sync(kAll, expert);
+        if (__any_sync(kAll, live && (same & (same - 1u)) != 0u)) {
+            for (int s = 0; s < a.top; ++s) {
+                if (lane == s && live) buf[expert] += c;
+                __syncwarp();
+            }
+        } else if (live) {
+            buf[expert] += c;
         }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) d[j] = buf[lane * NPL + j];
         T *out = static_cast<T *>(a.dlogits) + t * a.ldd;
         const int e0 = lane * NPL;
         if (NPL >= PV && a.vec_out) {
