@@ -2087,7 +2087,7 @@ gemm_status_t gemm_rows_gather(int64_t R, int64_t D, int64_t T, int64_t top, gem
     a.X = const_cast<void *>(X); a.ldx = ldx;
     a.Y = Y; a.ldy = ldy;
     a.source = source; a.weight = weight;
-    const bool vec = rows_at(X, T, ldx * es, 16) && rows_at(Y, R, ldy * es, 16) && D * es % 16 == 0;
+    const bool vec = rows_at(X, T, ldx * es, 16) && rows_at(Y, R, ldy * es, 16);
     return launch_rows_gather(dtype, a, vec, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GEMM_OK : GEMM_ERR_CUDA;
 }
@@ -2116,9 +2116,8 @@ gemm_status_t gemm_rows_combine(int64_t T, int64_t top, int64_t D, int64_t R, ge
     a.X = Out; a.ldx = ldo;
     a.Y = const_cast<void *>(Y); a.ldy = ldy;
     a.row = row; a.weight = weight; a.beta = beta;
-    const bool vec = (R == 0 || rows_at(Y, R, ldy * es, 16)) && rows_at(Out, T, ldo * os, 16) && D * es % 16 == 0 &&
-                     D * os % 8 == 0;
-    return launch_rows_combine(y_dtype, out_dtype, a, vec, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+    const bool vec = R == 0 || rows_at(Y, R, ldy * es, 16);
+    return launch_rows_combine(y_dtype, out_dtype, a, vec, rows_at(Out, T, ldo * os, 16), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
                ? GEMM_OK : GEMM_ERR_CUDA;
 }
 
@@ -2157,9 +2156,8 @@ gemm_status_t gemm_rows_combine_grad(int64_t T, int64_t top, int64_t D, int64_t 
     a.row = row; a.weight = weight;
     a.dY = writes ? dY : nullptr; a.lddy = lddy;
     a.dweight = dweight;
-    const int widest = std::min(ds, es);  // 16 bytes of the narrower type hold the most values
     const bool vec = (D == 0 || rows_at(dOut, T, ldd * ds, 16)) && (!reads_y || rows_at(Y, R, ldy * es, 16)) &&
-                     (!writes || rows_at(dY, R, lddy * es, 16)) && D * widest % 16 == 0;
+                     (!writes || rows_at(dY, R, lddy * es, 16));
     return launch_rows_combine_grad(d_dtype, y_dtype, a, vec, dev->num_sms, reinterpret_cast<cudaStream_t>(stream)) ==
                    cudaSuccess
                ? GEMM_OK : GEMM_ERR_CUDA;

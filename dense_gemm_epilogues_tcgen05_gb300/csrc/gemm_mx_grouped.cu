@@ -25,6 +25,22 @@
 //                rows of W and of all the tile's rows of X, on a barrier of its own;
 //   warps 4-11   epilogue: two per 32-lane quadrant of tensor memory, each half of
 //                the tile's columns (store_chunk_t).
+//
+// Bound and measured (GB300).  Few rows: HBM (64 rows over 64 experts of 2048 x 4096
+// E2M1, 45 of them busy: 36 us, 5.7 TB/s, of which 5 % are the last of five rounds of
+// tiles).  Many rows: no unit alone.  A k-block of 128 bytes writes 29 KB into shared
+// memory, and its MMAs read 29 KB (42 KB if an SM reads both halves of X): 450 to 560
+// of its 660 clocks; the issuing thread's own time was 470.  32768 rows over 32 experts
+// of 4096 x 4096, bias and SiLU, bf16 out: 226 us, 4.9 PFLOP/s, with new inputs each
+// time, 212 with the same.  What there is to gain, from copies that leave work out (of
+// a first version at 222): C's writes 31, W from L2 alone 21, a quarter of the MMAs 20,
+// the scales' copies to tensor memory 18, X's loads 13, the scales' loads 10; without
+// C, copies, X and scales, and with a quarter of the MMAs, 165 are left.
+// Tried: stages of 256 bytes (219, and 16.7 against 12.8 for 777 rows over 24 experts of
+// 1000 x 1056 E4M3), copies one block ahead of their MMAs (250 against 222), two pairs
+// sharing X by multicast (214 against 203: they fit 144 of the 152 SMs), W prefetched to
+// L2 (208 against 210), operands without the evict-last policy (262 against 214), C
+// stored evict-first, past L1 or in pairs of lanes (209 to 217 against 212 to 214).
 #include "gemm_tcgen05.cuh"
 #include "grouped.cuh"
 #include "mx_traits.cuh"

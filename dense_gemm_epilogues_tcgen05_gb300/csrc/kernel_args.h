@@ -357,12 +357,14 @@ cudaError_t launch_mx_quantize(int elem, int x_dtype, const MxQuantArgs &args, i
                                cudaStream_t stream);
 cudaError_t launch_mx_dequantize(int elem, int y_dtype, const MxQuantArgs &args, bool q_vec, bool y_vec,
                                  cudaStream_t stream);
-//   routing and its gradient, the sort by expert, the movement of rows (vec: 16-byte pieces):
+//   routing and its gradient, the sort by expert, the movement of rows (vec: rows may be accessed in 16-byte pieces;
+//   of a combination, those of Y, and with out_vec those of the output):
 cudaError_t launch_route(int l_dtype, const RouteArgs &args, int sms, cudaStream_t stream);
 cudaError_t launch_route_grad(int l_dtype, const RouteGradArgs &args, int sms, cudaStream_t stream);
 cudaError_t launch_route_rows(const RouteRowsArgs &args, cudaStream_t stream);
 cudaError_t launch_rows_gather(int dtype, const RowsArgs &args, bool vec, int sms, cudaStream_t stream);
-cudaError_t launch_rows_combine(int y_dtype, int out_dtype, const RowsArgs &args, bool vec, cudaStream_t stream);
+cudaError_t launch_rows_combine(int y_dtype, int out_dtype, const RowsArgs &args, bool vec, bool out_vec,
+                                cudaStream_t stream);
 cudaError_t launch_rows_combine_grad(int d_dtype, int y_dtype, const RowsArgs &args, bool vec, int sms,
                                      cudaStream_t stream);
 cudaError_t launch_wait_selftest(const unsigned int *never_set, unsigned long long limit_ns, unsigned int *status,

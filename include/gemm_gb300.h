@@ -877,8 +877,8 @@ size_t gemm_route_rows_workspace_size(int64_t T, int64_t top, int64_t E);
  * No row may be named twice, as gemm_route_rows names none; rows of dY that are not
  * named stay as they were.
  *
- * D <= GEMM_ROWS_MAX_D.  Bases and pitches of 16 bytes and D of whole 16-byte pieces
- * run fastest; any others work.  The output must not overlap the inputs.
+ * D <= GEMM_ROWS_MAX_D.  Bases and pitches of whole 16 bytes run fastest; any
+ * others work.  The output must not overlap the inputs.
  */
 #define GEMM_ROWS_MAX_D 8388608 /* 2^23 */
 gemm_status_t gemm_rows_gather(int64_t R, int64_t D, int64_t T, int64_t top, gemm_dtype_t dtype, const void *X,

@@ -20,7 +20,8 @@ def scores(x, kind):
         e = np.exp(-np.abs(x))
         s = np.where(x >= 0, 1 / (1 + e), e / (1 + e))
     elif live.any():
-        s = np.exp(np.maximum(x - x[live].max(), -745.0 * 2))
+        with np.errstate(over="ignore"):  # (values that are not live are left out below)
+            s = np.exp(np.clip(x - x[live].max(), -1500.0, 0.0))
         s = s / s[live].sum()
     return np.where(live, s, 0.0)
 

@@ -29,11 +29,11 @@ def coded(rng, shape, K, elem, kind):
     """Codes (one per element), scales and values of shape[0] x ... rows of K."""
     n = int(np.prod(shape))
     if kind == "integer":
-        vals = np.array([-2, -1, -0.0, 0, 1, 2]) if elem == E2M1 else np.arange(-4, 5)
-        codes = om.nearest_codes(rng.choice(vals, (n, K)), elem)
+        vals = np.array([-2, -1, -0.0, 0, 1, 2]) if elem == E2M1 else np.arange(-4.0, 5.0)
+        pick = rng.integers(0, len(vals), (n, K), dtype=np.uint8)
         scale = rng.integers(127, 130, (n, K // 32))
-    else:
-        codes, scale = om.quantize_reference(rng.standard_normal((n, K)) * 10.0 ** rng.uniform(-2, 2, (n, 1)), elem)
+        return om.nearest_codes(vals, elem)[pick], scale, vals[pick] * np.repeat(2.0 ** (scale - 127), 32, 1)
+    codes, scale = om.quantize_reference(rng.standard_normal((n, K)) * 10.0 ** rng.uniform(-2, 2, (n, 1)), elem)
     return codes, scale, om.values_of(codes, scale, elem)
 
 
@@ -189,3 +189,52 @@ def test_long_one_sided_sums(cuda_lib, elem):
     g.gemm_mx_grouped(1, M, N, K, elem, None, X, K, XS, K // 32, W, 0, K, WS, 0, K // 32, C, N, F32, 1.0, 0.0, None, 0)
     want = xv @ wv.T
     check(C.cpu().double().numpy(), want, want, F32, K, elem)
+
+
+def test_the_largest_table_and_single_rows(cuda_lib):
+    """1024 groups; one row and one channel, whose pitches are not used and may be anything."""
+    rng = np.random.default_rng(1)
+    sizes = rng.integers(0, 4, 1024).tolist()
+    got, want, _ = run(cuda_lib, sizes, 40, 64, E2M1, F32, seed=2)
+    np.testing.assert_array_equal(got, want)
+    g, K = cuda_lib, 96
+    x, w = (torch.full((K // 2,), 0x22, dtype=torch.uint8, device="cuda") for _ in range(2))
+    s = torch.full((K // 32,), 127, dtype=torch.uint8, device="cuda")
+    C = torch.full((1,), float("nan"), device="cuda")
+    g.gemm_mx_grouped(1, 1, 1, K, E2M1, None, x, K + 2, s, 3, w, 0, K + 6, s, 0, 5, C, 1, F32, 1.0, 0.0, None, 0)
+    assert g.gemm_device_status() == 0 and C.item() == K
+
+
+@pytest.mark.parametrize("elem", [E2M1, E4M3], ids=["e2m1", "e4m3"])
+def test_the_same_call_gives_the_same_bits(cuda_lib, elem):
+    """A row's result depends neither on the rows beside it nor on the run."""
+    g, K, N, M = cuda_lib, 1024, 300, 900
+    rng = np.random.default_rng(3)
+    xc, xs, _ = coded(rng, (M,), K, elem, "normal")
+    wc, ws, _ = coded(rng, (N,), K, elem, "normal")
+    X, XS, W, WS = (torch.from_numpy(a).cuda() for a in (om.packed(xc, elem), xs.astype(np.uint8), om.packed(wc, elem),
+                                                         ws.astype(np.uint8)))
+
+    def product(rows):
+        C = torch.empty(len(rows), N, device="cuda")
+        g.gemm_mx_grouped(1, len(rows), N, K, elem, None, X[rows].contiguous(), K, XS[rows].contiguous(), K // 32, W, 0, K,
+                          WS, 0, K // 32, C, N, F32, 1.0, 0.0, None, 0)
+        return C
+
+    whole = product(list(range(M)))
+    assert torch.equal(whole, product(list(range(M))))
+    for rows in ([5], [899, 3, 400], list(range(100, 350))):
+        assert torch.equal(product(rows), whole[rows])
+
+
+def test_row_blocks_past_2_to_the_31_elements(cuda_lib):
+    """Outputs whose offsets pass 32 bits."""
+    g, K, N, M = cuda_lib, 32, 2048, (1 << 20) + 5
+    x = torch.full((M, 16), 0x22, dtype=torch.uint8, device="cuda")
+    w = torch.full((N, 16), 0x22, dtype=torch.uint8, device="cuda")
+    xs, ws = (torch.full((r, 16), 127, dtype=torch.uint8, device="cuda") for r in (M, N))
+    xs[-1], ws[-1] = 128, 129
+    C = torch.zeros(M, N, dtype=torch.bfloat16, device="cuda")
+    g.gemm_mx_grouped(1, M, N, K, E2M1, None, x, K, xs, 16, w, 0, K, ws, 0, 16, C, N, BF16, 1.0, 0.0, None, 0)
+    assert g.gemm_device_status() == 0
+    assert (C[:-1, :-1] == K).all() and (C[-1, :-1] == 2 * K).all() and (C[:-1, -1] == 4 * K).all() and C[-1, -1] == 8 * K

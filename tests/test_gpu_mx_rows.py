@@ -148,3 +148,16 @@ def test_round_trip(cuda_lib, elem):
     q, s = quantize(cuda_lib, x, 64, 256, elem, F32, 256)
     np.testing.assert_array_equal(s, scale)
     np.testing.assert_array_equal(q, om.packed(codes, elem))
+
+
+def test_rows_past_2_to_the_31_elements(cuda_lib):
+    """Offsets in 64 bits, both ways: the last rows of 2^31 values and more."""
+    K, M = 8192, (1 << 18) + 3
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device="cuda")
+    x[-2:] = torch.arange(2 * K, device="cuda").view(2, K).remainder(7).bfloat16()
+    q = torch.empty(M, K, dtype=torch.uint8, device="cuda")
+    s = torch.empty(M, K // 32, dtype=torch.uint8, device="cuda")
+    cuda_lib.gemm_mx_quantize(M, K, E4M3, BF16, x, K, q, K, s, K // 32)
+    y = torch.full_like(x, float("nan"))
+    cuda_lib.gemm_mx_dequantize(M, K, E4M3, q, K, s, K // 32, BF16, y, K)
+    assert torch.equal(y, x)  # small integers survive

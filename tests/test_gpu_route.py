@@ -229,3 +229,60 @@ def test_rows(cuda_lib, T, top, E):
         assert (off[E + 1:] == -7).all() and (row[P:] == -7).all() and (src[P:] == -7).all()
         cuda_lib.gemm_route_rows(T, top, E, torch.from_numpy(expert).int().cuda(), off, None, src, ws, need)
         np.testing.assert_array_equal(src[:P].cpu().numpy(), want[2])
+
+
+@pytest.mark.parametrize("E,top", [(8, 20), (3, 32), (40, 32), (64, 31), (256, 32)])
+@pytest.mark.parametrize("biased", [False, True])
+def test_more_slots_than_experts_or_nearly(cuda_lib, E, top, biased):
+    """Slots left over get -1 and weight 0; 31 and 32 slots, which the lanes' maxima cannot bound; equal logits, whose
+    candidates are more than the lanes."""
+    T = 19
+    _, x = logits_of(T, E, F32, E)
+    x[5], x[6] = 0.25, np.round(x[6])
+    b = torch.from_numpy(np.random.default_rng(top).normal(0, 0.1, E)).float() if biased else None
+    if biased:
+        x[7] = -1.5  # equal scores but for the bias
+    for score in (SOFTMAX, SIGMOID):
+        kw = dict(bias=b, score=score, renormalise=True)
+        got = route(cuda_lib, torch.from_numpy(x).float().cuda(), T, E, top, F32, **kw)
+        check(x, got, reference(x, top, **kw))
+
+
+def test_all_equal(cuda_lib):
+    """A router before training: every logit and bias 0.  The lower indexes, groups among them."""
+    T, E, top = 300, 256, 8
+    x = torch.zeros(T, E, device="cuda")
+    kw = dict(bias=torch.zeros(E), score=SIGMOID, groups=8, top_groups=4, group_sum=2)
+    e, w = route(cuda_lib, x, T, E, top, F32, **kw)
+    assert (e == np.arange(top)).all() and (w == 0.125).all()
+
+
+def test_large_biases(cuda_lib):
+    """Sums of a group's two that nearly cancel, and biases far above the scores: decided by 64-bit sums."""
+    rng = np.random.default_rng(4)
+    T, E = 64, 64
+    x = rng.normal(0, 1, (T, E)).astype(np.float32)
+    b = np.where(rng.random(E) < 0.5, 1000.0, -1000.0) + rng.normal(0, 1e-4, E)
+    b = torch.from_numpy(b).float()
+    kw = dict(bias=b, score=SIGMOID, groups=16, top_groups=5, group_sum=2)
+    check(x.astype(np.float64), route(cuda_lib, torch.from_numpy(x).cuda(), T, E, 6, F32, **kw),
+          reference(x.astype(np.float64), 6, **kw))
+
+
+def test_gradient_of_many_tokens(cuda_lib):
+    """More tokens than the grid's warps; the same bits on every call."""
+    T, E, top = 20003, 64, 4
+    dev, _ = logits_of(T, E, F32, 2)
+    expert = torch.topk(dev, top).indices.int()
+    dw = torch.randn(T, top, device="cuda")
+    outs = []
+    for _ in range(3):
+        out = torch.empty(T, E, device="cuda")
+        cuda_lib.gemm_route_grad(T, E, top, F32, dev, E, expert, dw, out, E, SOFTMAX, False, 1.0)
+        outs.append(out)
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    p = torch.softmax(dev.double(), 1)
+    d = torch.zeros(T, E, dtype=torch.float64, device="cuda").scatter_(1, expert.long(), dw.double())
+    want = p * (d - (d * p).sum(1, keepdim=True))
+    size = p * (d.abs() + (d * p).abs().sum(1, keepdim=True))
+    assert ((out.double() - want).abs() <= 300 * U * size + 2.0 ** -120).all()

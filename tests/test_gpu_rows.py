@@ -167,3 +167,65 @@ def test_rows_past_2_to_the_31_elements(cuda_lib):
     src[-1] = 1
     cuda_lib.gemm_rows_gather(R, D, 2, 1, BF16, out, D, src, None, Y, D)
     assert torch.equal(Y[-1], out[1])
+
+
+def test_many_tokens_and_slots(cuda_lib):
+    """More items than resident blocks, more slots than are in flight at once; twice the same bits."""
+    T, top, D, R = 3000, 11, 72, 3000 * 11
+    rng = np.random.default_rng(6)
+    row, source, n = order(rng, T, top, 0.1)
+    dO, Y = torch.randn(T, D, device="cuda"), torch.randn(R, D, device="cuda")
+    w = torch.rand(T, top, device="cuda")
+    outs = []
+    for _ in range(2):
+        dY, dw = torch.zeros(R, D, device="cuda"), torch.full((T, top), CANARY, device="cuda")
+        cuda_lib.gemm_rows_combine_grad(T, top, D, R, F32, dO, D, F32, Y, D, dev(row), w, dY, D, dw)
+        outs.append((dY, dw))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    r = torch.from_numpy(row).cuda()
+    live = r >= 0
+    terms = dO.double()[:, None] * Y.double()[r.clamp_min(0)]
+    want = torch.where(live, terms.sum(2), torch.zeros(()).cuda().double())
+    assert ((dw.double() - want).abs() <= (D + 1) * U * terms.abs().sum(2)).all()
+    moved = torch.zeros(R, D, dtype=torch.float64, device="cuda")
+    moved[r[live]] = (w.double()[..., None] * dO.double()[:, None])[live]
+    assert ((dY.double() - moved).abs() <= U * moved.abs()).all()
+
+
+@pytest.mark.parametrize("D", [1, 5, 9, 1001, 2059])
+@pytest.mark.parametrize("y_dtype,out", [(F32, F32), (F32, BF16), (F16, F32), (F16, F16), (BF16, F32), (BF16, BF16)])
+@pytest.mark.parametrize("out_pad", [None, 0])
+def test_aligned_rows_that_end_inside_a_piece(cuda_lib, D, y_dtype, out, out_pad):
+    """D of no whole 16-byte pieces in rows whose pitch is; outputs of such rows, and of rows at any element."""
+    rng = np.random.default_rng(D)
+    T, top = 41, 3
+    R, pitch = T * top, (D + 7) // 8 * 8
+    row, source, n = order(rng, T, top, 0.2)
+    w = torch.from_numpy(rng.standard_normal((T, top))).float()
+    Y, yv = rows(rng, R, D, y_dtype, pitch - D)
+    ldo = pitch if out_pad is None else D
+    for beta in (0.0, 0.5):
+        o = blank(T, D, out, ldo - D)
+        o0 = torch.from_numpy(rng.standard_normal((T, D))).to(DT[out])
+        o[1:T + 1, :D] = o0.cuda() if beta else float("nan")
+        cuda_lib.gemm_rows_combine(T, top, D, R, y_dtype, Y, pitch, dev(row), w.cuda(), beta, out, o[1:], ldo)
+        want, size = orr.combine_reference(yv, row, w.double().numpy(), beta, o0.double().numpy())
+        assert (np.abs(inside(o, T, D) - want) <= (top + 2) * U * size + HALF[out] * np.abs(want) + 2.0 ** -25).all()
+    if out != y_dtype and out != F32:
+        return
+    # the incoming gradient in `out`, the rows in y_dtype; and the tokens gathered
+    X, xv = rows(rng, T, D, out, pitch - D)
+    dY, dw = blank(R, D, y_dtype, ldo - D), torch.empty(T, top, device="cuda")
+    cuda_lib.gemm_rows_combine_grad(T, top, D, R, out, X, pitch, y_dtype, Y, pitch, dev(row), w.cuda(), dY[1:], ldo, dw)
+    live = row >= 0
+    moved = (w.double().numpy()[..., None] * xv[:, None])[live]
+    got = inside(dY, R, D)
+    assert (np.abs(got[row[live]] - moved) <= (U + HALF[y_dtype]) * np.abs(moved) + 2.0 ** -25).all()
+    assert (got[n:] == CANARY).all()
+    terms = np.repeat(xv[:, None], top, 1)[live] * yv[row[live]]
+    assert (np.abs(dw.cpu().numpy()[live] - terms.sum(1)) <= (D + 1) * U * np.abs(terms).sum(1)).all()
+    g = blank(R, D, out, ldo - D)
+    cuda_lib.gemm_rows_gather(R, D, T, top, out, X, pitch, dev(source), None, g[1:], ldo)
+    got = inside(g, R, D)
+    np.testing.assert_array_equal(got[:n], xv[source[:n] // top])
+    assert (got[n:] == CANARY).all()
