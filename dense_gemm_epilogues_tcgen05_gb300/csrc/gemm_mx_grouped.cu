@@ -27,20 +27,23 @@
 //                the tile's columns (store_chunk_t).
 //
 // Bound and measured (GB300).  Few rows: HBM (64 rows over 64 experts of 2048 x 4096
-// E2M1, 45 of them busy: 36 us, 5.7 TB/s, of which 5 % are the last of five rounds of
+// E2M1, 45 of them busy: 35 us, 5.9 TB/s, of which 5 % are the last of five rounds of
 // tiles).  Many rows: no unit alone.  A k-block of 128 bytes writes 29 KB into shared
 // memory, and its MMAs read 29 KB (42 KB if an SM reads both halves of X): 450 to 560
-// of its 660 clocks; the issuing thread's own time was 470.  32768 rows over 32 experts
-// of 4096 x 4096, bias and SiLU, bf16 out: 226 us, 4.9 PFLOP/s, with new inputs each
-// time, 212 with the same.  What there is to gain, from copies that leave work out (of
-// a first version at 222): C's writes 31, W from L2 alone 21, a quarter of the MMAs 20,
-// the scales' copies to tensor memory 18, X's loads 13, the scales' loads 10; without
-// C, copies, X and scales, and with a quarter of the MMAs, 165 are left.
-// Tried: stages of 256 bytes (219, and 16.7 against 12.8 for 777 rows over 24 experts of
-// 1000 x 1056 E4M3), copies one block ahead of their MMAs (250 against 222), two pairs
-// sharing X by multicast (214 against 203: they fit 144 of the 152 SMs), W prefetched to
-// L2 (208 against 210), operands without the evict-last policy (262 against 214), C
-// stored evict-first, past L1 or in pairs of lanes (209 to 217 against 212 to 214).
+// of its 640 clocks, in which the tensor pipe is busy for 370; what the issuing thread
+// does besides waiting counts in full.  32768 rows over 32 experts of 4096 x 4096, bias
+// and SiLU, bf16 out: 222 us, 4.9 PFLOP/s, with new inputs each time, 205 with the same.
+// What there is to gain, from copies that leave work out (of a first version at 222):
+// C's writes 31, W from L2 alone 21, a quarter of the MMAs 20, the scales' copies to
+// tensor memory 18, X's loads 13, the scales' loads 10; without C, copies, X and scales,
+// and with a quarter of the MMAs, 165 are left.
+// Tried: a wait per block (212; with another for its scales 226), both blocks loaded and
+// freed as one stage (219, and 16.7 against 12.8 for 777 rows over 24 experts of 1000 x
+// 1056 E4M3), four stages (260), copies one block ahead of their MMAs (250 against
+// 222), two pairs sharing X by multicast (214 against 203: they fit 144 of the 152
+// SMs), W prefetched to L2 (208 against 210), operands without the evict-last policy
+// (262 against 214), C stored evict-first, past L1 or in pairs of lanes (209 to 217
+// against 212 to 214).
 #include "gemm_tcgen05.cuh"
 #include "grouped.cuh"
 #include "mx_traits.cuh"
@@ -62,7 +65,7 @@ struct MxgConfig {
     static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
     static constexpr int BAR_BYTES = 256, SMEM_MAX = 232448;
     static_assert(2 * ACC_STRIDE + SF_SLOTS * SF_COLS <= TMEM_COLS, "accumulators and scales fit");
-    static_assert((2 * STAGES + PAIRS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
+    static_assert((STAGES + 2 * PAIRS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
     static_assert(B_BYTES % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle atoms stay aligned");
     // after up to 1023 bytes of alignment: [stages][scales][barriers][group table]
     static int smem_bytes(int G) {
@@ -123,9 +126,9 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
     unsigned char *smem =
         reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     unsigned char *scales = smem + Cfg::STAGES * Cfg::STAGE_BYTES;
-    uint64_t *full = reinterpret_cast<uint64_t *>(scales + Cfg::PAIRS * Cfg::SF_BYTES);  // (leader's) operands landed;
-                                                  // a pair's first stage: and both CTAs' scales laid out
-    uint64_t *empty = full + Cfg::STAGES;
+    uint64_t *full = reinterpret_cast<uint64_t *>(scales + Cfg::PAIRS * Cfg::SF_BYTES);  // (leader's) a pair's operands
+                                                  // landed and both CTAs' scales laid out
+    uint64_t *empty = full + Cfg::PAIRS;          // a stage's MMAs are done
     uint64_t *landed = empty + Cfg::STAGES;       // this CTA's scales of a pair have landed
     uint64_t *tfull = landed + Cfg::PAIRS;
     uint64_t *tempty = tfull + 2;
@@ -138,11 +141,11 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
     const int cluster = blockIdx.x / CL, nclusters = gridDim.x / CL;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Cfg::STAGES; ++s) {
-            mbar_init(&full[s], s % 2 == 0 ? 1 + CL : 1);
-            mbar_init(&empty[s], 1);
+        for (int s = 0; s < Cfg::STAGES; ++s) mbar_init(&empty[s], 1);
+        for (int s = 0; s < Cfg::PAIRS; ++s) {
+            mbar_init(&full[s], 1 + CL);
+            mbar_init(&landed[s], 1);
         }
-        for (int s = 0; s < Cfg::PAIRS; ++s) mbar_init(&landed[s], 1);
         for (int b = 0; b < 2; ++b) {
             mbar_init(&tfull[b], 1);
             mbar_init(&tempty[b], CL * Cfg::EPI_WARPS);
@@ -194,14 +197,12 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
                     }
                     issued = true;
                     unsigned char *sA = smem + stage * Cfg::STAGE_BYTES;
-                    const uint32_t fbar = full0_leader + 8u * stage;
+                    const uint32_t fbar = full0_leader + 8u * (stage >> 1);
                     if (warp == 0) {
-                        if (b < blocks) {
-                            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2u * bytes);
-                            tma_load_3d_pair(sA, &maps.w, fbar, b * Cfg::BLOCK, f, t.g, keep);
-                        } else if (rank == 0) {
-                            mbar_arrive(&full[stage]);  // nothing to load
-                        }
+                        // (of a pair without a second block, its first alone is waited for)
+                        if (rank == 0 && b % 2 == 0)
+                            mbar_arrive_expect_tx(&full[stage >> 1], (b + 1 < blocks ? 4u : 2u) * bytes);
+                        if (b < blocks) tma_load_3d_pair(sA, &maps.w, fbar, b * Cfg::BLOCK, f, t.g, keep);
                     } else {
                         if (b % 2 == 0) {
                             uint64_t *bar = &landed[stage / 2];
@@ -231,13 +232,14 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
         if (rank == 0) {
             // ---------------------------------------------------- MMA issuer --
             // The whole warp walks the loop and one elected lane issues, so that
-            // addresses and descriptors stay in uniform registers; the next stage is
-            // asked for before this one's instructions issue.
+            // addresses and descriptors stay in uniform registers.  A step is a pair of
+            // blocks: one wait and one fence for both, and each block's stage freed by
+            // itself.
             const uint64_t a_desc0 = sw128_desc(smem_u32(smem), 16u, 1024u);
             const uint64_t b_desc0 = sw128_desc(smem_u32(smem) + Cfg::A_BYTES, 16u, 1024u);
             const uint64_t sf_desc0 = plain16_desc(smem_u32(scales));
-            uint32_t stage = 0, phase = 0, slot = 0;
-            bool ok = true, issued = false, is_full = false;
+            uint32_t pair = 0, phase = 0, slot = 0;
+            bool ok = true, issued = false;
             int local = 0;
             while (ok && steps > 0 && walk.next(t)) {
                 const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
@@ -247,57 +249,53 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
                 if (!ok) break;
                 const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
                 const uint32_t idesc0 = mma_idesc_bs(MxTraits<ELEM>::kFmt, 256, t.bn, 0, 0);
-                for (int b = 0; b < 2 * steps; ++b) {
-                    if (!is_full) {
-                        ok = pair_wait<CL>(&full[stage], phase, abort_flag, args.status, abort_local, rank);
-                        ok = __all_sync(0xffffffffu, ok);
-                        if (!ok) break;
-                    }
-                    if (b % 2 == 0) smem_acquire_cluster();  // the scales, written by ordinary stores
+                const bool wide = t.bn > 128;
+                for (int st = 0; st < steps; ++st) {
+                    ok = pair_wait<CL>(&full[pair], phase, abort_flag, args.status, abort_local, rank);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    smem_acquire_cluster();  // the scales, written by ordinary stores
                     tc_fence_after();
-                    const uint32_t next = stage + 1 == Cfg::STAGES ? 0u : stage + 1;
-                    const uint32_t next_phase = next == 0 ? phase ^ 1u : phase;
-                    const bool next_full = mbar_test_wait(smem_u32(&full[next]), next_phase);
-                    const uint32_t at = stage * (Cfg::STAGE_BYTES >> 4);  // addresses are in 16-byte units, below 2^14
+                    const uint32_t at = pair * (2 * Cfg::STAGE_BYTES >> 4);  // addresses are in 16-byte units, below 2^14
                     const uint64_t ad = a_desc0 + at, bd = b_desc0 + at;
                     // E4M3: the second half of the box in odd pairs
-                    const uint64_t sd = sf_desc0 + (stage >> 1) * (Cfg::SF_BYTES >> 4) +
-                                        (ELEM == kMxE4M3 ? static_cast<uint32_t>(b >> 1 & 1) * 2 * 32u : 0u);
+                    const uint64_t sd = sf_desc0 + pair * (Cfg::SF_BYTES >> 4) +
+                                        (ELEM == kMxE4M3 ? static_cast<uint32_t>(st & 1) * 2 * 32u : 0u);
                     // (the slot's last MMAs, two pairs back, are done: the scale warp waited for them)
                     const uint32_t sfa = tmem_base + 2 * Cfg::ACC_STRIDE + slot * Cfg::SF_COLS;
                     const uint32_t sfb = sfa + 2 * 4 * Cfg::CHUNKS;
-                    const bool both = b + 1 < blocks;
+                    const bool both = 2 * st + 1 < blocks;
                     if (elect_one()) {
-                        if (b % 2 == 0) {
 #pragma unroll
-                            for (int c = 0; c < 2 * Cfg::CHUNKS; ++c) {
-                                if (c >= Cfg::CHUNKS && !both) break;
-                                tc_cp_32x128b_x4_pair(sfa + 4 * c, sd + c * 32u);
-                                tc_cp_32x128b_x4_pair(sfb + 8 * c, sd + (Cfg::SFA_BYTES >> 4) + c * 32u);
-                                if (t.bn > 128)
-                                    tc_cp_32x128b_x4_pair(sfb + 8 * c + 4, sd + ((Cfg::SFA_BYTES + 2048) >> 4) + c * 32u);
-                            }
+                        for (int c = 0; c < 2 * Cfg::CHUNKS; ++c) {
+                            if (c >= Cfg::CHUNKS && !both) break;
+                            tc_cp_32x128b_x4_pair(sfa + 4 * c, sd + c * 32u);
+                            tc_cp_32x128b_x4_pair(sfb + 8 * c, sd + (Cfg::SFA_BYTES >> 4) + c * 32u);
+                            if (wide) tc_cp_32x128b_x4_pair(sfb + 8 * c + 4, sd + ((Cfg::SFA_BYTES + 2048) >> 4) + c * 32u);
                         }
-                        if (b < blocks) {
-                            const uint32_t c0 = static_cast<uint32_t>(b & 1) * Cfg::CHUNKS;
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) {
-                                const uint32_t chunk = c0 + (Cfg::CHUNKS == 1 ? 0 : ks >> 1);
-                                const uint32_t sf_id = Cfg::CHUNKS == 1 ? ks : (ks & 1) * 2;
-                                tc_mma_bs_pair<MxTraits<ELEM>::kKind>(d_tmem, ad + ks * 2, bd + ks * 2,
-                                                                       idesc0 | (sf_id << 4) | (sf_id << 29),
-                                                                       sfa + 4 * chunk, sfb + 8 * chunk,
-                                                                       (b | ks) != 0 ? 1u : 0u);
+                        for (int h = 0; h < 2; ++h) {
+                            if (h == 0 || both) {
+#pragma unroll
+                                for (int ks = 0; ks < 4; ++ks) {
+                                    const uint32_t chunk = Cfg::CHUNKS * h + (Cfg::CHUNKS == 1 ? 0 : ks >> 1);
+                                    const uint32_t sf_id = Cfg::CHUNKS == 1 ? ks : (ks & 1) * 2;
+                                    tc_mma_bs_pair<MxTraits<ELEM>::kKind>(
+                                        d_tmem, ad + h * (Cfg::STAGE_BYTES >> 4) + ks * 2,
+                                        bd + h * (Cfg::STAGE_BYTES >> 4) + ks * 2, idesc0 | (sf_id << 4) | (sf_id << 29),
+                                        sfa + 4 * chunk, sfb + 8 * chunk, (st | h | ks) != 0 ? 1u : 0u);
+                                }
                             }
+                            tc_commit_pair(&empty[2 * pair + h], 0x3);
                         }
-                        tc_commit_pair(&empty[stage], 0x3);
-                        if (b + 1 == 2 * steps) tc_commit_pair(&tfull[acc], 0x3);
+                        if (st + 1 == steps) tc_commit_pair(&tfull[acc], 0x3);
                     }
                     issued = true;
-                    is_full = __all_sync(0xffffffffu, next_full);
-                    slot ^= static_cast<uint32_t>(b) & 1u;
-                    stage = next;
-                    phase = next_phase;
+                    slot ^= 1u;
+                    if (++pair == Cfg::PAIRS) {
+                        pair = 0;
+                        phase ^= 1u;
+                    }
                 }
             }
             if (*abort_flag && issued) {
@@ -338,7 +336,7 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) {
                     smem_release_cluster();
-                    mbar_arrive_remote_relaxed(full0_leader + 16u * pair);
+                    mbar_arrive_remote_relaxed(full0_leader + 8u * pair);
                 }
                 if (++pair == Cfg::PAIRS) {
                     pair = 0;
