@@ -36,7 +36,7 @@ class MoeLayer:
     def choose(self, x):
         """The router's logits, each token's experts and their weights (tokens x top)."""
         T, dev = x.shape[0], x.device
-        logits = x.float() @ self.router.t()
+        logits = x.float().contiguous() @ self.router.t()
         expert = torch.empty(T, self.top, dtype=torch.int32, device=dev)
         weight = torch.empty(T, self.top, device=dev)
         g.gemm_route(T, self.experts, self.top, g.F32, logits, self.experts, expert, weight)
@@ -61,7 +61,8 @@ class MoeLayer:
     def gather(self, x, source):
         """The tokens' rows in the experts' order."""
         rows = torch.empty(source.numel(), x.shape[1], dtype=x.dtype, device=x.device)
-        g.gemm_rows_gather(rows.shape[0], x.shape[1], x.shape[0], self.top, g.BF16, x, x.stride(0), source, None, rows,
+        x, pitch = pitched(x)
+        g.gemm_rows_gather(rows.shape[0], x.shape[1], x.shape[0], self.top, g.BF16, x, pitch, source, None, rows,
                            rows.shape[1])
         return rows
 
@@ -148,8 +149,9 @@ class MoeLayer:
         out = self.combine(y, row, weight)
 
         dr, dw = torch.empty_like(y), torch.empty_like(weight) if router else None
-        g.gemm_rows_combine_grad(T, self.top, self.d, rows, g.BF16, dy, dy.stride(0), g.BF16, y, self.d, row, weight, dr,
-                                 self.d, dw)
+        dy, pitch = pitched(dy if dy.dtype == torch.bfloat16 else dy.float())
+        g.gemm_rows_combine_grad(T, self.top, self.d, rows, g.BF16 if dy.dtype == torch.bfloat16 else g.F32, dy, pitch,
+                                 g.BF16, y, self.d, row, weight, dr, self.d, dw)
         dw2 = torch.empty(E, self.d, self.f, device=x.device)
         g.gemm_grouped_wgrad(E, rows, self.d, self.f, g.BF16, offsets, dr, self.d, 1, h, self.f, 1, dw2,
                              self.d * self.f, self.f, g.F32, 1.0, 0.0)
@@ -193,6 +195,12 @@ class MoeLayer:
         return (out, leaf) if requires_grad else out
 
 
+def pitched(x):
+    """x with its rows contiguous (a copy where they are not, or overlap), and their pitch."""
+    x = x if x.stride(1) == 1 and x.stride(0) >= x.shape[1] else x.contiguous()
+    return x, max(x.stride(0), x.shape[1])
+
+
 def quantize_rows(x):
     q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
     scale = torch.empty(x.shape[0], device=x.device)
@@ -205,7 +213,8 @@ def quantize_mx_rows(x, source=None, top=1):
     rows, k = x.shape[0] if source is None else source.numel(), x.shape[1]
     codes = torch.empty(rows, (k // 2 + 15) // 16 * 16, dtype=torch.uint8, device=x.device)
     scale = torch.empty(rows, (k // 32 + 15) // 16 * 16, dtype=torch.uint8, device=x.device)
-    g.gemm_mx_quantize(rows, k, g.MX_E2M1, g.BF16, x, x.stride(0), codes, 2 * codes.shape[1], scale, scale.shape[1], source,
+    x, pitch = pitched(x)
+    g.gemm_mx_quantize(rows, k, g.MX_E2M1, g.BF16, x, pitch, codes, 2 * codes.shape[1], scale, scale.shape[1], source,
                        top, x.shape[0])
     return codes, scale
 

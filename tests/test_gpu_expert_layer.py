@@ -103,6 +103,34 @@ def test_the_example_in_4_bits_and_its_router_gradient(moe):
     assert moe.g.gemm_device_status() == 0
 
 
+@pytest.mark.parametrize("T", [1, 45])
+def test_rows_and_gradients_as_callers_have_them(moe, T):
+    """Inputs with a pitch, transposed, broadcast, a lone row of an odd stride, and an fp32 output gradient: what their
+    contiguous bf16 copies give (fp32 values that bf16 holds give the same products)."""
+    D = 256
+    layer = moe.MoeLayer(D, 192, 16, 4)
+    layer.quantize_mx()
+    x, dy = tokens_of(T, D, 7), tokens_of(T, D, 8)
+
+    def run(x, dy):
+        out, grads = layer.train_step(x, dy)
+        return [layer.forward(x), layer.forward_mx(x), out, *grads.values()]
+
+    want = run(x, dy)
+    wide = torch.full((T, D + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:8 + D] = x
+    forms = [(wide[:, 8:8 + D], dy.float()), (x.t().contiguous().t(), dy.t().contiguous().t()),
+             (x, dy.double()), (x.repeat(1, 2)[:, :D], dy.float().repeat(1, 2)[:, D:])]
+    if T == 1:
+        forms.append((x.as_strided((1, D), (1, 1)), dy.as_strided((1, D), (3, 1))))
+    for xi, di in forms:
+        assert all(torch.equal(a, b) for a, b in zip(run(xi, di), want))
+    same = dy[:1].expand(T, D)
+    assert all(torch.equal(a, b) for a, b in zip(run(x[:1].expand(T, D), same),
+                                                 run(x[:1].repeat(T, 1), same.contiguous())))
+    assert moe.g.gemm_device_status() == 0
+
+
 @pytest.mark.parametrize("T", [3, 700])
 def test_graphs_and_streams_give_the_same_bits(moe, T):
     """Whole layers captured and replayed on new tokens, two graphs one after the other, beside a copy that no kernel
