@@ -53,10 +53,12 @@ class MoeLayer:
         return offsets, row, source
 
     def route(self, x):
-        """Offsets of the experts' rows, the token of each row and its weight, rows sorted by expert."""
+        """Offsets of the experts' rows, the token of each row and its weight, rows sorted by expert (behind the last:
+        token 0, weight 0)."""
         _, expert, weight = self.choose(x)
         offsets, _, source = self.sort(expert)
-        return offsets, source.long() // self.top, weight.flatten()[source.long()]
+        pair = source.long().clamp(min=0)
+        return offsets, pair // self.top, weight.flatten()[pair] * (source >= 0)
 
     def gather(self, x, source):
         """The tokens' rows in the experts' order."""
@@ -72,6 +74,11 @@ class MoeLayer:
         g.gemm_rows_combine(row.shape[0], self.top, y.shape[1], y.shape[0], g.BF16, y, y.shape[1], row, weight, 0.0, g.F32,
                             out, out.shape[1])
         return out
+
+    @staticmethod
+    def marked(out, expert):
+        """out, NaN for tokens whose logits are all NaN: they have no expert, and a sum of none would hide it."""
+        return out.masked_fill(expert[:, :1] < 0, float("nan"))
 
     def _up(self, rows, offsets, epilogue):
         out = torch.empty(rows.shape[0], self.f, dtype=torch.bfloat16, device=rows.device)
@@ -90,7 +97,7 @@ class MoeLayer:
         _, expert, weight = self.choose(x)
         offsets, row, source = self.sort(expert)
         y = self._down(self._up(self.gather(x, source), offsets, g.EPI_BIAS_SILU), offsets)
-        return self.combine(y, row, weight)
+        return self.marked(self.combine(y, row, weight), expert)
 
     def quantize(self):
         """8-bit weights, a scale for each output channel."""
@@ -99,17 +106,18 @@ class MoeLayer:
 
     def forward_i8(self, x):
         """Serving with 8-bit weights and activations: the rows are quantised before each product."""
-        offsets, token, weight = self.route(x)
-        rows = token.shape[0]
+        _, expert, weight = self.choose(x)
+        offsets, row, source = self.sort(expert)
+        rows, token = source.numel(), source.long().clamp(min=0) // self.top
         qx, sx = quantize_rows(x)
         h = torch.empty(rows, self.f, dtype=torch.bfloat16, device=x.device)
         g.gemm_i8_grouped(self.experts, rows, self.f, self.d, offsets, qx[token], self.d, sx[token], self.q1,
                           self.f * self.d, self.d, self.s1, h, self.f, g.BF16, 1.0, 0.0, self.b1, g.EPI_BIAS_SILU)
         qh, sh = quantize_rows(h)
         y = torch.empty(rows, self.d, dtype=torch.bfloat16, device=x.device)
-        g.gemm_i8_grouped(self.experts, rows, self.d, self.f, offsets, qh, self.f, sh * weight, self.q2,
+        g.gemm_i8_grouped(self.experts, rows, self.d, self.f, offsets, qh, self.f, sh, self.q2,
                           self.d * self.f, self.f, self.s2, y, self.d, g.BF16, 1.0, 0.0, None, g.EPI_NONE)
-        return torch.zeros_like(x, dtype=torch.float32).index_add_(0, token, y.float())
+        return self.marked(self.combine(y, row, weight), expert)
 
     def quantize_mx(self):
         """4-bit weights, a power of two for each 32 inputs."""
@@ -127,7 +135,7 @@ class MoeLayer:
                          g.EPI_BIAS_SILU, h)
         y = torch.empty(rows, self.d, dtype=torch.bfloat16, device=x.device)
         self._mx_product(quantize_mx_rows(h), (self.m2, self.ms2), offsets, self.f, None, g.EPI_NONE, y)
-        return self.combine(y, row, weight)
+        return self.marked(self.combine(y, row, weight), expert)
 
     def _mx_product(self, x, w, offsets, k, bias, epilogue, out):
         (qx, sx), (qw, sw), n = x, w, out.shape[1]
@@ -146,7 +154,7 @@ class MoeLayer:
         sig = torch.sigmoid(z.float())
         h = (z.float() * sig).to(torch.bfloat16)
         y = self._down(h, offsets)
-        out = self.combine(y, row, weight)
+        out = self.marked(self.combine(y, row, weight), expert)
 
         dr, dw = torch.empty_like(y), torch.empty_like(weight) if router else None
         dy, pitch = pitched(dy if dy.dtype == torch.bfloat16 else dy.float())
@@ -177,21 +185,22 @@ class MoeLayer:
     def reference(self, x, requires_grad=False, router=False):
         """The same layer expert by expert in plain fp32 operations; with gradients, its leaves as well (with `router`,
         the router's weights among them)."""
-        offsets, token, weight = self.route(x)
+        _, expert, weight = self.choose(x)
+        offsets, _, source = self.sort(expert)
+        pair = source.long()[:int(offsets[-1])]
+        token, weight = pair // self.top, weight.flatten()[pair]
         leaf = [t.float().requires_grad_(requires_grad) for t in (x, self.w1, self.b1, self.w2)]
         if router:
             leaf.append(self.router.clone().requires_grad_(requires_grad))
-            _, expert, _ = self.choose(x)
-            _, _, source = self.sort(expert)
-            chosen = torch.softmax((leaf[0] @ leaf[4].t()).gather(1, expert.long()), 1)
-            weight = chosen.flatten()[source.long()]
+            chosen = torch.softmax((leaf[0] @ leaf[4].t()).gather(1, expert.long().clamp(min=0)), 1)
+            weight = chosen.flatten()[pair]
         x, w1, b1, w2 = leaf[:4]
         ends, parts = offsets.tolist(), []
         for e in range(self.experts):
             r = slice(ends[e], ends[e + 1])
             h = torch.nn.functional.silu(x[token[r]] @ w1[e].t() + b1[e])
             parts.append(weight[r, None] * (h @ w2[e].t()))
-        out = torch.zeros_like(x).index_add(0, token, torch.cat(parts))
+        out = self.marked(torch.zeros_like(x).index_add(0, token, torch.cat(parts)), expert)
         return (out, leaf) if requires_grad else out
 
 

@@ -131,6 +131,35 @@ def test_rows_and_gradients_as_callers_have_them(moe, T):
     assert moe.g.gemm_device_status() == 0
 
 
+def test_tokens_of_nan(moe):
+    """A token with a NaN has NaN logits and no expert: its output is NaN on every path, the other tokens' outputs and
+    the weights' gradients are those without it (bounds of the example's tests; fp32 against fp32, four sums of 256
+    terms whose roundings reach 256 x 2^-24 = 1.5e-5 each).  Its place behind the last row is no token's."""
+    T, D = 50, 256
+    layer = moe.MoeLayer(D, 192, 16, 4)
+    layer.quantize()
+    layer.quantize_mx()
+    x, dy = tokens_of(T, D, 9), tokens_of(T, D, 10)
+    bad = torch.zeros(T, dtype=torch.bool, device="cuda")
+    bad[[0, 17, T - 1]] = True
+    x[bad, 5] = float("nan")
+    offsets, token, weight = layer.route(x)
+    assert int(offsets[-1]) == 47 * 4 and (weight[47 * 4:] == 0).all() and int(token.min()) >= 0
+    out, grads = layer.train_step(x, dy, router=False)
+    outs = [layer.forward(x), layer.forward_i8(x), layer.forward_mx(x), out]
+    keep, dkeep = x[~bad].contiguous(), dy[~bad].contiguous()
+    want, leaf = layer.reference(keep, requires_grad=True)
+    want.backward(dkeep.float())
+    for got, bound in zip(outs, (1.6e-2, 4e-2, 1 / 3, 1.6e-2)):
+        assert got[bad].isnan().all() and moe.relative(got[~bad], want) < bound
+    assert moe.relative(grads["x"][~bad], leaf[0].grad) < 1.6e-2
+    for name, t in zip(("w1", "b1", "w2"), leaf[1:]):
+        assert moe.relative(grads[name], t.grad) < 1.6e-2, name
+    full = layer.reference(x)
+    assert full[bad].isnan().all() and moe.relative(full[~bad], want) < 6.2e-5
+    assert moe.g.gemm_device_status() == 0
+
+
 @pytest.mark.parametrize("T", [3, 700])
 def test_graphs_and_streams_give_the_same_bits(moe, T):
     """Whole layers captured and replayed on new tokens, two graphs one after the other, beside a copy that no kernel
