@@ -7,11 +7,11 @@
 //     w = scale s, or scale s / (sum of the chosen s)
 //
 // A warp takes a token; lane l holds the experts l NPL .. l NPL + NPL - 1 in
-// registers, so that the lowest lane of a ballot is the lowest expert, and the
-// experts of a group lie in neighbouring lanes.  A warp's maximum is one redux.  The top-th largest of the lanes'
-// maxima bounds the chosen ones from below: what reaches it, rarely more than a few
-// values over `top`, is gathered one to a lane (in the experts' order), and each
-// further round costs a redux and a ballot, no search through a lane's registers.
+// registers, so that lanes are in the experts' order and the experts of a group lie
+// in neighbouring lanes.  A warp's maximum is one redux.  The top-th largest of the
+// lanes' maxima bounds the chosen ones from below: what reaches it, rarely more than a
+// few values over `top`, is gathered one to a lane (in the experts' order), and each
+// counts those before it.
 //
 // Which experts are chosen is decided as by 64-bit scores.  Without a bias (and
 // without sums over a group) the scores have the logits' order, and the logits
@@ -103,8 +103,8 @@ __device__ __forceinline__ void take_top2(F &t1, F &t2, F v) {
     t2 = t2 < low ? low : t2;
 }
 
-// Which groups stay, one bit each; lane g * per holds the worth of group g (-infinity: none), and the lanes beside it.
-// `close`: whether the last that stays and the first that does not are within margin (1 + their size).
+// Whether this lane's group stays; lane g * per holds the worth of group g (-infinity: none), and the lanes beside it.
+// Returns whether the lane has a group.
 template <typename F>
 __device__ __forceinline__ bool group_stays(F worth, int per, const RouteArgs &a, bool &kept) {
     const int lane = threadIdx.x & 31, g = lane / per;
@@ -141,9 +141,9 @@ struct Candidate {
 };
 
 // The chosen experts of a token by fp32 values: lane s gets the s-th (or -1).  sel: the lane's selection scores,
-// -infinity where there is none, no NaN; cand: 32 slots of the warp; margin: too_close's.  `exactly`(expert) is a selection
-// score in 64 bits (warp-collective; -1: -infinity): it decides among the candidates where fp32 ones cannot.  Returns whether even that is not enough
-// (groups too close, or more candidates than lanes).
+// -infinity where there is none, no NaN; cand: 32 slots of the warp; margin: too_close's.  `exactly`(expert) is a
+// selection score in 64 bits (warp-collective; -1: -infinity): it decides among the candidates where fp32 ones cannot.
+// Returns whether even that is not enough (groups too close, or more candidates than lanes).
 template <int NPL, typename Exactly>
 __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs &a, float *stage, Candidate *cand,
                                        float margin, int &expert, Exactly exactly) {
@@ -232,63 +232,52 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
     }
     const int rounds = margin > 0.0f ? a.top + 1 : a.top;  // one more than is chosen, to compare with
     float best = val[0], least = -INFINITY;
-    if (NPL > 1) {
 #pragma unroll
-        for (int j = 1; j < NPL; ++j) best = fmaxf(best, val[j]);
-        float rest = best;
-        for (int s = 0; s < rounds; ++s) {
-            least = warp_max(rest);
-            rest = rest == least ? -INFINITY : rest;
-        }
-        // and what may in truth reach it
-        if (margin > 0.0f && fabsf(least) < INFINITY) least -= margin + 0x1p-22f * fabsf(least);
+    for (int j = 1; j < NPL; ++j) best = fmaxf(best, val[j]);
+    float rest = best;
+    for (int s = 0; s < rounds; ++s) {
+        least = warp_max(rest);
+        rest = rest == least ? -INFINITY : rest;
     }
+    // and what may in truth reach it
+    if (margin > 0.0f && fabsf(least) < INFINITY) least -= margin + 0x1p-22f * fabsf(least);
     least = fmaxf(least, -FLT_MAX);
     int n = 0;
 #pragma unroll
     for (int j = 0; j < NPL; ++j) n += val[j] >= least;
-    float mine = -INFINITY;
-    int my_expert = -1, owner_of = -1;
     const int total = __reduce_add_sync(kAll, n);
     expert = -1;
-    float value = 0.0f;  // of the lane's choice
-    int found = 0;
     if (total <= 32) {
-        if (NPL > 1) {
-            int at = lanes_before(n);
+        int at = lanes_before(n);
 #pragma unroll
-            for (int j = 0; j < NPL; ++j)
-                if (val[j] >= least) cand[at++] = {val[j], lane * NPL + j};
-            __syncwarp();
-            if (lane < total) {
-                mine = cand[lane].value;
-                my_expert = cand[lane].expert;
+        for (int j = 0; j < NPL; ++j)
+            if (val[j] >= least) cand[at++] = {val[j], lane * NPL + j};
+        __syncwarp();
+        const bool candidate = lane < total;
+        const float mine = candidate ? cand[lane].value : -INFINITY;
+        const int my_expert = candidate ? cand[lane].expert : -1;
+        __syncwarp();
+        // each candidate's rank; the candidates are in the experts' order
+        int rank = 0;
+        for (int i = 0; i < total; i += 4) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float o = __shfl_sync(kAll, mine, i + k);
+                rank += o > mine || (o == mine && i + k < lane);
             }
-            __syncwarp();
-        } else {
-            mine = val[0];
-            my_expert = lane;
         }
-        const bool candidate = mine > -INFINITY;
-        for (; found < rounds; ++found) {
-            const float top = warp_max(mine);
-            if (top == -INFINITY) break;
-            const int owner = __ffs(__ballot_sync(kAll, mine == top)) - 1;
-            if (lane == found) {
-                owner_of = owner;
-                value = top;
-            }
-            if (lane == owner) mine = -INFINITY;
-        }
-        expert = __shfl_sync(kAll, my_expert, owner_of & 31);
-        expert = owner_of >= 0 && lane < a.top ? expert : -1;
+        if (candidate) cand[rank] = {mine, my_expert};
+        __syncwarp();
+        const int found = min(rounds, total);
+        const float value = lane < found ? cand[lane].value : 0.0f;
+        expert = lane < min(found, a.top) ? cand[lane].expert : -1;
+        __syncwarp();
         if (margin > 0.0f) {
             const float next = __shfl_down_sync(kAll, value, 1);
             if (__any_sync(kAll, lane + 1 < found && too_close(value, next, margin))) {
-                // each candidate's rank by its 64-bit score; the candidates are in the experts' order
-                const double v = exactly(candidate ? my_expert : -1);
-                int rank = 0;
-                for (int i = 0; i < (NPL > 1 ? total : 32); ++i) {
+                const double v = exactly(my_expert);
+                rank = 0;
+                for (int i = 0; i < total; ++i) {
                     const double o = __shfl_sync(kAll, v, i);
                     rank += o > v || (o == v && i < lane);
                 }
@@ -301,7 +290,7 @@ __device__ __forceinline__ bool choose(const float (&sel)[NPL], const RouteArgs 
     } else {
         // many equal maxima, or more experts to choose than lanes can bound: through the registers
         float last = 0.0f;
-        for (; found < rounds; ++found) {
+        for (int found = 0; found < rounds; ++found) {
             const float top = warp_max(best);
             if (top == -INFINITY) break;
             if (margin > 0.0f && found > 0 && too_close(last, top, margin)) return true;
