@@ -21,11 +21,11 @@
 // with 256 experts; each of a token's in a lane of its own, since a 64-bit
 // exponential takes a lane some microseconds).
 //
-// Bound by instructions (GB300: about 970 per token of a warp, 16384 tokens to 8 of 256
-// experts in 8 groups with a bias 20.6 us, without both 10.2; the logits' bytes would
-// take 2.5): with a search through a lane's registers in each round 43 us.  The
-// gradient over 16384 x 128 softmax scores 6.3 us (bytes: 2.6), with the chosen parts
-// passed around the warp slot by slot 8.4.  One token: 5.7 us, the call's host side.
+// Bound by instructions (GB300: 900 per token of a warp, 16384 tokens to 8 of 256
+// experts in 8 groups with a bias 18.4 us, without both 9.0; the logits' bytes would
+// take 2.5): with a maximum of the warp per chosen expert 19.6 and 10.2, with a search
+// through a lane's registers in each round 43.  The gradient over 16384 x 128 softmax
+// scores 6.7 us (bytes: 2.6).  One token: 5.6 us, the call's host side.
 #include <cfloat>
 
 #include "epilogue.cuh"
@@ -492,6 +492,23 @@ __global__ void __launch_bounds__(32 * kRouteWarps, NPL <= 8 ? 8 : 1) route_kern
 //     renormalised   dx_j += d_j w_j (g_j - sum_i g_i w_i)
 //     sigmoid        dx_j += g_j s_j (1 - s_j)
 //     softmax        dx_j += g_j p_j, and every expert's dx_e -= p_e sum_i g_i p_i
+//
+// The order of experts does not matter here, so lanes take a row in pieces that
+// lie beside each other.
+// A row's elements over a warp: f(j, e) for this lane's j-th, expert e.  16-byte pieces (V) or single elements, each
+// neighbouring lanes' (16384 tokens of 512 13 us, with NPL consecutive ones to a lane 20).
+template <int PV, int NPL, typename F>
+__device__ __forceinline__ void spread(bool v, F f) {
+    const int lane = threadIdx.x & 31;
+    if (NPL >= PV && v) {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) f(j, (j / PV * 32 + lane) * PV + j % PV);
+    } else {
+#pragma unroll
+        for (int j = 0; j < NPL; ++j) f(j, j * 32 + lane);
+    }
+}
+
 template <int LT, int NPL>
 __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __grid_constant__ RouteGradArgs a) {
     begin_after();
@@ -501,23 +518,56 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     float *buf = rows[warp];
     const bool whole = a.score == kScoreSoftmax && !a.renorm;  // every logit has a gradient
-    for (long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp; t < a.T;
-         t += static_cast<long long>(gridDim.x) * kRouteWarps) {
+    const long long step = static_cast<long long>(gridDim.x) * kRouteWarps;
+    // Up to 256 experts the next token's arrays are on their way while a token is computed (65536 tokens of 256 29 us
+    // instead of 32); with more, their registers cost more than that (16384 of 512 13.0, 14.1 with).
+    constexpr bool kAhead = NPL <= 8;
+    int next_expert = -1;
+    float next_g = 0.0f, next_x[NPL];
+    auto fetch = [&](long long t) {
+        if (t >= a.T) return;
+        next_expert = lane < a.top ? __ldg(a.expert + t * a.top + lane) : -1;
+        next_g = lane < a.top ? __ldg(a.dweight + t * a.top + lane) : 0.0f;
+        if (!whole) return;
         const T *row = static_cast<const T *>(a.logits) + t * a.ldl;
-        int expert = lane < a.top ? a.expert[t * a.top + lane] : -1;
-        const bool live = expert >= 0 && expert < a.E;
-        expert = live ? expert : -1;
-        const float g = live ? a.scale * a.dweight[t * a.top + lane] : 0.0f;
-        const float xs = live ? logit_value(Elem<LT>::load(row + expert)) : 0.0f;
-        float d[NPL], m = 0.0f, sum = 1.0f;
+        if (NPL >= PV && a.vec) {
+#pragma unroll
+            for (int v = 0; v < NPL / PV; ++v) {
+                const int e = (v * 32 + lane) * PV;
+                if (e < a.E) {
+                    Vec16<LT>::unpack(__ldg(reinterpret_cast<const uint4 *>(row + e)), &next_x[v * PV]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < PV; ++j) next_x[v * PV + j] = -INFINITY;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) next_x[j] = j * 32 + lane < a.E ? Elem<LT>::load(row + j * 32 + lane) : -INFINITY;
+        }
+    };
+    long long t = static_cast<long long>(blockIdx.x) * kRouteWarps + warp;
+    if (kAhead) fetch(t);
+    for (; t < a.T; t += step) {
+        if (!kAhead) fetch(t);
+        const bool live = next_expert >= 0 && next_expert < a.E;
+        const int expert = live ? next_expert : -1;
+        const float g = live ? a.scale * next_g : 0.0f;
+        float d[NPL], m = 0.0f, sum = 1.0f, xs = 0.0f;
         if (whole) {
             float x[NPL];
-            load_logits<LT, NPL>(row, a.E, a.vec, x);
+#pragma unroll
+            for (int j = 0; j < NPL; ++j) x[j] = logit_value(next_x[j]);
+            if (kAhead) fetch(t + step);
+            spread<PV, NPL>(a.vec, [&](int j, int e) { buf[e] = x[j]; });
+            __syncwarp();
+            if (live) xs = buf[expert];
+            __syncwarp();
             m = warp_max_of(x);
             sum = softmax_parts<NPL>(x, m, d);
-            const float inv = sum > 0.0f ? __fdiv_rn(1.0f, sum) : 0.0f;
-#pragma unroll
-            for (int j = 0; j < NPL; ++j) d[j] *= inv;
+        } else {
+            if (live) xs = logit_value(Elem<LT>::load(static_cast<const T *>(a.logits) + t * a.ldl + expert));
+            if (kAhead) fetch(t + step);
         }
         float total;
         const float v = chosen_score(xs, live, a.score, a.renorm, m, sum, total);
@@ -527,17 +577,12 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
                                                      : __fdiv_rn(xs > 0.0f ? expf(-xs) : 1.0f, 1.0f + expf(-fabsf(xs)));
         const float mean = a.renorm || whole ? warp_sum(g * w) : 0.0f;
         const float c = slope * w * (a.renorm ? g - mean : g);
-        if (whole) {
+        const float share = sum > 0.0f ? -__fdiv_rn(mean, sum) : 0.0f;
 #pragma unroll
-            for (int j = 0; j < NPL; ++j) d[j] = -d[j] * mean;
-        } else {
-#pragma unroll
-            for (int j = 0; j < NPL; ++j) d[j] = 0.0f;
-        }
+        for (int j = 0; j < NPL; ++j) d[j] = whole ? d[j] * share : 0.0f;
         // The chosen experts' parts, added in the row's place in shared memory: by their lanes at once, or one after
         // the other where an expert is in two slots.
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) buf[lane * NPL + j] = d[j];
+        spread<PV, NPL>(a.vec, [&](int j, int e) { buf[e] = d[j]; });
         __syncwarp();
         const unsigned same = __match_any_sync(kAll, expert);
         if (__any_sync(kAll, live && (same & (same - 1u)) != 0u)) {
@@ -549,18 +594,19 @@ __global__ void __launch_bounds__(32 * kRouteWarps) route_grad_kernel(const __gr
             buf[expert] += c;
         }
         __syncwarp();
-#pragma unroll
-        for (int j = 0; j < NPL; ++j) d[j] = buf[lane * NPL + j];
+        spread<PV, NPL>(a.vec_out, [&](int j, int e) { d[j] = buf[e]; });
+        __syncwarp();
         T *out = static_cast<T *>(a.dlogits) + t * a.ldd;
-        const int e0 = lane * NPL;
         if (NPL >= PV && a.vec_out) {
 #pragma unroll
-            for (int v4 = 0; v4 < NPL / PV; ++v4)
-                if (e0 + v4 * PV < a.E) reinterpret_cast<uint4 *>(out + e0)[v4] = Vec16<LT>::pack(&d[v4 * PV]);
+            for (int v4 = 0; v4 < NPL / PV; ++v4) {
+                const int e = (v4 * 32 + lane) * PV;
+                if (e < a.E) *reinterpret_cast<uint4 *>(out + e) = Vec16<LT>::pack(&d[v4 * PV]);
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < NPL; ++j)
-                if (e0 + j < a.E) out[e0 + j] = Elem<LT>::cvt(d[j]);
+                if (j * 32 + lane < a.E) out[j * 32 + lane] = Elem<LT>::cvt(d[j]);
         }
     }
 }
