@@ -13,6 +13,8 @@
 // 51 with two blocks per SM, which spill nothing, instead of three; with a warp to a
 // token and no barrier 55, and 4 % less only for 16384 tokens of 2048), 8192 tokens of
 // 4096, 8 slots, in 190, 6.0 TB/s.
+#include <algorithm>
+
 #include "epilogue.cuh"
 #include "kernel_args.h"
 #include "launch.cuh"
@@ -259,26 +261,29 @@ __device__ __forceinline__ void move_row(const void *x, void *y, int i, int piec
     }
 }
 
-// Y[r] = w[source[r]] X[source[r] / top]; places without a pair stay as they are.  A warp takes a row, and the next
-// row's pair while it does.
+// Y[r] = w[source[r]] X[source[r] / top]; places without a pair stay as they are.  A warp takes a part of a row of
+// `part` pieces (all of it where there are rows for every warp), and the next one's pair while it does.
 template <int DT, bool V>
 __global__ void __launch_bounds__(kMoveThreads) rows_gather_kernel(const __grid_constant__ RowsArgs a) {
     begin_after();
     constexpr int N = Piece<DT, V>::N;
     const int lane = threadIdx.x & 31, whole = a.D / N;
-    const long long step = static_cast<long long>(gridDim.x) * (kMoveThreads / 32);
-    long long r = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
-    int next = r < a.R ? __ldg(a.source + r) : -1;
-    for (; r < a.R; r += step) {
+    const long long step = static_cast<long long>(gridDim.x) * (kMoveThreads / 32), items = a.R * a.parts;
+    const auto row_of = [&](long long i) { return a.parts == 1 ? i : static_cast<unsigned>(i) / static_cast<unsigned>(a.parts); };
+    long long i = static_cast<long long>(blockIdx.x) * (kMoveThreads / 32) + (threadIdx.x >> 5);
+    int next = i < items ? __ldg(a.source + row_of(i)) : -1;
+    for (; i < items; i += step) {
         const int p = next;
-        next = r + step < a.R ? __ldg(a.source + r + step) : -1;
+        next = i + step < items ? __ldg(a.source + row_of(i + step)) : -1;
         if (static_cast<unsigned>(p) >= static_cast<unsigned>(a.T) * static_cast<unsigned>(a.top)) continue;
         const bool scaled = a.weight != nullptr;
         const float w = scaled ? __ldg(a.weight + p) : 1.0f;
+        const long long r = row_of(i);
+        const int k = static_cast<int>(i - r * a.parts);
         const void *x = row_at<DT>(a.X, p / a.top, a.ldx);
         void *y = row_at<DT>(a.Y, r, a.ldy);
-        move_row<DT, V>(x, y, lane, whole, scaled, w);
-        if (V) move_row<DT, false>(x, y, whole * N + lane, a.D, scaled, w);
+        move_row<DT, V>(x, y, k * a.part + lane, k + 1 < a.parts ? (k + 1) * a.part : whole, scaled, w);
+        if (V && k + 1 == a.parts) move_row<DT, false>(x, y, whole * N + lane, a.D, scaled, w);
     }
 }
 
@@ -544,8 +549,17 @@ cudaError_t launch_route_rows(const RouteRowsArgs &in, cudaStream_t s) {
     return launch_after(route_rows_kernel, dim3(chunks), 32 * warps, bytes, s, a);
 }
 
-cudaError_t launch_rows_gather(int dtype, const RowsArgs &a, bool vec, int sms, cudaStream_t s) {
-    const long long want = (a.R + kMoveThreads / 32 - 1) / (kMoveThreads / 32), most = 8ll * sms;
+// Few rows are split into parts, whole rounds of a warp, up to a warp for every part that the SMs hold: 8 rows of 6644
+// bf16 in 4.7 us, 864 of 6931 fp32 with an odd pitch in 8.5; with a warp to a row 8.9 and 18.5.
+cudaError_t launch_rows_gather(int dtype, const RowsArgs &in, bool vec, int sms, cudaStream_t s) {
+    RowsArgs a = in;
+    constexpr int kWarps = kMoveThreads / 32;
+    const long long most = 8ll * sms;  // blocks
+    const int pieces = vec ? a.D / (dtype == kDtF32 ? 4 : 8) : a.D, rounds = (pieces + 31) / 32;
+    const long long parts = std::min<long long>(rounds, most * kWarps / a.R);
+    a.part = parts > 1 ? static_cast<int>((rounds + parts - 1) / parts) * 32 : pieces;
+    a.parts = parts > 1 ? (pieces + a.part - 1) / a.part : 1;
+    const long long want = (a.R * a.parts + kWarps - 1) / kWarps;
     const unsigned grid = static_cast<unsigned>(want < most ? want : most);
     const auto launch = [&](auto whole, auto single) {
         return launch_after(vec ? whole : single, dim3(grid), kMoveThreads, 0, s, a);

@@ -237,6 +237,7 @@ struct RowsArgs {
     void *dY;
     long long lddy;
     float *dweight;
+    int parts, part;                // set by the launcher of a gather: parts of a row, pieces of one
 };
 
 // Rows to block-scaled numbers and back (gemm_mx_quantize.cu); pitches of codes and scales in bytes.

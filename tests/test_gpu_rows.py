@@ -229,3 +229,11 @@ def test_aligned_rows_that_end_inside_a_piece(cuda_lib, D, y_dtype, out, out_pad
     got = inside(g, R, D)
     np.testing.assert_array_equal(got[:n], xv[source[:n] // top])
     assert (got[n:] == CANARY).all()
+
+
+@pytest.mark.parametrize("T,top,D", [(1, 1, 70001), (2, 4, 6644), (3, 1, 31), (216, 4, 6931), (1, 3, 100008), (700, 2, 1000)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("pad,shift", [(0, 0), (8, 0), (3, 1)])
+def test_gather_of_few_long_rows(cuda_lib, T, top, D, dtype, pad, shift):
+    """Rows that several warps share: every element, the ends of the parts and of the rows, nothing beside them."""
+    test_gather(cuda_lib, T, top, D, dtype, pad, shift)
