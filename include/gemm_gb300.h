@@ -829,7 +829,8 @@ gemm_status_t gemm_mx_grouped(int64_t G, int64_t M, int64_t N, int64_t K, gemm_m
  * gemm_route_grad -- dlogits (T x E, pitch ldd, l_dtype; every element written) for
  * the weights' gradient dweight, the choice held fixed.  Takes the logits, score,
  * renormalise and scale of the forward call and its `expert`; slots whose expert is
- * outside 0 .. E-1 are left out.  The bias has no gradient.
+ * outside 0 .. E-1 are left out.  The bias has no gradient.  dlogits and logits must not
+ * overlap.
  */
 #define GEMM_ROUTE_MAX_TOP 32
 #define GEMM_ROUTE_MAX_GROUPS 32
