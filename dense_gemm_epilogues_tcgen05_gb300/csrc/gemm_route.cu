@@ -22,9 +22,9 @@
 // exponential takes a lane some microseconds).
 //
 // Bound by instructions (GB300: 900 per token of a warp, 16384 tokens to 8 of 256
-// experts in 8 groups with a bias 18.4 us, without both 9.0; the logits' bytes would
-// take 2.5): with a maximum of the warp per chosen expert 19.6 and 10.2, with a search
-// through a lane's registers in each round 43.  The gradient over 16384 x 128 softmax
+// experts in 8 groups with a bias 18.4 to 19.2 us, without both 9.0; the logits' bytes
+// would take 2.5): with a maximum of the warp per chosen expert 0.4 to 1.2 us more, with a
+// search through a lane's registers in each round 43.  The gradient over 16384 x 128 softmax
 // scores 6.7 us (bytes: 2.6).  One token: 5.6 us, the call's host side.
 #include <cfloat>
 
