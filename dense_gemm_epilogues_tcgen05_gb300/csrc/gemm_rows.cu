@@ -36,7 +36,7 @@ constexpr int kCountThreads = 256;
 
 __global__ void __launch_bounds__(kCountThreads) route_count_kernel(const __grid_constant__ RouteRowsArgs a) {
     extern __shared__ int counts[];
-    begin_after();  // (the second kernel then begins to count its own chunks)
+    begin_after();
     for (int e = threadIdx.x; e < a.E; e += kCountThreads) counts[e] = 0;
     __syncthreads();
     const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.P);
@@ -64,10 +64,8 @@ __device__ __forceinline__ void warp_pairs(const RouteRowsArgs &a, int begin, in
 
 __global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant__ RouteRowsArgs a) {
     extern __shared__ int smem[];
+    begin_after();  // (for the pairs too: only who has waited is promised to see what earlier grids wrote)
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // Many blocks: the first kernel, which ran after all before it, has begun, so the pairs are there; what it writes
-    // is waited for below.
-    if (gridDim.x == 1) begin_after();
     int *first = smem;              // E + 1: pairs of the experts before
     int *start = first + a.E + 1;   // E: an expert's pairs in the chunks before
     int *own = start + a.E;         // warps x E: counts, then places
@@ -84,7 +82,6 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant_
     __syncthreads();
     // every expert's total, and what lies before this chunk (a warp takes an expert, its lanes the chunks)
     if (gridDim.x > 1) {
-        begin_after();  // for the first kernel's counts
         const int chunks = gridDim.x;
         constexpr int kPer = (kRowsChunks + 31) / 32, kAtOnce = 8;  // loads of a lane per expert, experts at once
         for (int e0 = warp; e0 < a.E; e0 += kAtOnce * warps) {
