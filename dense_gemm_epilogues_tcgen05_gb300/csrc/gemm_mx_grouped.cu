@@ -26,6 +26,19 @@
 //   warps 4-11   epilogue: two per 32-lane quadrant of tensor memory, each half of
 //                the tile's columns (store_chunk_t).
 //
+// Sums: the tensor cores cut each instruction's sum off towards zero.  E4M3 products
+// span 36 bits, so that nearly every instruction loses about half a unit in the last
+// place: of the terms' absolute sum 3.9e-6 for 8192 of one sign, 2.0e-5 with elements
+// four powers of ten apart (fp32 sums 4e-7 and 7e-6).  So every 32 instructions, 1024 k,
+// the accumulator is added into fp32 registers, rounded to nearest: 1.9e-7 and 1.9e-6 at
+// any depth, for 4 % of the time of a product 8192 deep and 7 % of one 4096 deep (every
+// 16 instructions: 11 and 20 %).  E2M1 products are multiples of a quarter of their
+// scales' product, 144 of these at most, and sums below 2^24 of the smallest quarter are
+// exact: 8192 deep, whatever the signs, if the scales' products are within three powers
+// of two.  They stay in the accumulator, which beyond that loses at most a unit in the
+// last place per 64 k; with these joined too the prompt below took 233 us instead of 204
+// (every 16 instructions 300).
+//
 // Bound and measured (GB300).  Few rows: HBM (64 rows over 64 experts of 2048 x 4096
 // E2M1, 45 of them busy: 35 us, 5.9 TB/s, of which 5 % are the last of five rounds of
 // tiles).  Many rows: no unit alone.  A k-block of 128 bytes writes 29 KB into shared
@@ -64,6 +77,9 @@ struct MxgConfig {
     static constexpr int EPI_WARP0 = 4, EPI_WARPS = 8;
     static constexpr int THREADS = 32 * (EPI_WARP0 + EPI_WARPS);
     static constexpr int BAR_BYTES = 256, SMEM_MAX = 232448;
+    // pairs of blocks (8 instructions each) summed in tensor memory before the sum moves to registers
+    static constexpr bool JOINS = ELEM == kMxE4M3;
+    static constexpr int SEG = JOINS ? 4 : 1 << 30;
     static_assert(2 * ACC_STRIDE + SF_SLOTS * SF_COLS <= TMEM_COLS, "accumulators and scales fit");
     static_assert((STAGES + 2 * PAIRS + 5) * 8 + 8 <= BAR_BYTES, "barriers fit their slot");
     static_assert(B_BYTES % 1024 == 0 && STAGE_BYTES % 1024 == 0, "swizzle atoms stay aligned");
@@ -242,15 +258,20 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
             bool ok = true, issued = false;
             int local = 0;
             while (ok && steps > 0 && walk.next(t)) {
-                const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
-                ++local;
-                ok = pair_wait<CL>(&tempty[acc], acc_phase ^ 1u, abort_flag, args.status, abort_local, rank);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
                 const uint32_t idesc0 = mma_idesc_bs(MxTraits<ELEM>::kFmt, 256, t.bn, 0, 0);
                 const bool wide = t.bn > 128;
+                uint32_t acc = 0;
                 for (int st = 0; st < steps; ++st) {
+                    const bool opens = st % Cfg::SEG == 0, closes = st + 1 == steps || (st + 1) % Cfg::SEG == 0;
+                    if (opens) {
+                        acc = local & 1;
+                        const uint32_t acc_phase = (local >> 1) & 1;
+                        ++local;
+                        ok = pair_wait<CL>(&tempty[acc], acc_phase ^ 1u, abort_flag, args.status, abort_local, rank);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                    }
+                    const uint32_t d_tmem = tmem_base + acc * Cfg::ACC_STRIDE;
                     ok = pair_wait<CL>(&full[pair], phase, abort_flag, args.status, abort_local, rank);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
@@ -283,12 +304,12 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
                                     tc_mma_bs_pair<MxTraits<ELEM>::kKind>(
                                         d_tmem, ad + h * (Cfg::STAGE_BYTES >> 4) + ks * 2,
                                         bd + h * (Cfg::STAGE_BYTES >> 4) + ks * 2, idesc0 | (sf_id << 4) | (sf_id << 29),
-                                        sfa + 4 * chunk, sfb + 8 * chunk, (st | h | ks) != 0 ? 1u : 0u);
+                                        sfa + 4 * chunk, sfb + 8 * chunk, !opens || (h | ks) != 0 ? 1u : 0u);
                                 }
                             }
                             tc_commit_pair(&empty[2 * pair + h], 0x3);
                         }
-                        if (st + 1 == steps) tc_commit_pair(&tfull[acc], 0x3);
+                        if (closes) tc_commit_pair(&tfull[acc], 0x3);
                     }
                     issued = true;
                     slot ^= 1u;
@@ -360,6 +381,55 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
             const int chunks = (t.bn + 31) >> 5;  // (a last half chunk reads columns that are not stored)
             const int c_begin = half ? (chunks + 1) >> 1 : 0, nch = (half ? chunks : (chunks + 1) >> 1) - c_begin;
             const uint32_t t_quad = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + c_begin * 32;
+            auto store = [&](float (&v)[32], int row, int nrow) {
+                OutT *c0 = c + row * args.ldc;
+                chunk_values_t<OUT>(v, c0, args.F - f, nrow, rs != nullptr ? rs + row : nullptr, 1.0f, bias, e);
+                store_chunk_t<OUT>(v, c0, args.F - f, nrow, args.ldc);
+            };
+            if constexpr (Cfg::JOINS) {
+                if (steps > Cfg::SEG) {
+                    // halves of whole 16 columns: at most seven, 112 registers (of whole 32, 128: some spilled, 2 % slower)
+                    constexpr int kMost = (kMxgMost / 16 + 1) / 2;
+                    const int all = t.bn >> 4, first = half ? (all + 1) >> 1 : 0, n = (half ? all : (all + 1) >> 1) - first;
+                    const uint32_t t_first = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + first * 16;
+                    float sum[kMost][16];
+#pragma unroll
+                    for (int u = 0; u < kMost; ++u)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[u][j] = 0.0f;
+                    bool ok = true;
+                    for (int st = 0; st < steps; st += Cfg::SEG) {
+                        const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
+                        ++local;
+                        const bool got = pair_wait<CL>(&tfull[acc], acc_phase, abort_flag, args.status, abort_local, rank);
+                        ok = __all_sync(0xffffffffu, got);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int u = 0; u < kMost; ++u)
+                            if (u < n) {
+                                uint32_t raw[16];
+                                __syncwarp();
+                                tmem_ld_x16(t_first + acc * Cfg::ACC_STRIDE + u * 16, raw);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) sum[u][j] += __uint_as_float(raw[j]);
+                            }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
+                    }
+                    if (!ok) break;
+#pragma unroll
+                    for (int u = 0; u < kMost; u += 2)
+                        if (u < n) {
+                            float v[32];
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = u + j / 16 < kMost ? sum[(u + j / 16) % kMost][j % 16] : 0.0f;
+                            store(v, (first + u) * 16, min(t.nr - (first + u) * 16, (n - u) * 16));
+                        }
+                    continue;
+                }
+            }
             const uint32_t acc = local & 1, acc_phase = (local >> 1) & 1;
             if (steps > 0) {
                 ++local;
@@ -388,9 +458,7 @@ __global__ void __launch_bounds__(MxgConfig<ELEM>::THREADS, 1)
                     if (lane == 0) mbar_arrive_remote(tempty0_leader + 8u * acc);
                 }
                 const int row = (c_begin + ch) * 32;
-                OutT *c0 = c + row * args.ldc;
-                chunk_values_t<OUT>(v, c0, args.F - f, t.nr - row, rs != nullptr ? rs + row : nullptr, 1.0f, bias, e);
-                store_chunk_t<OUT>(v, c0, args.F - f, t.nr - row, args.ldc);
+                store(v, row, t.nr - row);
             }
             if (steps > 0 && nch == 0) {  // a tile of up to 32 columns has no second half
                 tc_fence_before();
