@@ -213,7 +213,8 @@ def pitched(x):
 def quantize_rows(x):
     q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
     scale = torch.empty(x.shape[0], device=x.device)
-    g.gemm_i8_quantize(x.shape[0], x.shape[1], g.BF16, x, x.shape[1], q, x.shape[1], scale)
+    x, pitch = pitched(x)
+    g.gemm_i8_quantize(x.shape[0], x.shape[1], g.BF16, x, pitch, q, x.shape[1], scale)
     return q, scale
 
 

@@ -1,0 +1,40 @@
+"""GPU tests of what callers of the mixture-of-experts example give it, beside its plain use."""
+import os
+import sys
+
+import pytest
+import torch
+
+from conftest import REPO
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def moe(cuda_lib):
+    sys.path.insert(0, os.path.join(REPO, "examples"))
+    import moe_layer
+    return moe_layer
+
+
+def tokens_of(T, D, seed):
+    return torch.randn(T, D, device="cuda", generator=torch.Generator(device="cuda").manual_seed(seed)).bfloat16()
+
+
+@pytest.mark.parametrize("T", [1, 45])
+def test_8_bit_serving_of_rows_as_callers_have_them(moe, T):
+    """Inputs with a pitch, transposed, broadcast, a lone row of an odd stride: what their contiguous copies give."""
+    D = 256
+    layer = moe.MoeLayer(D, 192, 16, 4)
+    layer.quantize()
+    x = tokens_of(T, D, 7)
+    want = layer.forward_i8(x)
+    wide = torch.full((T, D + 24), float("nan"), dtype=torch.bfloat16, device="cuda")
+    wide[:, 8:8 + D] = x
+    forms = [wide[:, 8:8 + D], x.t().contiguous().t(), x.repeat(1, 2)[:, D:]]
+    if T == 1:
+        forms.append(x.as_strided((1, D), (1, 1)))
+    for xi in forms:
+        assert torch.equal(layer.forward_i8(xi), want)
+    assert torch.equal(layer.forward_i8(x[:1].expand(T, D)), layer.forward_i8(x[:1].repeat(T, 1)))
+    assert moe.g.gemm_device_status() == 0
