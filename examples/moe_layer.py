@@ -76,9 +76,10 @@ class MoeLayer:
         return out
 
     @staticmethod
-    def marked(out, expert):
-        """out, NaN for tokens whose logits are all NaN: they have no expert, and a sum of none would hide it."""
-        return out.masked_fill(expert[:, :1] < 0, float("nan"))
+    def marked(out, logits):
+        """out, NaN for tokens whose softmax is NaN (a logit that is NaN or infinity, or all -infinity): the routing
+        leaves out experts without a score, and would hide it."""
+        return out.masked_fill(~torch.isfinite(logits.amax(1, keepdim=True)), float("nan"))
 
     def _up(self, rows, offsets, epilogue):
         out = torch.empty(rows.shape[0], self.f, dtype=torch.bfloat16, device=rows.device)
@@ -94,10 +95,10 @@ class MoeLayer:
 
     def forward(self, x):
         """Serving: rows gathered, two grouped products with bias and SiLU in the first, the weighted sum."""
-        _, expert, weight = self.choose(x)
+        logits, expert, weight = self.choose(x)
         offsets, row, source = self.sort(expert)
         y = self._down(self._up(self.gather(x, source), offsets, g.EPI_BIAS_SILU), offsets)
-        return self.marked(self.combine(y, row, weight), expert)
+        return self.marked(self.combine(y, row, weight), logits)
 
     def quantize(self):
         """8-bit weights, a scale for each output channel."""
@@ -106,7 +107,7 @@ class MoeLayer:
 
     def forward_i8(self, x):
         """Serving with 8-bit weights and activations: the rows are quantised before each product."""
-        _, expert, weight = self.choose(x)
+        logits, expert, weight = self.choose(x)
         offsets, row, source = self.sort(expert)
         rows, token = source.numel(), source.long().clamp(min=0) // self.top
         qx, sx = quantize_rows(x)
@@ -117,7 +118,7 @@ class MoeLayer:
         y = torch.empty(rows, self.d, dtype=torch.bfloat16, device=x.device)
         g.gemm_i8_grouped(self.experts, rows, self.d, self.f, offsets, qh, self.f, sh, self.q2,
                           self.d * self.f, self.f, self.s2, y, self.d, g.BF16, 1.0, 0.0, None, g.EPI_NONE)
-        return self.marked(self.combine(y, row, weight), expert)
+        return self.marked(self.combine(y, row, weight), logits)
 
     def quantize_mx(self):
         """4-bit weights, a power of two for each 32 inputs."""
@@ -127,7 +128,7 @@ class MoeLayer:
     def forward_mx(self, x):
         """Serving with 4-bit block-scaled weights and activations (D and F multiples of 32): tokens are quantised as
         they are gathered."""
-        _, expert, weight = self.choose(x)
+        logits, expert, weight = self.choose(x)
         offsets, row, source = self.sort(expert)
         rows = source.numel()
         h = torch.empty(rows, self.f, dtype=torch.bfloat16, device=x.device)
@@ -135,7 +136,7 @@ class MoeLayer:
                          g.EPI_BIAS_SILU, h)
         y = torch.empty(rows, self.d, dtype=torch.bfloat16, device=x.device)
         self._mx_product(quantize_mx_rows(h), (self.m2, self.ms2), offsets, self.f, None, g.EPI_NONE, y)
-        return self.marked(self.combine(y, row, weight), expert)
+        return self.marked(self.combine(y, row, weight), logits)
 
     def _mx_product(self, x, w, offsets, k, bias, epilogue, out):
         (qx, sx), (qw, sw), n = x, w, out.shape[1]
@@ -154,7 +155,7 @@ class MoeLayer:
         sig = torch.sigmoid(z.float())
         h = (z.float() * sig).to(torch.bfloat16)
         y = self._down(h, offsets)
-        out = self.marked(self.combine(y, row, weight), expert)
+        out = self.marked(self.combine(y, row, weight), logits)
 
         dr, dw = torch.empty_like(y), torch.empty_like(weight) if router else None
         dy, pitch = pitched(dy if dy.dtype == torch.bfloat16 else dy.float())
@@ -185,7 +186,7 @@ class MoeLayer:
     def reference(self, x, requires_grad=False, router=False):
         """The same layer expert by expert in plain fp32 operations; with gradients, its leaves as well (with `router`,
         the router's weights among them)."""
-        _, expert, weight = self.choose(x)
+        logits, expert, weight = self.choose(x)
         offsets, _, source = self.sort(expert)
         pair = source.long()[:int(offsets[-1])]
         token, weight = pair // self.top, weight.flatten()[pair]
@@ -200,7 +201,7 @@ class MoeLayer:
             r = slice(ends[e], ends[e + 1])
             h = torch.nn.functional.silu(x[token[r]] @ w1[e].t() + b1[e])
             parts.append(weight[r, None] * (h @ w2[e].t()))
-        out = self.marked(torch.zeros_like(x).index_add(0, token, torch.cat(parts)), expert)
+        out = self.marked(torch.zeros_like(x).index_add(0, token, torch.cat(parts)), logits)
         return (out, leaf) if requires_grad else out
 
 

@@ -38,3 +38,29 @@ def test_8_bit_serving_of_rows_as_callers_have_them(moe, T):
         assert torch.equal(layer.forward_i8(xi), want)
     assert torch.equal(layer.forward_i8(x[:1].expand(T, D)), layer.forward_i8(x[:1].repeat(T, 1)))
     assert moe.g.gemm_device_status() == 0
+
+
+@pytest.mark.parametrize("what", ["router", "token"])
+def test_softmax_scores_of_nan_are_not_hidden(moe, what):
+    """A router with a NaN in one expert's weights gives every token NaN scores, a token with an infinity its own: NaN
+    in their outputs on every path, and the other tokens' outputs those without it."""
+    T, D = 40, 256
+    layer = moe.MoeLayer(D, 192, 16, 4)
+    layer.quantize()
+    layer.quantize_mx()
+    x, dy = tokens_of(T, D, 11), tokens_of(T, D, 12)
+
+    def run():
+        return [layer.forward(x), layer.forward_i8(x), layer.forward_mx(x), layer.train_step(x, dy)[0], layer.reference(x)]
+
+    want = run()
+    bad = torch.ones(T, dtype=torch.bool, device="cuda")
+    if what == "router":
+        layer.router[3, 5] = float("nan")
+    else:
+        bad[4:] = False
+        x[:4, 7] = float("inf")
+    for got, w in zip(run(), want):
+        assert got[bad].isnan().all()
+        assert moe.relative(got[~bad], w[~bad]) < 1e-3 if what == "token" else True
+    assert moe.g.gemm_device_status() == 0
