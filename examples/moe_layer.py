@@ -37,6 +37,10 @@ class MoeLayer:
         """The router's logits, each token's experts and their weights (tokens x top)."""
         T, dev = x.shape[0], x.device
         logits = x.float().contiguous() @ self.router.t()
+        if self.top > g.ROUTE_MAX_TOP:  # more than gemm_route chooses
+            chosen, expert = logits.topk(self.top)
+            weight = torch.softmax(chosen, 1)
+            return logits, expert.int().masked_fill(weight.isnan(), -1), weight
         expert = torch.empty(T, self.top, dtype=torch.int32, device=dev)
         weight = torch.empty(T, self.top, device=dev)
         g.gemm_route(T, self.experts, self.top, g.F32, logits, self.experts, expert, weight)
@@ -145,8 +149,8 @@ class MoeLayer:
                           bias, epilogue)
 
     def train_step(self, x, dy, router=False):
-        """Output and the gradients of x, W1, b1 and W2 for the output's gradient dy; with `router` also that of the
-        router, through the weights (the choice of experts held fixed)."""
+        """Output and the gradients of x, W1, b1 and W2 for the output's gradient dy; with `router` (top up to
+        g.ROUTE_MAX_TOP) also that of the router, through the weights (the choice of experts held fixed)."""
         logits, expert, weight = self.choose(x)
         offsets, row, source = self.sort(expert)
         rows, E, T = source.numel(), self.experts, x.shape[0]

@@ -64,3 +64,27 @@ def test_softmax_scores_of_nan_are_not_hidden(moe, what):
         assert got[bad].isnan().all()
         assert moe.relative(got[~bad], w[~bad]) < 1e-3 if what == "token" else True
     assert moe.g.gemm_device_status() == 0
+
+
+def test_more_experts_a_token_than_the_routing_call_takes(moe):
+    """48 of 64 experts: bounds of the example's tests (bf16 1.6e-2, 8 bits 4e-2, 4 bits 1/3)."""
+    T, D = 21, 256
+    layer = moe.MoeLayer(D, 192, 64, 48)
+    layer.quantize()
+    layer.quantize_mx()
+    x, dy = tokens_of(T, D, 13), tokens_of(T, D, 14)
+    want, leaf = layer.reference(x, requires_grad=True)
+    want.backward(dy.float())
+    out, grads = layer.train_step(x, dy)
+    for got, bound in ((layer.forward(x), 1.6e-2), (layer.forward_i8(x), 4e-2), (layer.forward_mx(x), 1 / 3), (out, 1.6e-2)):
+        assert moe.relative(got, want) < bound
+    for (name, grad), t in zip(grads.items(), leaf):
+        assert moe.relative(grad, t.grad) < 1.6e-2, name
+    with pytest.raises(moe.g.GemmError):
+        layer.train_step(x, dy, router=True)
+    x[3, 0] = float("nan")
+    offsets, _, weight = layer.route(x)
+    assert int(offsets[-1]) == 20 * 48 and not weight[:20 * 48].isnan().any()
+    got = layer.forward(x)
+    assert got[3].isnan().all() and moe.relative(got[4:], want[4:]) < 1.6e-2
+    assert moe.g.gemm_device_status() == 0
