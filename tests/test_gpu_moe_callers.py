@@ -88,3 +88,14 @@ def test_more_experts_a_token_than_the_routing_call_takes(moe):
     got = layer.forward(x)
     assert got[3].isnan().all() and moe.relative(got[4:], want[4:]) < 1.6e-2
     assert moe.g.gemm_device_status() == 0
+
+
+@pytest.mark.parametrize("options,paths", [("--d 256 --f 192 --experts 8 --top 2", 3), ("--d 48 --f 80 --experts 8 --top 2", 2),
+                                           ("--d 64 --f 64 --experts 40 --top 36", 3)])
+def test_the_command(moe, monkeypatch, capsys, options, paths):
+    """Widths that are multiples of 16 and not of 32 (no 4-bit products), more experts a token than the routing call
+    takes (no router gradient)."""
+    monkeypatch.setattr(sys, "argv", ["moe_layer.py", "--tokens", "50", *options.split()])
+    moe.main()
+    out = capsys.readouterr().out
+    assert out.count("serving") == 2 * paths and out.count("training, d") == (4 if "36" in options else 5)
