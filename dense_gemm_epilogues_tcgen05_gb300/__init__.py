@@ -440,9 +440,13 @@ def gemm_mx_quantize(M, K, elem, x_dtype, X, ldx, Q, ldq, scale, lds, source=Non
                      stream=None) -> int:
     """Rows of X to block-scaled codes Q (MX_E4M3 / MX_E2M1, pitch ldq elements) and E8M0 scales (one per 32 k,
     pitch lds bytes).  With ``source`` (int32 device array of M) row i is row source[i] // top of X, which has
-    rows_x rows (M without a source); rows whose source is none stay as they were."""
-    st = lib.gemm_mx_quantize(M, K, elem, x_dtype, _ptr(X), ldx, M if rows_x is None else rows_x, _ptr(source), top,
-                              _ptr(Q), ldq, _ptr(scale), lds, _stream(stream))
+    rows_x rows (to be given then; M without a source); rows whose source is none stay as they were."""
+    if rows_x is None:
+        if source is not None:  # (M would leave out every row past it)
+            raise TypeError("gemm_mx_quantize: rows_x, the number of X's rows, is needed with a source")
+        rows_x = M
+    st = lib.gemm_mx_quantize(M, K, elem, x_dtype, _ptr(X), ldx, rows_x, _ptr(source), top, _ptr(Q), ldq, _ptr(scale), lds,
+                              _stream(stream))
     return _check(st, "gemm_mx_quantize")
 
 
