@@ -187,6 +187,31 @@ gemm_status_t make_plan(int64_t M, int64_t N, int64_t K, int ab, const void *A, 
 
 // ------------------------------------------------------- pointer checks --
 
+// The end of what is mapped from `first` on, at least `bytes` further, where one
+// mapping [start, start + extent) of the driver's holds `first` but not all of it:
+// virtual memory that was reserved at once and mapped in pieces (a caching
+// allocator's growing segments).  0: some of it is not mapped, or the rest belongs
+// to another allocation -- the driver's range of an ordinary one is its mapping.
+uint64_t mapped_end(uint64_t first, size_t bytes, uint64_t start, uint64_t extent) {
+    const DriverFns &f = driver_fns();
+    void *range = nullptr;
+    size_t reserved = 0;
+    if (f.ptr_attr == nullptr ||
+        f.ptr_attr(&range, CU_POINTER_ATTRIBUTE_RANGE_START_ADDR, static_cast<CUdeviceptr>(first)) != CUDA_SUCCESS ||
+        f.ptr_attr(&reserved, CU_POINTER_ATTRIBUTE_RANGE_SIZE, static_cast<CUdeviceptr>(first)) != CUDA_SUCCESS)
+        return 0;
+    const uint64_t from = reinterpret_cast<uint64_t>(range);
+    if (first < from || first - from > reserved || bytes > reserved - (first - from)) return 0;
+    uint64_t at = start + extent;
+    while (at < first + bytes) {
+        CUdeviceptr s = 0;
+        size_t n = 0;
+        if (f.addr_range(&s, &n, static_cast<CUdeviceptr>(at)) != CUDA_SUCCESS || s > at || n <= at - s) return 0;
+        at = s + n;
+    }
+    return at;
+}
+
 // The byte range [p, p + bytes) must lie inside one allocation the device can
 // address: device memory, or pinned / managed host memory.  Plain pageable
 // host pointers are rejected: a kernel given one would fault.  Where the
@@ -206,7 +231,8 @@ gemm_status_t check_range(const void *p, size_t bytes, int ordinal = -1, bool *l
         const DriverFns &f = driver_fns();
         if (f.ok && f.addr_range(&start, &extent, reinterpret_cast<CUdeviceptr>(p)) == CUDA_SUCCESS && extent > 0) {
             const uint64_t first = reinterpret_cast<uint64_t>(p);
-            return first >= start && first + bytes <= start + extent ? GEMM_OK : GEMM_ERR_INVALID_ARG;
+            return first >= start && (first + bytes <= start + extent || mapped_end(first, bytes, start, extent) != 0)
+                       ? GEMM_OK : GEMM_ERR_INVALID_ARG;
         }
     }
     cudaPointerAttributes attr;
@@ -231,7 +257,10 @@ gemm_status_t check_range(const void *p, size_t bytes, int ordinal = -1, bool *l
     }
     if (size > 0) {
         const uint64_t first = reinterpret_cast<uint64_t>(p);
-        if (first < base || first + bytes > base + size) return GEMM_ERR_INVALID_ARG;
+        if (first < base) return GEMM_ERR_INVALID_ARG;
+        if (first + bytes > base + size)  // (pieces: not for a multicast map)
+            return attr.type == cudaMemoryTypeDevice && mapped_end(first, bytes, base, size) != 0 ? GEMM_OK
+                                                                                                 : GEMM_ERR_INVALID_ARG;
     }
     if (local != nullptr) *local = attr.type == cudaMemoryTypeDevice && attr.device == ordinal;
     return GEMM_OK;
@@ -252,8 +281,12 @@ public:
             extent > 0) {
             start_ = start;
             extent_ = extent;
-            return first >= start && first - start <= extent && bytes <= extent - (first - start) ? GEMM_OK
-                                                                                                  : GEMM_ERR_INVALID_ARG;
+            if (first < start || first - start > extent) return GEMM_ERR_INVALID_ARG;
+            if (bytes <= extent - (first - start)) return GEMM_OK;
+            const uint64_t end = mapped_end(first, bytes, start, extent);
+            if (end == 0) return GEMM_ERR_INVALID_ARG;
+            extent_ = end - start_;
+            return GEMM_OK;
         }
         return check_range(p, bytes);
     }
