@@ -6,8 +6,9 @@
 // expert order and `source` each place's pair; -1: none (a slot without an
 // expert, a place behind the last pair).
 //
-// Measured (GB300): 16384 x 8 pairs over 256 experts sorted in 8.6 us, 512 over 64 in
-// 5.0 (the call's host side); 8 x 8192 rows of 4096 bf16 summed in 93 us, 6.5 TB/s; the
+// Measured (GB300): 16384 x 8 pairs over 256 experts sorted in 8.8 us (8.4 when the
+// second kernel counted its own pairs before it waited, which nothing promises to
+// work; over 1024 experts 41 and 38), 512 over 64 in 5.0 (the call's host side); 8 x 8192 rows of 4096 bf16 summed in 93 us, 6.5 TB/s; the
 // gradients of that for 4099 tokens of 2056, 6 slots, in 43 us, 4.8 TB/s (209 MB; 84
 // us with the loaded pieces unpacked at once, which left few of a thread's in flight;
 // 51 with two blocks per SM, which spill nothing, instead of three; with a warp to a
@@ -49,37 +50,40 @@ __global__ void __launch_bounds__(kCountThreads) route_count_kernel(const __grid
         a.counts[static_cast<long long>(e) * gridDim.x + blockIdx.x] = counts[e];
 }
 
-// Pairs begin .. end - 1 of one warp, 32 at a time: f(pair, expert, lanes of the same expert), expert -1 where there
-// is none.
+// The expert of this lane's pair p (-1: none, or the pair is not below `end`).
+__device__ __forceinline__ int expert_of(const RouteRowsArgs &a, int p, int end) {
+    const int e = p < end ? __ldg(a.expert + p) : -1;
+    return static_cast<unsigned>(e) < static_cast<unsigned>(a.E) ? e : -1;
+}
+
+// Pairs begin .. end - 1 of one warp, 32 at a time: f(pair, expert, lanes of the same expert).  e_first, same_first: of
+// the first 32.
 template <typename F>
-__device__ __forceinline__ void warp_pairs(const RouteRowsArgs &a, int begin, int end, F f) {
+__device__ __forceinline__ void warp_pairs(const RouteRowsArgs &a, int begin, int end, int e_first, unsigned same_first,
+                                           F f) {
     const int lane = threadIdx.x & 31;
-    for (int p0 = begin; p0 < end; p0 += 32) {
-        const int p = p0 + lane;
-        int e = p < end ? __ldg(a.expert + p) : -1;
-        if (static_cast<unsigned>(e) >= static_cast<unsigned>(a.E)) e = -1;
-        f(p, e, __match_any_sync(kAll, e));
+    if (begin < end) f(begin + lane, e_first, same_first);
+    for (int p0 = begin + 32; p0 < end; p0 += 32) {
+        const int e = expert_of(a, p0 + lane, end);
+        f(p0 + lane, e, __match_any_sync(kAll, e));
     }
 }
 
 __global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant__ RouteRowsArgs a) {
     extern __shared__ int smem[];
-    begin_after();  // (for the pairs too: only who has waited is promised to see what earlier grids wrote)
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int *first = smem;              // E + 1: pairs of the experts before
     int *start = first + a.E + 1;   // E: an expert's pairs in the chunks before
     int *own = start + a.E;         // warps x E: counts, then places
     for (int i = threadIdx.x; i < warps * a.E; i += blockDim.x) own[i] = 0;
+    if (threadIdx.x == 0) first[0] = 0;
     __syncthreads();
+    begin_after();  // (for the pairs too: only who has waited is promised to see what earlier grids wrote)
     const int begin = blockIdx.x * a.chunk, end = min(begin + a.chunk, a.P);
     const int per = (a.chunk + warps * 32 - 1) / (warps * 32) * 32;  // pairs of a warp
     const int w0 = min(begin + warp * per, end), w1 = min(w0 + per, end);
     int *mine = own + warp * a.E;
-    warp_pairs(a, w0, w1, [&](int, int e, unsigned same) {
-        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
-        __syncwarp();
-    });
-    __syncthreads();
+    const int e_first = expert_of(a, w0 + lane, w1);  // on its way beside the counts
     // every expert's total, and what lies before this chunk (a warp takes an expert, its lanes the chunks)
     if (gridDim.x > 1) {
         const int chunks = gridDim.x;
@@ -110,22 +114,14 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant_
                 }
             }
         }
-        __syncthreads();
     }
-    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
-        const int before = gridDim.x > 1 ? start[e] : 0;
-        int at = before;
-#pragma unroll 8
-        for (int w = 0; w < warps; ++w) {
-            const int n = own[w * a.E + e];
-            own[w * a.E + e] = at;
-            at += n;
-        }
-        if (gridDim.x == 1) first[e + 1] = at;
-    }
-    if (threadIdx.x == 0) first[0] = 0;
+    const unsigned same_first = __match_any_sync(kAll, e_first);
+    warp_pairs(a, w0, w1, e_first, same_first, [&](int, int e, unsigned same) {
+        if (e >= 0 && lane == __ffs(same) - 1) mine[e] += __popc(same);
+        __syncwarp();
+    });
     __syncthreads();
-    if (warp == 0) {
+    const auto sum_totals = [&] {  // by one warp: `first` from the experts' totals
         int base = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int e = e0 + lane;
@@ -138,11 +134,26 @@ __global__ void __launch_bounds__(1024) route_rows_kernel(const __grid_constant_
             if (e < a.E) first[e + 1] = base + v;
             base += __shfl_sync(kAll, v, 31);
         }
+    };
+    if (gridDim.x > 1 && warp == warps - 1) sum_totals();  // (while the others, if there are, place their warps)
+    for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+        int at = gridDim.x > 1 ? start[e] : 0;
+#pragma unroll 8
+        for (int w = 0; w < warps; ++w) {
+            const int n = own[w * a.E + e];
+            own[w * a.E + e] = at;
+            at += n;
+        }
+        if (gridDim.x == 1) first[e + 1] = at;
     }
     __syncthreads();
+    if (gridDim.x == 1) {
+        if (warp == 0) sum_totals();
+        __syncthreads();
+    }
     if (blockIdx.x == 0)
         for (int e = threadIdx.x; e <= a.E; e += blockDim.x) a.offsets[e] = first[e];
-    warp_pairs(a, w0, w1, [&](int p, int e, unsigned same) {
+    warp_pairs(a, w0, w1, e_first, same_first, [&](int p, int e, unsigned same) {
         int at = -1;
         if (e >= 0) {
             at = first[e] + mine[e] + __popc(same & ((1u << lane) - 1u));
@@ -549,8 +560,9 @@ cudaError_t launch_route_rows(const RouteRowsArgs &in, cudaStream_t s) {
     return launch_after(route_rows_kernel, dim3(chunks), 32 * warps, bytes, s, a);
 }
 
-// Few rows are split into parts, whole rounds of a warp, up to a warp for every part that the SMs hold: 8 rows of 6644
-// bf16 in 4.7 us, 864 of 6931 fp32 with an odd pitch in 8.5; with a warp to a row 8.9 and 18.5.
+// Few rows are split into parts, whole rounds of a warp, up to as many as 8 blocks per SM have warps: 8 rows of 6644
+// bf16 in 4.7 us, 864 of 6931 fp32 with an odd pitch in 8.5; with a warp to a row 8.9 and 18.5.  (The single elements'
+// kernels hold that many at a time; of the 16-byte pieces', whose registers are on their way, 3 run at once.)
 cudaError_t launch_rows_gather(int dtype, const RowsArgs &in, bool vec, int sms, cudaStream_t s) {
     RowsArgs a = in;
     constexpr int kWarps = kMoveThreads / 32;
