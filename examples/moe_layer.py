@@ -188,21 +188,25 @@ class MoeLayer:
         return out, grads
 
     def reference(self, x, requires_grad=False, router=False):
-        """The same layer expert by expert in plain fp32 operations; with gradients, its leaves as well (with `router`,
-        the router's weights among them)."""
-        logits, expert, weight = self.choose(x)
-        offsets, _, source = self.sort(expert)
-        pair = source.long()[:int(offsets[-1])]
-        token, weight = pair // self.top, weight.flatten()[pair]
+        """The same layer expert by expert in plain fp32 operations, the routing among them; with gradients, its leaves
+        as well (with `router`, the router's weights among them)."""
+        logits = x.float().contiguous() @ self.router.t()
+        expert = logits.argsort(dim=1, descending=True, stable=True)[:, :self.top]
+        expert = torch.where(logits.isnan().all(1, keepdim=True), self.experts, expert)  # (no expert)
+        weight = torch.softmax(logits.gather(1, expert.clamp(max=self.experts - 1)), 1).flatten()
+        counts = torch.bincount(expert.flatten(), minlength=self.experts + 1).tolist()
+        pair = expert.flatten().argsort(stable=True)[:sum(counts[:self.experts])]
+        token, weight = pair // self.top, weight[pair]
         leaf = [t.float().requires_grad_(requires_grad) for t in (x, self.w1, self.b1, self.w2)]
         if router:
             leaf.append(self.router.clone().requires_grad_(requires_grad))
-            chosen = torch.softmax((leaf[0] @ leaf[4].t()).gather(1, expert.long().clamp(min=0)), 1)
+            chosen = torch.softmax((leaf[0] @ leaf[4].t()).gather(1, expert.clamp(max=self.experts - 1)), 1)
             weight = chosen.flatten()[pair]
         x, w1, b1, w2 = leaf[:4]
-        ends, parts = offsets.tolist(), []
+        parts, end = [], 0
         for e in range(self.experts):
-            r = slice(ends[e], ends[e + 1])
+            r = slice(end, end + counts[e])
+            end += counts[e]
             h = torch.nn.functional.silu(x[token[r]] @ w1[e].t() + b1[e])
             parts.append(weight[r, None] * (h @ w2[e].t()))
         out = self.marked(torch.zeros_like(x).index_add(0, token, torch.cat(parts)), logits)

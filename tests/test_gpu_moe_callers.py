@@ -99,3 +99,14 @@ def test_the_command(moe, monkeypatch, capsys, options, paths):
     moe.main()
     out = capsys.readouterr().out
     assert out.count("serving") == 2 * paths and out.count("training, d") == (4 if "36" in options else 5)
+
+
+def test_the_reference_does_not_use_the_library(moe, monkeypatch):
+    """What the paths are compared with is computed without them."""
+    layer = moe.MoeLayer(64, 64, 8, 2)
+    x = tokens_of(9, 64, 15)
+    want = layer.reference(x)
+    for name in [n for n in moe.g.__all__ if n.startswith("gemm")]:
+        monkeypatch.setattr(moe.g, name, None)
+    again, leaf = layer.reference(x, requires_grad=True, router=True)
+    assert moe.relative(again, want) < 1e-5 and len(leaf) == 5
