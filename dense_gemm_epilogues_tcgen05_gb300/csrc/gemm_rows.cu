@@ -8,12 +8,14 @@
 //
 // Measured (GB300): 16384 x 8 pairs over 256 experts sorted in 8.8 us (8.4 when the
 // second kernel counted its own pairs before it waited, which nothing promises to
-// work; over 1024 experts 41 and 38), 512 over 64 in 5.0 (the call's host side); 8 x 8192 rows of 4096 bf16 summed in 93 us, 6.5 TB/s; the
-// gradients of that for 4099 tokens of 2056, 6 slots, in 43 us, 4.8 TB/s (209 MB; 84
-// us with the loaded pieces unpacked at once, which left few of a thread's in flight;
-// 51 with two blocks per SM, which spill nothing, instead of three; with a warp to a
-// token and no barrier 55, and 4 % less only for 16384 tokens of 2048), 8192 tokens of
-// 4096, 8 slots, in 190, 6.0 TB/s.
+// work; over 1024 experts 41 and 38), 512 over 64 in 5.0 (the call's host side); 8 x
+// 8192 rows of 4096 bf16 summed in 93 us, 6.5 TB/s; the gradients of that for 4099
+// tokens of 2056, 6 slots, in 43 us, 4.8 TB/s (209 MB; 84 us with the loaded pieces
+// unpacked at once, which left few of a thread's in flight; 51 with two blocks per SM,
+// which spill nothing, instead of three; with a warp to a token and no barrier 55, and
+// 4 % less only for 16384 tokens of 2048), 8192 tokens of 4096, 8 slots, in 190, 6.0
+// TB/s.  What is on its way is held in registers; copies into shared memory, which need
+// none, were not tried.
 #include <algorithm>
 
 #include "epilogue.cuh"

@@ -91,7 +91,8 @@ __device__ __forceinline__ int group_of(const GroupTable &t, int tile) {
 
 // ------------------------------------------------------------- row tiles --
 // The tensor-core kernels give a group of n rows ceil(n / most) tiles of one
-// common width, a multiple of 32 (`most` is one too).
+// common width, a multiple of 32 as `most` is (of 16 in the block-scaled product,
+// which walks its tiles itself).
 struct RowTilesOf {
     int most;
     __device__ __forceinline__ int operator()(int rows) const { return (rows + most - 1) / most; }
@@ -106,7 +107,7 @@ struct GroupedTile {
     int g;          // group
     int f0;         // first column of C (256 of them)
     int r0, nr;     // first row of C (gradient: of its index m) and how many this tile stores
-    int bn;         // MMA columns, nr rounded up to 32
+    int bn;         // MMA columns, nr rounded up to 32 (block-scaled: 16)
     int k0, nk;     // gradient: first row summed and how many; forward: 0 and K
 };
 

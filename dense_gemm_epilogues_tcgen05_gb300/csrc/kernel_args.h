@@ -172,7 +172,7 @@ struct GtcArgs {
     uint32_t a_mn;                  // forward: the weights are contiguous along F
     int a_whole, b_whole;           // see launch_grouped_tc
     const float *col_scale;         // integer product: G x F, NULL: 1
-    int most;                       // integer product: widest row tile (a multiple of 64)
+    int most;                       // widest row tile: integer product a multiple of 64, block-scaled kMxgMost
     int stages;                     // set by the launcher
     unsigned int *status;
 };
