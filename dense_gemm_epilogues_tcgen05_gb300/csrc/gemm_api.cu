@@ -46,7 +46,7 @@ typedef CUresult (*PtrAttrFn)(void *, CUpointer_attribute, CUdeviceptr);
 struct DriverFns {
     EncodeTiledFn encode = nullptr;
     AddrRangeFn addr_range = nullptr;
-    PtrAttrFn ptr_attr = nullptr;  // optional: extents of host allocations
+    PtrAttrFn ptr_attr = nullptr;  // optional: extents of host allocations and of reservations
     bool ok = false;
 };
 
@@ -212,8 +212,8 @@ uint64_t mapped_end(uint64_t first, size_t bytes, uint64_t start, uint64_t exten
     return at;
 }
 
-// The byte range [p, p + bytes) must lie inside one allocation the device can
-// address: device memory, or pinned / managed host memory.  Plain pageable
+// The byte range [p, p + bytes) must lie inside one allocation (or one reservation,
+// mapped in pieces) the device can address: device memory, or pinned / managed host memory.  Plain pageable
 // host pointers are rejected: a kernel given one would fault.  Where the
 // driver reports the allocation's extent (device memory always; host
 // allocations where it knows them) the range must fit inside it.  When

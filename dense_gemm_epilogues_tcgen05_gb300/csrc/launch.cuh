@@ -8,14 +8,15 @@
 
 namespace gb300 {
 
-// Begins every kernel launched by launch_after: the grids before it in the stream
-// are done and their memory is visible; the next grid may be set up meanwhile.
+// Begins every kernel launched by launch_after, which touches its shared memory at
+// most before it: the grids before it in the stream are done and their memory is
+// visible to the thread that waited; the next grid may be set up meanwhile.
 __device__ __forceinline__ void begin_after() {
     grid_dep_wait();
     grid_dep_launch();
 }
 
-// Launches `kernel`, which calls begin_after first, so that its blocks are set up
+// Launches `kernel`, which begins with begin_after, so that its blocks are set up
 // while the grid before it in the stream ends.
 template <typename Args>
 cudaError_t launch_after(void (*kernel)(const Args), dim3 grid, int threads, int smem, cudaStream_t stream,
